@@ -13,6 +13,14 @@ raise.
     o, S, per_token = decode(q, k, v, beta, log_alpha, state)   # m tokens per sequence
     y, conv_state = short_conv(x, weight, conv_state)            # rolling causal conv
     dq, dk, dv, dbeta, dlog_alpha, dS0 = backward(q, k, v, beta, log_alpha, d_o)
+    dx, dweight, dbias, dstate = short_conv_backward(x, weight, d_y)
+
+The stages and the recurrence a hybrid model runs beside it (``sublayer.py``):
+
+    y, S = ssm_prefill(x, dt, A, B, C, D=D, dt_bias=bias, dt_softplus=True)
+    y, S, per_token = ssm_decode(x, dt, A, B, C, state)          # a few tokens
+    out, normed = block_norm(x, residual, post_weight=w, gate=z, pre_weight=w2)
+    dx, dres, dw, dz, ds, dw2 = block_norm_backward(x, d_out, d_normed, residual, ...)
 
 ``prologue`` (prefill and decode) fuses the stages that precede the
 recurrence: PROLOGUE_GATE_SOFTPLUS (log_alpha holds x, log alpha =
@@ -34,7 +42,10 @@ import torch
 
 __all__ = ["prefill", "prefill_noalloc", "NOALLOC_SCRATCH_BYTES", "decode_step", "decode", "short_conv", "backward", "workspace_bytes", "max_chunks",
            "lib", "KDAError", "PrefillArgs", "DecodeArgs", "ConvArgs", "BackwardArgs", "KDA_F32", "KDA_BF16", "PROLOGUE_GATE_SOFTPLUS",
-           "PROLOGUE_BETA_SIGMOID", "PROLOGUE_QK_L2NORM", "PROLOGUE_ALL"]
+           "PROLOGUE_BETA_SIGMOID", "PROLOGUE_QK_L2NORM", "PROLOGUE_ALL",
+           "short_conv_backward", "ssm_prefill", "ssm_decode", "block_norm", "block_norm_backward",
+           "ConvBackwardArgs", "SsmArgs", "SsmDecodeArgs", "BlockNormArgs", "BlockNormBackwardArgs",
+           "GATE_SIGMOID", "GATE_SILU", "SSM_CHUNK"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkda.so")
@@ -43,6 +54,8 @@ KDA_F32, KDA_BF16 = 0, 1
 PROLOGUE_GATE_SOFTPLUS, PROLOGUE_BETA_SIGMOID, PROLOGUE_QK_L2NORM = 1, 2, 4
 PROLOGUE_ALL = 7
 _STATUS_BAD_SEQLENS = 6
+GATE_SIGMOID, GATE_SILU = 0, 1
+SSM_CHUNK = 64  # tokens between the scan's chunk states (KDA_SSM_CHUNK)
 # fixed per-GPU scratch of kda_prefill_chunked_noalloc (KDA_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 256 << 20
 
@@ -111,6 +124,55 @@ class BackwardArgs(ctypes.Structure):
     ]
 
 
+def _fields(text):
+    """ctypes fields from "kind: name name ..." lines: i = int32, l = int64, p = pointer, f = float, z = size_t."""
+    kinds = {"i": ctypes.c_int32, "l": ctypes.c_int64, "p": ctypes.c_void_p, "f": ctypes.c_float, "z": ctypes.c_size_t}
+    return [(name, kinds[line.split(":")[0].strip()]) for line in text.strip().splitlines()
+            for name in line.split(":")[1].split()]
+
+
+class ConvBackwardArgs(ctypes.Structure):
+    """Mirror of ``kda_conv_backward_args`` (include/kda.h)."""
+    _fields_ = _fields("""
+        i: B T C W num_seqs in_dtype grad_dtype activation
+        p: x weight bias cu_seqlens initial_state d_y d_final_state dx dweight dbias d_initial_state workspace
+        z: workspace_bytes""")
+
+
+class SsmArgs(ctypes.Structure):
+    """Mirror of ``kda_ssm_args`` (include/kda.h)."""
+    _fields_ = _fields("""
+        i: B T H G d_head d_state num_seqs in_dtype out_dtype dt_softplus
+        l: x_stride_b x_stride_t b_stride_b b_stride_t c_stride_b c_stride_t
+        p: x dt Bm Cm A D dt_bias cu_seqlens initial_state final_state chunk_states y device_status workspace
+        z: workspace_bytes""")
+
+
+class SsmDecodeArgs(ctypes.Structure):
+    """Mirror of ``kda_ssm_decode_args`` (include/kda.h)."""
+    _fields_ = _fields("""
+        i: B H G d_head d_state n_tokens in_dtype out_dtype dt_softplus
+        l: x_stride_b x_stride_t b_stride_b b_stride_t c_stride_b c_stride_t
+        p: x dt Bm Cm A D dt_bias initial_state final_state token_states y""")
+
+
+class BlockNormArgs(ctypes.Structure):
+    """Mirror of ``kda_block_norm_args`` (include/kda.h)."""
+    _fields_ = _fields("""
+        l: rows
+        i: dim group dtype gate_activation gate_first post_per_channel
+        f: eps
+        l: x_stride gate_stride residual_stride
+        p: x gate residual post_weight scale pre_weight out normed""")
+
+
+class BlockNormBackwardArgs(ctypes.Structure):
+    """Mirror of ``kda_block_norm_backward_args`` (include/kda.h)."""
+    _fields_ = [("f", BlockNormArgs)] + _fields("""
+        p: d_out d_normed dx dgate dresidual dpost_weight dscale dpre_weight workspace
+        z: workspace_bytes""")
+
+
 _lib = None
 
 
@@ -143,6 +205,16 @@ def lib():
         L.kda_backward_workspace_bytes.restype = ctypes.c_size_t
         L.kda_backward.argtypes = [BP, P]
         L.kda_backward.restype = I32
+        for name, cls in (("kda_short_conv_backward", ConvBackwardArgs), ("kda_ssm_prefill", SsmArgs),
+                          ("kda_ssm_decode", SsmDecodeArgs),
+                          ("kda_block_norm", BlockNormArgs), ("kda_block_norm_backward", BlockNormBackwardArgs)):
+            fn = getattr(L, name)
+            fn.argtypes, fn.restype = [ctypes.POINTER(cls), P], I32
+        for name, cls in (("kda_short_conv_backward_workspace_bytes", ConvBackwardArgs), ("kda_ssm_workspace_bytes", SsmArgs),
+                          ("kda_block_norm_backward_workspace_bytes", BlockNormBackwardArgs)):
+            fn = getattr(L, name)
+            fn.argtypes, fn.restype = [ctypes.POINTER(cls)], ctypes.c_size_t
+        L.kda_ssm_max_chunks.argtypes, L.kda_ssm_max_chunks.restype = [ctypes.POINTER(SsmArgs)], ctypes.c_int64
         L.kda_status_string.argtypes = [I32]
         L.kda_status_string.restype = ctypes.c_char_p
         L.kda_abi_version.restype = I32
@@ -547,3 +619,7 @@ def backward(q, k, v, beta, log_alpha, d_o, initial_state=None, d_final_state=No
     if device_status is not None:  # the workspace's first word is the call's status
         device_status.copy_(ws[:4].view(torch.int32))
     return out["dq"], out["dk"], out["dv"], out["dbeta"], out["dlog_alpha"], out["d_initial_state"]
+
+
+from .sublayer import (block_norm, block_norm_backward, short_conv_backward,  # noqa: E402
+                       ssm_decode, ssm_prefill)

@@ -3,10 +3,12 @@
 // argument has been checked; nothing here allocates or synchronises.
 #include "../../include/kda.h"
 #include "kda_launch.hpp"
+#include "kda_ssm_scan.hpp"
 
 #include <atomic>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 using namespace kda;
@@ -440,6 +442,218 @@ kda_status kda_backward(const kda_backward_args *a, void *hip_stream) {
     p.cu_seqlens = a->cu_seqlens; p.chunk_off = tp.chunk_off; p.status = tp.status;
     p.B = a->B; p.T = a->T; p.H = a->H; p.dk = a->d_k; p.dv = a->d_v; p.N = a->num_seqs;
     e = launch_backward(p, a->in_dtype, s);
+    return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+// ---------------------------------------------------------------- conv grad
+namespace {
+kda_status check_conv_backward(const kda_conv_backward_args *a, bool need_ptrs) {
+    if (!a) return KDA_ERR_NULL_ARG;
+    if (a->B < 1 || a->T < 0 || a->C < 1 || a->W < 1 || a->num_seqs < 0) return KDA_ERR_BAD_SHAPE;
+    if (a->W > 8 || a->C % 8 != 0) return KDA_ERR_UNSUPPORTED;
+    if (!dtype_ok(a->in_dtype) || !dtype_ok(a->grad_dtype)) return KDA_ERR_UNSUPPORTED;
+    if (a->activation != KDA_CONV_NONE && a->activation != KDA_CONV_SILU) return KDA_ERR_UNSUPPORTED;
+    if (a->cu_seqlens) {
+        if (a->B != 1 || a->num_seqs < 1) return KDA_ERR_BAD_SHAPE;
+    } else if (a->num_seqs != a->B) {
+        return KDA_ERR_BAD_SHAPE;
+    }
+    const int64_t most = (static_cast<int64_t>(1) << 31) - 1;
+    if (static_cast<int64_t>(a->B) * a->T * a->C > most || static_cast<int64_t>(a->num_seqs) * a->C > most)
+        return KDA_ERR_UNSUPPORTED;
+    if (!need_ptrs) return KDA_OK;
+    const bool any_tokens = static_cast<int64_t>(a->B) * a->T > 0;
+    if (!a->weight || !a->dweight || !a->workspace || (any_tokens && (!a->x || !a->d_y || !a->dx))) return KDA_ERR_NULL_ARG;
+    for (const void *ptr : {a->x, a->d_y, static_cast<const void *>(a->dx)})
+        if (reinterpret_cast<uintptr_t>(ptr) % 16) return KDA_ERR_UNSUPPORTED;  // rows are moved as vectors
+    return KDA_OK;
+}
+ConvGradParams conv_backward_params(const kda_conv_backward_args *a) {
+    ConvGradParams p{};
+    p.x = a->x; p.d_y = a->d_y; p.weight = a->weight; p.bias = a->bias; p.cu_seqlens = a->cu_seqlens;
+    p.initial_state = a->initial_state; p.d_final = a->d_final_state;
+    p.dx = a->dx; p.dweight = a->dweight; p.dbias = a->dbias; p.d_initial = a->d_initial_state;
+    p.partial = static_cast<float *>(a->workspace);
+    p.B = a->B; p.T = a->T; p.C = a->C; p.W = a->W; p.N = a->num_seqs;
+    p.silu = a->activation == KDA_CONV_SILU;
+    return p;
+}
+}  // namespace
+
+size_t kda_short_conv_backward_workspace_bytes(const kda_conv_backward_args *a) {
+    return check_conv_backward(a, false) == KDA_OK ? conv_grad_bytes(conv_backward_params(a)) : 0;
+}
+
+kda_status kda_short_conv_backward(const kda_conv_backward_args *a, void *hip_stream) {
+    const kda_status st = check_conv_backward(a, true);
+    if (st != KDA_OK) return st;
+    if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign) return KDA_ERR_BAD_SHAPE;
+    if (a->workspace_bytes < kda_short_conv_backward_workspace_bytes(a)) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    const hipError_t e = launch_short_conv_grad(conv_backward_params(a), a->in_dtype, a->grad_dtype,
+                                                static_cast<hipStream_t>(hip_stream));
+    return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+// --------------------------------------------------------------- block norm
+namespace {
+kda_status check_block_norm(const kda_block_norm_args *a, bool need_ptrs, bool need_out) {
+    if (!a) return KDA_ERR_NULL_ARG;
+    if (a->rows < 0 || a->dim < 1 || a->group < 1 || a->dim % a->group != 0) return KDA_ERR_BAD_SHAPE;
+    if (a->dim > 16384 || a->rows > (static_cast<int64_t>(1) << 40) / a->dim) return KDA_ERR_UNSUPPORTED;
+    if (!dtype_ok(a->dtype)) return KDA_ERR_UNSUPPORTED;
+    if (a->gate_activation != KDA_GATE_SIGMOID && a->gate_activation != KDA_GATE_SILU) return KDA_ERR_UNSUPPORTED;
+    if (!(a->eps >= 0.f)) return KDA_ERR_BAD_SHAPE;
+    if (!need_ptrs || a->rows == 0) return KDA_OK;
+    if (!a->x || (need_out && (!a->out || (a->pre_weight && !a->normed)))) return KDA_ERR_NULL_ARG;
+    if (need_out && !a->pre_weight && a->normed) return KDA_ERR_BAD_SHAPE;
+    if (a->rows > 1)  // rows may repeat (stride 0) or be padded, not overlap in part
+        for (const int64_t st : {a->x_stride, a->gate ? a->gate_stride : 0, a->residual ? a->residual_stride : 0})
+            if (st < 0 || (st > 0 && st < a->dim)) return KDA_ERR_BAD_SHAPE;
+    return KDA_OK;
+}
+NormParams norm_params(const kda_block_norm_args *a) {
+    NormParams p{};
+    p.x = a->x; p.gate = a->gate; p.residual = a->residual;
+    p.post_weight = a->post_weight; p.scale = a->scale; p.pre_weight = a->pre_weight;
+    p.out = a->out; p.normed = a->normed;
+    p.rows = a->rows; p.x_stride = a->x_stride; p.gate_stride = a->gate_stride; p.residual_stride = a->residual_stride;
+    p.dim = a->dim; p.group = a->group; p.silu = a->gate_activation == KDA_GATE_SILU;
+    p.gate_first = a->gate_first != 0; p.post_per_channel = a->post_per_channel != 0;
+    p.eps = a->eps; p.inv_group = 1.f / static_cast<float>(a->group); p.inv_dim = 1.f / static_cast<float>(a->dim);
+    return p;
+}
+}  // namespace
+
+kda_status kda_block_norm(const kda_block_norm_args *a, void *hip_stream) {
+    const kda_status st = check_block_norm(a, true, true);
+    if (st != KDA_OK) return st;
+    if (a->rows == 0) return KDA_OK;
+    const hipError_t e = launch_block_norm(norm_params(a), a->dtype, static_cast<hipStream_t>(hip_stream));
+    return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+size_t kda_block_norm_backward_workspace_bytes(const kda_block_norm_backward_args *a) {
+    if (!a || check_block_norm(&a->f, false, false) != KDA_OK) return 0;
+    return block_norm_grad_bytes(norm_params(&a->f));
+}
+
+kda_status kda_block_norm_backward(const kda_block_norm_backward_args *a, void *hip_stream) {
+    if (!a) return KDA_ERR_NULL_ARG;
+    const kda_status st = check_block_norm(&a->f, true, false);
+    if (st != KDA_OK) return st;
+    if ((a->d_normed && !a->f.pre_weight) || (a->dgate && !a->f.gate) || (a->dresidual && !a->f.residual) ||
+        (a->dpost_weight && !a->f.post_weight) || (a->dscale && !a->f.scale) || (a->dpre_weight && !a->f.pre_weight))
+        return KDA_ERR_BAD_SHAPE;
+    if (!a->workspace || (a->f.rows > 0 && !a->dx)) return KDA_ERR_NULL_ARG;
+    if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign) return KDA_ERR_BAD_SHAPE;
+    if (a->workspace_bytes < kda_block_norm_backward_workspace_bytes(a)) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    NormGradParams g{};
+    g.f = norm_params(&a->f);
+    g.f.out = nullptr; g.f.normed = nullptr;
+    g.d_out = a->d_out; g.d_normed = a->d_normed;
+    g.dx = a->dx; g.dgate = a->dgate; g.dresidual = a->dresidual;
+    g.dscale = a->dscale; g.dpre = a->dpre_weight; g.dpost = a->dpost_weight;
+    g.partial = static_cast<float *>(a->workspace);
+    const hipError_t e = launch_block_norm_grad(g, a->f.dtype, static_cast<hipStream_t>(hip_stream));
+    return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+// ------------------------------------------------------ state space scan
+namespace {
+// the checks that the scan's three calls share; tokens = B T (or B m)
+struct SsmShape {
+    int32_t B, T, H, G, P, Ns, in_dtype, out_dtype, softplus;
+    int64_t xb, xt, bb, bt, cb, ct;
+};
+kda_status check_ssm(const SsmShape &s) {
+    if (s.B < 0 || s.T < 0 || s.H < 1 || s.G < 1 || s.H % s.G != 0) return KDA_ERR_BAD_SHAPE;
+    if (!dim_ok(s.P) || !dim_ok(s.Ns)) return (s.P < 1 || s.Ns < 1) ? KDA_ERR_BAD_SHAPE : KDA_ERR_UNSUPPORTED;
+    if (!dtype_ok(s.in_dtype) || !dtype_ok(s.out_dtype)) return KDA_ERR_UNSUPPORTED;
+    if (s.softplus != 0 && s.softplus != 1) return KDA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(s.B) * s.T * s.H > (static_cast<int64_t>(1) << 31) - 1) return KDA_ERR_UNSUPPORTED;
+    for (const int64_t st : {s.xb, s.xt, s.bb, s.bt, s.cb, s.ct}) {
+        if (st < 0) return KDA_ERR_BAD_SHAPE;
+        if (st % 8) return KDA_ERR_UNSUPPORTED;
+    }
+    return KDA_OK;
+}
+bool misaligned(std::initializer_list<const void *> ptrs) {
+    for (const void *p : ptrs)
+        if (reinterpret_cast<uintptr_t>(p) % 16) return true;
+    return false;
+}
+}  // namespace
+
+namespace {
+kda_status check_ssm_prefill(const kda_ssm_args *a, bool need_ptrs) {
+    if (!a) return KDA_ERR_NULL_ARG;
+    if (a->B < 1 || a->num_seqs < 0) return KDA_ERR_BAD_SHAPE;
+    if (a->cu_seqlens ? a->B != 1 || a->num_seqs < 1 : a->num_seqs != a->B) return KDA_ERR_BAD_SHAPE;
+    const kda_status st = check_ssm({a->B, a->T, a->H, a->G, a->d_head, a->d_state, a->in_dtype, a->out_dtype, a->dt_softplus,
+                                     a->x_stride_b, a->x_stride_t, a->b_stride_b, a->b_stride_t, a->c_stride_b, a->c_stride_t});
+    if (st != KDA_OK) return st;
+    if (static_cast<int64_t>(a->num_seqs) * a->H > (1 << 24)) return KDA_ERR_UNSUPPORTED;
+    if (!need_ptrs) return KDA_OK;
+    if (!a->A || (a->T > 0 && (!a->x || !a->dt || !a->Bm || !a->Cm || !a->y))) return KDA_ERR_NULL_ARG;
+    if (misaligned({a->x, a->Bm, a->Cm, a->initial_state, a->final_state, a->chunk_states, a->y})) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+SsmParams ssm_params(const kda_ssm_args *a) {
+    SsmParams p{};
+    p.x = a->x; p.dt = a->dt; p.Bm = a->Bm; p.Cm = a->Cm; p.A = a->A; p.D = a->D; p.dt_bias = a->dt_bias;
+    p.cu_seqlens = a->cu_seqlens; p.initial_state = a->initial_state; p.final_state = a->final_state;
+    p.chunk_states = a->chunk_states; p.y = a->y;
+    p.x_sb = a->x_stride_b; p.x_st = a->x_stride_t; p.b_sb = a->b_stride_b; p.b_st = a->b_stride_t;
+    p.c_sb = a->c_stride_b; p.c_st = a->c_stride_t;
+    p.B = a->B; p.T = a->T; p.H = a->H; p.G = a->G; p.P = a->d_head; p.Ns = a->d_state; p.N = a->num_seqs;
+    p.softplus = a->dt_softplus;
+    return p;
+}
+}  // namespace
+
+int64_t kda_ssm_max_chunks(const kda_ssm_args *a) {
+    return check_ssm_prefill(a, false) == KDA_OK ? ssm_plan(ssm_params(a), a->cu_seqlens != nullptr).chunks_bound : 0;
+}
+
+size_t kda_ssm_workspace_bytes(const kda_ssm_args *a) {
+    return check_ssm_prefill(a, false) == KDA_OK ? ssm_plan(ssm_params(a), a->cu_seqlens != nullptr).bytes() : 0;
+}
+
+kda_status kda_ssm_prefill(const kda_ssm_args *a, void *hip_stream) {
+    const kda_status st = check_ssm_prefill(a, true);
+    if (st != KDA_OK) return st;
+    if (!a->workspace) return KDA_ERR_NULL_ARG;
+    if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign) return KDA_ERR_BAD_SHAPE;
+    SsmScan q{};
+    q.p = ssm_params(a);
+    const SsmPlan plan = ssm_plan(q.p, a->cu_seqlens != nullptr);
+    if (a->workspace_bytes < plan.bytes()) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    ssm_layout(q, plan, static_cast<char *>(a->workspace));
+    q.user_status = a->device_status;
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    hipError_t e = a->cu_seqlens ? launch_ssm_table(q, s) : hipSuccess;
+    if (e == hipSuccess) e = launch_ssm_scan(q, plan, SSM_FULL, a->in_dtype, a->out_dtype, s);
+    return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+kda_status kda_ssm_decode(const kda_ssm_decode_args *a, void *hip_stream) {
+    if (!a) return KDA_ERR_NULL_ARG;
+    if (a->n_tokens < 1) return KDA_ERR_BAD_SHAPE;
+    const kda_status st = check_ssm({a->B, a->n_tokens, a->H, a->G, a->d_head, a->d_state, a->in_dtype, a->out_dtype,
+                                     a->dt_softplus, a->x_stride_b, a->x_stride_t, a->b_stride_b, a->b_stride_t,
+                                     a->c_stride_b, a->c_stride_t});
+    if (st != KDA_OK) return st;
+    if (a->B == 0) return KDA_OK;
+    if (!a->x || !a->dt || !a->Bm || !a->Cm || !a->A || !a->initial_state || !a->y) return KDA_ERR_NULL_ARG;
+    if (misaligned({a->x, a->Bm, a->Cm, a->initial_state, a->final_state, a->token_states, a->y})) return KDA_ERR_UNSUPPORTED;
+    SsmParams p{};
+    p.x = a->x; p.dt = a->dt; p.Bm = a->Bm; p.Cm = a->Cm; p.A = a->A; p.D = a->D; p.dt_bias = a->dt_bias;
+    p.initial_state = a->initial_state; p.final_state = a->final_state; p.y = a->y;
+    p.x_sb = a->x_stride_b; p.x_st = a->x_stride_t; p.b_sb = a->b_stride_b; p.b_st = a->b_stride_t;
+    p.c_sb = a->c_stride_b; p.c_st = a->c_stride_t;
+    p.B = a->B; p.T = a->n_tokens; p.H = a->H; p.G = a->G; p.P = a->d_head; p.Ns = a->d_state; p.N = a->B;
+    p.softplus = a->dt_softplus;
+    const hipError_t e = launch_ssm_decode(p, a->token_states, a->in_dtype, a->out_dtype, static_cast<hipStream_t>(hip_stream));
     return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 

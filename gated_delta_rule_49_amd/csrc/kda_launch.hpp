@@ -3,6 +3,8 @@
 #pragma once
 #include <hip/hip_runtime.h>
 #include "kda_prefill_common.hpp"
+#include <algorithm>
+#include <type_traits>
 
 namespace kda {
 
@@ -98,6 +100,60 @@ bool f32mm_supported(int dk, int dv, int C, uint32_t prologue);
 bool f32mm_overlap_shape(int N, int H, int dk, int dv);
 hipError_t launch_prefill_f32mm(const PrefillParams &p, float *blocks, int in_dtype, int out_dtype, hipStream_t s,
                                 hipEvent_t mid);
+
+// gradients of the short convolution (validated arguments)
+struct ConvGradParams {
+    const void *x, *d_y;        // [B, T, C]
+    const float *weight, *bias; // [C, W], nullable [C]
+    const int32_t *cu_seqlens;  // nullable
+    const float *initial_state; // nullable [N, C, W - 1]
+    const float *d_final;       // nullable [N, C, W - 1]
+    void *dx;                   // [B, T, C]
+    float *dweight, *dbias;     // [C, W], nullable [C]
+    float *d_initial;           // nullable [N, C, W - 1]
+    float *partial;             // workspace
+    int32_t B, T, C, W, N;
+    int32_t silu;
+};
+size_t conv_grad_bytes(const ConvGradParams &p);
+hipError_t launch_short_conv_grad(const ConvGradParams &p, int in_dtype, int grad_dtype, hipStream_t s);
+
+// norm after a block, gate, scaled residual, norm before the next (validated)
+struct NormParams {
+    const void *x, *gate, *residual;  // gate, residual nullable
+    const float *post_weight, *scale, *pre_weight;  // each nullable
+    void *out, *normed;
+    int64_t rows, x_stride, gate_stride, residual_stride;
+    int32_t dim, group, silu, gate_first, post_per_channel;
+    float eps, inv_group, inv_dim;
+};
+struct NormGradParams {
+    NormParams f;
+    const void *d_out, *d_normed;
+    void *dx, *dgate, *dresidual;
+    float *dscale, *dpre, *dpost;
+    float *partial;  // workspace: [teams][norm_partial_cols]
+};
+__host__ __device__ inline int64_t norm_partial_cols(const NormParams &p) { return 3 * static_cast<int64_t>(p.dim); }
+size_t block_norm_grad_bytes(const NormParams &p);
+hipError_t launch_block_norm(const NormParams &p, int dtype, hipStream_t s);
+hipError_t launch_block_norm_grad(const NormGradParams &g, int dtype, hipStream_t s);
+
+// selective state space scan (validated arguments)
+struct SsmParams {
+    const void *x, *dt, *Bm, *Cm;
+    const float *A, *D, *dt_bias;    // D, dt_bias nullable
+    const int32_t *cu_seqlens;       // nullable
+    const float *initial_state;      // nullable
+    float *final_state, *chunk_states;  // nullable
+    void *y;
+    int64_t x_sb, x_st, b_sb, b_st, c_sb, c_st;  // strides in elements
+    int32_t B, T, H, G, P, Ns;       // P = d_head, Ns = d_state
+    int32_t N;                       // sequences
+    int32_t softplus;
+};
+// m tokens per sequence (T = m, N = B)
+hipError_t launch_ssm_decode(const SsmParams &p, float *token_states, int in_dtype, int out_dtype, hipStream_t s);
 
 // m tokens per sequence; state_out and token_states nullable, state_out may
 // alias state_in

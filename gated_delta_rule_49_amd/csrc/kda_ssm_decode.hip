@@ -1,0 +1,124 @@
+// Selective state space scan, a few tokens per sequence (include/kda.h):
+//     S_t = a_t S_{t-1} + dt_t B_t x_t^T ,  y_t = S_t^T C_t + D x_t ,
+//     dt_t = softplus(dt + bias), a_t = exp(A dt_t).
+// Bound by the state's HBM traffic: every (sequence, head) reads its
+// d_state x d_head fp32 state once and writes it once whatever the number of
+// tokens.  A workgroup owns one state: a thread holds float4 columns of R
+// rows, so consecutive threads move consecutive 16-byte pieces of the state;
+// the sum over rows goes through lane exchanges and one LDS exchange between
+// the waves per token.
+#include "kda_ssm_scan.hpp"
+
+namespace kda {
+
+namespace {
+
+template <int NS, int P>
+struct DecodeShape {
+    static constexpr int LANES = P / 4;                             // float4 columns of a row
+    static constexpr int NT = NS * LANES < 64 ? 64 : NS * LANES > 256 ? 256 : NS * LANES;
+    static constexpr int RG = NT / LANES;                           // rows in flight
+    static constexpr int R = NS / RG;                               // rows of a thread
+    static constexpr int WAVES = NT / 64;
+};
+
+template <typename TI, typename TO, int NS, int P>
+__global__ void __launch_bounds__(256) ssm_decode_kernel(SsmParams p, float *token_states) {
+    using Sh = DecodeShape<NS, P>;
+    constexpr int LANES = Sh::LANES, RG = Sh::RG, R = Sh::R;
+    __shared__ f32x4 part[2][Sh::WAVES][LANES];
+    const int tid = threadIdx.x;
+    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    const int g = h / (p.H / p.G);
+    const int lane_p = tid % LANES, rg = tid / LANES;
+    const int64_t so = (static_cast<int64_t>(b) * p.H + h) * (NS * P);
+    auto at = [&](int i) { return (rg + i * RG) * P + lane_p * 4; };
+    f32x4 S[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) S[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p.initial_state + so + at(i)));
+    const TI *x = static_cast<const TI *>(p.x) + b * p.x_sb + static_cast<int64_t>(h) * P + lane_p * 4;
+    const TI *Bm = static_cast<const TI *>(p.Bm) + b * p.b_sb + static_cast<int64_t>(g) * NS + rg;
+    const TI *Cm = static_cast<const TI *>(p.Cm) + b * p.c_sb + static_cast<int64_t>(g) * NS + rg;
+    const TI *dtp = static_cast<const TI *>(p.dt) + static_cast<int64_t>(b) * p.T * p.H + h;
+    TO *y = static_cast<TO *>(p.y) + (static_cast<int64_t>(b) * p.T * p.H + h) * P + lane_p * 4;
+    const float A = p.A[h] * kLog2e, D = p.D ? p.D[h] : 0.f, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+    for (int t = 0; t < p.T; ++t) {
+        float dt = io<TI>::ld(dtp, static_cast<int64_t>(t) * p.H) + bias;
+        if (p.softplus) dt = softplus_rel(dt);
+        const float a = fast_exp2(A * dt);
+        f32x4 xv;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) xv[c] = io<TI>::ld(x, t * p.x_st + c);
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const float bn = dt * io<TI>::ld(Bm, t * p.b_st + i * RG);
+            const float cn = io<TI>::ld(Cm, t * p.c_st + i * RG);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                S[i][c] = fmaf(bn, xv[c], a * S[i][c]);
+                acc[c] = fmaf(cn, S[i][c], acc[c]);
+            }
+        }
+        if (token_states) {
+            float *ts = token_states + ((static_cast<int64_t>(b) * p.T + t) * p.H + h) * (NS * P);
+#pragma unroll
+            for (int i = 0; i < R; ++i) __builtin_nontemporal_store(S[i], reinterpret_cast<f32x4 *>(ts + at(i)));
+        }
+#pragma unroll
+        for (int m = LANES; m < 64; m <<= 1)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[c] += __shfl_xor(acc[c], m);
+        if (Sh::WAVES > 1) {  // two buffers: one barrier per token orders their reuse
+            if ((tid & 63) < LANES) part[t & 1][tid >> 6][lane_p] = acc;
+            lds_barrier();
+        }
+        if (tid < LANES) {
+            if (Sh::WAVES > 1) {
+                acc = part[t & 1][0][lane_p];
+#pragma unroll
+                for (int w = 1; w < Sh::WAVES; ++w) acc += part[t & 1][w][lane_p];
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) io<TO>::st(y, static_cast<int64_t>(t) * p.H * P + c, acc[c] + D * xv[c]);
+        }
+    }
+    if (p.final_state)
+#pragma unroll
+        for (int i = 0; i < R; ++i) __builtin_nontemporal_store(S[i], reinterpret_cast<f32x4 *>(p.final_state + so + at(i)));
+}
+
+template <typename TI, typename TO, int NS, int P>
+hipError_t run(const SsmParams &p, float *ts, hipStream_t s) {
+    hipLaunchKernelGGL((ssm_decode_kernel<TI, TO, NS, P>), dim3(static_cast<unsigned>(p.B) * p.H),
+                       dim3(DecodeShape<NS, P>::NT), 0, s, p, ts);
+    return hipGetLastError();
+}
+template <typename TI, typename TO, int NS>
+hipError_t run_p(const SsmParams &p, float *ts, hipStream_t s) {
+    switch (p.P) {
+        case 16: return run<TI, TO, NS, 16>(p, ts, s);
+        case 32: return run<TI, TO, NS, 32>(p, ts, s);
+        case 64: return run<TI, TO, NS, 64>(p, ts, s);
+        default: return run<TI, TO, NS, 128>(p, ts, s);
+    }
+}
+template <typename TI, typename TO>
+hipError_t run_n(const SsmParams &p, float *ts, hipStream_t s) {
+    switch (p.Ns) {
+        case 16: return run_p<TI, TO, 16>(p, ts, s);
+        case 32: return run_p<TI, TO, 32>(p, ts, s);
+        case 64: return run_p<TI, TO, 64>(p, ts, s);
+        default: return run_p<TI, TO, 128>(p, ts, s);
+    }
+}
+}  // namespace
+
+hipError_t launch_ssm_decode(const SsmParams &p, float *token_states, int in_dtype, int out_dtype, hipStream_t s) {
+    if (in_dtype == 0 && out_dtype == 0) return run_n<float, float>(p, token_states, s);
+    if (in_dtype == 0 && out_dtype == 1) return run_n<float, bf16_t>(p, token_states, s);
+    if (in_dtype == 1 && out_dtype == 0) return run_n<bf16_t, float>(p, token_states, s);
+    return run_n<bf16_t, bf16_t>(p, token_states, s);
+}
+
+}  // namespace kda

@@ -1,0 +1,263 @@
+// Selective state space scan in chunked form: shared by the prompt scan
+// (kda_ssm_prefill.hip) and the gradients (kda_ssm_backward.hip).
+//
+// Over a chunk of L tokens, with la_t = A dt_t (all logs base 2 in the code),
+// suf_t = sum_{s > t} la_s, tot = sum la, w_t = dt_t 2^suf_t:
+//     S_out = 2^tot S_in + sum_t B_t (w_t x_t)^T
+//     y_t   = 2^(-suf_t) [ C_t^T (2^tot S_in) + sum_{s <= t} (C_t . B_s) w_s x_s ] + D x_t
+// The causal scores C_t . B_s do not depend on the head: a workgroup whose
+// waves own heads of one group computes them once, and per head only the row
+// factors 2^(-suf_t) and the scaled inputs w_t x_t are left.  That form is
+// exact while 2^tot stays a normal number with room for its low-order parts;
+// a chunk that decays by more than kFastTot takes the second form,
+//     y_t = 2^(cum_t) C_t^T S_in + sum_{s <= t} (C_t . B_s) 2^(suf_s - suf_t) dt_s x_s ,
+// every exponent <= 0.
+//
+// Precision: bf16 inputs enter the matrix cores as they are; the state, the
+// scores and the scaled inputs are fp32 values split into bf16 parts (2 parts:
+// 2^-17 of the value).  fp32 inputs are split into 3 parts, and the products
+// of parts down to 2^-24 are kept.  Everything accumulates in fp32.
+#pragma once
+#include "kda_launch.hpp"
+
+namespace kda {
+
+// log(1 + e^x) to a few 2^-24 of ITSELF (softplus_f32 is so only in absolute
+// terms): step sizes of 0.001 multiply logs that add up over a long memory.
+//   e^-|x| = 2^n 2^r with n = rint(-|x| log2 e), r by a fused multiply-add
+//            against both halves of log2 e, |r| <= 1/2
+//   log(1 + y) = 2 atanh(y / (2 + y)), |y / (2 + y)| <= 1/3: seven odd terms
+//            leave less than (1/9)^7 / 15 = 1.4e-8 of it
+__device__ __forceinline__ float softplus_rel(float x) {
+    constexpr float kLog2eLo = 1.92596299e-08f;  // log2 e - kLog2e
+    const float m = -fabsf(x);
+    const float n = rintf(m * kLog2e);
+    const float r = fmaf(m, kLog2eLo, fmaf(m, kLog2e, -n));
+    const float y = ldexpf(fast_exp2(r), static_cast<int>(fmaxf(n, -200.f)));
+    const float s = y / (2.f + y), q = s * s;
+    float p = 1.f / 13.f;
+    p = fmaf(p, q, 1.f / 11.f);
+    p = fmaf(p, q, 1.f / 9.f);
+    p = fmaf(p, q, 1.f / 7.f);
+    p = fmaf(p, q, 1.f / 5.f);
+    p = fmaf(p, q, 1.f / 3.f);
+    const float l = 2.f * fmaf(s * q, p, s);
+    return x != x ? x : fmaxf(x, 0.f) + l;
+}
+
+// a chunk whose total decay is above 2^-kFastTot may use the first form: the
+// parts of 2^tot S_in reach down to about 2^(-kFastTot - 24), far above the
+// smallest normal number 2^-126, and 2^(-suf) <= 2^kFastTot does not overflow
+// with values below 2^64
+constexpr float kFastTot = 56.f;
+
+struct SsmScan {
+    SsmParams p;
+    const int32_t *seg_off;   // packed: [N + 1] first segment of each sequence
+    const int4 *seg_info;     // packed: (first token, length, sequence, index in its sequence)
+    const int32_t *chunk_off; // packed: [N + 1] first chunk of each sequence
+    const int32_t *status;    // packed: 0 = offsets valid
+    int32_t *user_status;     // nullable
+    float *seg_state;         // [segments, H, Ns, P]: the state entering each (phase 1: its own end state); null = unsplit
+    float *seg_log;           // [segments, H]: log2 of each segment's decay
+    int32_t seg_chunks;       // chunks of KDA_SSM_CHUNK tokens per segment
+    int32_t segs_bound;       // grid bound on the number of segments
+    int32_t segs_per_seq;     // unpacked
+    int32_t chunks_per_seq;   // unpacked
+};
+
+struct SsmSeg {
+    int row, t0, len, n, s, count;  // batch row, first token of it, tokens, sequence, index, segments of the sequence
+    int chunk;                      // first chunk's index among all chunks
+    bool valid;
+};
+__device__ __forceinline__ SsmSeg ssm_seg(const SsmScan &q, int x) {
+    SsmSeg g;
+    if (q.p.cu_seqlens) {
+        g.valid = *q.status == 0 && x < q.seg_off[q.p.N];
+        if (!g.valid) return g;
+        const int4 i = q.seg_info[x];
+        g.row = 0; g.t0 = i.x; g.len = i.y; g.n = i.z; g.s = i.w;
+        g.count = q.seg_off[g.n + 1] - q.seg_off[g.n];
+        g.chunk = q.chunk_off[g.n] + g.s * q.seg_chunks;
+    } else {
+        g.valid = x < q.p.N * q.segs_per_seq;
+        g.n = x / q.segs_per_seq;
+        g.s = x % q.segs_per_seq;
+        g.row = g.n;
+        g.t0 = g.s * q.seg_chunks * 64;
+        g.len = min(q.p.T - g.t0, q.seg_chunks * 64);
+        g.count = q.segs_per_seq;
+        g.chunk = g.n * q.chunks_per_seq + g.s * q.seg_chunks;
+    }
+    return g;
+}
+
+// Blocks of one segment and group are neighbours in the logical order; the
+// hardware deals consecutive block numbers to the 8 XCDs in turn, so each XCD
+// takes a contiguous run of the logical order and shares B and C in its L2.
+__device__ __forceinline__ int xcd_order(int block, int grid) { return (block & 7) * (grid >> 3) + (block >> 3); }
+
+// ---------------------------------------------------------------- operands --
+// NPART bf16 parts of 8 values
+template <int N> struct parts8 { frag8 f[N]; };
+
+template <int N>
+__device__ __forceinline__ void split_to(parts8<N> &o, int slot, float v) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const bf16_t h = f32_to_bf16(v);
+        o.f[i].s[slot] = h;
+        if (i + 1 < N) v -= bf16_to_f32(h);
+    }
+}
+
+// c += A B over the parts' products whose orders add up to less than ORD
+template <int NA, int NB, int ORD>
+__device__ __forceinline__ void mfma_parts(f32x4 &c, const parts8<NA> &a, const parts8<NB> &b) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            if (i + j < ORD) c = mfma16(a.f[i].v, b.f[j].v, c);
+}
+
+// Position of the 4-element granule q of a 32-column step: an operand's lane
+// group g = l / 16 reads granules g and 4 + g (kperm's slots) as one 16-byte
+// piece.
+__device__ __forceinline__ constexpr int granule_pos(int q) { return q < 4 ? 2 * q : 2 * (q - 4) + 1; }
+// element offset of column k (a multiple of 4) in a row of 32-column steps
+__device__ __forceinline__ constexpr int col_pos(int k) { return (k & ~31) + granule_pos((k >> 2) & 7) * 4; }
+
+union granule {
+    bf16_t s[4];
+    uint2 u;
+};
+
+// Four tokens by four channels of B or C as loaded
+template <typename T> struct quad;
+template <> struct quad<bf16_t> {
+    uint2 r[4];
+    static constexpr int PARTS = 1;
+    __device__ __forceinline__ void ld(int i, const bf16_t *p) { r[i] = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void zero(int i) { r[i] = make_uint2(0, 0); }
+    // part `part` of the four channels of token i / the four tokens of channel i
+    __device__ __forceinline__ granule row(int i, int) const { granule g; g.u = r[i]; return g; }
+    __device__ __forceinline__ granule col(int i, int) const {
+        granule g;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t w = i < 2 ? r[t].x : r[t].y;
+            g.s[t] = static_cast<bf16_t>((i & 1) ? w >> 16 : w & 0xffffu);
+        }
+        return g;
+    }
+};
+template <> struct quad<float> {
+    f32x4 r[4];
+    static constexpr int PARTS = 3;
+    __device__ __forceinline__ void ld(int i, const float *p) { r[i] = *reinterpret_cast<const f32x4 *>(p); }
+    __device__ __forceinline__ void zero(int i) { r[i] = f32x4{0.f, 0.f, 0.f, 0.f}; }
+    __device__ __forceinline__ static bf16_t part_of(float v, int part) {
+        for (int k = 0; k < part; ++k) v -= bf16_to_f32(f32_to_bf16(v));
+        return f32_to_bf16(v);
+    }
+    __device__ __forceinline__ granule row(int i, int part) const {
+        granule g;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) g.s[c] = part_of(r[i][c], part);
+        return g;
+    }
+    __device__ __forceinline__ granule col(int i, int part) const {
+        granule g;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) g.s[t] = part_of(r[t][i], part);
+        return g;
+    }
+};
+
+// PW / 16 neighbouring channels of one token, as a lane loads and stores them
+template <typename T, int CT> struct lanevec;
+template <> struct lanevec<bf16_t, 1> {
+    bf16_t u;
+    __device__ __forceinline__ void ld(const bf16_t *p) { u = *p; }
+    __device__ __forceinline__ void zero() { u = 0; }
+    __device__ __forceinline__ float get(int) const { return bf16_to_f32(u); }
+    __device__ __forceinline__ static void st(bf16_t *p, const float (&v)[1]) { *p = f32_to_bf16(v[0]); }
+};
+template <> struct lanevec<bf16_t, 2> {
+    uint32_t u;
+    __device__ __forceinline__ void ld(const bf16_t *p) { u = *reinterpret_cast<const uint32_t *>(p); }
+    __device__ __forceinline__ void zero() { u = 0; }
+    __device__ __forceinline__ float get(int c) const { return __uint_as_float(c ? (u & 0xffff0000u) : (u << 16)); }
+    __device__ __forceinline__ static void st(bf16_t *p, const float (&v)[2]) {
+        *reinterpret_cast<uint32_t *>(p) = static_cast<uint32_t>(f32_to_bf16(v[0])) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
+    }
+};
+template <> struct lanevec<float, 1> {
+    float u;
+    __device__ __forceinline__ void ld(const float *p) { u = *p; }
+    __device__ __forceinline__ void zero() { u = 0.f; }
+    __device__ __forceinline__ float get(int) const { return u; }
+    __device__ __forceinline__ static void st(float *p, const float (&v)[1]) { *p = v[0]; }
+};
+template <> struct lanevec<float, 2> {
+    float2 u;
+    __device__ __forceinline__ void ld(const float *p) { u = *reinterpret_cast<const float2 *>(p); }
+    __device__ __forceinline__ void zero() { u = make_float2(0.f, 0.f); }
+    __device__ __forceinline__ float get(int c) const { return c ? u.y : u.x; }
+    __device__ __forceinline__ static void st(float *p, const float (&v)[2]) { *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]); }
+};
+
+// A wave's exchange with itself through LDS: its own writes before its reads.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// inclusive sums over the lanes at and below / above each lane
+__device__ __forceinline__ float prefix_sum(float v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const float o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+__device__ __forceinline__ float suffix_sum(float v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const float o = __shfl_down(v, d);
+        if (lane + d < 64) v += o;
+    }
+    return v;
+}
+
+// Workspace layout, the tables of packed sequences and how a scan is split
+// (host).  bytes: of the whole layout; the state and log arrays are there
+// only where the scan may be split.
+struct SsmPlan {
+    int32_t seg_chunks, segs_bound, segs_per_seq, chunks_per_seq;
+    int64_t chunks_bound;
+    int32_t waves, blocks_per_group;  // of a workgroup; workgroups per segment and group
+    bool split;
+    size_t table_bytes, state_bytes, log_bytes;
+    size_t bytes() const { return table_bytes + state_bytes + log_bytes; }
+};
+SsmPlan ssm_plan(const SsmParams &p, bool packed);
+// fills the tables' pointers of q from a workspace laid out by the plan
+void ssm_layout(SsmScan &q, const SsmPlan &plan, char *ws);
+// segment and chunk tables of packed sequences; checks the offsets
+hipError_t launch_ssm_table(const SsmScan &q, hipStream_t s);
+// chains the segments' end states into the states entering each, in place;
+// reverse: from the last segment to the first
+hipError_t launch_ssm_combine(const SsmScan &q, const float *first, bool reverse, hipStream_t s);
+// one phase of a scan; FULL writes y, the others only states.  phase 1: from
+// zero, the end state and log decay of every segment but the last (reverse:
+// but the first); phase 2: from the entering states.
+enum { SSM_FULL = 0, SSM_STATES = 1, SSM_REVERSE = 2 };
+hipError_t launch_ssm_phase(const SsmScan &q, const SsmPlan &plan, int mode, int phase, int in_dtype, int out_dtype, hipStream_t s);
+// a whole scan: phases and combination
+hipError_t launch_ssm_scan(const SsmScan &q, const SsmPlan &plan, int mode, int in_dtype, int out_dtype, hipStream_t s);
+
+}  // namespace kda

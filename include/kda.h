@@ -30,6 +30,12 @@
  *                        recurrence in the sublayer, with its rolling state.
  *   kda_backward         gradients of the recurrence (reverse mode through the
  *                        chunked form, from the prefill's chunk checkpoints).
+ *   kda_short_conv_backward  gradients of the short convolution.
+ *   kda_ssm_prefill, kda_ssm_decode  the selective state space scan for
+ *                        prompts and for a few tokens.
+ *   kda_block_norm, kda_block_norm_backward  the norm after a block with its
+ *                        gate, the scaled residual and the norm before the
+ *                        next block, and their gradients.
  *
  * Both recurrence families can fuse the stages that run just before the
  * recurrence (KDA_PROLOGUE_* flags below).
@@ -40,7 +46,8 @@
  *     prefill is a caller-provided workspace sized by
  *     kda_prefill_workspace_bytes(), or, for kda_prefill_chunked_noalloc, a
  *     fixed array the library's code holds on each GPU.
- *   - Tensors are contiguous, row-major, with the layouts given below.
+ *   - Tensors are contiguous, row-major, with the layouts given below, except
+ *     where a stride argument is named.
  *   - Every argument is validated on the host before the first launch; on an
  *     error nothing is launched and nothing is written.  After the launches
  *     a launch failure maps to KDA_ERR_HIP.  Execution is asynchronous on
@@ -394,6 +401,211 @@ typedef struct kda_backward_args {
 
 size_t kda_backward_workspace_bytes(const kda_backward_args *a);
 kda_status kda_backward(const kda_backward_args *a, void *hip_stream);
+
+/*
+ * Selective state space scan: the other recurrence a hybrid model's sublayer
+ * runs behind the same short convolution.  Per sequence and head h of group
+ * g = h / (H / G), with state S [d_state, d_head] in fp32:
+ *
+ *     dt_t = dt[t, h] (+ dt_bias[h]), then log(1 + e^dt) with dt_softplus
+ *     a_t  = exp(A[h] dt_t)
+ *     S_t  = a_t S_{t-1} + dt_t B_t x_t^T ,   y_t = S_t^T C_t (+ D[h] x_t)
+ *
+ * x, B and C may be slices of one wider tensor (the convolution's output):
+ * their token and batch strides are given in elements, the last two axes are
+ * contiguous.
+ *
+ *   x            DEVICE [B, T, H, d_head]   in_dtype, strides x_stride_*
+ *   Bm, Cm       DEVICE [B, T, G, d_state]  in_dtype, strides b_/c_stride_*
+ *   dt           DEVICE [B, T, H]           in_dtype, contiguous
+ *   A            DEVICE fp32 [H], <= 0 (not checked)
+ *   D, dt_bias   DEVICE fp32 [H], NULL = none
+ *   cu_seqlens   DEVICE int32 [num_seqs + 1], NULL = the B rows are the
+ *                sequences; else B == 1 and documents are packed along T.
+ *                Checked on the device before any other kernel reads it: if
+ *                malformed, no kernel writes y or any state and
+ *                *device_status (if given) is KDA_ERR_BAD_SEQLENS.
+ *   initial_state DEVICE fp32 [num_seqs, H, d_state, d_head], NULL = zeros
+ *   final_state  DEVICE fp32, same shape, NULL = not written; may alias
+ *                initial_state
+ *   chunk_states DEVICE fp32, NULL = not written: the state entering every
+ *                chunk of KDA_SSM_CHUNK tokens, documents in order,
+ *                [sum_n ceil(len_n / KDA_SSM_CHUNK), H, d_state, d_head]
+ *   y            DEVICE [B, T, H, d_head]   out_dtype, contiguous
+ *   device_status DEVICE int32, NULL = not reported; written 0 or an error
+ *   workspace    DEVICE, >= kda_ssm_workspace_bytes(args), 256-byte aligned
+ *
+ * Supported: d_head, d_state in {16, 32, 64, 128}; G divides H; in_dtype and
+ * out_dtype f32 or bf16; B * T * H, B * T * G < 2^31; strides multiples of 8;
+ * x, Bm, Cm 16-byte aligned, the states too (else KDA_ERR_UNSUPPORTED).
+ */
+#define KDA_SSM_CHUNK 64
+typedef struct kda_ssm_args {
+    int32_t B, T, H, G, d_head, d_state;
+    int32_t num_seqs;
+    int32_t in_dtype;              /* kda_dtype */
+    int32_t out_dtype;             /* kda_dtype */
+    int32_t dt_softplus;           /* 0 or 1 */
+    int64_t x_stride_b, x_stride_t;
+    int64_t b_stride_b, b_stride_t;
+    int64_t c_stride_b, c_stride_t;
+    const void *x, *dt, *Bm, *Cm;
+    const float *A, *D, *dt_bias;
+    const int32_t *cu_seqlens;
+    const float *initial_state;
+    float *final_state;
+    float *chunk_states;
+    void *y;
+    int32_t *device_status;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_ssm_args;
+
+/* Workspace bytes the call needs (0 if a is NULL or invalid); upper bound of
+ * the rows of chunk_states.  Pure host functions. */
+size_t kda_ssm_workspace_bytes(const kda_ssm_args *a);
+int64_t kda_ssm_max_chunks(const kda_ssm_args *a);
+kda_status kda_ssm_prefill(const kda_ssm_args *a, void *hip_stream);
+
+/*
+ * m >= 1 consecutive tokens of the scan for each of B sequences in one
+ * launch; the state is read once and written once.  Layouts as above with
+ * T = n_tokens (x and y [B, m, H, d_head], Bm and Cm [B, m, G, d_state],
+ * dt [B, m, H]).
+ *   initial_state DEVICE fp32 [B, H, d_state, d_head]: the state before
+ *   final_state   DEVICE fp32, same shape, NULL = not written; may alias
+ *                 initial_state
+ *   token_states  DEVICE fp32 [B, m, H, d_state, d_head], NULL = not written:
+ *                 the state after every token (a rollback restores one)
+ */
+typedef struct kda_ssm_decode_args {
+    int32_t B, H, G, d_head, d_state;
+    int32_t n_tokens;
+    int32_t in_dtype;              /* kda_dtype */
+    int32_t out_dtype;             /* kda_dtype */
+    int32_t dt_softplus;           /* 0 or 1 */
+    int64_t x_stride_b, x_stride_t;
+    int64_t b_stride_b, b_stride_t;
+    int64_t c_stride_b, c_stride_t;
+    const void *x, *dt, *Bm, *Cm;
+    const float *A, *D, *dt_bias;
+    const float *initial_state;
+    float *final_state;
+    float *token_states;
+    void *y;
+} kda_ssm_decode_args;
+kda_status kda_ssm_decode(const kda_ssm_decode_args *a, void *hip_stream);
+
+/*
+ * Gradients of kda_short_conv: of x, the weight, the bias and the initial
+ * state, from the gradients of y and of the final state.
+ *   x .. initial_state  as for kda_short_conv
+ *   d_y           DEVICE [B, T, C] grad_dtype
+ *   d_final_state DEVICE fp32 [num_seqs, C, W - 1], NULL = zeros
+ *   dx            DEVICE [B, T, C] in_dtype
+ *   dweight       DEVICE fp32 [C, W];  dbias DEVICE fp32 [C], NULL = not written
+ *   d_initial_state DEVICE fp32 [num_seqs, C, W - 1], NULL = not written
+ *   workspace     DEVICE, >= kda_short_conv_backward_workspace_bytes(args),
+ *                 256-byte aligned
+ * Supported sizes, alignment and the treatment of malformed offsets as for
+ * kda_short_conv.  Results are the same from run to run.
+ */
+typedef struct kda_conv_backward_args {
+    int32_t B, T, C, W;
+    int32_t num_seqs;
+    int32_t in_dtype;              /* kda_dtype */
+    int32_t grad_dtype;            /* kda_dtype */
+    int32_t activation;            /* KDA_CONV_NONE or KDA_CONV_SILU */
+    const void *x;
+    const float *weight;
+    const float *bias;
+    const int32_t *cu_seqlens;
+    const float *initial_state;
+    const void *d_y;
+    const float *d_final_state;
+    void *dx;
+    float *dweight;
+    float *dbias;
+    float *d_initial_state;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_conv_backward_args;
+size_t kda_short_conv_backward_workspace_bytes(const kda_conv_backward_args *a);
+kda_status kda_short_conv_backward(const kda_conv_backward_args *a, void *hip_stream);
+
+/*
+ * The stages after a block and before the next one in a single pass over the
+ * rows: the norm of the block's output with its gate (the sublayer's gated
+ * output norm), the scaled residual, and the norm in front of the next block
+ * (Module 04 — KDA II, §3 "The sublayer is bigger than the recurrence").
+ * Per row of dim channels, rms(v) = v / sqrt(mean(v^2) + eps):
+ *
+ *     p      = rms_group(x) * post_weight   over groups of `group` channels
+ *              (p = x when post_weight is NULL)
+ *     p      = p * act(gate)                when gate is given; with gate_first
+ *              the gate multiplies x before the norm instead
+ *     out    = residual + scale * p         (residual NULL = none, scale NULL = 1)
+ *     normed = rms(out) * pre_weight        when pre_weight is given; from out
+ *              before its rounding to dtype
+ *
+ *   x, gate, residual  DEVICE [rows, dim] dtype, row strides *_stride in
+ *                elements (channels contiguous); gate, residual nullable
+ *   post_weight  DEVICE fp32 [group] (post_per_channel 0: shared by the groups)
+ *                or [dim] (post_per_channel 1), NULL = no norm after the block
+ *   scale        DEVICE fp32 [dim], NULL = 1
+ *   pre_weight   DEVICE fp32 [dim], NULL = no second norm
+ *   out          DEVICE [rows, dim] dtype, contiguous
+ *   normed       DEVICE [rows, dim] dtype, contiguous; required with
+ *                pre_weight, NULL without
+ * out may alias x, residual or gate (contiguous), normed not out.
+ * Supported: 1 <= dim <= 16384, group divides dim, rows * dim < 2^40.  Rows
+ * whose sizes, strides and addresses are multiples of 8 channels and 16 bytes
+ * are moved as 128-bit vectors; any other row element by element.
+ */
+#define KDA_GATE_SIGMOID 0
+#define KDA_GATE_SILU 1
+typedef struct kda_block_norm_args {
+    int64_t rows;
+    int32_t dim, group;
+    int32_t dtype;                 /* kda_dtype */
+    int32_t gate_activation;       /* KDA_GATE_* */
+    int32_t gate_first;            /* 0 or 1 */
+    int32_t post_per_channel;      /* 0 or 1 */
+    float eps;
+    int64_t x_stride, gate_stride, residual_stride;
+    const void *x, *gate, *residual;
+    const float *post_weight, *scale, *pre_weight;
+    void *out, *normed;
+} kda_block_norm_args;
+kda_status kda_block_norm(const kda_block_norm_args *a, void *hip_stream);
+
+/*
+ * Gradients of kda_block_norm with respect to everything it reads, from the
+ * gradients of out and of normed; the forward's values are recomputed from
+ * its inputs.
+ *   f            the forward's arguments (out and normed are not read)
+ *   d_out        DEVICE [rows, dim] dtype, contiguous, NULL = zeros
+ *   d_normed     DEVICE [rows, dim] dtype, contiguous, NULL = zeros (needs
+ *                f.pre_weight)
+ *   dx           DEVICE [rows, dim] dtype, contiguous
+ *   dgate, dresidual  DEVICE [rows, dim] dtype, contiguous, NULL = not written
+ *   dpost_weight (shape of post_weight), dscale, dpre_weight [dim]  DEVICE
+ *                fp32, NULL = not written
+ *   workspace    DEVICE, >= kda_block_norm_backward_workspace_bytes(args),
+ *                256-byte aligned
+ * A gradient whose input is not given is refused (KDA_ERR_BAD_SHAPE).
+ * Results are the same from run to run.
+ */
+typedef struct kda_block_norm_backward_args {
+    kda_block_norm_args f;
+    const void *d_out, *d_normed;
+    void *dx, *dgate, *dresidual;
+    float *dpost_weight, *dscale, *dpre_weight;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_block_norm_backward_args;
+size_t kda_block_norm_backward_workspace_bytes(const kda_block_norm_backward_args *a);
+kda_status kda_block_norm_backward(const kda_block_norm_backward_args *a, void *hip_stream);
 
 /* Static description of a status code (never NULL). */
 const char *kda_status_string(int32_t status);

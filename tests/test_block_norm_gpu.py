@@ -1,0 +1,179 @@
+"""Norm after a block, gate, scaled residual, norm before the next block: the
+HIP kernels against the fp64 forms, through the Python binding."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_49_amd as kda
+from oracle import sublayer as R
+from sublayer_testutil import TOL, check, rounded
+
+pytestmark = pytest.mark.gpu
+
+
+def make(seed, rows, dim, group, dtype, gate, residual, scale, pre, post=True, channel=False):
+    rng = np.random.default_rng(seed)
+
+    def t(*shape, kind=dtype, base=0.0, width=1.0):
+        return rounded(base + width * rng.standard_normal(shape), kind)
+
+    x = t(rows, dim, width=1.5)
+    got = {"x": x, "residual": t(rows, dim, width=2.0) if residual else None,
+           "post_weight": t(dim if channel else group, kind=torch.float32, base=1.0, width=0.2) if post else None,
+           "gate": t(rows, dim) if gate else None,
+           "scale": t(dim, kind=torch.float32, base=0.8, width=0.3) if scale else None,
+           "pre_weight": t(dim, kind=torch.float32, base=1.0, width=0.2) if pre else None}
+    dev = {k: None if v is None else v[0].cuda() for k, v in got.items()}
+    ref = {k: None if v is None else v[1] for k, v in got.items()}
+    return dev, ref
+
+
+def oracle_args(ref, group, act, first):
+    return dict(residual=ref["residual"], post=ref["post_weight"], gate=ref["gate"], scale=ref["scale"], pre=ref["pre_weight"],
+                group=group if ref["post_weight"] is not None else None, activation=act, gate_first=first)
+
+
+def both(dev, ref, group, act="silu", first=False, seed=0, name=""):
+    """Forward and gradients of one setting against the oracle."""
+    dtype = dev["x"].dtype
+    kw = {k: v for k, v in dev.items() if k != "x"}
+    kw.update(group_size=group if dev["post_weight"] is not None else None, gate_activation=act, gate_first=first)
+    out, normed = kda.block_norm(dev["x"], **kw)
+    out_r, normed_r = R.block_norm(ref["x"], **oracle_args(ref, group, act, first))
+    check(f"{name} out", out, out_r, TOL[dtype])
+    if normed is not None:
+        check(f"{name} normed", normed, normed_r, TOL[dtype])
+    rng = np.random.default_rng(seed + 1)
+    do, do64 = rounded(rng.standard_normal(ref["x"].shape), dtype)
+    dn, dn64 = rounded(rng.standard_normal(ref["x"].shape), dtype) if normed is not None else (None, None)
+    got = kda.block_norm_backward(dev["x"], do.cuda(), None if dn is None else dn.cuda(), **kw)
+    want = R.block_norm_backward(ref["x"], do64, dn64, **oracle_args(ref, group, act, first))
+    for n, a, b in zip(("dx", "dresidual", "dpost", "dgate", "dscale", "dpre"), got, want):
+        assert (a is None) == (b is None), n
+        if a is None:
+            continue
+        tol = TOL[a.dtype]
+        if n == "dx" and group == 1 and ref["post_weight"] is not None:
+            # a group of one channel: dx = q e - q hat mean(e hat) with hat^2 = 1 - eps q^2, so both
+            # terms are about q e and their difference is eps q^2 of that.  Each term is off by a few
+            # 2^-24 of itself: the bound holds against the terms, which are 1 / (eps q^2) times the
+            # result, q^2 = 1 / (a^2 + eps)
+            a64 = ref["x"] * (R._gate(ref["gate"], act)[0] if first else 1.0)
+            tol = tol * np.linalg.norm(b * (a64 ** 2 + 1e-6) / 1e-6) / np.linalg.norm(b)
+        check(f"{name} {n}", a, b, tol)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("gate,first,residual,pre", [c for c in itertools.product(["", "silu", "sigmoid"], [False, True], [False, True], [False, True])
+                                                     if c[0] or not c[1]])
+def test_every_combination(dtype, gate, first, residual, pre):
+    dev, ref = make(1, 13, 256, 64, dtype, gate, residual, residual, pre)
+    both(dev, ref, 64, gate or "sigmoid", first, name=f"{gate} {first} {residual} {pre}")
+
+
+@pytest.mark.parametrize("rows", [1, 2, 5, 1030])
+@pytest.mark.parametrize("dim,group", [(8, 8), (1, 1), (7, 7), (77, 11), (512, 512), (520, 104), (1024, 128), (1232, 77), (4096, 4096),
+                                       (4096, 128), (2056, 2056)])
+def test_sizes(rows, dim, group):
+    for dtype in (torch.float32, torch.bfloat16):
+        dev, ref = make(2, rows, dim, group, dtype, "silu", True, True, True)
+        both(dev, ref, group, name=f"{rows}x{dim}/{group}")
+
+
+@pytest.mark.parametrize("dim,group", [(16384, 16384), (16384, 256), (16383, 129), (10000, 1000), (8200, 8200)])
+def test_widest_rows(dim, group):
+    for dtype in (torch.float32, torch.bfloat16):
+        dev, ref = make(3, 3, dim, group, dtype, "sigmoid", True, True, True)
+        both(dev, ref, group, "sigmoid", name=f"{dim}/{group}")
+
+
+def test_weight_of_every_channel_and_none():
+    dev, ref = make(4, 9, 384, 64, torch.bfloat16, "silu", True, True, True, channel=True)
+    both(dev, ref, 64, name="per channel")
+    dev, ref = make(5, 9, 384, 384, torch.float32, "silu", True, False, True, post=False)
+    both(dev, ref, 384, name="no norm after the block")
+    dev, ref = make(6, 9, 384, 384, torch.float32, "", False, False, False, post=False)
+    both(dev, ref, 384, name="nothing at all")
+
+
+@pytest.mark.parametrize("offset", [0, 8, 3])
+def test_slices_of_wider_rows(offset):
+    """x and the gate as slices of one projection's rows: aligned ones on the
+    vector path, the odd offset on the other; equal values either way."""
+    rng = np.random.default_rng(7)
+    wide, w64 = rounded(rng.standard_normal((2, 50, 1000)), torch.bfloat16)
+    wide = wide.cuda()
+    w, w_64 = rounded(1 + 0.1 * rng.standard_normal(96), torch.float32)
+    x, z = wide[..., offset:offset + 192], wide[..., 400 + offset:400 + offset + 192]
+    out, _ = kda.block_norm(x, post_weight=w.cuda(), gate=z)
+    want, _ = R.block_norm(w64[..., offset:offset + 192], post=w_64, gate=w64[..., 400 + offset:592 + offset])
+    check("sliced rows", out, want, TOL[torch.bfloat16])
+    dense, _ = kda.block_norm(x.contiguous(), post_weight=w.cuda(), gate=z.contiguous())
+    # another order of a group's sum may move a result by a rounding of the stored type
+    check("sliced against dense", out, dense.double().cpu().numpy(), 2.0 ** -8)
+
+
+def test_in_place_and_broadcast_rows():
+    dev, ref = make(8, 40, 512, 128, torch.bfloat16, "silu", True, True, True)
+    kw = {k: v for k, v in dev.items() if k != "x"}
+    want, want_n = kda.block_norm(dev["x"], **kw)
+    kw["residual"] = dev["residual"].clone()
+    got, got_n = kda.block_norm(dev["x"], out=kw["residual"], **kw)
+    assert got.data_ptr() == kw["residual"].data_ptr() and torch.equal(got, want) and torch.equal(got_n, want_n)
+    one = dev["gate"][:1].expand(40, 512)  # one gate for all rows
+    a, _ = kda.block_norm(dev["x"], gate=one)
+    b, _ = kda.block_norm(dev["x"], gate=one.contiguous())
+    assert torch.equal(a, b)
+
+
+def test_rows_of_zeros_and_large_values():
+    x = torch.zeros((4, 256), device="cuda")
+    x[1] = 1e18
+    x[2] = 1e-30
+    w = torch.ones(256, device="cuda")
+    out, normed = kda.block_norm(x, post_weight=w, pre_weight=w)
+    assert torch.isfinite(out).all() and torch.isfinite(normed).all() and (out[0] == 0).all()
+    assert torch.allclose(out[1], torch.ones_like(out[1]), rtol=1e-6)
+    dx = kda.block_norm_backward(x, torch.ones_like(x), torch.ones_like(x), post_weight=w, pre_weight=w)[0]
+    assert torch.isfinite(dx).all()
+
+
+def test_no_rows():
+    x = torch.zeros((0, 64), device="cuda")
+    w = torch.ones(64, device="cuda")
+    out, normed = kda.block_norm(x, post_weight=w, pre_weight=w)
+    assert out.shape == normed.shape == (0, 64)
+    got = kda.block_norm_backward(x, x, x, post_weight=w, pre_weight=w)
+    assert (got[2] == 0).all() and (got[5] == 0).all()
+
+
+def test_gradient_against_differences():
+    """fp32 central differences of a weighted sum of both results."""
+    dev, ref = make(9, 3, 64, 16, torch.float32, "silu", True, True, True)
+    kw = oracle_args(ref, 16, "silu", False)
+    rng = np.random.default_rng(10)
+    do, dn = rng.standard_normal((3, 64)), rng.standard_normal((3, 64))
+
+    def loss(x):
+        o, n = R.block_norm(x, **kw)
+        return (o * do).sum() + (n * dn).sum()
+
+    kd = {k: v for k, v in dev.items() if k != "x"}
+    dx = kda.block_norm_backward(dev["x"], torch.from_numpy(do).float().cuda(), torch.from_numpy(dn).float().cuda(),
+                                 gate_activation="silu", **kd)[0].cpu().numpy()
+    for i, j in [(0, 0), (1, 17), (2, 63)]:
+        e = np.zeros((3, 64))
+        e[i, j] = 1e-5
+        d = (loss(ref["x"] + e) - loss(ref["x"] - e)) / 2e-5
+        assert abs(d - dx[i, j]) <= 1e-5 * max(1.0, abs(d)), (i, j, d, dx[i, j])
+
+
+def test_same_results_from_run_to_run():
+    dev, _ = make(11, 3000, 1000, 100, torch.bfloat16, "silu", True, True, True)
+    kw = {k: v for k, v in dev.items() if k != "x"}
+    d = torch.randn((3000, 1000), device="cuda").bfloat16()
+    a = kda.block_norm_backward(dev["x"], d, d, **kw)
+    b = kda.block_norm_backward(dev["x"], d, d, **kw)
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
