@@ -19,6 +19,7 @@ The stages and the recurrence a hybrid model runs beside it (``sublayer.py``):
 
     y, S = ssm_prefill(x, dt, A, B, C, D=D, dt_bias=bias, dt_softplus=True)
     y, S, per_token = ssm_decode(x, dt, A, B, C, state)          # a few tokens
+    dx, ddt, dA, dB, dC, dD, dbias, dS0 = ssm_backward(x, dt, A, B, C, d_y)
     out, normed = block_norm(x, residual, post_weight=w, gate=z, pre_weight=w2)
     dx, dres, dw, dz, ds, dw2 = block_norm_backward(x, d_out, d_normed, residual, ...)
 
@@ -43,8 +44,8 @@ import torch
 __all__ = ["prefill", "prefill_noalloc", "NOALLOC_SCRATCH_BYTES", "decode_step", "decode", "short_conv", "backward", "workspace_bytes", "max_chunks",
            "lib", "KDAError", "PrefillArgs", "DecodeArgs", "ConvArgs", "BackwardArgs", "KDA_F32", "KDA_BF16", "PROLOGUE_GATE_SOFTPLUS",
            "PROLOGUE_BETA_SIGMOID", "PROLOGUE_QK_L2NORM", "PROLOGUE_ALL",
-           "short_conv_backward", "ssm_prefill", "ssm_decode", "block_norm", "block_norm_backward",
-           "ConvBackwardArgs", "SsmArgs", "SsmDecodeArgs", "BlockNormArgs", "BlockNormBackwardArgs",
+           "short_conv_backward", "ssm_prefill", "ssm_decode", "ssm_backward", "block_norm", "block_norm_backward",
+           "ConvBackwardArgs", "SsmArgs", "SsmDecodeArgs", "SsmBackwardArgs", "BlockNormArgs", "BlockNormBackwardArgs",
            "GATE_SIGMOID", "GATE_SILU", "SSM_CHUNK"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -156,6 +157,16 @@ class SsmDecodeArgs(ctypes.Structure):
         p: x dt Bm Cm A D dt_bias initial_state final_state token_states y""")
 
 
+class SsmBackwardArgs(ctypes.Structure):
+    """Mirror of ``kda_ssm_backward_args`` (include/kda.h)."""
+    _fields_ = _fields("""
+        i: B T H G d_head d_state num_seqs in_dtype dt_softplus
+        l: x_stride_b x_stride_t b_stride_b b_stride_t c_stride_b c_stride_t
+        p: x dt Bm Cm A D dt_bias cu_seqlens initial_state d_y d_final_state
+        p: dx ddt dB dC dA dD ddt_bias d_initial_state workspace
+        z: workspace_bytes""")
+
+
 class BlockNormArgs(ctypes.Structure):
     """Mirror of ``kda_block_norm_args`` (include/kda.h)."""
     _fields_ = _fields("""
@@ -206,11 +217,12 @@ def lib():
         L.kda_backward.argtypes = [BP, P]
         L.kda_backward.restype = I32
         for name, cls in (("kda_short_conv_backward", ConvBackwardArgs), ("kda_ssm_prefill", SsmArgs),
-                          ("kda_ssm_decode", SsmDecodeArgs),
+                          ("kda_ssm_decode", SsmDecodeArgs), ("kda_ssm_backward", SsmBackwardArgs),
                           ("kda_block_norm", BlockNormArgs), ("kda_block_norm_backward", BlockNormBackwardArgs)):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = [ctypes.POINTER(cls), P], I32
         for name, cls in (("kda_short_conv_backward_workspace_bytes", ConvBackwardArgs), ("kda_ssm_workspace_bytes", SsmArgs),
+                          ("kda_ssm_backward_workspace_bytes", SsmBackwardArgs),
                           ("kda_block_norm_backward_workspace_bytes", BlockNormBackwardArgs)):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = [ctypes.POINTER(cls)], ctypes.c_size_t
@@ -621,5 +633,5 @@ def backward(q, k, v, beta, log_alpha, d_o, initial_state=None, d_final_state=No
     return out["dq"], out["dk"], out["dv"], out["dbeta"], out["dlog_alpha"], out["d_initial_state"]
 
 
-from .sublayer import (block_norm, block_norm_backward, short_conv_backward,  # noqa: E402
+from .sublayer import (block_norm, block_norm_backward, short_conv_backward, ssm_backward,  # noqa: E402
                        ssm_decode, ssm_prefill)

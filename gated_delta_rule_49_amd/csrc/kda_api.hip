@@ -657,4 +657,52 @@ kda_status kda_ssm_decode(const kda_ssm_decode_args *a, void *hip_stream) {
     return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
+namespace {
+kda_status check_ssm_backward(const kda_ssm_backward_args *a, bool need_ptrs) {
+    if (!a) return KDA_ERR_NULL_ARG;
+    if (a->B < 1 || a->num_seqs < 0) return KDA_ERR_BAD_SHAPE;
+    if (a->cu_seqlens ? a->B != 1 || a->num_seqs < 1 : a->num_seqs != a->B) return KDA_ERR_BAD_SHAPE;
+    const kda_status st = check_ssm({a->B, a->T, a->H, a->G, a->d_head, a->d_state, a->in_dtype, a->in_dtype, a->dt_softplus,
+                                     a->x_stride_b, a->x_stride_t, a->b_stride_b, a->b_stride_t, a->c_stride_b, a->c_stride_t});
+    if (st != KDA_OK) return st;
+    if (static_cast<int64_t>(a->num_seqs) * a->H > (1 << 24)) return KDA_ERR_UNSUPPORTED;
+    if (!need_ptrs) return KDA_OK;
+    if (!a->A || !a->dA || (a->T > 0 && (!a->x || !a->dt || !a->Bm || !a->Cm || !a->d_y || !a->dx || !a->ddt || !a->dB || !a->dC)))
+        return KDA_ERR_NULL_ARG;
+    if ((a->dD && !a->D) || (a->ddt_bias && !a->dt_bias)) return KDA_ERR_BAD_SHAPE;
+    if (misaligned({a->x, a->Bm, a->Cm, a->d_y, a->initial_state, a->d_final_state, a->d_initial_state, a->dx, a->dB, a->dC}))
+        return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+SsmParams ssm_grad_params(const kda_ssm_backward_args *a) {
+    SsmParams p{};
+    p.x = a->x; p.dt = a->dt; p.Bm = a->Bm; p.Cm = a->Cm; p.A = a->A; p.D = a->D; p.dt_bias = a->dt_bias;
+    p.cu_seqlens = a->cu_seqlens; p.initial_state = a->initial_state;
+    p.x_sb = a->x_stride_b; p.x_st = a->x_stride_t; p.b_sb = a->b_stride_b; p.b_st = a->b_stride_t;
+    p.c_sb = a->c_stride_b; p.c_st = a->c_stride_t;
+    p.B = a->B; p.T = a->T; p.H = a->H; p.G = a->G; p.P = a->d_head; p.Ns = a->d_state; p.N = a->num_seqs;
+    p.softplus = a->dt_softplus;
+    return p;
+}
+}  // namespace
+
+size_t kda_ssm_backward_workspace_bytes(const kda_ssm_backward_args *a) {
+    return check_ssm_backward(a, false) == KDA_OK ? ssm_grad_plan(ssm_grad_params(a), a->cu_seqlens != nullptr, a->in_dtype).bytes() : 0;
+}
+
+kda_status kda_ssm_backward(const kda_ssm_backward_args *a, void *hip_stream) {
+    const kda_status st = check_ssm_backward(a, true);
+    if (st != KDA_OK) return st;
+    if (!a->workspace) return KDA_ERR_NULL_ARG;
+    if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign) return KDA_ERR_BAD_SHAPE;
+    if (a->workspace_bytes < kda_ssm_backward_workspace_bytes(a)) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    SsmGradOut o{};
+    o.d_y = a->d_y; o.d_final = a->d_final_state;
+    o.dx = a->dx; o.ddt = a->ddt; o.dB = a->dB; o.dC = a->dC;
+    o.dA = a->dA; o.dD = a->dD; o.ddt_bias = a->ddt_bias; o.d_initial = a->d_initial_state;
+    const hipError_t e = launch_ssm_backward(ssm_grad_params(a), o, static_cast<char *>(a->workspace), a->in_dtype,
+                                             static_cast<hipStream_t>(hip_stream));
+    return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
 }  // extern "C"

@@ -1,0 +1,527 @@
+// Gradients of the selective state space scan, from the state entering every
+// chunk (a forward pass over the states alone) and the state gradient arriving
+// at every chunk's end (the same pass in reverse over C and dy).  Within a
+// chunk, with suf, cum, tot as in kda_ssm_scan.hpp, S = S_in, G = the gradient
+// of the state at the chunk's end, and for s <= t
+//     D_ts = 2^(suf_s - suf_t),  Q_ts = dy_t . x_s,  K_ts = C_t . B_s,
+//     E_ts = Q_ts K_ts D_ts :
+//   dC_t = sum_s Q_ts D_ts dt_s B_s + 2^cum_t S dy_t
+//   dB_s = sum_t Q_ts D_ts dt_s C_t + dt_s 2^suf_s G x_s
+//   du_s = sum_t K_ts D_ts dy_t     + 2^suf_s G^T B_s ,   dx_s = dt_s du_s + D dy_s
+//   ddt_s = sum_t E_ts + 2^suf_s B_s . G x_s  +  A dlog_s
+//   dlog_t = sum_{i >= t > j} E_ij dt_j + sum_{i >= t} 2^cum_i C_i . S dy_i
+//            + sum_{j < t} dt_j 2^suf_j B_j . G x_j + 2^tot <G, S>
+// Every exponent is <= 0 for decays, and dlog is a sum over what passes
+// through token t, so nothing is recovered as a small difference of sums over
+// the sequence.  (The first sum runs over row minus column sums of the same
+// E without its diagonal, inside the chunk.)
+//
+// One workgroup takes a chunk, a group and some of its heads, one after the
+// other; wave w owns 16 rows n of the states and the same 16 columns of dB and
+// dC, whose sums over the heads stay in its accumulators.  Each head's states
+// are read once, straight into operand order.
+#pragma once
+#include "kda_ssm_scan.hpp"
+
+namespace kda {
+
+namespace {
+
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+
+// Operand with its contraction along the rows [r0, r0 + 32) of a granule-
+// ordered LDS tile and its 16 columns from c0 (ds_read_b64_tr_b16: lane i of
+// group g addresses four columns of row r0 + 4 g + i / 4 and receives column
+// c0 + i of rows r0 + 4 g + 0..3).
+__device__ __forceinline__ void load_cols(frag8 &f, const bf16_t *tile, int stride, int r0, int c0, int g, int c16) {
+    const bf16_t *at = tile + (r0 + 4 * g + (c16 >> 2)) * stride + col_pos(c0 + 4 * (c16 & 3));
+    const v4i16 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)(at));
+    const v4i16 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)(at + 16 * stride));
+    const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
+    f.u = make_uint4(ua.x, ua.y, ub.x, ub.y);
+}
+// Operand with its contraction along a row: rows [r0, r0 + 16), step kk
+__device__ __forceinline__ void load_rows(frag8 &f, const bf16_t *tile, int stride, int r0, int kk, int g, int c16) {
+    f.u = *reinterpret_cast<const uint4 *>(tile + (r0 + c16) * stride + kk * 32 + 8 * g);
+}
+
+// Sums of V = 8 or 16 values over the 16 lanes of a lane group: each exchange
+// halves the values a lane carries; lane c ends with the sum of value
+// sum16_index<V>(c).
+template <int V>
+__device__ __forceinline__ float sum16(float (&v)[V], int c16) {
+    int bit = 8;
+#pragma unroll
+    for (int n = V; n > 1; n >>= 1, bit >>= 1) {
+        const bool up = c16 & bit;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float keep = up ? v[i + n / 2] : v[i];
+            const float give = up ? v[i] : v[i + n / 2];
+            v[i] = keep + __shfl_xor(give, bit);
+        }
+    }
+    float s = v[0];
+    for (; bit; bit >>= 1) s += __shfl_xor(s, bit);
+    return s;
+}
+template <int V>
+__device__ __forceinline__ int sum16_index(int c16) { return V == 16 ? c16 : c16 >> 1; }
+
+template <typename TI, int NS, int P>
+struct GradCfg {
+    static constexpr bool BF = std::is_same<TI, bf16_t>::value;
+    static constexpr int EX = quad<TI>::PARTS, ORD = BF ? 2 : 3, XP = BF ? 2 : 3;
+    // the states' products also make the fp32 sums dA and ddt_bias: all three parts
+    static constexpr int SP = 3;
+    static constexpr int L = BF ? 64 : 32, SUB = 64 / L, ST = L / 16, TK = L / 32;
+    static constexpr int NT = NS / 16, NKS = (NS + 31) / 32, PT = P / 16, PKS = (P + 31) / 32;
+    static constexpr int RN = NKS * 32 + 8, RP = PKS * 32 + 8, RL = L + 8;
+    // LDS, in bf16 elements
+    static constexpr int BN = 0, CN = BN + EX * L * RN, XN = CN + EX * L * RN, YN = XN + EX * L * RP;
+    static constexpr int M1 = YN + EX * L * RP, M2 = M1 + XP * L * RL, END = M2 + XP * L * RL;
+    // then floats: dt, suf, 2^cum, 2^suf, diagonals of Q and E, suf's rounding; row and column sums per tile; inter and outer per wave; <G, S> per wave
+    static constexpr int FDT = 0, FSUF = L, FCUM = 2 * L, FWS = 3 * L, FQD = 4 * L, FED = 5 * L, FLO = 6 * L, FR = 7 * L, FC = FR + ST * L,
+                         FI = FC + ST * L, FO = FI + NT * L, FX = FO + NT * L, FEND = FX + 8;
+    static constexpr size_t BYTES = sizeof(bf16_t) * END + sizeof(float) * FEND;
+};
+
+template <typename TI, int NS, int P>
+__global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
+    using Cf = GradCfg<TI, NS, P>;
+    constexpr int EX = Cf::EX, ORD = Cf::ORD, XP = Cf::XP, SP = Cf::SP, L = Cf::L, SUB = Cf::SUB, ST = Cf::ST, TK = Cf::TK, NT = Cf::NT;
+    constexpr int NKS = Cf::NKS, PT = Cf::PT, PKS = Cf::PKS, RN = Cf::RN, RP = Cf::RP, RL = Cf::RL;
+    __shared__ __attribute__((aligned(16))) char smem[Cf::BYTES];
+    bf16_t *lds = reinterpret_cast<bf16_t *>(smem);
+    float *fl = reinterpret_cast<float *>(smem + sizeof(bf16_t) * Cf::END);
+    const SsmParams &p = a.q.p;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, c16 = lane & 15;
+
+    // block -> (chunk of 64, part of it, group, split of the group's heads)
+    const int block = xcd_order(blockIdx.x, gridDim.x);
+    const int per_item = p.G * a.splits;
+    const int item = block / per_item, grp = block / a.splits % p.G, split = block % a.splits;
+    const int chunk = item / SUB, sub = item % SUB;
+    int row, t0, len, items;
+    if (p.cu_seqlens) {
+        if (*a.q.status != 0 || chunk >= a.q.chunk_off[p.N]) return;
+        const int n = chunk_to_seq(a.q.chunk_off, p.N, chunk);
+        row = 0;
+        t0 = (chunk - a.q.chunk_off[n]) * 64 + sub * L;
+        len = min(p.cu_seqlens[n + 1] - p.cu_seqlens[n] - t0, L);
+        t0 += p.cu_seqlens[n];
+        items = (a.q.chunks_per_seq + p.N) * SUB;
+    } else {
+        if (chunk >= p.N * a.q.chunks_per_seq) return;
+        row = chunk / a.q.chunks_per_seq;
+        t0 = (chunk % a.q.chunks_per_seq) * 64 + sub * L;
+        len = min(p.T - t0, L);
+        items = p.N * a.q.chunks_per_seq * SUB;
+    }
+    const int hpg = p.H / p.G;
+    const int h0 = grp * hpg + split * a.heads_per_block, h1 = min(h0 + a.heads_per_block, (grp + 1) * hpg);
+    if (len <= 0) {  // the second part of a short chunk: its share of the sums is zero
+        for (int h = h0; h < h1; ++h)
+            if (tid < 3) a.scalars[(static_cast<int64_t>(tid) * p.H + h) * items + item] = 0.f;
+        return;
+    }
+    const int64_t flat0 = static_cast<int64_t>(row) * p.T + t0;
+    const TI *xb = static_cast<const TI *>(p.x) + row * p.x_sb + t0 * p.x_st;
+    const TI *bb = static_cast<const TI *>(p.Bm) + row * p.b_sb + t0 * p.b_st + static_cast<int64_t>(grp) * NS;
+    const TI *cb = static_cast<const TI *>(p.Cm) + row * p.c_sb + t0 * p.c_st + static_cast<int64_t>(grp) * NS;
+
+    // a [tokens, width] tile into LDS in granule order, tokens past the chunk as zeros
+    auto stage = [&](int at, int stride, int width, const TI *src, int64_t st) {
+        for (int i = tid; i < (L / 4) * (width / 4); i += 512) {
+            const int tq = i / (width / 4), cq = i % (width / 4);
+            quad<TI> v;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                v.zero(r);
+                if (tq * 4 + r < len) v.ld(r, src + (tq * 4 + r) * st + cq * 4);
+            }
+#pragma unroll
+            for (int part = 0; part < EX; ++part)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    *reinterpret_cast<uint2 *>(lds + at + part * L * stride + (tq * 4 + r) * stride + col_pos(cq * 4)) = v.row(r, part).u;
+        }
+    };
+    // columns past d_state and d_head, the score tiles above the diagonal and
+    // the sums no tile writes stay zero
+    for (int i = tid; i < Cf::END / 2; i += 512) reinterpret_cast<uint32_t *>(lds)[i] = 0;
+    for (int i = tid; i < Cf::FEND; i += 512) fl[i] = 0.f;
+    lds_barrier();
+    stage(Cf::BN, RN, NS, bb, p.b_st);
+    stage(Cf::CN, RN, NS, cb, p.c_st);
+    lds_barrier();
+
+    constexpr int TILES = ST * (ST + 1) / 2, MT = (TILES + 7) / 8;
+    f32x4 K[MT];  // scores of this wave's tiles: rows s, columns t
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        K[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+        int ti = 0, tj = wave + 8 * m;
+        if (tj >= TILES) continue;
+        while (tj > ti) { tj -= ti + 1; ++ti; }
+        for (int kk = 0; kk < NKS; ++kk) {
+            parts8<EX> u, v;
+#pragma unroll
+            for (int part = 0; part < EX; ++part) {
+                load_rows(u.f[part], lds + Cf::BN + part * L * RN, RN, 16 * tj, kk, g, c16);
+                load_rows(v.f[part], lds + Cf::CN + part * L * RN, RN, 16 * ti, kk, g, c16);
+            }
+            mfma_parts<EX, EX, ORD>(K[m], u, v);
+        }
+    }
+    // this wave's 16 columns of B and C with the tokens as contraction; slot
+    // (s % 2) 4 + r of step s / 2 is the element of row 16 s + 4 g + r
+    const bool rows_on = wave < NT;
+    const int n0 = (rows_on ? wave : 0) * 16;
+    parts8<EX> Bt[TK], Ct[TK];
+#pragma unroll
+    for (int ks = 0; ks < TK; ++ks)
+#pragma unroll
+        for (int part = 0; part < EX; ++part) {
+            load_cols(Bt[ks].f[part], lds + Cf::BN + part * L * RN, RN, 32 * ks, n0, g, c16);
+            load_cols(Ct[ks].f[part], lds + Cf::CN + part * L * RN, RN, 32 * ks, n0, g, c16);
+        }
+    auto elem = [&](const parts8<EX> (&f)[TK], int s, int r) {
+        float v = 0.f;
+#pragma unroll
+        for (int part = EX - 1; part >= 0; --part) v += bf16_to_f32(f[s / 2].f[part].s[(s % 2) * 4 + r]);
+        return v;
+    };
+    f32x4 dCs[ST], dBs[ST];  // sums over the heads: rows 16 s + 4 g + r, column n0 + c16
+#pragma unroll
+    for (int s = 0; s < ST; ++s) dCs[s] = dBs[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    for (int h = h0; h < h1; ++h) {
+        // ---- stage x, dy and the decays
+        stage(Cf::XN, RP, P, xb + static_cast<int64_t>(h) * P, p.x_st);
+        stage(Cf::YN, RP, P, static_cast<const TI *>(a.d_y) + (flat0 * p.H + h) * P, static_cast<int64_t>(p.H) * P);
+        const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+        const float raw = lane < len ? io<TI>::ld(static_cast<const TI *>(p.dt), (flat0 + lane) * p.H + h) + bias : 0.f;
+        float dt = p.softplus ? softplus_rel(raw) : raw;
+        if (lane >= len) dt = 0.f;
+        const float la = A * kLog2e * dt;
+        // D compares sums over the rest of the chunk whose difference may be
+        // one token's log: kept in 64 bits, as two floats in LDS
+        double sum = static_cast<double>(A) * 1.4426950408889634 * dt;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double o = __shfl_down(sum, d);
+            if (lane + d < 64) sum += o;
+        }
+        const float tot = static_cast<float>(__shfl(sum, 0));
+        double rest = __shfl_down(sum, 1);
+        if (lane == 63) rest = 0.0;
+        const float suf = static_cast<float>(rest);
+        const float ecum = fast_exp2(prefix_sum(la, lane)), esuf = fast_exp2(suf);
+        if (wave == 0 && lane < L) {
+            fl[Cf::FDT + lane] = dt;
+            fl[Cf::FSUF + lane] = suf;
+            fl[Cf::FLO + lane] = static_cast<float>(rest - suf);
+            fl[Cf::FCUM + lane] = ecum;
+            fl[Cf::FWS + lane] = esuf;
+        }
+        // this wave's rows of both states, channels in the operand's slot order
+        const int64_t so = ((static_cast<int64_t>(item) * p.H + h) * NS + n0 + c16) * P;
+        f32x4 Sv[PKS][2], Gv[PKS][2];
+#pragma unroll
+        for (int ks = 0; ks < PKS; ++ks)
+#pragma unroll
+            for (int hq = 0; hq < 2; ++hq) {
+                const int c = 32 * ks + 16 * hq + 4 * g;
+                Sv[ks][hq] = Gv[ks][hq] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (rows_on && c < P) {
+                    Sv[ks][hq] = *reinterpret_cast<const f32x4 *>(a.states + so + c);
+                    Gv[ks][hq] = *reinterpret_cast<const f32x4 *>(a.gstates + so + c);
+                }
+            }
+        lds_barrier();
+
+        // ---- causal tiles of Q; M1 = Q D dt_s, M2 = K D into LDS; sums of E
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            int ti = 0, tj = wave + 8 * m;
+            if (tj >= TILES) continue;
+            while (tj > ti) { tj -= ti + 1; ++ti; }
+            f32x4 q = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kk = 0; kk < PKS; ++kk) {
+                parts8<EX> u, v;
+#pragma unroll
+                for (int part = 0; part < EX; ++part) {
+                    load_rows(u.f[part], lds + Cf::XN + part * L * RP, RP, 16 * tj, kk, g, c16);
+                    load_rows(v.f[part], lds + Cf::YN + part * L * RP, RP, 16 * ti, kk, g, c16);
+                }
+                mfma_parts<EX, EX, ORD>(q, u, v);
+            }
+            const int t = 16 * ti + c16, s0 = 16 * tj + 4 * g;
+            const float suf_t = fl[Cf::FSUF + t];
+            const f32x4 suf_s = *reinterpret_cast<const f32x4 *>(fl + Cf::FSUF + s0);
+            const float lo_t = fl[Cf::FLO + t];
+            const f32x4 lo_s = *reinterpret_cast<const f32x4 *>(fl + Cf::FLO + s0);
+            const f32x4 dt_s = *reinterpret_cast<const f32x4 *>(fl + Cf::FDT + s0);
+            float rowsum = 0.f, E[4];
+            granule m1[XP], m2[XP];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float d = s0 + r <= t ? fast_exp2((suf_s[r] - suf_t) + (lo_s[r] - lo_t)) : 0.f;
+                const float qd = q[r] * d, kd = K[m][r] * d;
+                E[r] = q[r] * kd;
+                // the diagonal passes through no token's decay: kept apart, it
+                // would only leave its rounding in the difference of the sums
+                if (s0 + r == t) {
+                    fl[Cf::FQD + t] = q[r];
+                    fl[Cf::FED + t] = E[r];
+                    E[r] = 0.f;
+                }
+                rowsum = fmaf(E[r], dt_s[r], rowsum);
+                float v1 = qd * dt_s[r], v2 = kd;
+#pragma unroll
+                for (int part = 0; part < XP; ++part) {
+                    m1[part].s[r] = f32_to_bf16(v1);
+                    m2[part].s[r] = f32_to_bf16(v2);
+                    v1 -= bf16_to_f32(m1[part].s[r]);
+                    v2 -= bf16_to_f32(m2[part].s[r]);
+                }
+            }
+#pragma unroll
+            for (int part = 0; part < XP; ++part) {
+                *reinterpret_cast<uint2 *>(lds + Cf::M1 + part * L * RL + t * RL + col_pos(s0)) = m1[part].u;
+                *reinterpret_cast<uint2 *>(lds + Cf::M2 + part * L * RL + t * RL + col_pos(s0)) = m2[part].u;
+            }
+            rowsum += __shfl_xor(rowsum, 16);
+            rowsum += __shfl_xor(rowsum, 32);
+            if (g == 0) fl[Cf::FR + tj * L + t] = rowsum;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int b = 1; b < 16; b <<= 1) E[r] += __shfl_xor(E[r], b);
+            if (c16 == 0)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) fl[Cf::FC + ti * L + s0 + r] = E[r];
+        }
+
+        // ---- the states' shares of dC and dB, and their sums with C and B
+        if (rows_on) {
+            parts8<SP> Sf[PKS], Gf[PKS];
+            float gs = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < PKS; ++ks)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    gs = fmaf(Sv[ks][j / 4][j % 4], Gv[ks][j / 4][j % 4], gs);
+                    split_to<SP>(Sf[ks], j, Sv[ks][j / 4][j % 4]);
+                    split_to<SP>(Gf[ks], j, Gv[ks][j / 4][j % 4]);
+                }
+#pragma unroll
+            for (int b = 1; b < 64; b <<= 1) gs += __shfl_xor(gs, b);
+            if (lane == 0) fl[Cf::FX + wave] = gs;
+            float vi[4 * ST], vo[4 * ST];
+#pragma unroll
+            for (int s = 0; s < ST; ++s) {
+                f32x4 ts = {0.f, 0.f, 0.f, 0.f}, tg = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < PKS; ++ks) {
+                    parts8<EX> y, x;
+#pragma unroll
+                    for (int part = 0; part < EX; ++part) {
+                        load_rows(y.f[part], lds + Cf::YN + part * L * RP, RP, 16 * s, ks, g, c16);
+                        load_rows(x.f[part], lds + Cf::XN + part * L * RP, RP, 16 * s, ks, g, c16);
+                    }
+                    mfma_parts<EX, SP, 3>(ts, y, Sf[ks]);
+                    mfma_parts<EX, SP, 3>(tg, x, Gf[ks]);
+                }
+                const f32x4 cum = *reinterpret_cast<const f32x4 *>(fl + Cf::FCUM + 16 * s + 4 * g);
+                const f32x4 ws = *reinterpret_cast<const f32x4 *>(fl + Cf::FWS + 16 * s + 4 * g);
+                const f32x4 dts = *reinterpret_cast<const f32x4 *>(fl + Cf::FDT + 16 * s + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    ts[r] *= cum[r];
+                    tg[r] *= ws[r];
+                    vi[4 * s + r] = ts[r] * elem(Ct, s, r);
+                    vo[4 * s + r] = tg[r] * elem(Bt, s, r);
+                    dCs[s][r] += ts[r];
+                    dBs[s][r] = fmaf(dts[r], tg[r], dBs[s][r]);
+                }
+            }
+            const float si = sum16<4 * ST>(vi, c16), sg = sum16<4 * ST>(vo, c16);
+            const int k = sum16_index<4 * ST>(c16);
+            const int t = 16 * (k / 4) + 4 * g + k % 4;
+            if (ST == 4 || !(c16 & 1)) {
+                fl[Cf::FI + wave * L + t] = si;
+                fl[Cf::FO + wave * L + t] = sg;
+            }
+        }
+        lds_barrier();
+
+        // ---- the chunk's own shares of dC and dB
+        if (rows_on) {
+#pragma unroll
+            for (int s = 0; s < ST; ++s) {
+#pragma unroll
+                for (int ks = 0; ks <= s / 2; ++ks) {
+                    parts8<XP> m;
+#pragma unroll
+                    for (int part = 0; part < XP; ++part) load_rows(m.f[part], lds + Cf::M1 + part * L * RL, RL, 16 * s, ks, g, c16);
+                    mfma_parts<XP, EX, ORD>(dCs[s], m, Bt[ks]);
+                }
+#pragma unroll
+                for (int ks = s / 2; ks < TK; ++ks) {
+                    parts8<XP> m;
+#pragma unroll
+                    for (int part = 0; part < XP; ++part) load_cols(m.f[part], lds + Cf::M1 + part * L * RL, RL, 32 * ks, 16 * s, g, c16);
+                    mfma_parts<XP, EX, ORD>(dBs[s], m, Ct[ks]);
+                }
+            }
+        }
+        // ---- du and dx: 16 x 16 tiles (strip s, channel tile pt)
+        const float Dh = p.D ? p.D[h] : 0.f;
+        for (int u = wave; u < PT * ST; u += 8) {
+            const int pt = u % PT, s = u / PT;
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            const float *Gp = a.gstates + (static_cast<int64_t>(item) * p.H + h) * NS * P + 16 * pt + c16;
+#pragma unroll
+            for (int kk = 0; kk < NKS; ++kk) {
+                parts8<XP> gf;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int n = 32 * kk + kperm(g, j);
+                    split_to<XP>(gf, j, n < NS ? Gp[n * P] : 0.f);
+                }
+                parts8<EX> b;
+#pragma unroll
+                for (int part = 0; part < EX; ++part) load_rows(b.f[part], lds + Cf::BN + part * L * RN, RN, 16 * s, kk, g, c16);
+                mfma_parts<EX, XP, ORD>(acc, b, gf);
+            }
+            acc *= *reinterpret_cast<const f32x4 *>(fl + Cf::FWS + 16 * s + 4 * g);
+            const f32x4 dts = *reinterpret_cast<const f32x4 *>(fl + Cf::FDT + 16 * s + 4 * g);
+            float dyv[4] = {};
+#pragma unroll
+            for (int ks = 0; ks < TK; ++ks) {
+                if (ks < s / 2) continue;
+                parts8<EX> y;
+                parts8<XP> m;
+#pragma unroll
+                for (int part = 0; part < EX; ++part) load_cols(y.f[part], lds + Cf::YN + part * L * RP, RP, 32 * ks, 16 * pt, g, c16);
+#pragma unroll
+                for (int part = 0; part < XP; ++part) load_cols(m.f[part], lds + Cf::M2 + part * L * RL, RL, 32 * ks, 16 * s, g, c16);
+                mfma_parts<XP, EX, ORD>(acc, m, y);
+                if (ks == s / 2)
+#pragma unroll
+                    for (int part = EX - 1; part >= 0; --part)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) dyv[r] += bf16_to_f32((s & 1) ? y.f[part].s[4 + r] : y.f[part].s[r]);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = 16 * s + 4 * g + r;
+                if (t < len)
+                    io<TI>::st(static_cast<TI *>(a.dx), ((flat0 + t) * p.H + h) * P + 16 * pt + c16, fmaf(dts[r], acc[r], Dh * dyv[r]));
+            }
+        }
+        // ---- the step sizes: one token a lane
+        if (wave == 7) {
+            float R = 0.f, Cs = 0.f, in = 0.f, out = 0.f, X = 0.f;
+            if (lane < L) {
+#pragma unroll
+                for (int k = 0; k < ST; ++k) {
+                    R += fl[Cf::FR + k * L + lane];
+                    Cs += fl[Cf::FC + k * L + lane];
+                }
+#pragma unroll
+                for (int k = 0; k < NT; ++k) {
+                    in += fl[Cf::FI + k * L + lane];
+                    out += fl[Cf::FO + k * L + lane];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < NT; ++k) X += fl[Cf::FX + k];
+            const float o = dt * out;
+            const float dlog = suffix_sum(R - dt * Cs + in, lane) + before(prefix_sum(o, lane), lane) + fast_exp2(tot) * X;
+            float dd = Cs + (lane < L ? fl[Cf::FED + lane] : 0.f) + out + A * dlog;
+            if (p.softplus) dd *= sigmoid_f32(raw);
+            if (lane >= len) dd = 0.f;
+            if (lane < len) io<TI>::st(static_cast<TI *>(a.ddt), (flat0 + lane) * p.H + h, dd);
+            const float sa = prefix_sum(dt * dlog, lane), sd = prefix_sum(lane < L ? fl[Cf::FQD + lane] : 0.f, lane);
+            const float sb = prefix_sum(dd, lane);
+            if (lane == 63) {
+                a.scalars[(0 * static_cast<int64_t>(p.H) + h) * items + item] = sa;
+                a.scalars[(1 * static_cast<int64_t>(p.H) + h) * items + item] = sd;
+                a.scalars[(2 * static_cast<int64_t>(p.H) + h) * items + item] = sb;
+            }
+        }
+        lds_barrier();  // the next head's tiles may be written
+    }
+    if (rows_on)
+#pragma unroll
+        for (int s = 0; s < ST; ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = 16 * s + 4 * g + r;
+                if (t >= len) continue;
+                const int64_t at = ((flat0 + t) * p.G + grp) * NS + n0 + c16;
+                if (a.part_B) {
+                    const int64_t plane = static_cast<int64_t>(p.B) * p.T * p.G * NS;
+                    a.part_B[split * plane + at] = dBs[s][r];
+                    a.part_C[split * plane + at] = dCs[s][r];
+                } else {
+                    io<TI>::st(static_cast<TI *>(a.dB), at, dBs[s][r]);
+                    io<TI>::st(static_cast<TI *>(a.dC), at, dCs[s][r]);
+                }
+            }
+}
+
+// dB and dC from the splits' sums, 4 values a thread
+template <typename TI>
+__global__ void __launch_bounds__(256) ssm_grad_sum_kernel(SsmGrad a, int64_t plane) {
+    if (a.q.p.cu_seqlens && *a.q.status != 0) return;
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (i >= 2 * plane) return;
+    const float *src = i < plane ? a.part_B + i : a.part_C + (i - plane);
+    TI *dst = i < plane ? static_cast<TI *>(a.dB) + i : static_cast<TI *>(a.dC) + (i - plane);
+    f32x4 v = *reinterpret_cast<const f32x4 *>(src);
+    for (int k = 1; k < a.splits; ++k) v += *reinterpret_cast<const f32x4 *>(src + k * plane);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) io<TI>::st(dst, c, v[c]);
+}
+
+template <typename TI, int NS, int P>
+hipError_t grad_run(const SsmGrad &a, hipStream_t s) {
+    const int64_t items = a.q.p.cu_seqlens ? static_cast<int64_t>(a.q.chunks_per_seq) + a.q.p.N
+                                           : static_cast<int64_t>(a.q.p.N) * a.q.chunks_per_seq;
+    const int64_t want = items * GradCfg<TI, NS, P>::SUB * a.q.p.G * a.splits;
+    if (want == 0) return hipSuccess;
+    hipLaunchKernelGGL((ssm_grad_kernel<TI, NS, P>), dim3(static_cast<unsigned>((want + 7) / 8 * 8)), dim3(512), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.part_B || a.q.p.T == 0) return e;
+    const int64_t plane = static_cast<int64_t>(a.q.p.B) * a.q.p.T * a.q.p.G * NS;
+    hipLaunchKernelGGL((ssm_grad_sum_kernel<TI>), dim3(static_cast<unsigned>((2 * plane / 4 + 255) / 256)), dim3(256), 0, s, a, plane);
+    return hipGetLastError();
+}
+template <typename TI, int NS>
+hipError_t grad_p(const SsmGrad &a, hipStream_t s) {
+    switch (a.q.p.P) {
+        case 16: return grad_run<TI, NS, 16>(a, s);
+        case 32: return grad_run<TI, NS, 32>(a, s);
+        case 64: return grad_run<TI, NS, 64>(a, s);
+        default: return grad_run<TI, NS, 128>(a, s);
+    }
+}
+template <typename TI>
+hipError_t grad_n(const SsmGrad &a, hipStream_t s) {
+    switch (a.q.p.Ns) {
+        case 16: return grad_p<TI, 16>(a, s);
+        case 32: return grad_p<TI, 32>(a, s);
+        case 64: return grad_p<TI, 64>(a, s);
+        default: return grad_p<TI, 128>(a, s);
+    }
+}
+
+}  // namespace
+}  // namespace kda

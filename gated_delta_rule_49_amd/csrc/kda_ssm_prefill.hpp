@@ -26,7 +26,8 @@ struct ScanCfg {
     static constexpr int EX = quad<TI>::PARTS;            // parts of an input
     static constexpr int L = BF ? 64 : 32;                // tokens of a chunk
     static constexpr int ORD = BF ? 2 : 3;
-    static constexpr int XP = BF ? 2 : 3;                 // parts of w x, and of the scores
+    static constexpr int XP = 3;                          // parts of w x: the state keeps fp32 accuracy
+    static constexpr int GP = BF ? 2 : 3;                 // parts of the scores
     // the state as an operand of C S: a bf16 y carries a rounding of up to
     // 2^-9 of its own; one part of S adds an error of that size only to what
     // the state contributes
@@ -37,7 +38,7 @@ struct ScanCfg {
     static constexpr int NBUF = BF ? 2 : 1;
     static constexpr int CN = FULL ? EX * L * RN : 0;     // C, and B by rows
     static constexpr int BT = EX * NS * RT;               // B transposed
-    static constexpr int GT = FULL ? XP * L * RT : 0;     // causal scores
+    static constexpr int GT = FULL ? GP * L * RT : 0;     // causal scores
     static constexpr int BUF = 2 * CN + BT + GT;
     static constexpr int WV = 4 * L;                      // per wave: w, row factor, suf, dt
     static constexpr size_t BYTES = sizeof(bf16_t) * NBUF * BUF + sizeof(float) * NW * WV;
@@ -46,7 +47,7 @@ struct ScanCfg {
 template <typename TI, typename TO, int NS, int PW, int NW, int MODE>
 __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks_per_group, int phase) {
     using Cf = ScanCfg<TI, TO, NS, PW, NW, MODE>;
-    constexpr int EX = Cf::EX, L = Cf::L, ORD = Cf::ORD, XP = Cf::XP, SP = Cf::SP, NT = Cf::NT, KS = Cf::KS;
+    constexpr int EX = Cf::EX, L = Cf::L, ORD = Cf::ORD, XP = Cf::XP, GP = Cf::GP, SP = Cf::SP, NT = Cf::NT, KS = Cf::KS;
     constexpr int CT = Cf::CT, ST = Cf::ST, TK = Cf::TK, RN = Cf::RN, RT = Cf::RT, NBUF = Cf::NBUF;
     constexpr bool FULL = MODE == SSM_FULL, REV = MODE == SSM_REVERSE;
     __shared__ __attribute__((aligned(16))) char smem[Cf::BYTES];
@@ -179,18 +180,18 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                 }
                 mfma_parts<EX, EX, ORD>(acc, a, bf);
             }
-            granule out[XP];
+            granule out[GP];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 float v = ti == tj && 4 * g + r > c16 ? 0.f : acc[r];
 #pragma unroll
-                for (int part = 0; part < XP; ++part) {
+                for (int part = 0; part < GP; ++part) {
                     out[part].s[r] = f32_to_bf16(v);
                     v -= bf16_to_f32(out[part].s[r]);
                 }
             }
 #pragma unroll
-            for (int part = 0; part < XP; ++part)
+            for (int part = 0; part < GP; ++part)
                 *reinterpret_cast<uint2 *>(Gt(b, part) + (16 * ti + c16) * RT + col_pos(16 * tj + 4 * g)) = out[part].u;
         }
     };
@@ -234,8 +235,8 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
         if (i + 1 < chunks) fetch_x(order(i + 1), xn, dtn);
         if (on) {
             // the state entering the 64-token chunk (from the right in the reverse order)
-            if (phase == 2 && p.chunk_states && (REV ? (t0 + L) % 64 == 0 || i == 0 : t0 % 64 == 0))
-                store_state(p.chunk_states + (static_cast<int64_t>(sg.chunk + t0 / 64) * p.H + h) * per_head);
+            if (phase == 2 && p.chunk_states && t0 % q.state_chunk == 0)
+                store_state(p.chunk_states + ((static_cast<int64_t>(sg.chunk + t0 / 64) * (64 / q.state_chunk) + t0 % 64 / q.state_chunk) * p.H + h) * per_head);
             // decays, one token a lane
             float dt = io<TI>::ld(&dtr, 0) + bias;
             if (p.softplus) dt = softplus_rel(dt);
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
             const float la = A2 * dt;
             const float incl = suffix_sum(la, lane);
             const float tot = __shfl(incl, 0);
-            const float suf = incl - la;
+            const float suf = after(incl, lane);
             const bool fast = fabsf(tot) < kFastTot;
             if (lane < L) {
                 if (REV) {
@@ -313,12 +314,12 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                     for (int s = 0; s < ST; ++s) {
 #pragma unroll
                         for (int ks = 0; ks <= s / 2; ++ks) {
-                            parts8<XP> a;
+                            parts8<GP> a;
 #pragma unroll
-                            for (int part = 0; part < XP; ++part)
+                            for (int part = 0; part < GP; ++part)
                                 a.f[part].u = *reinterpret_cast<const uint4 *>(Gt(b, part) + (16 * s + c16) * RT + ks * 32 + 8 * g);
 #pragma unroll
-                            for (int ct = 0; ct < CT; ++ct) mfma_parts<XP, XP, ORD>(acc[s][ct], a, xw[ks][ct]);
+                            for (int ct = 0; ct < CT; ++ct) mfma_parts<GP, XP, ORD>(acc[s][ct], a, xw[ks][ct]);
                         }
                         const f32x4 f = *reinterpret_cast<const f32x4 *>(fv + 16 * s + 4 * g);
 #pragma unroll
@@ -334,16 +335,16 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                         const float suf_row = sv[row];
 #pragma unroll
                         for (int ks = 0; ks <= s / 2; ++ks) {
-                            parts8<XP> m;
+                            parts8<GP> m;
 #pragma unroll
-                            for (int part = 0; part < XP; ++part)
+                            for (int part = 0; part < GP; ++part)
                                 m.f[part].u = *reinterpret_cast<const uint4 *>(Gt(b, part) + row * RT + ks * 32 + 8 * g);
                             float mv[8];
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 mv[j] = 0.f;
 #pragma unroll
-                                for (int part = XP - 1; part >= 0; --part) mv[j] += bf16_to_f32(m.f[part].s[j]);
+                                for (int part = GP - 1; part >= 0; --part) mv[j] += bf16_to_f32(m.f[part].s[j]);
                             }
 #pragma unroll
                             for (int hq = 0; hq < 2; ++hq) {
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
 #pragma unroll
                                 for (int r = 0; r < 4; ++r) {
                                     const float k = col + r <= row ? dc[r] * fast_exp2(sc[r] - suf_row) : 0.f;
-                                    split_to<XP>(m, 4 * hq + r, mv[4 * hq + r] * k);
+                                    split_to<GP>(m, 4 * hq + r, mv[4 * hq + r] * k);
                                 }
                             }
 #pragma unroll
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                                 parts8<EX> xe;
 #pragma unroll
                                 for (int j = 0; j < 8; ++j) split_to<EX>(xe, j, xr[ks][j].get(ct));
-                                mfma_parts<XP, EX, ORD>(acc[s][ct], m, xe);
+                                mfma_parts<GP, EX, ORD>(acc[s][ct], m, xe);
                             }
                         }
                     }
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                     for (int part = 0; part < EX; ++part)
                         a.f[part].u = *reinterpret_cast<const uint4 *>(Bt(b, part) + (16 * nt + c16) * RT + ks * 32 + 8 * g);
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mfma_parts<EX, XP, ORD>(S[nt][ct], a, xw[ks][ct]);
+                    for (int ct = 0; ct < CT; ++ct) mfma_parts<EX, XP, 3>(S[nt][ct], a, xw[ks][ct]);
                 }
         }
         lds_barrier();

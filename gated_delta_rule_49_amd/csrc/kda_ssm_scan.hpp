@@ -63,7 +63,8 @@ struct SsmScan {
     int32_t seg_chunks;       // chunks of KDA_SSM_CHUNK tokens per segment
     int32_t segs_bound;       // grid bound on the number of segments
     int32_t segs_per_seq;     // unpacked
-    int32_t chunks_per_seq;   // unpacked
+    int32_t chunks_per_seq;   // ceil(T / 64)
+    int32_t state_chunk;      // tokens between the chunk_states written: 64, or 32 (fp32 gradients)
 };
 
 struct SsmSeg {
@@ -247,8 +248,21 @@ struct SsmPlan {
 SsmPlan ssm_plan(const SsmParams &p, bool packed);
 // fills the tables' pointers of q from a workspace laid out by the plan
 void ssm_layout(SsmScan &q, const SsmPlan &plan, char *ws);
+// the same without the lane's own value (taken from the neighbour's sum, not
+// by subtracting: the own value may be far larger than the sum)
+__device__ __forceinline__ float before(float inclusive, int lane) {
+    const float o = __shfl_up(inclusive, 1);
+    return lane > 0 ? o : 0.f;
+}
+__device__ __forceinline__ float after(float inclusive, int lane) {
+    const float o = __shfl_down(inclusive, 1);
+    return lane < 63 ? o : 0.f;
+}
+
 // segment and chunk tables of packed sequences; checks the offsets
 hipError_t launch_ssm_table(const SsmScan &q, hipStream_t s);
+// the status word where there are no offsets to check
+hipError_t launch_ssm_status(const SsmScan &q, hipStream_t s);
 // chains the segments' end states into the states entering each, in place;
 // reverse: from the last segment to the first
 hipError_t launch_ssm_combine(const SsmScan &q, const float *first, bool reverse, hipStream_t s);
@@ -257,6 +271,34 @@ hipError_t launch_ssm_combine(const SsmScan &q, const float *first, bool reverse
 // but the first); phase 2: from the entering states.
 enum { SSM_FULL = 0, SSM_STATES = 1, SSM_REVERSE = 2 };
 hipError_t launch_ssm_phase(const SsmScan &q, const SsmPlan &plan, int mode, int phase, int in_dtype, int out_dtype, hipStream_t s);
+// Gradients (kda_ssm_backward.hpp)
+struct SsmGrad {
+    SsmScan q;                  // p.x, p.Bm, p.Cm, p.dt as in the forward
+    const void *d_y;            // [B, T, H, P]
+    const float *states, *gstates;  // [chunks * SUB, H, Ns, P]: entering each chunk, from the left / from the right
+    void *dx, *ddt, *dB, *dC;
+    float *part_B, *part_C;     // [splits, B T, G, Ns] where a group's heads are split, else null
+    float *scalars;             // [3, H, items]: dA, dD, ddt_bias of every chunk
+    int32_t heads_per_block, splits;
+};
+hipError_t ssm_grad_bf16(const SsmGrad &a, hipStream_t s);
+hipError_t ssm_grad_f32(const SsmGrad &a, hipStream_t s);
+// all of a backward pass; the workspace's layout is the plan's
+struct SsmGradPlan {
+    SsmPlan scan;
+    int32_t sub, splits, heads_per_block;
+    int64_t items;  // bound on the chunks (parts of 64 tokens in fp32)
+    size_t state_bytes, part_bytes, scalar_bytes;
+    size_t bytes() const { return scan.bytes() + 2 * state_bytes + 2 * part_bytes + scalar_bytes; }
+};
+SsmGradPlan ssm_grad_plan(const SsmParams &p, bool packed, int in_dtype);
+struct SsmGradOut {
+    const void *d_y;
+    const float *d_final;
+    void *dx, *ddt, *dB, *dC;
+    float *dA, *dD, *ddt_bias, *d_initial;
+};
+hipError_t launch_ssm_backward(const SsmParams &p, const SsmGradOut &o, char *ws, int in_dtype, hipStream_t s);
 // a whole scan: phases and combination
 hipError_t launch_ssm_scan(const SsmScan &q, const SsmPlan &plan, int mode, int in_dtype, int out_dtype, hipStream_t s);
 

@@ -140,6 +140,7 @@ SsmPlan ssm_plan(const SsmParams &p, bool packed) {
 }
 
 void ssm_layout(SsmScan &q, const SsmPlan &plan, char *ws) {
+    q.state_chunk = 64;
     q.seg_chunks = plan.seg_chunks; q.segs_bound = plan.segs_bound;
     q.segs_per_seq = plan.segs_per_seq; q.chunks_per_seq = plan.chunks_per_seq;
     const size_t words = align_up(sizeof(int32_t) * (static_cast<size_t>(q.p.N) + 1));
@@ -154,6 +155,13 @@ void ssm_layout(SsmScan &q, const SsmPlan &plan, char *ws) {
 hipError_t launch_ssm_table(const SsmScan &q, hipStream_t s) {
     hipLaunchKernelGGL(ssm_table_kernel, dim3(1), dim3(1024), 0, s, q, const_cast<int32_t *>(q.seg_off),
                        const_cast<int4 *>(q.seg_info), const_cast<int32_t *>(q.chunk_off), const_cast<int32_t *>(q.status));
+    return hipGetLastError();
+}
+
+__global__ void ssm_status_kernel(int32_t *status) { *status = 0; }
+
+hipError_t launch_ssm_status(const SsmScan &q, hipStream_t s) {
+    hipLaunchKernelGGL(ssm_status_kernel, dim3(1), dim3(1), 0, s, const_cast<int32_t *>(q.status));
     return hipGetLastError();
 }
 

@@ -4,8 +4,8 @@ and marshal torch tensors, allocate outputs and workspaces with torch, and
 launch on torch's current stream of the tensors' device.
 
 ``short_conv_backward``  gradients of the short causal convolution
-``ssm_prefill`` / ``ssm_decode``  the selective state space scan for prompts and
-    for a few tokens
+``ssm_prefill`` / ``ssm_decode`` / ``ssm_backward``  the selective state space
+    scan for prompts, for a few tokens, and its gradients
 ``block_norm`` / ``block_norm_backward``  the norm after a block with its
     gate, the scaled residual and the norm before the next block
 """
@@ -16,7 +16,7 @@ import ctypes
 import torch
 
 from . import (GATE_SIGMOID, GATE_SILU, SSM_CHUNK, BlockNormArgs, BlockNormBackwardArgs, ConvBackwardArgs, KDAError,
-               SsmArgs, SsmDecodeArgs, _check_buffer, _check_dev, _dt, _host_chunk_count, lib)
+               SsmArgs, SsmBackwardArgs, SsmDecodeArgs, _check_buffer, _check_dev, _dt, _host_chunk_count, lib)
 
 _F32 = (torch.float32,)
 
@@ -221,6 +221,48 @@ def ssm_decode(x, dt, A, B, C, state, D=None, dt_bias=None, dt_softplus=False, o
     a.initial_state, a.final_state, a.token_states, a.y = _p(state), _p(final_state), _p(ts), _p(y)
     _run(lib().kda_ssm_decode, a, dev, "kda_ssm_decode")
     return y, final_state, ts
+
+
+def ssm_backward(x, dt, A, B, C, d_y, D=None, dt_bias=None, dt_softplus=False, initial_state=None, d_final_state=None,
+                 cu_seqlens=None, device_status=None):
+    """Gradients of the scan from d_y [B,T,H,d_head] (x's dtype) and
+    d_final_state fp32 [N,H,d_state,d_head] (None = zeros): (dx, ddt, dA, dB,
+    dC, dD, ddt_bias, d_initial_state).  dx, ddt, dB and dC have x's dtype
+    (dt's through its softplus and bias; those of B and C summed over a
+    group's heads), the others are float32; dD is None without D, ddt_bias
+    without dt_bias.  The states entering the chunks are recomputed from
+    ``initial_state``.  Nothing synchronises; ``device_status`` (int32 [1] on
+    the device) receives the call's device-side status: with malformed
+    cu_seqlens the gradients are not written."""
+    a, dev, (nb, t, h, p, g, n) = _scan_args(SsmBackwardArgs, x, dt, A, B, C, D, dt_bias, dt_softplus)
+    N = _packed(cu_seqlens, nb, dev)
+    _dense(dev, d_y, initial_state, d_final_state, device_status)
+    _check_buffer(d_y, "d_y", (nb, t, h, p), (x.dtype,))
+    for name, v in (("initial_state", initial_state), ("d_final_state", d_final_state)):
+        _check_buffer(v, name, (N, h, n, p), _F32)
+    _check_buffer(device_status, "device_status", (1,), (torch.int32,))
+    like = dict(dtype=x.dtype, device=dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    dx, ddt = torch.empty((nb, t, h, p), **like), torch.empty((nb, t, h), **like)
+    dB, dC = torch.empty((nb, t, g, n), **like), torch.empty((nb, t, g, n), **like)
+    dA, d_initial = torch.empty(h, **f32), torch.empty((N, h, n, p), **f32)
+    dD = torch.empty(h, **f32) if D is not None else None
+    dbias = torch.empty(h, **f32) if dt_bias is not None else None
+    a.T, a.num_seqs = t, N
+    a.cu_seqlens, a.initial_state = _p(cu_seqlens), _p(initial_state)
+    a.d_y, a.d_final_state = _p(d_y), _p(d_final_state)
+    a.dx, a.ddt, a.dB, a.dC, a.dA, a.dD, a.ddt_bias = _p(dx), _p(ddt), _p(dB), _p(dC), _p(dA), _p(dD), _p(dbias)
+    a.d_initial_state = _p(d_initial)
+    L = lib()
+    need = int(L.kda_ssm_backward_workspace_bytes(ctypes.byref(a)))
+    if need == 0:
+        raise KDAError(L.kda_ssm_backward(ctypes.byref(a), None), "kda_ssm_backward")
+    ws = _workspace(need, dev)
+    a.workspace, a.workspace_bytes = _p(ws), need
+    _run(L.kda_ssm_backward, a, dev, "kda_ssm_backward")
+    if device_status is not None:  # the workspace's first word is the call's status
+        device_status.copy_(ws[:4].view(torch.int32))
+    return dx, ddt, dA, dB, dC, dD, dbias, d_initial
 
 
 # ----------------------------------------------------------------- block norm

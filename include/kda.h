@@ -31,8 +31,9 @@
  *   kda_backward         gradients of the recurrence (reverse mode through the
  *                        chunked form, from the prefill's chunk checkpoints).
  *   kda_short_conv_backward  gradients of the short convolution.
- *   kda_ssm_prefill, kda_ssm_decode  the selective state space scan for
- *                        prompts and for a few tokens.
+ *   kda_ssm_prefill, kda_ssm_decode, kda_ssm_backward  the selective state
+ *                        space scan for prompts, for a few tokens, and its
+ *                        gradients.
  *   kda_block_norm, kda_block_norm_backward  the norm after a block with its
  *                        gate, the scaled residual and the norm before the
  *                        next block, and their gradients.
@@ -495,6 +496,49 @@ typedef struct kda_ssm_decode_args {
     void *y;
 } kda_ssm_decode_args;
 kda_status kda_ssm_decode(const kda_ssm_decode_args *a, void *hip_stream);
+
+/*
+ * Gradients of the scan: of x, dt (as given: through the softplus and the
+ * bias), A, B, C, D, dt_bias and the initial state, from the gradients of y
+ * and of the final state.
+ *   x .. cu_seqlens  as for kda_ssm_prefill
+ *   d_y           DEVICE [B, T, H, d_head] in_dtype, contiguous
+ *   d_final_state DEVICE fp32 [num_seqs, H, d_state, d_head], NULL = zeros
+ *   dx, ddt, dB, dC  DEVICE, shapes of x, dt, Bm, Cm, contiguous, in_dtype
+ *   dA            DEVICE fp32 [H];  dD, ddt_bias DEVICE fp32 [H], NULL = not
+ *                 written
+ *   d_initial_state DEVICE fp32 [num_seqs, H, d_state, d_head], NULL = not
+ *                 written
+ *   workspace     DEVICE, >= kda_ssm_backward_workspace_bytes(args), 256-byte
+ *                 aligned; its first int32 word holds the call's device
+ *                 status once it has run
+ * The states entering the chunks are recomputed from initial_state in the
+ * workspace, whose size is about 2 fp32 states per 64 tokens (32 with fp32
+ * inputs) and head.  With malformed cu_seqlens nothing is written.  Results
+ * are the same from run to run (no floating-point atomics).
+ */
+typedef struct kda_ssm_backward_args {
+    int32_t B, T, H, G, d_head, d_state;
+    int32_t num_seqs;
+    int32_t in_dtype;              /* kda_dtype */
+    int32_t dt_softplus;           /* 0 or 1 */
+    int64_t x_stride_b, x_stride_t;
+    int64_t b_stride_b, b_stride_t;
+    int64_t c_stride_b, c_stride_t;
+    const void *x, *dt, *Bm, *Cm;
+    const float *A, *D, *dt_bias;
+    const int32_t *cu_seqlens;
+    const float *initial_state;
+    const void *d_y;
+    const float *d_final_state;
+    void *dx, *ddt, *dB, *dC;
+    float *dA, *dD, *ddt_bias;
+    float *d_initial_state;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_ssm_backward_args;
+size_t kda_ssm_backward_workspace_bytes(const kda_ssm_backward_args *a);
+kda_status kda_ssm_backward(const kda_ssm_backward_args *a, void *hip_stream);
 
 /*
  * Gradients of kda_short_conv: of x, the weight, the bias and the initial

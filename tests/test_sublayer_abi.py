@@ -28,7 +28,7 @@ def names(cls):
 
 
 @pytest.mark.parametrize("cname,cls", [("kda_conv_backward_args", kda.ConvBackwardArgs), ("kda_ssm_args", kda.SsmArgs),
-                                       ("kda_ssm_decode_args", kda.SsmDecodeArgs), ("kda_block_norm_args", kda.BlockNormArgs),
+                                       ("kda_ssm_decode_args", kda.SsmDecodeArgs), ("kda_ssm_backward_args", kda.SsmBackwardArgs), ("kda_block_norm_args", kda.BlockNormArgs),
                                        ("kda_block_norm_backward_args", kda.BlockNormBackwardArgs)])
 def test_struct_layout_matches_header(tmp_path, cname, cls):
     body = "".join(f'printf("%zu\\n", offsetof({cname}, {f}));' for f in names(cls))
@@ -96,6 +96,19 @@ def test_scan_sizes(L):
     assert L.kda_ssm_max_chunks(ctypes.byref(a)) == 7
 
 
+SSM_GRAD = dict({k: v for k, v in SSM.items() if k not in ("out_dtype", "y")}, d_y=FAKE, dx=FAKE, ddt=FAKE, dB=FAKE, dC=FAKE, dA=FAKE)
+
+
+@pytest.mark.parametrize("over,status", SSM_REFUSED + [
+    (dict(B=0), BAD_SHAPE), (dict(T=-1), BAD_SHAPE), (dict(num_seqs=1), BAD_SHAPE), (dict(cu_seqlens=FAKE), BAD_SHAPE),
+    (dict(T=1 << 29), UNSUPPORTED), (dict(d_y=None), NULL_ARG), (dict(dx=None), NULL_ARG), (dict(ddt=None), NULL_ARG), (dict(dB=None), NULL_ARG),
+    (dict(dC=None), NULL_ARG), (dict(dA=None), NULL_ARG), (dict(dD=FAKE), BAD_SHAPE), (dict(ddt_bias=FAKE), BAD_SHAPE),
+    (dict(workspace=None), NULL_ARG), (dict(workspace=FAKE + 128), BAD_SHAPE), (dict(workspace_bytes=8), TOO_SMALL),
+    (dict(d_y=FAKE + 8), UNSUPPORTED), (dict(d_initial_state=FAKE + 4), UNSUPPORTED), (dict(dB=FAKE + 2), UNSUPPORTED)])
+def test_scan_backward(L, over, status):
+    assert L.kda_ssm_backward(ctypes.byref(fill(kda.SsmBackwardArgs, SSM_GRAD, over)), None) == status
+
+
 DECODE = dict({k: v for k, v in SSM.items() if k not in ("T", "num_seqs", "workspace", "workspace_bytes")}, n_tokens=2, initial_state=FAKE)
 
 
@@ -138,9 +151,9 @@ def test_block_norm_backward(L, inner, over, status):
 
 
 def test_null_arguments(L):
-    for fn in (L.kda_short_conv_backward, L.kda_ssm_prefill, L.kda_ssm_decode, L.kda_block_norm, L.kda_block_norm_backward):
+    for fn in (L.kda_short_conv_backward, L.kda_ssm_prefill, L.kda_ssm_decode, L.kda_ssm_backward, L.kda_block_norm, L.kda_block_norm_backward):
         assert fn(None, None) == NULL_ARG
-    for fn in (L.kda_short_conv_backward_workspace_bytes, L.kda_ssm_workspace_bytes, L.kda_ssm_max_chunks,
+    for fn in (L.kda_short_conv_backward_workspace_bytes, L.kda_ssm_workspace_bytes, L.kda_ssm_max_chunks, L.kda_ssm_backward_workspace_bytes,
                L.kda_block_norm_backward_workspace_bytes):
         assert fn(None) == 0
 
@@ -149,6 +162,8 @@ def test_binding_refuses_cpu_tensors():
     z = torch.zeros
     with pytest.raises(ValueError, match="GPU"):
         kda.ssm_prefill(z(1, 4, 2, 16), z(1, 4, 2), z(2), z(1, 4, 1, 16), z(1, 4, 1, 16))
+    with pytest.raises(ValueError, match="GPU"):
+        kda.ssm_backward(z(1, 4, 2, 16), z(1, 4, 2), z(2), z(1, 4, 1, 16), z(1, 4, 1, 16), z(1, 4, 2, 16))
     with pytest.raises(ValueError, match="GPU"):
         kda.ssm_decode(z(1, 4, 2, 16), z(1, 4, 2), z(2), z(1, 4, 1, 16), z(1, 4, 1, 16), z(1, 2, 16, 16))
     with pytest.raises(ValueError, match="GPU"):
