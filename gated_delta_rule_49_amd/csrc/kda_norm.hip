@@ -56,6 +56,27 @@ template <> struct rowvec<float, 8> {
         reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
 };
+template <> struct rowvec<bf16_t, 4> {
+    uint2 u;
+    __device__ void ld(const bf16_t *p) { u = *reinterpret_cast<const uint2 *>(p); }
+    __device__ void zero() { u = make_uint2(0, 0); }
+    __device__ float get(int c) const {
+        const uint32_t w = c < 2 ? u.x : u.y;
+        return __uint_as_float((c & 1) ? (w & 0xffff0000u) : (w << 16));
+    }
+    __device__ static void st(bf16_t *p, const float (&v)[4]) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(
+            static_cast<uint32_t>(f32_to_bf16(v[0])) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16),
+            static_cast<uint32_t>(f32_to_bf16(v[2])) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16));
+    }
+};
+template <> struct rowvec<float, 4> {
+    float4 u;
+    __device__ void ld(const float *p) { u = *reinterpret_cast<const float4 *>(p); }
+    __device__ void zero() { u = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ float get(int c) const { return c == 0 ? u.x : c == 1 ? u.y : c == 2 ? u.z : u.w; }
+    __device__ static void st(float *p, const float (&v)[4]) { *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]); }
+};
 template <typename T> struct rowvec<T, 1> {
     T u;
     __device__ void ld(const T *p) { u = *p; }
@@ -64,15 +85,18 @@ template <typename T> struct rowvec<T, 1> {
     __device__ static void st(T *p, const float (&v)[1]) { io<T>::st(p, 0, v[0]); }
 };
 
+// 1 / (1 + e^-z) with the hardware's reciprocal (1 ulp); e^-z overflows to
+// infinity where the result is 0
+__device__ __forceinline__ float gate_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + fast_exp2(-z * kLog2e)); }
 // the gate's activation and its derivative
 __device__ __forceinline__ float gate_act(float z, int silu) {
-    const float s = sigmoid_f32(z);
+    const float s = gate_sigmoid(z);
     return silu ? z * s : s;
 }
 __device__ __forceinline__ void gate_act_grad(float z, int silu, float &act, float &slope) {
-    const float s = sigmoid_f32(z);
+    const float s = gate_sigmoid(z);
     act = silu ? z * s : s;
-    slope = silu ? s + z * s * (1.f - s) : s * (1.f - s);
+    slope = silu ? fmaf(z * s, 1.f - s, s) : s * (1.f - s);
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -100,34 +124,35 @@ __device__ __forceinline__ float team_sum(float v, float *slot, int tid) {
 // wave, or through LDS (any other group).
 enum { GROUP_ROW = 0, GROUP_LANES = 1, GROUP_LDS = 2 };
 
-// For every channel vector of the thread, the sums over its channels' groups
-// of val[j][c].  GROUP_LDS: every channel's value goes through LDS `buf`
-// [dim], the waves of the team sum the groups into `sums` [dim / group], and
-// each channel looks its own up.
-template <int VEC, int CPT, int TS>
-__device__ __forceinline__ void group_sums(float (&val)[CPT][VEC], const NormParams &p, int mode, float *slot, float *buf,
-                                           int tid) {
-    if (mode == GROUP_ROW) {
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < CPT; ++j)
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) s += val[j][c];
-        s = team_sum<TS>(s, slot, tid);
-#pragma unroll
-        for (int j = 0; j < CPT; ++j)
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) val[j][c] = s;
-    } else if (mode == GROUP_LANES) {
-        const int lanes = p.group / VEC;
+// The sums over each channel's group of val[j][c].  Where a group is a row or
+// 2^k lanes, a thread's vector lies in one group and has one sum.  LDS: every
+// channel's value goes through LDS `buf` [dim], the waves of the team sum the
+// groups into `sums` [dim / group], and each channel looks its own up.
+template <int VEC, int CPT, int TS, bool LDS>
+__device__ __forceinline__ void group_sums(const float (&val)[CPT][VEC], float (&sum)[CPT][LDS ? VEC : 1], const NormParams &p, int mode,
+                                           float *slot, float *buf, int tid) {
+    if constexpr (!LDS) {
+        float part[CPT];
 #pragma unroll
         for (int j = 0; j < CPT; ++j) {
+            part[j] = 0.f;
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) part[j] += val[j][c];
+        }
+        if (mode == GROUP_ROW) {
             float s = 0.f;
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) s += val[j][c];
-            for (int m = 1; m < lanes; m <<= 1) s += __shfl_xor(s, m);
+            for (int j = 0; j < CPT; ++j) s += part[j];
+            s = team_sum<TS>(s, slot, tid);
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) val[j][c] = s;
+            for (int j = 0; j < CPT; ++j) sum[j][0] = s;
+        } else {
+            const int lanes = p.group / VEC;
+#pragma unroll
+            for (int j = 0; j < CPT; ++j) {
+                for (int m = 1; m < lanes; m <<= 1) part[j] += __shfl_xor(part[j], m);
+                sum[j][0] = part[j];
+            }
         }
     } else {
         float *sums = buf + p.dim;
@@ -152,10 +177,17 @@ __device__ __forceinline__ void group_sums(float (&val)[CPT][VEC], const NormPar
             const int e0 = (tid + j * TS) * VEC;
             if (e0 < p.dim)
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) val[j][c] = sums[(e0 + c) / p.group];
+                for (int c = 0; c < VEC; ++c) sum[j][c] = sums[(e0 + c) / p.group];
         }
         lds_barrier();  // buf is free again
     }
+    // channels past the row hold zeros; their mean stays one, so that no
+    // 0 / 0 of theirs reaches the row's sums (eps may be 0)
+#pragma unroll
+    for (int j = 0; j < CPT; ++j)
+        if ((tid + j * TS) * VEC >= p.dim)
+#pragma unroll
+            for (int c = 0; c < (LDS ? VEC : 1); ++c) sum[j][c] = 1.f;
 }
 
 // LDS floats one team needs
@@ -182,34 +214,48 @@ struct RowBuf {  // one row's inputs as loaded
     }
 };
 
-template <int VEC, int CPT, int TS>
+// The weights of a thread's channels: kept in registers over the rows (KEEP),
+// or read from L2 for every row where the registers are short.
+template <int VEC, int CPT, int TS, bool KEEP>
 struct Weights {
-    float w[CPT][VEC], s[CPT][VEC], w2[CPT][VEC];
-    __device__ __forceinline__ void load(const NormParams &p, int tid) {
+    const NormParams &p;
+    const int tid;
+    float kw[KEEP ? CPT : 1][KEEP ? VEC : 1], ks[KEEP ? CPT : 1][KEEP ? VEC : 1], kw2[KEEP ? CPT : 1][KEEP ? VEC : 1];
+    __device__ __forceinline__ Weights(const NormParams &p, int tid) : p(p), tid(tid) {
+        if constexpr (KEEP)
 #pragma unroll
-        for (int j = 0; j < CPT; ++j)
+            for (int j = 0; j < CPT; ++j)
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                const int e = (tid + j * TS) * VEC + c;
-                const bool in = e < p.dim;
-                w[j][c] = in && p.post_weight ? p.post_weight[p.post_per_channel ? e : e % p.group] : 1.f;
-                s[j][c] = in && p.scale ? p.scale[e] : 1.f;
-                w2[j][c] = in && p.pre_weight ? p.pre_weight[e] : 1.f;
-            }
+                for (int c = 0; c < VEC; ++c) {
+                    kw[j][c] = post(j, c);
+                    ks[j][c] = scaled(j, c);
+                    kw2[j][c] = pre(j, c);
+                }
     }
+    __device__ __forceinline__ int at(int j, int c) const { return (tid + j * TS) * VEC + c; }
+    __device__ __forceinline__ float post(int j, int c) const {
+        const int e = at(j, c);
+        return e < p.dim && p.post_weight ? p.post_weight[p.post_per_channel ? e : e % p.group] : 1.f;
+    }
+    __device__ __forceinline__ float scaled(int j, int c) const { return at(j, c) < p.dim && p.scale ? p.scale[at(j, c)] : 1.f; }
+    __device__ __forceinline__ float pre(int j, int c) const { return at(j, c) < p.dim && p.pre_weight ? p.pre_weight[at(j, c)] : 1.f; }
+    __device__ __forceinline__ float w(int j, int c) const { if constexpr (KEEP) return kw[j][c]; else return post(j, c); }
+    __device__ __forceinline__ float s(int j, int c) const { if constexpr (KEEP) return ks[j][c]; else return scaled(j, c); }
+    __device__ __forceinline__ float w2(int j, int c) const { if constexpr (KEEP) return kw2[j][c]; else return pre(j, c); }
 };
+// channels a thread can hold all of it for: 1024 threads have 128 registers each
+template <int VEC, int CPT, int TS> constexpr bool keep_weights(bool grad) { return CPT * VEC <= (TS == 1024 ? (grad ? 4 : 8) : 16); }
 
-template <typename T, int VEC, int CPT, int TS>
+template <typename T, int VEC, int CPT, int TS, bool LDS>
 __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_kernel(NormParams p, int mode) {
-    constexpr int WG = TS > 256 ? TS : 256, TEAMS = WG / TS;
+    constexpr int WG = TS > 256 ? TS : 256, TEAMS = WG / TS, S = LDS ? VEC : 1;
     extern __shared__ float lds[];
     const int tid = threadIdx.x % TS, team = threadIdx.x / TS;
     float *slot = lds + team * team_lds_floats(TS, mode, p.dim, p.group);
     float *buf = slot + 3 * (TS / 64);
     const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * TEAMS;
-    Weights<VEC, CPT, TS> w;
-    w.load(p, tid);
+    const Weights<VEC, CPT, TS, keep_weights<VEC, CPT, TS>(false)> w(p, tid);
     RowBuf<T, VEC, CPT, TS> in;
     // every team of a workgroup takes part in every step (the barriers are the
     // workgroup's); a row past the end repeats the last one and writes nothing
@@ -234,16 +280,19 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_kernel(NormPar
 #pragma unroll
                 for (int c = 0; c < VEC; ++c) a[j][c] *= act[j][c];
         if (p.post_weight) {
-            float q[CPT][VEC];
+            float sq[CPT][VEC], q[CPT][S];
 #pragma unroll
             for (int j = 0; j < CPT; ++j)
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) q[j][c] = a[j][c] * a[j][c];
-            group_sums<VEC, CPT, TS>(q, p, mode, slot, buf, tid);
+                for (int c = 0; c < VEC; ++c) sq[j][c] = a[j][c] * a[j][c];
+            group_sums<VEC, CPT, TS, LDS>(sq, q, p, mode, slot, buf, tid);
 #pragma unroll
-            for (int j = 0; j < CPT; ++j)
+            for (int j = 0; j < CPT; ++j) {
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) a[j][c] *= rsqrtf(q[j][c] * p.inv_group + p.eps) * w.w[j][c];
+                for (int c = 0; c < S; ++c) q[j][c] = rsqrtf(q[j][c] * p.inv_group + p.eps);
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) a[j][c] *= q[j][c % S] * w.w(j, c);
+            }
         }
         if (p.gate && !p.gate_first)
 #pragma unroll
@@ -255,7 +304,7 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_kernel(NormPar
         for (int j = 0; j < CPT; ++j)
 #pragma unroll
             for (int c = 0; c < VEC; ++c) {
-                a[j][c] = r[j][c] + w.s[j][c] * a[j][c];
+                a[j][c] = r[j][c] + w.s(j, c) * a[j][c];
                 sq += a[j][c] * a[j][c];  // channels past dim hold zeros
             }
         if (live) {
@@ -273,7 +322,7 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_kernel(NormPar
             for (int j = 0; j < CPT; ++j) {
                 const int e = (tid + j * TS) * VEC;
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) a[j][c] *= q2 * w.w2[j][c];
+                for (int c = 0; c < VEC; ++c) a[j][c] *= q2 * w.w2(j, c);
                 if (live && e < p.dim) rowvec<T, VEC>::st(pn + e, a[j]);
             }
         }
@@ -285,9 +334,9 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_kernel(NormPar
 // gradients in registers and writes one row of partial sums at its end,
 // [dscale dim | dpre dim | dpost dim or group]; norm_partial_kernel adds the
 // teams' rows in a fixed order.
-template <typename T, int VEC, int CPT, int TS>
+template <typename T, int VEC, int CPT, int TS, bool LDS>
 __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_grad_kernel(NormGradParams g, int mode) {
-    constexpr int WG = TS > 256 ? TS : 256, TEAMS = WG / TS;
+    constexpr int WG = TS > 256 ? TS : 256, TEAMS = WG / TS, S = LDS ? VEC : 1;
     extern __shared__ float lds[];
     const NormParams &p = g.f;
     const int tid = threadIdx.x % TS, team = threadIdx.x / TS;
@@ -295,8 +344,8 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_grad_kernel(No
     float *buf = slot + 3 * (TS / 64);
     const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * TEAMS;
-    Weights<VEC, CPT, TS> w;
-    w.load(p, tid);
+    constexpr bool AHEAD = keep_weights<VEC, CPT, TS>(true);  // request the next row's vectors early
+    const Weights<VEC, CPT, TS, AHEAD> w(p, tid);
     float gw[CPT][VEC] = {}, gs[CPT][VEC] = {}, gw2[CPT][VEC] = {};
     RowBuf<T, VEC, CPT, TS> in;
     rowvec<T, VEC> rdo[CPT], rdn[CPT];
@@ -310,10 +359,11 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_grad_kernel(No
             if (e < p.dim && g.d_normed) rdn[j].ld(static_cast<const T *>(g.d_normed) + row * p.dim + e);
         }
     };
-    if (first < p.rows) load(min(first + team, p.rows - 1));
+    if (AHEAD && first < p.rows) load(min(first + team, p.rows - 1));
     for (int64_t base = first; base < p.rows; base += step) {
         const int64_t row = base + team;
         const bool live = row < p.rows;
+        if (!AHEAD) load(min(row, p.rows - 1));
         float x[CPT][VEC], r[CPT][VEC], act[CPT][VEC], slope[CPT][VEC], dO[CPT][VEC], dn[CPT][VEC];
 #pragma unroll
         for (int j = 0; j < CPT; ++j)
@@ -326,26 +376,26 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_grad_kernel(No
                 dO[j][c] = rdo[j].get(c);
                 dn[j][c] = rdn[j].get(c);
             }
-        if (base + step < p.rows) load(min(base + step + team, p.rows - 1));
+        if (AHEAD && base + step < p.rows) load(min(base + step + team, p.rows - 1));
         // forward again: hat = a q, v
-        float hat[CPT][VEC], q[CPT][VEC];
+        float hat[CPT][VEC], q[CPT][S], e1[CPT][VEC];
         const bool first_gate = p.gate && p.gate_first, after_gate = p.gate && !p.gate_first;
 #pragma unroll
         for (int j = 0; j < CPT; ++j)
 #pragma unroll
             for (int c = 0; c < VEC; ++c) {
                 hat[j][c] = first_gate ? x[j][c] * act[j][c] : x[j][c];
-                q[j][c] = hat[j][c] * hat[j][c];
+                e1[j][c] = hat[j][c] * hat[j][c];
             }
         if (p.post_weight) {
-            group_sums<VEC, CPT, TS>(q, p, mode, slot, buf, tid);
+            group_sums<VEC, CPT, TS, LDS>(e1, q, p, mode, slot, buf, tid);
 #pragma unroll
-            for (int j = 0; j < CPT; ++j)
+            for (int j = 0; j < CPT; ++j) {
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) {
-                    q[j][c] = rsqrtf(q[j][c] * p.inv_group + p.eps);
-                    hat[j][c] *= q[j][c];
-                }
+                for (int c = 0; c < S; ++c) q[j][c] = rsqrtf(q[j][c] * p.inv_group + p.eps);
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) hat[j][c] *= q[j][c % S];
+            }
         }
         if (p.pre_weight) {
             float s1 = 0.f, s2 = 0.f;
@@ -354,10 +404,10 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_grad_kernel(No
             for (int j = 0; j < CPT; ++j)
 #pragma unroll
                 for (int c = 0; c < VEC; ++c) {
-                    const float v = hat[j][c] * w.w[j][c] * (after_gate ? act[j][c] : 1.f);
-                    out[j][c] = r[j][c] + w.s[j][c] * v;
+                    const float v = hat[j][c] * w.w(j, c) * (after_gate ? act[j][c] : 1.f);
+                    out[j][c] = r[j][c] + w.s(j, c) * v;
                     s1 += out[j][c] * out[j][c];
-                    s2 += dn[j][c] * w.w2[j][c] * out[j][c];
+                    s2 += dn[j][c] * w.w2(j, c) * out[j][c];
                 }
             s1 = wave_sum(s1);
             s2 = wave_sum(s2);
@@ -380,7 +430,7 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_grad_kernel(No
             for (int j = 0; j < CPT; ++j)
 #pragma unroll
                 for (int c = 0; c < VEC; ++c) {
-                    dO[j][c] += q2 * dn[j][c] * w.w2[j][c] - out[j][c] * k2;
+                    dO[j][c] += q2 * dn[j][c] * w.w2(j, c) - out[j][c] * k2;
                     if (live) gw2[j][c] += dn[j][c] * out[j][c] * q2;
                 }
         }
@@ -391,27 +441,28 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_grad_kernel(No
                 if (e < p.dim) rowvec<T, VEC>::st(static_cast<T *>(g.dresidual) + row * p.dim + e, dO[j]);
             }
         // through the scale, the gate behind the norm and the norm
-        float e1[CPT][VEC], dz[CPT][VEC];
+        float dz[CPT][VEC];
 #pragma unroll
         for (int j = 0; j < CPT; ++j)
 #pragma unroll
             for (int c = 0; c < VEC; ++c) {
-                const float n1 = hat[j][c] * w.w[j][c];
+                const float n1 = hat[j][c] * w.w(j, c);
                 if (live) gs[j][c] += dO[j][c] * n1 * (after_gate ? act[j][c] : 1.f);
-                float dv = dO[j][c] * w.s[j][c];
+                float dv = dO[j][c] * w.s(j, c);
                 dz[j][c] = dv * n1 * slope[j][c];
                 if (after_gate) dv *= act[j][c];
                 if (live) gw[j][c] += dv * hat[j][c];
-                dO[j][c] = dv * w.w[j][c];
+                dO[j][c] = dv * w.w(j, c);
                 e1[j][c] = dO[j][c] * hat[j][c];
             }
         if (p.post_weight) {
             if (TS > 64 && mode == GROUP_ROW) lds_barrier();  // the first sum's slot is read by now
-            group_sums<VEC, CPT, TS>(e1, p, mode, slot, buf, tid);
+            float es[CPT][S];
+            group_sums<VEC, CPT, TS, LDS>(e1, es, p, mode, slot, buf, tid);
 #pragma unroll
             for (int j = 0; j < CPT; ++j)
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) dO[j][c] = q[j][c] * (dO[j][c] - hat[j][c] * e1[j][c] * p.inv_group);
+                for (int c = 0; c < VEC; ++c) dO[j][c] = q[j][c % S] * (dO[j][c] - hat[j][c] * (es[j][c % S] * p.inv_group));
         }
         if (first_gate)
 #pragma unroll
@@ -496,28 +547,32 @@ int group_mode(const NormParams &p, int vec) {
     return GROUP_LDS;
 }
 
+// Channels per vector, vectors per thread, threads per row.  Forward: 8
+// channels a thread.  Gradients: about 24 live values per channel, so 4
+// channels a thread, whatever the threads (8192 rows of 4096 channels: 897 us
+// with 256 threads of 16 channels, which spill, against XXX us).
 struct Shape { int vec, cpt, ts; };
-Shape pick(const NormParams &p, bool vec) {
-    const int chunks = vec ? p.dim / 8 : p.dim;
-    if (vec) {
+Shape pick(const NormParams &p, bool vec, bool grad) {
+    if (!vec) {
         for (int ts : {64, 256, 1024})
-            for (int cpt : {1, 2})
-                if (chunks <= ts * cpt) return {8, cpt, ts};
-    } else {
-        if (chunks <= 256) return {1, 4, 64};
-        if (chunks <= 4096) return {1, 16, 256};
+            if (p.dim <= 4 * ts) return {1, 4, ts};
         return {1, 16, 1024};
     }
-    return {0, 0, 0};  // unreachable: dim <= 16384
+    const int v = grad ? 4 : 8, chunks = p.dim / v;
+    for (int ts : {64, 128, 256, 512, 1024})
+        if (chunks <= ts) return {v, 1, ts};
+    return {v, chunks <= 2048 ? 2 : 4, 1024};
 }
 
-template <typename F>
+template <int V, int C, int TS> struct ShapeC { static constexpr int VEC = V, CPT = C, S = TS; };
+template <bool GRAD, typename F>
 hipError_t with_shape(const Shape &s, F &&f) {
-#define KDA_NORM_CASE(V, C, S) if (s.vec == V && s.cpt == C && s.ts == S) return f(std::integral_constant<int, V>(), std::integral_constant<int, C>(), std::integral_constant<int, S>())
-    KDA_NORM_CASE(8, 1, 64); KDA_NORM_CASE(8, 2, 64);
-    KDA_NORM_CASE(8, 1, 256); KDA_NORM_CASE(8, 2, 256);
-    KDA_NORM_CASE(8, 1, 1024); KDA_NORM_CASE(8, 2, 1024);
-    KDA_NORM_CASE(1, 4, 64); KDA_NORM_CASE(1, 16, 256); KDA_NORM_CASE(1, 16, 1024);
+#define KDA_NORM_CASE(V, C, S) if (s.vec == V && s.cpt == C && s.ts == S) return f(ShapeC<V, C, S>())
+    constexpr int V = GRAD ? 4 : 8;
+    KDA_NORM_CASE(V, 1, 64); KDA_NORM_CASE(V, 1, 128); KDA_NORM_CASE(V, 1, 256); KDA_NORM_CASE(V, 1, 512);
+    KDA_NORM_CASE(V, 1, 1024); KDA_NORM_CASE(V, 2, 1024);
+    if constexpr (GRAD) KDA_NORM_CASE(V, 4, 1024);
+    KDA_NORM_CASE(1, 4, 64); KDA_NORM_CASE(1, 4, 256); KDA_NORM_CASE(1, 4, 1024); KDA_NORM_CASE(1, 16, 1024);
 #undef KDA_NORM_CASE
     return hipErrorInvalidValue;
 }
@@ -526,15 +581,18 @@ int wg_of(int ts) { return ts > 256 ? ts : 256; }
 
 template <typename T>
 hipError_t run_norm(const NormParams &p, hipStream_t s) {
-    const Shape sh = pick(p, vector_rows(p));
+    const Shape sh = pick(p, vector_rows(p), false);
     const int mode = group_mode(p, sh.vec);
-    return with_shape(sh, [&](auto V, auto C, auto S) {
-        constexpr int VEC = decltype(V)::value, CPT = decltype(C)::value, TS = decltype(S)::value;
+    return with_shape<false>(sh, [&](auto shape) {
+        constexpr int VEC = decltype(shape)::VEC, CPT = decltype(shape)::CPT, TS = decltype(shape)::S;
         constexpr int WG = TS > 256 ? TS : 256, TEAMS = WG / TS;
         const int64_t want = (p.rows + TEAMS - 1) / TEAMS;
         const unsigned grid = static_cast<unsigned>(std::min<int64_t>(want, 256 * (2048 / WG)));
         const size_t lds = sizeof(float) * TEAMS * team_lds_floats(TS, mode, p.dim, p.group);
-        hipLaunchKernelGGL((block_norm_kernel<T, VEC, CPT, TS>), dim3(grid), dim3(WG), lds, s, p, mode);
+        if (mode == GROUP_LDS)
+            hipLaunchKernelGGL((block_norm_kernel<T, VEC, CPT, TS, true>), dim3(grid), dim3(WG), lds, s, p, mode);
+        else
+            hipLaunchKernelGGL((block_norm_kernel<T, VEC, CPT, TS, false>), dim3(grid), dim3(WG), lds, s, p, mode);
         return hipGetLastError();
     });
 }
@@ -552,8 +610,8 @@ static int grad_teams(const NormParams &p, int ts) {
 // The workspace must hold the partial rows of either path (which one runs
 // depends on addresses, which the size query does not know).
 size_t block_norm_grad_bytes(const NormParams &p) {
-    int teams = grad_teams(p, pick(p, false).ts);
-    if (p.dim % 8 == 0) teams = std::max(teams, grad_teams(p, pick(p, true).ts));
+    int teams = grad_teams(p, pick(p, false, true).ts);
+    if (p.dim % 8 == 0) teams = std::max(teams, grad_teams(p, pick(p, true, true).ts));
     return align_up(sizeof(float) * static_cast<size_t>(teams) * norm_partial_cols(p));
 }
 
@@ -568,14 +626,17 @@ static hipError_t run_norm_grad(const NormGradParams &g, hipStream_t s) {
     for (const void *ptr : {g.d_out, g.d_normed, static_cast<const void *>(g.dx), static_cast<const void *>(g.dgate),
                             static_cast<const void *>(g.dresidual)})
         vec = vec && aligned_rows(ptr, 8);
-    const Shape sh = pick(p, vec);
+    const Shape sh = pick(p, vec, true);
     const int mode = group_mode(p, sh.vec);
     const int teams = grad_teams(p, sh.ts);
-    hipError_t e = with_shape(sh, [&](auto V, auto C, auto S) {
-        constexpr int VEC = decltype(V)::value, CPT = decltype(C)::value, TS = decltype(S)::value;
+    hipError_t e = with_shape<true>(sh, [&](auto shape) {
+        constexpr int VEC = decltype(shape)::VEC, CPT = decltype(shape)::CPT, TS = decltype(shape)::S;
         constexpr int WG = TS > 256 ? TS : 256, TEAMS = WG / TS;
         const size_t lds = sizeof(float) * TEAMS * team_lds_floats(TS, mode, p.dim, p.group);
-        hipLaunchKernelGGL((block_norm_grad_kernel<T, VEC, CPT, TS>), dim3(teams / TEAMS), dim3(WG), lds, s, g, mode);
+        if (mode == GROUP_LDS)
+            hipLaunchKernelGGL((block_norm_grad_kernel<T, VEC, CPT, TS, true>), dim3(teams / TEAMS), dim3(WG), lds, s, g, mode);
+        else
+            hipLaunchKernelGGL((block_norm_grad_kernel<T, VEC, CPT, TS, false>), dim3(teams / TEAMS), dim3(WG), lds, s, g, mode);
         return hipGetLastError();
     });
     if (e != hipSuccess || !(g.dscale || g.dpre || g.dpost)) return e;

@@ -177,3 +177,20 @@ def test_same_results_from_run_to_run():
     a = kda.block_norm_backward(dev["x"], d, d, **kw)
     b = kda.block_norm_backward(dev["x"], d, d, **kw)
     assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.parametrize("dim,group", [(264, 264), (264, 88), (77, 11), (320, 64)])
+def test_no_epsilon(dim, group):
+    """eps = 0: the threads past the row's end must not put 0 / 0 into its sums."""
+    dev, ref = make(12, 5, dim, group, torch.float32, "silu", True, True, True)
+    kw = {k: v for k, v in dev.items() if k != "x"}
+    out, normed = kda.block_norm(dev["x"], eps=0.0, group_size=group, gate_activation="silu", **kw)
+    out_r, normed_r = R.block_norm(ref["x"], eps=0.0, **oracle_args(ref, group, "silu", False))
+    check("out", out, out_r, TOL[torch.float32])
+    check("normed", normed, normed_r, TOL[torch.float32])
+    d = torch.randn((5, dim), device="cuda")
+    got = kda.block_norm_backward(dev["x"], d, d, eps=0.0, group_size=group, gate_activation="silu", **kw)
+    d64 = d.double().cpu().numpy()
+    want = R.block_norm_backward(ref["x"], d64, d64, eps=0.0, **oracle_args(ref, group, "silu", False))
+    for a, b in zip(got, want):
+        check("gradient", a, b, TOL[torch.float32])
