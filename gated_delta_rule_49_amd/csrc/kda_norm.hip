@@ -191,8 +191,8 @@ __device__ __forceinline__ void group_sums(const float (&val)[CPT][VEC], float (
 }
 
 // LDS floats one team needs
-__host__ __device__ inline int team_lds_floats(int ts, int mode, int dim, int group) {
-    return 3 * (ts / 64) + (mode == GROUP_LDS ? dim + dim / group : 0);
+__host__ __device__ inline int team_lds_floats(int ts, bool buf, int dim, int group) {
+    return 3 * (ts / 64) + (buf ? dim + dim / group : 0);
 }
 
 template <typename T, int VEC, int CPT, int TS>
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_kernel(NormPar
     constexpr int WG = TS > 256 ? TS : 256, TEAMS = WG / TS, S = LDS ? VEC : 1;
     extern __shared__ float lds[];
     const int tid = threadIdx.x % TS, team = threadIdx.x / TS;
-    float *slot = lds + team * team_lds_floats(TS, mode, p.dim, p.group);
+    float *slot = lds + team * team_lds_floats(TS, LDS, p.dim, p.group);
     float *buf = slot + 3 * (TS / 64);
     const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * TEAMS;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_grad_kernel(No
     extern __shared__ float lds[];
     const NormParams &p = g.f;
     const int tid = threadIdx.x % TS, team = threadIdx.x / TS;
-    float *slot = lds + team * team_lds_floats(TS, mode, p.dim, p.group);
+    float *slot = lds + team * team_lds_floats(TS, LDS || p.group < p.dim, p.dim, p.group);
     float *buf = slot + 3 * (TS / 64);
     const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * TEAMS;
@@ -482,7 +482,9 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_grad_kernel(No
             }
         if (TS > 64) lds_barrier();  // the slots are free again
     }
-    // this team's partial sums
+    // this team's partial sums; a post_weight shared by the groups has them
+    // folded here, in order, through LDS
+    const bool fold = g.dpost && !p.post_per_channel && p.group < p.dim;
     float *part = g.partial + (static_cast<int64_t>(blockIdx.x) * TEAMS + team) * norm_partial_cols(p);
 #pragma unroll
     for (int j = 0; j < CPT; ++j)
@@ -492,33 +494,44 @@ __global__ void __launch_bounds__(TS > 256 ? TS : 256) block_norm_grad_kernel(No
             if (e >= p.dim) continue;
             if (g.dscale) part[e] = gs[j][c];
             if (g.dpre) part[p.dim + e] = gw2[j][c];
-            if (g.dpost) part[2 * p.dim + e] = gw[j][c];
+            if (fold) buf[e] = gw[j][c];
+            else if (g.dpost) part[2 * p.dim + e] = gw[j][c];
         }
+    if (fold) {
+        lds_barrier();
+        for (int e = tid; e < p.group; e += TS) {
+            float v = 0.f;
+            for (int k = e; k < p.dim; k += p.group) v += buf[k];
+            part[2 * p.dim + e] = v;
+        }
+    }
 }
 
-// Column sums of the partial rows: 64 columns a workgroup, 16 rows at a time,
-// the sixteen partial sums of a column added in order through LDS.  A
-// post_weight shared by the groups also adds the groups' columns.
+// Column sums of the partial rows: 64 columns a workgroup, NP_ROWS rows at a
+// time, a column's partial sums added in order through LDS.
 constexpr int NP_ROWS = 16;
 __global__ void __launch_bounds__(64 * NP_ROWS) norm_partial_kernel(NormGradParams g, int teams) {
     const NormParams &p = g.f;
     __shared__ float sums[NP_ROWS][64];
     const int lane = threadIdx.x & 63, sub = threadIdx.x >> 6;
     const int blocks_d = (p.dim + 63) / 64;
-    int b = blockIdx.x;
-    const int which = b / blocks_d;  // 0 scale, 1 pre, 2 post
-    const int col = (b % blocks_d) * 64 + lane;
+    const int which = blockIdx.x / blocks_d;  // 0 scale, 1 pre, 2 post
+    const int col = (blockIdx.x % blocks_d) * 64 + lane;
     float *to = which == 0 ? g.dscale : which == 1 ? g.dpre : g.dpost;
     if (!to) return;  // the whole workgroup
-    const bool shared_post = which == 2 && !p.post_per_channel;
-    const int cols = shared_post ? p.group : p.dim;
+    const int cols = which == 2 && !p.post_per_channel ? p.group : p.dim;
     const int64_t stride = norm_partial_cols(p);
     float s = 0.f;
     if (col < cols) {
         const float *part = g.partial + which * p.dim + col;
-        const int reps = shared_post ? p.dim / p.group : 1;
-        for (int t = sub; t < teams; t += NP_ROWS)
-            for (int k = 0; k < reps; ++k) s += part[t * stride + static_cast<int64_t>(k) * p.group];
+        int t = sub;
+        for (; t + 3 * NP_ROWS < teams; t += 4 * NP_ROWS) {  // four rows requested together
+            float v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = part[(t + u * NP_ROWS) * stride];
+            s += (v[0] + v[1]) + (v[2] + v[3]);
+        }
+        for (; t < teams; t += NP_ROWS) s += part[t * stride];
     }
     sums[sub][lane] = s;
     __syncthreads();
@@ -588,7 +601,7 @@ hipError_t run_norm(const NormParams &p, hipStream_t s) {
         constexpr int WG = TS > 256 ? TS : 256, TEAMS = WG / TS;
         const int64_t want = (p.rows + TEAMS - 1) / TEAMS;
         const unsigned grid = static_cast<unsigned>(std::min<int64_t>(want, 256 * (2048 / WG)));
-        const size_t lds = sizeof(float) * TEAMS * team_lds_floats(TS, mode, p.dim, p.group);
+        const size_t lds = sizeof(float) * TEAMS * team_lds_floats(TS, mode == GROUP_LDS, p.dim, p.group);
         if (mode == GROUP_LDS)
             hipLaunchKernelGGL((block_norm_kernel<T, VEC, CPT, TS, true>), dim3(grid), dim3(WG), lds, s, p, mode);
         else
@@ -632,7 +645,7 @@ static hipError_t run_norm_grad(const NormGradParams &g, hipStream_t s) {
     hipError_t e = with_shape<true>(sh, [&](auto shape) {
         constexpr int VEC = decltype(shape)::VEC, CPT = decltype(shape)::CPT, TS = decltype(shape)::S;
         constexpr int WG = TS > 256 ? TS : 256, TEAMS = WG / TS;
-        const size_t lds = sizeof(float) * TEAMS * team_lds_floats(TS, mode, p.dim, p.group);
+        const size_t lds = sizeof(float) * TEAMS * team_lds_floats(TS, mode == GROUP_LDS || p.group < p.dim, p.dim, p.group);
         if (mode == GROUP_LDS)
             hipLaunchKernelGGL((block_norm_grad_kernel<T, VEC, CPT, TS, true>), dim3(teams / TEAMS), dim3(WG), lds, s, g, mode);
         else
