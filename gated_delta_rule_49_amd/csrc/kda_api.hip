@@ -575,6 +575,9 @@ kda_status check_ssm(const SsmShape &s) {
         if (st < 0) return KDA_ERR_BAD_SHAPE;
         if (st % 8) return KDA_ERR_UNSUPPORTED;
     }
+    for (const int64_t st : {s.xt, s.bt, s.ct, static_cast<int64_t>(s.H) * s.P}) {  // 32-bit offsets inside a chunk
+        if (st >= (1 << 23)) return KDA_ERR_UNSUPPORTED;
+    }
     return KDA_OK;
 }
 bool misaligned(std::initializer_list<const void *> ptrs) {

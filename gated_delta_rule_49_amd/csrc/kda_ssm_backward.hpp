@@ -27,25 +27,6 @@ namespace kda {
 
 namespace {
 
-typedef short v4i16 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
-
-// Operand with its contraction along the rows [r0, r0 + 32) of a granule-
-// ordered LDS tile and its 16 columns from c0 (ds_read_b64_tr_b16: lane i of
-// group g addresses four columns of row r0 + 4 g + i / 4 and receives column
-// c0 + i of rows r0 + 4 g + 0..3).
-__device__ __forceinline__ void load_cols(frag8 &f, const bf16_t *tile, int stride, int r0, int c0, int g, int c16) {
-    const bf16_t *at = tile + (r0 + 4 * g + (c16 >> 2)) * stride + col_pos(c0 + 4 * (c16 & 3));
-    const v4i16 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)(at));
-    const v4i16 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)(at + 16 * stride));
-    const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
-    f.u = make_uint4(ua.x, ua.y, ub.x, ub.y);
-}
-// Operand with its contraction along a row: rows [r0, r0 + 16), step kk
-__device__ __forceinline__ void load_rows(frag8 &f, const bf16_t *tile, int stride, int r0, int kk, int g, int c16) {
-    f.u = *reinterpret_cast<const uint4 *>(tile + (r0 + c16) * stride + kk * 32 + 8 * g);
-}
-
 // Sums of V = 8 or 16 values over the 16 lanes of a lane group: each exchange
 // halves the values a lane carries; lane c ends with the sum of value
 // sum16_index<V>(c).

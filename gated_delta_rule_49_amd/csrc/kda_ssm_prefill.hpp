@@ -36,11 +36,10 @@ struct ScanCfg {
     static constexpr int CT = PW / 16, ST = L / 16, TK = L / 32;
     static constexpr int RN = NK + 8, RT = L + 8;         // LDS row strides: 16-byte pieces of 16 rows hit all banks
     static constexpr int NBUF = BF ? 2 : 1;
-    static constexpr int CN = FULL ? EX * L * RN : 0;     // C, and B by rows
-    static constexpr int BT = EX * NS * RT;               // B transposed
+    static constexpr int BN = EX * L * RN;                // B by rows; C likewise
     static constexpr int GT = FULL ? GP * L * RT : 0;     // causal scores
-    static constexpr int BUF = 2 * CN + BT + GT;
-    static constexpr int WV = 4 * L;                      // per wave: w, row factor, suf, dt
+    static constexpr int BUF = BN + (FULL ? BN : 0) + GT;
+    static constexpr int WV = (FULL ? 4 : 1) * L;         // per wave: w, row factor, suf, dt
     static constexpr size_t BYTES = sizeof(bf16_t) * NBUF * BUF + sizeof(float) * NW * WV;
 };
 
@@ -61,44 +60,52 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
     // the last segment's end state is nobody's entering state (reverse: the first's)
     if (phase == 1 && (REV ? sg.s == 0 : sg.s == sg.count - 1)) return;
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int g = lane >> 4, c16 = lane & 15;
+    int tid = threadIdx.x;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int g = lane >> 4, c16 = lane & 15;
     const int grp = (block / blocks_per_group) % p.G, hpg = p.H / p.G, cb_n = p.P / PW;
     const int item = (block % blocks_per_group) * NW + wave;
     const bool on = item < hpg * cb_n;               // waves past the group's heads only stage
     const int h = grp * hpg + (on ? item / cb_n : 0);
-    const int pc = (on ? item % cb_n : 0) * PW + c16 * CT;  // the lane's channels pc .. pc + CT - 1
+    const int pw0 = (on ? item % cb_n : 0) * PW;     // first channel of the wave
+    const int pc = pw0 + c16 * CT;                   // the lane's channels pc .. pc + CT - 1
 
     bf16_t *lds = reinterpret_cast<bf16_t *>(smem);
     float *wv = reinterpret_cast<float *>(smem + sizeof(bf16_t) * NBUF * Cf::BUF) + wave * Cf::WV;
     float *fv = wv + L, *sv = wv + 2 * L, *dv = wv + 3 * L;
-    auto Cn = [&](int b, int part) { return lds + b * Cf::BUF + part * L * RN; };
-    auto Bn = [&](int b, int part) { return lds + b * Cf::BUF + Cf::CN + part * L * RN; };
-    auto Bt = [&](int b, int part) { return lds + b * Cf::BUF + 2 * Cf::CN + part * NS * RT; };
-    auto Gt = [&](int b, int part) { return lds + b * Cf::BUF + 2 * Cf::CN + Cf::BT + part * L * RT; };
+    auto Bn = [&](int b, int part) { return lds + b * Cf::BUF + part * L * RN; };
+    auto Cn = [&](int b, int part) { return lds + b * Cf::BUF + Cf::BN + part * L * RN; };
+    auto Gt = [&](int b, int part) { return lds + b * Cf::BUF + 2 * Cf::BN + part * L * RT; };
 
+    // Uniform bases; a lane adds a 32-bit byte offset (strides are below 2^23
+    // elements, so a chunk's rows stay below 2^31 bytes).
     const int64_t flat0 = static_cast<int64_t>(sg.row) * p.T + sg.t0;
     const int64_t per_head = static_cast<int64_t>(NS) * p.P;
-    const TI *xb = static_cast<const TI *>(p.x) + sg.row * p.x_sb + sg.t0 * p.x_st + static_cast<int64_t>(h) * p.P + pc;
+    const TI *xb = static_cast<const TI *>(p.x) + sg.row * p.x_sb + sg.t0 * p.x_st + static_cast<int64_t>(h) * p.P + pw0;
     const TI *bb = static_cast<const TI *>(p.Bm) + sg.row * p.b_sb + sg.t0 * p.b_st + static_cast<int64_t>(grp) * NS;
     const TI *cb = static_cast<const TI *>(p.Cm) + sg.row * p.c_sb + sg.t0 * p.c_st + static_cast<int64_t>(grp) * NS;
     const TI *dtb = static_cast<const TI *>(p.dt) + flat0 * p.H + h;
-    TO *yb = static_cast<TO *>(p.y) + (flat0 * p.H + h) * p.P + pc;
+    TO *yb = static_cast<TO *>(p.y) + (flat0 * p.H + h) * p.P + pw0;
+    const uint32_t x_st = static_cast<uint32_t>(p.x_st), y_st = static_cast<uint32_t>(p.H) * p.P;
     const float A2 = p.A[h] * kLog2e, Dh = p.D ? p.D[h] : 0.f, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
 
     // the state: a lane holds rows 16 nt + 4 g + r, channels pc + ct
     f32x4 S[NT][CT];
     {
         const float *src = phase == 1 ? nullptr
-                           : q.seg_state ? q.seg_state + (static_cast<int64_t>(x_seg) * p.H + h) * per_head
-                           : p.initial_state ? p.initial_state + (static_cast<int64_t>(sg.n) * p.H + h) * per_head : nullptr;
+                           : q.seg_state ? q.seg_state + (static_cast<int64_t>(x_seg) * p.H + h) * per_head + pw0
+                           : p.initial_state ? p.initial_state + (static_cast<int64_t>(sg.n) * p.H + h) * per_head + pw0 : nullptr;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) S[nt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (src)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 lanevec<float, CT> v;
-                v.zero();
-                if (src) v.ld(src + (16 * nt + 4 * g + r) * p.P + pc);
+                v.ld(src + (16 * nt + r) * p.P + static_cast<uint32_t>(4 * g * p.P + c16 * CT));
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) S[nt][ct][r] = v.get(ct);
             }
@@ -111,55 +118,55 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                 float v[CT];
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) v[ct] = S[nt][ct][r];
-                lanevec<float, CT>::st(dst + (16 * nt + 4 * g + r) * p.P + pc, v);
+                lanevec<float, CT>::st(dst + (16 * nt + r) * p.P + static_cast<uint32_t>(4 * g * p.P + c16 * CT), v);
             }
     };
 
     // zero what no staging writes: columns past d_state, the score tiles above the diagonal
-    if (FULL) {
-        if (NS < 32)
-            for (int i = tid; i < NBUF * 2 * Cf::CN; i += 64 * NW) lds[(i / (2 * Cf::CN + !Cf::CN)) * Cf::BUF + i % (2 * Cf::CN + !Cf::CN)] = 0;
+    if (NS < 32)
+        for (int b = 0; b < NBUF; ++b)
+            for (int i = tid; i < (FULL ? 2 : 1) * Cf::BN; i += 64 * NW) Bn(b, 0)[i] = 0;
+    if (FULL)
         for (int b = 0; b < NBUF; ++b)
             for (int i = tid; i < Cf::GT; i += 64 * NW) Gt(b, 0)[i] = 0;
-        lds_barrier();
-    }
+    if (FULL || NS < 32) lds_barrier();
 
-    // staging of a chunk's B and C: a thread takes 4 tokens by 4 channels
+    // Staging of a chunk's B and C: a thread takes 4 tokens by 4 channels.
+    // Rows past the segment repeat its last one: their step size is 0, so
+    // whatever they hold meets a factor of 0 or a row that is not stored.
     constexpr int BLOCKS = (L / 4) * (NS / 4), PER = (BLOCKS + 64 * NW - 1) / (64 * NW);
     quad<TI> rawB[PER], rawC[FULL ? PER : 1];
-    auto fetch = [&](int c) {
+    auto fetch_rows = [&](quad<TI> (&raw)[PER], const TI *base, int64_t stride, int c) {
+        const int rem = min(sg.len - c * L, L);
+        const TI *cbase = base + c * L * stride;
+        const uint32_t st = static_cast<uint32_t>(stride);
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const int i = tid + k * 64 * NW;
-            const int tq = i / (NS / 4), nq = i % (NS / 4);
+            const uint32_t tq = i / (NS / 4), nq = i % (NS / 4);
+            if (BLOCKS % (64 * NW) == 0 || i < BLOCKS) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = c * L + tq * 4 + r;
-                const bool in = i < BLOCKS && t < sg.len;
-                rawB[k].zero(r);
-                if (in) rawB[k].ld(r, bb + t * p.b_st + nq * 4);
-                if (FULL) {
-                    rawC[k].zero(r);
-                    if (in) rawC[k].ld(r, cb + t * p.c_st + nq * 4);
-                }
+                for (int r = 0; r < 4; ++r)
+                    raw[k].ld(r, cbase + (rem == L ? (4 * tq + r) * st : min(4 * tq + r, rem - 1u) * st) + 4 * nq);
             }
         }
+    };
+    auto fetch = [&](int c) {
+        fetch_rows(rawB, bb, p.b_st, c);
+        if constexpr (FULL) fetch_rows(rawC, cb, p.c_st, c);
     };
     auto stage = [&](int b) {
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const int i = tid + k * 64 * NW;
             const int tq = i / (NS / 4), nq = i % (NS / 4);
-            if (i < BLOCKS)
+            if (BLOCKS % (64 * NW) == 0 || i < BLOCKS)
 #pragma unroll
                 for (int part = 0; part < EX; ++part)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        if (FULL) {
-                            *reinterpret_cast<uint2 *>(Bn(b, part) + (tq * 4 + r) * RN + col_pos(nq * 4)) = rawB[k].row(r, part).u;
-                            *reinterpret_cast<uint2 *>(Cn(b, part) + (tq * 4 + r) * RN + col_pos(nq * 4)) = rawC[k].row(r, part).u;
-                        }
-                        *reinterpret_cast<uint2 *>(Bt(b, part) + (nq * 4 + r) * RT + col_pos(tq * 4)) = rawB[k].col(r, part).u;
+                        *reinterpret_cast<uint2 *>(Bn(b, part) + (tq * 4 + r) * RN + col_pos(nq * 4)) = rawB[k].row(r, part).u;
+                        if (FULL) *reinterpret_cast<uint2 *>(Cn(b, part) + (tq * 4 + r) * RN + col_pos(nq * 4)) = rawC[k].row(r, part).u;
                     }
         }
     };
@@ -175,8 +182,8 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                 parts8<EX> a, bf;
 #pragma unroll
                 for (int part = 0; part < EX; ++part) {
-                    a.f[part].u = *reinterpret_cast<const uint4 *>(Bn(b, part) + (16 * tj + c16) * RN + kk * 32 + 8 * g);
-                    bf.f[part].u = *reinterpret_cast<const uint4 *>(Cn(b, part) + (16 * ti + c16) * RN + kk * 32 + 8 * g);
+                    load_rows(a.f[part], Bn(b, part), RN, 16 * tj, kk, g, c16);
+                    load_rows(bf.f[part], Cn(b, part), RN, 16 * ti, kk, g, c16);
                 }
                 mfma_parts<EX, EX, ORD>(acc, a, bf);
             }
@@ -195,20 +202,30 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                 *reinterpret_cast<uint2 *>(Gt(b, part) + (16 * ti + c16) * RT + col_pos(16 * tj + 4 * g)) = out[part].u;
         }
     };
-    // x (rows in the operand's slot order) and dt of a chunk
+    // x (rows in the operand's slot order) and dt of a chunk; a lane's token is
+    // its own number in the reverse mode (sums from the chunk's start are
+    // wanted), else counted from the chunk's end
     lanevec<TI, CT> xr[TK][8], xn[TK][8];
     TI dtr = TI(0), dtn = TI(0);
+    auto token = [&] { return REV ? tid & 63 : L - 1 - (tid & 63); };
     auto fetch_x = [&](int c, lanevec<TI, CT> (&xv)[TK][8], TI &d) {
+        const int rem = min(sg.len - c * L, L);
+        const TI *base = xb + static_cast<int64_t>(c) * L * p.x_st;
+        if (rem == L) {
+            const uint32_t off = 4 * g * x_st + c16 * CT;
 #pragma unroll
-        for (int ks = 0; ks < TK; ++ks)
+            for (int ks = 0; ks < TK; ++ks)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int t = c * L + 32 * ks + kperm(g, j);
-                xv[ks][j].zero();
-                if (t < sg.len) xv[ks][j].ld(xb + t * p.x_st);
-            }
+                for (int j = 0; j < 8; ++j) xv[ks][j].ld(base + (32 * ks + kperm(0, j)) * static_cast<int64_t>(x_st) + off);
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < TK; ++ks)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) xv[ks][j].ld(base + min(32 * ks + kperm(g, j), rem - 1) * x_st + c16 * CT);
+        }
         d = TI(0);
-        if (lane < L && c * L + lane < sg.len) d = dtb[static_cast<int64_t>(c * L + lane) * p.H];
+        const int tok = token();
+        if (tok >= 0 && tok < rem) d = dtb[static_cast<int64_t>(c) * L * p.H + static_cast<uint32_t>(tok * p.H)];
     };
 
     const int chunks = (sg.len + L - 1) / L;
@@ -227,68 +244,52 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
     }
     for (int i = 0; i < chunks; ++i) {
         const int b = NBUF == 2 ? i & 1 : 0;
-        const int t0 = order(i) * L;
+        const int t0 = order(i) * L, rem = min(sg.len - t0, L);
+        // what follows from the lane's place is computed again in every
+        // iteration: kept over the loop it would push the tiles out of the registers
+        asm volatile("" : "+v"(g), "+v"(c16), "+v"(tid));
         if (NBUF == 2 && i + 1 < chunks) {  // the next chunk into the other buffer
             stage(b ^ 1);
             if (i + 2 < chunks) fetch(order(i + 2));
         }
         if (i + 1 < chunks) fetch_x(order(i + 1), xn, dtn);
         if (on) {
-            // the state entering the 64-token chunk (from the right in the reverse order)
+            // the state entering the chunk (from the right in the reverse order)
             if (phase == 2 && p.chunk_states && t0 % q.state_chunk == 0)
-                store_state(p.chunk_states + ((static_cast<int64_t>(sg.chunk + t0 / 64) * (64 / q.state_chunk) + t0 % 64 / q.state_chunk) * p.H + h) * per_head);
+                store_state(p.chunk_states + ((static_cast<int64_t>(sg.chunk + t0 / 64) * (64 / q.state_chunk) + t0 % 64 / q.state_chunk) * p.H + h) * per_head + pw0);
             // decays, one token a lane
+            const int tok = token(), lane = tid & 63;
             float dt = io<TI>::ld(&dtr, 0) + bias;
             if (p.softplus) dt = softplus_rel(dt);
-            if (lane >= L || t0 + lane >= sg.len) dt = 0.f;
+            if (tok < 0 || tok >= rem) dt = 0.f;
             const float la = A2 * dt;
-            const float incl = suffix_sum(la, lane);
-            const float tot = __shfl(incl, 0);
-            const float suf = after(incl, lane);
+            const float incl = lane_scan(la);  // from the chunk's end (reverse: its start) to the token
+            const float tot = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, incl), 63));
             const bool fast = fabsf(tot) < kFastTot;
-            if (lane < L) {
-                if (REV) {
-                    wv[lane] = fast_exp2(prefix_sum(la, lane));
-                } else {
-                    wv[lane] = dt * fast_exp2(suf);
-                }
-                if (FULL) {
-                    fv[lane] = fast ? fast_exp2(-suf) : fast_exp2(prefix_sum(la, lane));
-                    sv[lane] = suf;
-                    dv[lane] = dt;
+            if (REV) {
+                if (lane < L) wv[lane] = lane < rem ? fast_exp2(incl) : 0.f;
+            } else {
+                const float suf = lane_shift(incl);
+                float row = 0.f;
+                if (FULL) row = fast ? fast_exp2(-suf) : fast_exp2(suffix_sum(la, lane));
+                if (tok >= 0) {
+                    wv[tok] = dt * fast_exp2(suf);
+                    if (FULL) {
+                        fv[tok] = row;
+                        sv[tok] = suf;
+                        dv[tok] = dt;
+                    }
                 }
             }
             seg_log += tot;
             wave_lds_fence();
             const float dec = fast_exp2(tot);
-
-            parts8<XP> xw[TK][CT];
-#pragma unroll
-            for (int ks = 0; ks < TK; ++ks) {
-                float wq[8];
-#pragma unroll
-                for (int hq = 0; hq < 2; ++hq) {
-                    const f32x4 v = *reinterpret_cast<const f32x4 *>(wv + 32 * ks + 16 * hq + 4 * g);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) wq[4 * hq + r] = v[r];
-                }
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) split_to<XP>(xw[ks][ct], j, xr[ks][j].get(ct) * wq[j]);
-            }
-            if (fast || !FULL)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) S[nt][ct] *= dec;
-            if constexpr (FULL) {
-                f32x4 acc[ST][CT];
+            f32x4 acc[FULL ? ST : 1][CT];
+            if constexpr (FULL) {  // C S
 #pragma unroll
                 for (int s = 0; s < ST; ++s)
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) acc[s][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-                // C S
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) {
                     parts8<SP> sf[CT];
@@ -303,42 +304,29 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                     for (int s = 0; s < ST; ++s) {
                         parts8<EX> a;
 #pragma unroll
-                        for (int part = 0; part < EX; ++part)
-                            a.f[part].u = *reinterpret_cast<const uint4 *>(Cn(b, part) + (16 * s + c16) * RN + kk * 32 + 8 * g);
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) mfma_parts<EX, SP, ORD>(acc[s][ct], a, sf[ct]);
+                        for (int part = 0; part < EX; ++part) load_rows(a.f[part], Cn(b, part), RN, 16 * s, kk, g, c16);
+                        mfma_tiles<EX, SP, ORD, CT>(acc[s], a, sf);
                     }
                 }
-                if (fast) {
+#pragma unroll
+                for (int s = 0; s < ST; ++s) {
+                    f32x4 f = {dec, dec, dec, dec};
+                    if (!fast) f = *reinterpret_cast<const f32x4 *>(fv + 16 * s + 4 * g);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) acc[s][ct] *= f;
+                }
+                if (!fast) {  // the second form's intra-chunk part
 #pragma unroll
                     for (int s = 0; s < ST; ++s) {
-#pragma unroll
-                        for (int ks = 0; ks <= s / 2; ++ks) {
-                            parts8<GP> a;
-#pragma unroll
-                            for (int part = 0; part < GP; ++part)
-                                a.f[part].u = *reinterpret_cast<const uint4 *>(Gt(b, part) + (16 * s + c16) * RT + ks * 32 + 8 * g);
-#pragma unroll
-                            for (int ct = 0; ct < CT; ++ct) mfma_parts<GP, XP, ORD>(acc[s][ct], a, xw[ks][ct]);
-                        }
-                        const f32x4 f = *reinterpret_cast<const f32x4 *>(fv + 16 * s + 4 * g);
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) acc[s][ct] *= f;
-                    }
-                } else {
-#pragma unroll
-                    for (int s = 0; s < ST; ++s) {
-                        const f32x4 f = *reinterpret_cast<const f32x4 *>(fv + 16 * s + 4 * g);
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) acc[s][ct] *= f;
                         const int row = 16 * s + c16;
                         const float suf_row = sv[row];
 #pragma unroll
                         for (int ks = 0; ks <= s / 2; ++ks) {
+                            asm volatile("" ::: "memory");  // the factors are read again, not kept over the strips
+                            __builtin_amdgcn_sched_barrier(0);
                             parts8<GP> m;
 #pragma unroll
-                            for (int part = 0; part < GP; ++part)
-                                m.f[part].u = *reinterpret_cast<const uint4 *>(Gt(b, part) + row * RT + ks * 32 + 8 * g);
+                            for (int part = 0; part < GP; ++part) load_rows(m.f[part], Gt(b, part), RT, 16 * s, ks, g, c16);
                             float mv[8];
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
@@ -361,40 +349,67 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                             for (int ct = 0; ct < CT; ++ct) {
                                 parts8<EX> xe;
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) split_to<EX>(xe, j, xr[ks][j].get(ct));
+                                for (int j = 0; j < 8; ++j) {
+                                    lanevec<TI, CT> v = xr[ks][j];
+                                    asm volatile("" : "+v"(v.u));
+                                    split_to<EX>(xe, j, v.get(ct));
+                                }
                                 mfma_parts<GP, EX, ORD>(acc[s][ct], m, xe);
                             }
                         }
                     }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) S[nt][ct] *= dec;
                 }
-                // y: slot (s % 2) 4 + r of x's step s / 2 is the same row
-#pragma unroll
-                for (int s = 0; s < ST; ++s)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int t = t0 + 16 * s + 4 * g + r;
-                        float v[CT];
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) v[ct] = fmaf(Dh, xr[s / 2][(s % 2) * 4 + r].get(ct), acc[s][ct][r]);
-                        if (t < sg.len) lanevec<TO, CT>::st(yb + static_cast<int64_t>(t) * p.H * p.P, v);
-                    }
             }
-            // S += B (w x)^T
 #pragma unroll
-            for (int ks = 0; ks < TK; ++ks)
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) S[nt][ct] *= dec;
+            // w x, 32 tokens at a time: into y through the scores, into S through B
+#pragma unroll
+            for (int ks = 0; ks < TK; ++ks) {
+                parts8<XP> xw[CT];
+#pragma unroll
+                for (int hq = 0; hq < 2; ++hq) {
+                    const f32x4 wq = *reinterpret_cast<const f32x4 *>(wv + 32 * ks + 16 * hq + 4 * g);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) split_to<XP>(xw[ct], 4 * hq + r, xr[ks][4 * hq + r].get(ct) * wq[r]);
+                }
+                if constexpr (FULL) {
+                    if (fast)
+#pragma unroll
+                        for (int s = 2 * ks; s < ST; ++s) {
+                            parts8<GP> a;
+#pragma unroll
+                            for (int part = 0; part < GP; ++part) load_rows(a.f[part], Gt(b, part), RT, 16 * s, ks, g, c16);
+                            mfma_tiles<GP, XP, ORD, CT>(acc[s], a, xw);
+                        }
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     parts8<EX> a;
 #pragma unroll
-                    for (int part = 0; part < EX; ++part)
-                        a.f[part].u = *reinterpret_cast<const uint4 *>(Bt(b, part) + (16 * nt + c16) * RT + ks * 32 + 8 * g);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mfma_parts<EX, XP, 3>(S[nt][ct], a, xw[ks][ct]);
+                    for (int part = 0; part < EX; ++part) load_cols(a.f[part], Bn(b, part), RN, 32 * ks, 16 * nt, g, c16);
+                    mfma_tiles<EX, XP, 3, CT>(S[nt], a, xw);
                 }
+            }
+            if constexpr (FULL) {  // y: slot (s % 2) 4 + r of x's step s / 2 is the same row
+                TO *yc = yb + static_cast<int64_t>(t0) * y_st;
+#pragma unroll
+                for (int s = 0; s < ST; ++s) {
+                    f32x4 f = {1.f, 1.f, 1.f, 1.f};
+                    if (fast) f = *reinterpret_cast<const f32x4 *>(fv + 16 * s + 4 * g);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float v[CT];
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) v[ct] = fmaf(Dh, xr[s / 2][(s % 2) * 4 + r].get(ct), acc[s][ct][r] * f[r]);
+                        if (rem == L || 16 * s + 4 * g + r < rem)
+                            lanevec<TO, CT>::st(yc + (16 * s + r) * static_cast<int64_t>(y_st) + (4 * g * y_st + c16 * CT), v);
+                    }
+                }
+            }
         }
         lds_barrier();
         if (i + 1 < chunks) {
@@ -416,10 +431,10 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
     }
     if (!on) return;
     if (phase == 1) {
-        store_state(q.seg_state + (static_cast<int64_t>(x_seg) * p.H + h) * per_head);
+        store_state(q.seg_state + (static_cast<int64_t>(x_seg) * p.H + h) * per_head + pw0);
         if (pc == 0 && g == 0) q.seg_log[static_cast<int64_t>(x_seg) * p.H + h] = seg_log;
     } else if (p.final_state && (REV ? sg.s == 0 : sg.s == sg.count - 1)) {
-        store_state(p.final_state + (static_cast<int64_t>(sg.n) * p.H + h) * per_head);
+        store_state(p.final_state + (static_cast<int64_t>(sg.n) * p.H + h) * per_head + pw0);
     }
 }
 

@@ -123,12 +123,44 @@ __device__ __forceinline__ void mfma_parts(f32x4 &c, const parts8<NA> &a, const 
             if (i + j < ORD) c = mfma16(a.f[i].v, b.f[j].v, c);
 }
 
+// the same for CT neighbouring tiles, the tiles innermost: consecutive
+// instructions then accumulate into different registers
+template <int NA, int NB, int ORD, int CT>
+__device__ __forceinline__ void mfma_tiles(f32x4 (&c)[CT], const parts8<NA> &a, const parts8<NB> (&b)[CT]) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            if (i + j < ORD)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) c[ct] = mfma16(a.f[i].v, b[ct].f[j].v, c[ct]);
+}
+
 // Position of the 4-element granule q of a 32-column step: an operand's lane
 // group g = l / 16 reads granules g and 4 + g (kperm's slots) as one 16-byte
 // piece.
 __device__ __forceinline__ constexpr int granule_pos(int q) { return q < 4 ? 2 * q : 2 * (q - 4) + 1; }
 // element offset of column k (a multiple of 4) in a row of 32-column steps
 __device__ __forceinline__ constexpr int col_pos(int k) { return (k & ~31) + granule_pos((k >> 2) & 7) * 4; }
+
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+
+// Operand with its contraction along the rows [r0, r0 + 32) of a granule-
+// ordered LDS tile and its 16 columns from c0 (ds_read_b64_tr_b16: lane i of
+// group g addresses four columns of row r0 + 4 g + i / 4 and receives column
+// c0 + i of rows r0 + 4 g + 0..3).
+__device__ __forceinline__ void load_cols(frag8 &f, const bf16_t *tile, int stride, int r0, int c0, int g, int c16) {
+    const bf16_t *at = tile + (r0 + 4 * g + (c16 >> 2)) * stride + col_pos(c0 + 4 * (c16 & 3));
+    const v4i16 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)(at));
+    const v4i16 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)(at + 16 * stride));
+    const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
+    f.u = make_uint4(ua.x, ua.y, ub.x, ub.y);
+}
+// Operand with its contraction along a row: rows [r0, r0 + 16), step kk
+__device__ __forceinline__ void load_rows(frag8 &f, const bf16_t *tile, int stride, int r0, int kk, int g, int c16) {
+    f.u = *reinterpret_cast<const uint4 *>(tile + (r0 + c16) * stride + kk * 32 + 8 * g);
+}
 
 union granule {
     bf16_t s[4];
@@ -214,6 +246,27 @@ template <> struct lanevec<float, 2> {
 __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+}
+
+// Inclusive sums over the lanes up to each, without LDS: within rows of 16
+// lanes (row_shr), then each row's and each half's last value to the lanes
+// above (row_bcast:15, row_bcast:31).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, true));
+}
+__device__ __forceinline__ float lane_scan(float v) {
+    v = dpp_add<0x111, 0xf>(v);  // row_shr:1, 2, 4, 8
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
+    v = dpp_add<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+    return v;
+}
+// the value of the lane below, 0 for lane 0
+__device__ __forceinline__ float lane_shift(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x138, 0xf, 0xf, true));  // wave_shr:1
 }
 
 // inclusive sums over the lanes at and below / above each lane

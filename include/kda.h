@@ -437,7 +437,8 @@ kda_status kda_backward(const kda_backward_args *a, void *hip_stream);
  *   workspace    DEVICE, >= kda_ssm_workspace_bytes(args), 256-byte aligned
  *
  * Supported: d_head, d_state in {16, 32, 64, 128}; G divides H; in_dtype and
- * out_dtype f32 or bf16; B * T * H, B * T * G < 2^31; strides multiples of 8;
+ * out_dtype f32 or bf16; B * T * H < 2^31; strides multiples of 8, token strides
+ * and H * d_head below 2^23;
  * x, Bm, Cm 16-byte aligned, the states too (else KDA_ERR_UNSUPPORTED).
  */
 #define KDA_SSM_CHUNK 64
