@@ -27,28 +27,33 @@ namespace kda {
 
 namespace {
 
-// Sums of V = 8 or 16 values over the 16 lanes of a lane group: each exchange
-// halves the values a lane carries; lane c ends with the sum of value
-// sum16_index<V>(c).
-template <int V>
-__device__ __forceinline__ float sum16(float (&v)[V], int c16) {
-    int bit = 8;
-#pragma unroll
-    for (int n = V; n > 1; n >>= 1, bit >>= 1) {
-        const bool up = c16 & bit;
-#pragma unroll
-        for (int i = 0; i < n / 2; ++i) {
-            const float keep = up ? v[i + n / 2] : v[i];
-            const float give = up ? v[i] : v[i + n / 2];
-            v[i] = keep + __shfl_xor(give, bit);
-        }
-    }
-    float s = v[0];
-    for (; bit; bit >>= 1) s += __shfl_xor(s, bit);
-    return s;
+// the value of lane ^ BIT of the same 16
+template <int BIT>
+__device__ __forceinline__ float lane_xor(float v) {
+    const int x = __builtin_bit_cast(int, v);
+    if constexpr (BIT == 1) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, x, 0xb1, 0xf, 0xf, true));       // quad_perm 1,0,3,2
+    else if constexpr (BIT == 2) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, x, 0x4e, 0xf, 0xf, true));  // quad_perm 2,3,0,1
+    else if constexpr (BIT == 8) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, x, 0x128, 0xf, 0xf, true)); // row_ror:8
+    else return __shfl_xor(v, BIT);
 }
-template <int V>
-__device__ __forceinline__ int sum16_index(int c16) { return V == 16 ? c16 : c16 >> 1; }
+// Sums of V = 4, 8 or 16 values over the 16 lanes of a lane group: each
+// exchange halves the values a lane carries; lane c ends with the sum of value
+// c / (16 / V).
+template <int V, int BIT>
+__device__ __forceinline__ float sum16(const float *v, int c16) {
+    if constexpr (V > 1) {
+        const bool up = c16 & BIT;
+        float next[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) next[i] = (up ? v[i + V / 2] : v[i]) + lane_xor<BIT>(up ? v[i] : v[i + V / 2]);
+        return sum16<V / 2, BIT / 2>(next, c16);
+    } else if constexpr (BIT > 0) {
+        const float next = v[0] + lane_xor<BIT>(v[0]);
+        return sum16<1, BIT / 2>(&next, c16);
+    } else {
+        return v[0];
+    }
+}
 
 template <typename TI, int NS, int P>
 struct GradCfg {
@@ -61,10 +66,13 @@ struct GradCfg {
     static constexpr int RN = NKS * 32 + 8, RP = PKS * 32 + 8, RL = L + 8;
     // LDS, in bf16 elements
     static constexpr int BN = 0, CN = BN + EX * L * RN, XN = CN + EX * L * RN, YN = XN + EX * L * RP;
-    static constexpr int M1 = YN + EX * L * RP, M2 = M1 + XP * L * RL, END = M2 + XP * L * RL;
+    static constexpr int M1 = YN + EX * L * RP, M2 = M1 + XP * L * RL, GN = M2 + XP * L * RL;
     // then floats: dt, suf, 2^cum, 2^suf, diagonals of Q and E, suf's rounding; row and column sums per tile; inter and outer per wave; <G, S> per wave
     static constexpr int FDT = 0, FSUF = L, FCUM = 2 * L, FWS = 3 * L, FQD = 4 * L, FED = 5 * L, FLO = 6 * L, FR = 7 * L, FC = FR + ST * L,
                          FI = FC + ST * L, FO = FI + NT * L, FX = FO + NT * L, FEND = FX + 8;
+    // G by rows, for du: through LDS where it fits, else read a second time
+    static constexpr bool GLDS = sizeof(bf16_t) * (GN + XP * NS * RP) + sizeof(float) * FEND <= 160 * 1024;
+    static constexpr int END = GN + (GLDS ? XP * NS * RP : 0);
     static constexpr size_t BYTES = sizeof(bf16_t) * END + sizeof(float) * FEND;
 };
 
@@ -77,8 +85,9 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
     bf16_t *lds = reinterpret_cast<bf16_t *>(smem);
     float *fl = reinterpret_cast<float *>(smem + sizeof(bf16_t) * Cf::END);
     const SsmParams &p = a.q.p;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int g = lane >> 4, c16 = lane & 15;
+    int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int lane = tid & 63, g = lane >> 4, c16 = lane & 15;
 
     // block -> (chunk of 64, part of it, group, split of the group's heads)
     const int block = xcd_order(blockIdx.x, gridDim.x);
@@ -113,21 +122,49 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
     const TI *bb = static_cast<const TI *>(p.Bm) + row * p.b_sb + t0 * p.b_st + static_cast<int64_t>(grp) * NS;
     const TI *cb = static_cast<const TI *>(p.Cm) + row * p.c_sb + t0 * p.c_st + static_cast<int64_t>(grp) * NS;
 
-    // a [tokens, width] tile into LDS in granule order, tokens past the chunk as zeros
-    auto stage = [&](int at, int stride, int width, const TI *src, int64_t st) {
-        for (int i = tid; i < (L / 4) * (width / 4); i += 512) {
-            const int tq = i / (width / 4), cq = i % (width / 4);
+    // A [tokens, width] tile goes into LDS in granule order, 4 tokens by 4
+    // columns a thread.  Rows past the chunk are zeros: a token there has step
+    // size 0, but it must not meet another's finite factor with what it holds.
+    auto load_quad = [&](quad<TI> &v, const TI *src, int64_t stride, int tq, int cq) {
+        const uint32_t st = static_cast<uint32_t>(stride);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            v.zero(r);
+            if (len == L || tq * 4 + r < len) v.ld(r, src + (static_cast<uint32_t>(tq * 4 + r) * st + 4 * cq));
+        }
+    };
+    auto store_quad = [&](const quad<TI> &v, int at, int stride, int tq, int cq) {
+#pragma unroll
+        for (int part = 0; part < EX; ++part)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *reinterpret_cast<uint2 *>(lds + at + part * L * stride + (tq * 4 + r) * stride + col_pos(cq * 4)) = v.row(r, part).u;
+    };
+    auto stage = [&](int at, int stride, const TI *src, int64_t st) {
+        for (int i = tid; i < (L / 4) * (NS / 4); i += 512) {
             quad<TI> v;
+            load_quad(v, src, st, i / (NS / 4), i % (NS / 4));
+            store_quad(v, at, stride, i / (NS / 4), i % (NS / 4));
+        }
+    };
+    // x and dy of a head: half the workgroup each
+    constexpr int XB = (L / 4) * (P / 4), XPER = (XB + 255) / 256;
+    quad<TI> raw[XPER];
+    auto fetch_xy = [&](int h) {
+        const bool y = wave >= 4;
+        const TI *src = y ? static_cast<const TI *>(a.d_y) + (flat0 * p.H + h) * P : xb + static_cast<int64_t>(h) * P;
+        const int64_t st = y ? static_cast<int64_t>(p.H) * P : p.x_st;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                v.zero(r);
-                if (tq * 4 + r < len) v.ld(r, src + (tq * 4 + r) * st + cq * 4);
-            }
+        for (int k = 0; k < XPER; ++k) {
+            const int i = (tid & 255) + 256 * k;
+            if (XB % 256 == 0 || i < XB) load_quad(raw[k], src, st, i / (P / 4), i % (P / 4));
+        }
+    };
+    auto store_xy = [&] {
 #pragma unroll
-            for (int part = 0; part < EX; ++part)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    *reinterpret_cast<uint2 *>(lds + at + part * L * stride + (tq * 4 + r) * stride + col_pos(cq * 4)) = v.row(r, part).u;
+        for (int k = 0; k < XPER; ++k) {
+            const int i = (tid & 255) + 256 * k;
+            if (XB % 256 == 0 || i < XB) store_quad(raw[k], wave >= 4 ? Cf::YN : Cf::XN, RP, i / (P / 4), i % (P / 4));
         }
     };
     // columns past d_state and d_head, the score tiles above the diagonal and
@@ -135,18 +172,22 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
     for (int i = tid; i < Cf::END / 2; i += 512) reinterpret_cast<uint32_t *>(lds)[i] = 0;
     for (int i = tid; i < Cf::FEND; i += 512) fl[i] = 0.f;
     lds_barrier();
-    stage(Cf::BN, RN, NS, bb, p.b_st);
-    stage(Cf::CN, RN, NS, cb, p.c_st);
+    stage(Cf::BN, RN, bb, p.b_st);
+    stage(Cf::CN, RN, cb, p.c_st);
     lds_barrier();
 
     constexpr int TILES = ST * (ST + 1) / 2, MT = (TILES + 7) / 8;
     f32x4 K[MT];  // scores of this wave's tiles: rows s, columns t
+    int tile_i[MT], tile_j[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         K[m] = f32x4{0.f, 0.f, 0.f, 0.f};
         int ti = 0, tj = wave + 8 * m;
+        tile_i[m] = -1;
         if (tj >= TILES) continue;
         while (tj > ti) { tj -= ti + 1; ++ti; }
+        tile_i[m] = ti;
+        tile_j[m] = tj;
         for (int kk = 0; kk < NKS; ++kk) {
             parts8<EX> u, v;
 #pragma unroll
@@ -179,57 +220,73 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
 #pragma unroll
     for (int s = 0; s < ST; ++s) dCs[s] = dBs[s] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    for (int h = h0; h < h1; ++h) {
-        // ---- stage x, dy and the decays
-        stage(Cf::XN, RP, P, xb + static_cast<int64_t>(h) * P, p.x_st);
-        stage(Cf::YN, RP, P, static_cast<const TI *>(a.d_y) + (flat0 * p.H + h) * P, static_cast<int64_t>(p.H) * P);
-        const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-        const float raw = lane < len ? io<TI>::ld(static_cast<const TI *>(p.dt), (flat0 + lane) * p.H + h) + bias : 0.f;
-        float dt = p.softplus ? softplus_rel(raw) : raw;
-        if (lane >= len) dt = 0.f;
-        const float la = A * kLog2e * dt;
-        // D compares sums over the rest of the chunk whose difference may be
-        // one token's log: kept in 64 bits, as two floats in LDS
-        double sum = static_cast<double>(A) * 1.4426950408889634 * dt;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double o = __shfl_down(sum, d);
-            if (lane + d < 64) sum += o;
-        }
-        const float tot = static_cast<float>(__shfl(sum, 0));
-        double rest = __shfl_down(sum, 1);
-        if (lane == 63) rest = 0.0;
-        const float suf = static_cast<float>(rest);
-        const float ecum = fast_exp2(prefix_sum(la, lane)), esuf = fast_exp2(suf);
-        if (wave == 0 && lane < L) {
-            fl[Cf::FDT + lane] = dt;
-            fl[Cf::FSUF + lane] = suf;
-            fl[Cf::FLO + lane] = static_cast<float>(rest - suf);
-            fl[Cf::FCUM + lane] = ecum;
-            fl[Cf::FWS + lane] = esuf;
-        }
-        // this wave's rows of both states, channels in the operand's slot order
-        const int64_t so = ((static_cast<int64_t>(item) * p.H + h) * NS + n0 + c16) * P;
-        f32x4 Sv[PKS][2], Gv[PKS][2];
+    // this wave's rows of both states, channels in the operand's slot order
+    f32x4 Sv[PKS][2], Gv[PKS][2];
+    auto fetch_states = [&](int h) {
+        const int64_t so = ((static_cast<int64_t>(item) * p.H + h) * NS + n0) * P;
 #pragma unroll
         for (int ks = 0; ks < PKS; ++ks)
 #pragma unroll
             for (int hq = 0; hq < 2; ++hq) {
                 const int c = 32 * ks + 16 * hq + 4 * g;
                 Sv[ks][hq] = Gv[ks][hq] = f32x4{0.f, 0.f, 0.f, 0.f};
-                if (rows_on && c < P) {
-                    Sv[ks][hq] = *reinterpret_cast<const f32x4 *>(a.states + so + c);
-                    Gv[ks][hq] = *reinterpret_cast<const f32x4 *>(a.gstates + so + c);
+                if (rows_on && (P >= 32 || hq == 0)) {
+                    Sv[ks][hq] = *reinterpret_cast<const f32x4 *>(a.states + so + static_cast<uint32_t>(c16 * P + c));
+                    Gv[ks][hq] = *reinterpret_cast<const f32x4 *>(a.gstates + so + static_cast<uint32_t>(c16 * P + c));
                 }
             }
+    };
+    float rawdt = 0.f;  // wave 7: one token a lane
+    auto fetch_dt = [&](int h) {
+        if (wave == 7 && lane < len) rawdt = io<TI>::ld(static_cast<const TI *>(p.dt), (flat0 + lane) * p.H + h);
+    };
+    fetch_xy(h0);
+    fetch_states(h0);
+    fetch_dt(h0);
+    for (int h = h0; h < h1; ++h) {
+        // what follows from the lane's place is computed again for every head:
+        // kept over the loop it would push the tiles out of the registers
+        asm volatile("" : "+v"(tid), "+v"(lane), "+v"(g), "+v"(c16));
+        // ---- x, dy and the decays into LDS; the next head's x and dy on their way
+        store_xy();
+        const float A = p.A[h];
+        float raw_dt = 0.f, dt = 0.f, tot = 0.f;
+        if (wave == 7) {
+            raw_dt = rawdt + (p.dt_bias ? p.dt_bias[h] : 0.f);
+            dt = p.softplus ? softplus_rel(raw_dt) : raw_dt;
+            if (lane >= len) dt = 0.f;
+            // D compares sums over the rest of the chunk whose difference may
+            // be one token's log: kept in 64 bits, as two floats in LDS
+            double sum = static_cast<double>(A) * 1.4426950408889634 * dt;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const double o = __shfl_down(sum, d);
+                if (lane + d < 64) sum += o;
+            }
+            tot = static_cast<float>(__shfl(sum, 0));
+            double rest = __shfl_down(sum, 1);
+            if (lane == 63) rest = 0.0;
+            const float suf = static_cast<float>(rest);
+            const float ecum = fast_exp2(lane_scan(A * kLog2e * dt));
+            if (lane < L) {
+                fl[Cf::FDT + lane] = dt;
+                fl[Cf::FSUF + lane] = suf;
+                fl[Cf::FLO + lane] = static_cast<float>(rest - suf);
+                fl[Cf::FCUM + lane] = ecum;
+                fl[Cf::FWS + lane] = fast_exp2(suf);
+            }
+        }
+        if (h + 1 < h1) {
+            fetch_xy(h + 1);
+            fetch_dt(h + 1);
+        }
         lds_barrier();
 
         // ---- causal tiles of Q; M1 = Q D dt_s, M2 = K D into LDS; sums of E
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            int ti = 0, tj = wave + 8 * m;
-            if (tj >= TILES) continue;
-            while (tj > ti) { tj -= ti + 1; ++ti; }
+            const int ti = tile_i[m], tj = tile_j[m];
+            if (ti < 0) continue;
             f32x4 q = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kk = 0; kk < PKS; ++kk) {
@@ -279,62 +336,63 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
             rowsum += __shfl_xor(rowsum, 16);
             rowsum += __shfl_xor(rowsum, 32);
             if (g == 0) fl[Cf::FR + tj * L + t] = rowsum;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int b = 1; b < 16; b <<= 1) E[r] += __shfl_xor(E[r], b);
-            if (c16 == 0)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) fl[Cf::FC + ti * L + s0 + r] = E[r];
+            const float colsum = sum16<4, 8>(E, c16);
+            if (c16 % 4 == 0) fl[Cf::FC + ti * L + s0 + c16 / 4] = colsum;
         }
 
         // ---- the states' shares of dC and dB, and their sums with C and B
         if (rows_on) {
-            parts8<SP> Sf[PKS], Gf[PKS];
             float gs = 0.f;
+            f32x4 ts[ST], tg[ST];
 #pragma unroll
-            for (int ks = 0; ks < PKS; ++ks)
+            for (int s = 0; s < ST; ++s) ts[s] = tg[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < PKS; ++ks) {
+                parts8<SP> Sf, Gf;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     gs = fmaf(Sv[ks][j / 4][j % 4], Gv[ks][j / 4][j % 4], gs);
-                    split_to<SP>(Sf[ks], j, Sv[ks][j / 4][j % 4]);
-                    split_to<SP>(Gf[ks], j, Gv[ks][j / 4][j % 4]);
+                    split_to<SP>(Sf, j, Sv[ks][j / 4][j % 4]);
+                    split_to<SP>(Gf, j, Gv[ks][j / 4][j % 4]);
                 }
+                if (Cf::GLDS)
 #pragma unroll
-            for (int b = 1; b < 64; b <<= 1) gs += __shfl_xor(gs, b);
-            if (lane == 0) fl[Cf::FX + wave] = gs;
-            float vi[4 * ST], vo[4 * ST];
+                    for (int part = 0; part < XP; ++part)
+                        *reinterpret_cast<uint4 *>(lds + Cf::GN + part * NS * RP + (n0 + c16) * RP + 32 * ks + 8 * g) = Gf.f[part].u;
 #pragma unroll
-            for (int s = 0; s < ST; ++s) {
-                f32x4 ts = {0.f, 0.f, 0.f, 0.f}, tg = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int ks = 0; ks < PKS; ++ks) {
+                for (int s = 0; s < ST; ++s) {
                     parts8<EX> y, x;
 #pragma unroll
                     for (int part = 0; part < EX; ++part) {
                         load_rows(y.f[part], lds + Cf::YN + part * L * RP, RP, 16 * s, ks, g, c16);
                         load_rows(x.f[part], lds + Cf::XN + part * L * RP, RP, 16 * s, ks, g, c16);
                     }
-                    mfma_parts<EX, SP, 3>(ts, y, Sf[ks]);
-                    mfma_parts<EX, SP, 3>(tg, x, Gf[ks]);
+                    mfma_parts<EX, SP, 3>(ts[s], y, Sf);
+                    mfma_parts<EX, SP, 3>(tg[s], x, Gf);
                 }
+            }
+            if (h + 1 < h1) fetch_states(h + 1);
+            gs = lane_scan(gs);
+            if (lane == 63) fl[Cf::FX + wave] = gs;
+            float vi[4 * ST], vo[4 * ST];
+#pragma unroll
+            for (int s = 0; s < ST; ++s) {
                 const f32x4 cum = *reinterpret_cast<const f32x4 *>(fl + Cf::FCUM + 16 * s + 4 * g);
                 const f32x4 ws = *reinterpret_cast<const f32x4 *>(fl + Cf::FWS + 16 * s + 4 * g);
                 const f32x4 dts = *reinterpret_cast<const f32x4 *>(fl + Cf::FDT + 16 * s + 4 * g);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    ts[r] *= cum[r];
-                    tg[r] *= ws[r];
-                    vi[4 * s + r] = ts[r] * elem(Ct, s, r);
-                    vo[4 * s + r] = tg[r] * elem(Bt, s, r);
-                    dCs[s][r] += ts[r];
-                    dBs[s][r] = fmaf(dts[r], tg[r], dBs[s][r]);
+                    ts[s][r] *= cum[r];
+                    tg[s][r] *= ws[r];
+                    vi[4 * s + r] = ts[s][r] * elem(Ct, s, r);
+                    vo[4 * s + r] = tg[s][r] * elem(Bt, s, r);
+                    dCs[s][r] += ts[s][r];
+                    dBs[s][r] = fmaf(dts[r], tg[s][r], dBs[s][r]);
                 }
             }
-            const float si = sum16<4 * ST>(vi, c16), sg = sum16<4 * ST>(vo, c16);
-            const int k = sum16_index<4 * ST>(c16);
-            const int t = 16 * (k / 4) + 4 * g + k % 4;
-            if (ST == 4 || !(c16 & 1)) {
+            const float si = sum16<4 * ST, 8>(vi, c16), sg = sum16<4 * ST, 8>(vo, c16);
+            const int k = c16 / (4 / ST), t = 16 * (k / 4) + 4 * g + k % 4;
+            if (c16 % (4 / ST) == 0) {
                 fl[Cf::FI + wave * L + t] = si;
                 fl[Cf::FO + wave * L + t] = sg;
             }
@@ -363,17 +421,22 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
         }
         // ---- du and dx: 16 x 16 tiles (strip s, channel tile pt)
         const float Dh = p.D ? p.D[h] : 0.f;
+#pragma unroll 1
         for (int u = wave; u < PT * ST; u += 8) {
             const int pt = u % PT, s = u / PT;
             f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-            const float *Gp = a.gstates + (static_cast<int64_t>(item) * p.H + h) * NS * P + 16 * pt + c16;
+            const float *Gp = a.gstates + (static_cast<int64_t>(item) * p.H + h) * NS * P + 16 * pt;
 #pragma unroll
             for (int kk = 0; kk < NKS; ++kk) {
                 parts8<XP> gf;
+                if constexpr (Cf::GLDS && NS >= 32) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int n = 32 * kk + kperm(g, j);
-                    split_to<XP>(gf, j, n < NS ? Gp[n * P] : 0.f);
+                    for (int part = 0; part < XP; ++part)
+                        load_cols(gf.f[part], lds + Cf::GN + part * NS * RP, RP, 32 * kk, 16 * pt, g, c16);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        split_to<XP>(gf, j, NS >= 32 || j < 4 ? Gp[static_cast<uint32_t>((32 * kk + kperm(g, j)) * P + c16)] : 0.f);
                 }
                 parts8<EX> b;
 #pragma unroll
@@ -402,8 +465,9 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int t = 16 * s + 4 * g + r;
-                if (t < len)
-                    io<TI>::st(static_cast<TI *>(a.dx), ((flat0 + t) * p.H + h) * P + 16 * pt + c16, fmaf(dts[r], acc[r], Dh * dyv[r]));
+                if (len == L || t < len)
+                    io<TI>::st(static_cast<TI *>(a.dx) + ((flat0 + 16 * s + r) * p.H + h) * P + 16 * pt,
+                               static_cast<uint32_t>(4 * g * p.H * P + c16), fmaf(dts[r], acc[r], Dh * dyv[r]));
             }
         }
         // ---- the step sizes: one token a lane
@@ -424,13 +488,13 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
 #pragma unroll
             for (int k = 0; k < NT; ++k) X += fl[Cf::FX + k];
             const float o = dt * out;
-            const float dlog = suffix_sum(R - dt * Cs + in, lane) + before(prefix_sum(o, lane), lane) + fast_exp2(tot) * X;
+            const float dlog = suffix_sum(R - dt * Cs + in, lane) + lane_shift(lane_scan(o)) + fast_exp2(tot) * X;
             float dd = Cs + (lane < L ? fl[Cf::FED + lane] : 0.f) + out + A * dlog;
-            if (p.softplus) dd *= sigmoid_f32(raw);
+            if (p.softplus) dd *= sigmoid_f32(raw_dt);
             if (lane >= len) dd = 0.f;
             if (lane < len) io<TI>::st(static_cast<TI *>(a.ddt), (flat0 + lane) * p.H + h, dd);
-            const float sa = prefix_sum(dt * dlog, lane), sd = prefix_sum(lane < L ? fl[Cf::FQD + lane] : 0.f, lane);
-            const float sb = prefix_sum(dd, lane);
+            const float sa = lane_scan(dt * dlog), sd = lane_scan(lane < L ? fl[Cf::FQD + lane] : 0.f);
+            const float sb = lane_scan(dd);
             if (lane == 63) {
                 a.scalars[(0 * static_cast<int64_t>(p.H) + h) * items + item] = sa;
                 a.scalars[(1 * static_cast<int64_t>(p.H) + h) * items + item] = sd;
