@@ -71,6 +71,7 @@ __device__ __forceinline__ constexpr int kperm(int g, int j) {
 union frag8 {
     bf16x8 v;
     bf16_t s[8];
+    uint32_t w[4];
     uint4 u;
 };
 

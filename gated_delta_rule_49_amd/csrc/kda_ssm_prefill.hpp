@@ -34,11 +34,13 @@ struct ScanCfg {
     static constexpr int SP = !BF ? 3 : std::is_same<TO, bf16_t>::value ? 1 : 2;
     static constexpr int NT = NS / 16, KS = (NS + 31) / 32, NK = KS * 32;
     static constexpr int CT = PW / 16, ST = L / 16, TK = L / 32;
-    static constexpr int RN = NK + 8, RT = L + 8;         // LDS row strides: 16-byte pieces of 16 rows hit all banks
+    // LDS row strides: 16-byte pieces of 16 rows hit all banks (C, scores);
+    // 4 rows of transposed 8-byte pieces are 16 banks apart (B)
+    static constexpr int RN = NK + 8, RT = L + 8, RB = NK / 32 % 2 ? NK : NK + 32;
     static constexpr int NBUF = BF ? 2 : 1;
-    static constexpr int BN = EX * L * RN;                // B by rows; C likewise
+    static constexpr int BN = EX * L * RB, CN = EX * L * RN;
     static constexpr int GT = FULL ? GP * L * RT : 0;     // causal scores
-    static constexpr int BUF = BN + (FULL ? BN : 0) + GT;
+    static constexpr int BUF = BN + (FULL ? CN : 0) + GT;
     static constexpr int WV = (FULL ? 4 : 1) * L;         // per wave: w, row factor, suf, dt
     static constexpr size_t BYTES = sizeof(bf16_t) * NBUF * BUF + sizeof(float) * NW * WV;
 };
@@ -47,7 +49,7 @@ template <typename TI, typename TO, int NS, int PW, int NW, int MODE>
 __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks_per_group, int phase) {
     using Cf = ScanCfg<TI, TO, NS, PW, NW, MODE>;
     constexpr int EX = Cf::EX, L = Cf::L, ORD = Cf::ORD, XP = Cf::XP, GP = Cf::GP, SP = Cf::SP, NT = Cf::NT, KS = Cf::KS;
-    constexpr int CT = Cf::CT, ST = Cf::ST, TK = Cf::TK, RN = Cf::RN, RT = Cf::RT, NBUF = Cf::NBUF;
+    constexpr int CT = Cf::CT, ST = Cf::ST, TK = Cf::TK, RN = Cf::RN, RB = Cf::RB, RT = Cf::RT, NBUF = Cf::NBUF;
     constexpr bool FULL = MODE == SSM_FULL, REV = MODE == SSM_REVERSE;
     __shared__ __attribute__((aligned(16))) char smem[Cf::BYTES];
     const SsmParams &p = q.p;
@@ -73,9 +75,9 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
     bf16_t *lds = reinterpret_cast<bf16_t *>(smem);
     float *wv = reinterpret_cast<float *>(smem + sizeof(bf16_t) * NBUF * Cf::BUF) + wave * Cf::WV;
     float *fv = wv + L, *sv = wv + 2 * L, *dv = wv + 3 * L;
-    auto Bn = [&](int b, int part) { return lds + b * Cf::BUF + part * L * RN; };
+    auto Bn = [&](int b, int part) { return lds + b * Cf::BUF + part * L * RB; };
     auto Cn = [&](int b, int part) { return lds + b * Cf::BUF + Cf::BN + part * L * RN; };
-    auto Gt = [&](int b, int part) { return lds + b * Cf::BUF + 2 * Cf::BN + part * L * RT; };
+    auto Gt = [&](int b, int part) { return lds + b * Cf::BUF + Cf::BN + Cf::CN + part * L * RT; };
 
     // Uniform bases; a lane adds a 32-bit byte offset (strides are below 2^23
     // elements, so a chunk's rows stay below 2^31 bytes).
@@ -105,12 +107,24 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 lanevec<float, CT> v;
-                v.ld(src + (16 * nt + r) * p.P + static_cast<uint32_t>(4 * g * p.P + c16 * CT));
+                v.ld(lane_at(src + (16 * nt + r) * p.P, 4 * g * p.P + c16 * CT));
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) S[nt][ct][r] = v.get(ct);
             }
     }
+    // The state is kept as S 2^level: a chunk adds its tot to the level (in 64
+    // bits) and scales its own w x to match, and S is multiplied out only when
+    // the level has gone far, or before a store.
+    double level = 0.0;
+    auto scale_state = [&](float f) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) S[nt][ct] *= f;
+    };
     auto store_state = [&](float *dst) {
+        scale_state(fast_exp2(static_cast<float>(level)));
+        level = 0.0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -118,14 +132,14 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                 float v[CT];
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) v[ct] = S[nt][ct][r];
-                lanevec<float, CT>::st(dst + (16 * nt + r) * p.P + static_cast<uint32_t>(4 * g * p.P + c16 * CT), v);
+                lanevec<float, CT>::st(lane_at(dst + (16 * nt + r) * p.P, 4 * g * p.P + c16 * CT), v);
             }
     };
 
     // zero what no staging writes: columns past d_state, the score tiles above the diagonal
     if (NS < 32)
         for (int b = 0; b < NBUF; ++b)
-            for (int i = tid; i < (FULL ? 2 : 1) * Cf::BN; i += 64 * NW) Bn(b, 0)[i] = 0;
+            for (int i = tid; i < Cf::BN + (FULL ? Cf::CN : 0); i += 64 * NW) Bn(b, 0)[i] = 0;
     if (FULL)
         for (int b = 0; b < NBUF; ++b)
             for (int i = tid; i < Cf::GT; i += 64 * NW) Gt(b, 0)[i] = 0;
@@ -135,7 +149,8 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
     // Rows past the segment repeat its last one: their step size is 0, so
     // whatever they hold meets a factor of 0 or a row that is not stored.
     constexpr int BLOCKS = (L / 4) * (NS / 4), PER = (BLOCKS + 64 * NW - 1) / (64 * NW);
-    quad<TI> rawB[PER], rawC[FULL ? PER : 1];
+    constexpr int AHEAD = FULL ? 1 : 2;  // chunks between a request and its use: the states alone are a short iteration
+    quad<TI> rawB[AHEAD][PER], rawC[FULL ? PER : 1];
     auto fetch_rows = [&](quad<TI> (&raw)[PER], const TI *base, int64_t stride, int c) {
         const int rem = min(sg.len - c * L, L);
         const TI *cbase = base + c * L * stride;
@@ -146,16 +161,22 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
             const uint32_t tq = i / (NS / 4), nq = i % (NS / 4);
             if (BLOCKS % (64 * NW) == 0 || i < BLOCKS) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    raw[k].ld(r, cbase + (rem == L ? (4 * tq + r) * st : min(4 * tq + r, rem - 1u) * st) + 4 * nq);
+                for (int r = 0; r < 4; ++r) {
+                    if (rem == L) {
+                        raw[k].ld(r, lane_at(cbase + r * stride, 4 * tq * st + 4 * nq));
+                    } else {
+                        raw[k].ld(r, lane_at(cbase, min(4 * tq + r, rem - 1u) * st + 4 * nq));
+                        asm volatile("");
+                    }
+                }
             }
         }
     };
-    auto fetch = [&](int c) {
-        fetch_rows(rawB, bb, p.b_st, c);
+    auto fetch = [&](int c, quad<TI> (&raw)[PER]) {
+        fetch_rows(raw, bb, p.b_st, c);
         if constexpr (FULL) fetch_rows(rawC, cb, p.c_st, c);
     };
-    auto stage = [&](int b) {
+    auto stage = [&](int b, const quad<TI> (&raw)[PER]) {
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const int i = tid + k * 64 * NW;
@@ -165,7 +186,7 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                 for (int part = 0; part < EX; ++part)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        *reinterpret_cast<uint2 *>(Bn(b, part) + (tq * 4 + r) * RN + col_pos(nq * 4)) = rawB[k].row(r, part).u;
+                        *reinterpret_cast<uint2 *>(Bn(b, part) + (tq * 4 + r) * RB + col_pos(nq * 4)) = raw[k].row(r, part).u;
                         if (FULL) *reinterpret_cast<uint2 *>(Cn(b, part) + (tq * 4 + r) * RN + col_pos(nq * 4)) = rawC[k].row(r, part).u;
                     }
         }
@@ -182,7 +203,7 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                 parts8<EX> a, bf;
 #pragma unroll
                 for (int part = 0; part < EX; ++part) {
-                    load_rows(a.f[part], Bn(b, part), RN, 16 * tj, kk, g, c16);
+                    load_rows(a.f[part], Bn(b, part), RB, 16 * tj, kk, g, c16);
                     load_rows(bf.f[part], Cn(b, part), RN, 16 * ti, kk, g, c16);
                 }
                 mfma_parts<EX, EX, ORD>(acc, a, bf);
@@ -205,8 +226,8 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
     // x (rows in the operand's slot order) and dt of a chunk; a lane's token is
     // its own number in the reverse mode (sums from the chunk's start are
     // wanted), else counted from the chunk's end
-    lanevec<TI, CT> xr[TK][8], xn[TK][8];
-    TI dtr = TI(0), dtn = TI(0);
+    lanevec<TI, CT> xs[AHEAD][TK][8];
+    TI dts[AHEAD];
     auto token = [&] { return REV ? tid & 63 : L - 1 - (tid & 63); };
     auto fetch_x = [&](int c, lanevec<TI, CT> (&xv)[TK][8], TI &d) {
         const int rem = min(sg.len - c * L, L);
@@ -216,43 +237,34 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
 #pragma unroll
             for (int ks = 0; ks < TK; ++ks)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) xv[ks][j].ld(base + (32 * ks + kperm(0, j)) * static_cast<int64_t>(x_st) + off);
+                for (int j = 0; j < 8; ++j) xv[ks][j].ld(lane_at(base + (32 * ks + kperm(0, j)) * static_cast<int64_t>(x_st), off));
         } else {
 #pragma unroll
             for (int ks = 0; ks < TK; ++ks)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) xv[ks][j].ld(base + min(32 * ks + kperm(g, j), rem - 1) * x_st + c16 * CT);
+                for (int j = 0; j < 8; ++j) xv[ks][j].ld(lane_at(base, min(32 * ks + kperm(g, j), rem - 1) * x_st + c16 * CT));
+            asm volatile("");  // keeps the two branches' loads apart, each with its own addresses
         }
-        d = TI(0);
-        const int tok = token();
-        if (tok >= 0 && tok < rem) d = dtb[static_cast<int64_t>(c) * L * p.H + static_cast<uint32_t>(tok * p.H)];
+        d = *lane_at(dtb + static_cast<int64_t>(c) * L * p.H, max(0, min(token(), rem - 1)) * p.H);
     };
 
     const int chunks = (sg.len + L - 1) / L;
     float seg_log = 0.f;
     auto order = [&](int i) { return REV ? chunks - 1 - i : i; };
-    if (chunks > 0) {
-        fetch(order(0));
-        fetch_x(order(0), xr, dtr);
-        stage(0);
-        if (chunks > 1) fetch(order(1));
-        lds_barrier();
-        if (FULL) {
-            scores(0);
-            lds_barrier();
-        }
-    }
-    for (int i = 0; i < chunks; ++i) {
+    auto body = [&](int i, lanevec<TI, CT> (&xr)[TK][8], TI &dtr, quad<TI> (&raw)[PER]) {
         const int b = NBUF == 2 ? i & 1 : 0;
         const int t0 = order(i) * L, rem = min(sg.len - t0, L);
         // what follows from the lane's place is computed again in every
-        // iteration: kept over the loop it would push the tiles out of the registers
+        // iteration: kept over the loop it would push the tiles out of the
+        // registers, and every spill waits for all loads in flight
         asm volatile("" : "+v"(g), "+v"(c16), "+v"(tid));
         if (NBUF == 2 && i + 1 < chunks) {  // the next chunk into the other buffer
-            stage(b ^ 1);
-            if (i + 2 < chunks) fetch(order(i + 2));
+            stage(b ^ 1, raw);
+            if (i + 1 + AHEAD < chunks) fetch(order(i + 1 + AHEAD), raw);
         }
-        if (i + 1 < chunks) fetch_x(order(i + 1), xn, dtn);
+        float dec = 1.f;
+        bool fast = true, late = false;
+        f32x4 acc[FULL ? ST : 1][CT];
         if (on) {
             // the state entering the chunk (from the right in the reverse order)
             if (phase == 2 && p.chunk_states && t0 % q.state_chunk == 0)
@@ -265,26 +277,37 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
             const float la = A2 * dt;
             const float incl = lane_scan(la);  // from the chunk's end (reverse: its start) to the token
             const float tot = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, incl), 63));
-            const bool fast = fabsf(tot) < kFastTot;
+            fast = !FULL || fabsf(tot) < kFastTot;
+            const float from = static_cast<float>(level);
+            double next = level + tot;
+            const bool out = __builtin_amdgcn_readfirstlane(!(fabs(next) <= kLevel));
+            dec = fast_exp2(static_cast<float>(next));
+            if (out) next = 0.0;
+            level = next;
+            if (fast && out) scale_state(dec);  // the second form reads the state before this chunk's decay
+            const float hi = static_cast<float>(next), lo = static_cast<float>(next - hi);
             if (REV) {
-                if (lane < L) wv[lane] = lane < rem ? fast_exp2(incl) : 0.f;
+                if (lane < L) wv[lane] = lane < rem ? fast_exp2((incl - hi) - lo) : 0.f;
             } else {
                 const float suf = lane_shift(incl);
-                float row = 0.f;
-                if (FULL) row = fast ? fast_exp2(-suf) : fast_exp2(suffix_sum(la, lane));
                 if (tok >= 0) {
-                    wv[tok] = dt * fast_exp2(suf);
+                    wv[tok] = dt * fast_exp2((suf - hi) - lo);
                     if (FULL) {
-                        fv[tok] = row;
+                        fv[tok] = fast ? fast_exp2((hi - suf) + lo) : la;
                         sv[tok] = suf;
                         dv[tok] = dt;
                     }
                 }
+                if (FULL && !fast) {  // the sums from the chunk's start
+                    wave_lds_fence();
+                    const float cum = lane_scan(lane < L ? fv[lane] : 0.f);
+                    wave_lds_fence();
+                    if (lane < L) fv[lane] = fast_exp2(cum + from);
+                }
             }
             seg_log += tot;
+            late = !fast && out;
             wave_lds_fence();
-            const float dec = fast_exp2(tot);
-            f32x4 acc[FULL ? ST : 1][CT];
             if constexpr (FULL) {  // C S
 #pragma unroll
                 for (int s = 0; s < ST; ++s)
@@ -296,9 +319,11 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            split_to<SP>(sf[ct], r, S[2 * kk][ct][r]);
-                            split_to<SP>(sf[ct], 4 + r, 2 * kk + 1 < NT ? S[2 * kk + 1 < NT ? 2 * kk + 1 : 0][ct][r] : 0.f);
+                        for (int r = 0; r < 4; r += 2) {
+                            constexpr f32x4 none = {0.f, 0.f, 0.f, 0.f};
+                            const f32x4 &s1 = 2 * kk + 1 < NT ? S[2 * kk + 1 < NT ? 2 * kk + 1 : 0][ct] : none;
+                            split_pair<SP>(sf[ct], r, S[2 * kk][ct][r], S[2 * kk][ct][r + 1]);
+                            split_pair<SP>(sf[ct], 4 + r, s1[r], s1[r + 1]);
                         }
 #pragma unroll
                     for (int s = 0; s < ST; ++s) {
@@ -308,13 +333,22 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                         mfma_tiles<EX, SP, ORD, CT>(acc[s], a, sf);
                     }
                 }
+                if (!fast)
 #pragma unroll
-                for (int s = 0; s < ST; ++s) {
-                    f32x4 f = {dec, dec, dec, dec};
-                    if (!fast) f = *reinterpret_cast<const f32x4 *>(fv + 16 * s + 4 * g);
+                    for (int s = 0; s < ST; ++s) {
+                        const f32x4 f = *reinterpret_cast<const f32x4 *>(fv + 16 * s + 4 * g);
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) acc[s][ct] *= f;
-                }
+                        for (int ct = 0; ct < CT; ++ct) acc[s][ct] *= f;
+                    }
+                if (late) scale_state(dec);
+            }
+        }
+        if (FULL && NBUF == 2) {  // the next chunk is staged: its scores, beside this chunk's products
+            lds_barrier();
+            if (i + 1 < chunks) scores(b ^ 1);
+        }
+        if (on) {
+            if constexpr (FULL) {
                 if (!fast) {  // the second form's intra-chunk part
 #pragma unroll
                     for (int s = 0; s < ST; ++s) {
@@ -360,10 +394,6 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                     }
                 }
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) S[nt][ct] *= dec;
             // w x, 32 tokens at a time: into y through the scores, into S through B
 #pragma unroll
             for (int ks = 0; ks < TK; ++ks) {
@@ -374,7 +404,8 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) split_to<XP>(xw[ct], 4 * hq + r, xr[ks][4 * hq + r].get(ct) * wq[r]);
+                        for (int r = 0; r < 4; r += 2)
+                            split_pair<XP>(xw[ct], 4 * hq + r, xr[ks][4 * hq + r].get(ct) * wq[r], xr[ks][4 * hq + r + 1].get(ct) * wq[r + 1]);
                 }
                 if constexpr (FULL) {
                     if (fast)
@@ -390,7 +421,7 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                 for (int nt = 0; nt < NT; ++nt) {
                     parts8<EX> a;
 #pragma unroll
-                    for (int part = 0; part < EX; ++part) load_cols(a.f[part], Bn(b, part), RN, 32 * ks, 16 * nt, g, c16);
+                    for (int part = 0; part < EX; ++part) load_cols(a.f[part], Bn(b, part), RB, 32 * ks, 16 * nt, g, c16);
                     mfma_tiles<EX, XP, 3, CT>(S[nt], a, xw);
                 }
             }
@@ -406,28 +437,40 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
 #pragma unroll
                         for (int ct = 0; ct < CT; ++ct) v[ct] = fmaf(Dh, xr[s / 2][(s % 2) * 4 + r].get(ct), acc[s][ct][r] * f[r]);
                         if (rem == L || 16 * s + 4 * g + r < rem)
-                            lanevec<TO, CT>::st(yc + (16 * s + r) * static_cast<int64_t>(y_st) + (4 * g * y_st + c16 * CT), v);
+                            lanevec<TO, CT>::st(lane_at(yc + (16 * s + r) * static_cast<int64_t>(y_st), 4 * g * y_st + c16 * CT), v);
                     }
                 }
             }
         }
+        if (i + AHEAD < chunks) fetch_x(order(i + AHEAD), xr, dtr);
         lds_barrier();
-        if (i + 1 < chunks) {
-            if (NBUF == 1) {
-                stage(0);
-                if (i + 2 < chunks) fetch(order(i + 2));
-                lds_barrier();
-            }
+        if (NBUF == 1 && i + 1 < chunks) {
+            stage(0, raw);
+            if (i + 1 + AHEAD < chunks) fetch(order(i + 1 + AHEAD), raw);
+            lds_barrier();
             if (FULL) {
-                scores(NBUF == 2 ? b ^ 1 : 0);
+                scores(0);
                 lds_barrier();
             }
-#pragma unroll
-            for (int ks = 0; ks < TK; ++ks)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) xr[ks][j] = xn[ks][j];
-            dtr = dtn;
         }
+    };
+    if (chunks > 0) {
+        fetch(order(0), rawB[0]);
+        fetch_x(order(0), xs[0], dts[0]);
+        stage(0, rawB[0]);
+        // chunk c's B and C wait in set c % AHEAD
+        if (chunks > 1) fetch(order(1), rawB[1 % AHEAD]);
+        if (AHEAD == 2 && chunks > 2) fetch(order(2), rawB[0]);
+        if (AHEAD == 2 && chunks > 1) fetch_x(order(1), xs[AHEAD - 1], dts[AHEAD - 1]);
+        lds_barrier();
+        if (FULL) {
+            scores(0);
+            lds_barrier();
+        }
+    }
+    for (int i = 0; i < chunks; i += AHEAD) {
+        body(i, xs[0], dts[0], rawB[AHEAD - 1]);
+        if (AHEAD == 2 && i + 1 < chunks) body(i + 1, xs[AHEAD - 1], dts[AHEAD - 1], rawB[0]);
     }
     if (!on) return;
     if (phase == 1) {

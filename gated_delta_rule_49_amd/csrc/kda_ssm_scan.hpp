@@ -50,6 +50,8 @@ __device__ __forceinline__ float softplus_rel(float x) {
 // smallest normal number 2^-126, and 2^(-suf) <= 2^kFastTot does not overflow
 // with values below 2^64
 constexpr float kFastTot = 56.f;
+// how far a kept state's scale may go from 1 (log2) before it is multiplied out
+constexpr double kLevel = 24.0;
 
 struct SsmScan {
     SsmParams p;
@@ -111,6 +113,45 @@ __device__ __forceinline__ void split_to(parts8<N> &o, int slot, float v) {
         o.f[i].s[slot] = h;
         if (i + 1 < N) v -= bf16_to_f32(h);
     }
+}
+
+// v minus the bf16 in the low / high half of p, exact: v_dot2c_f32_bf16 with
+// (-1, 0) and (0, -1), held in registers (as immediates the two would be
+// written with the same inline constant)
+__device__ __forceinline__ float minus_half(uint32_t p, uint32_t which, float v) {
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+    asm("" : "+s"(which));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p), __builtin_bit_cast(bf16x2, which), v, false);
+}
+__device__ __forceinline__ float minus_low(uint32_t p, float v) { return minus_half(p, 0x0000bf80u, v); }
+__device__ __forceinline__ float minus_high(uint32_t p, float v) { return minus_half(p, 0xbf800000u, v); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {  // one v_cvt_pk_bf16_f32
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+// two neighbouring slots at once: one conversion and two subtractions a part
+template <int N>
+__device__ __forceinline__ void split_pair(parts8<N> &o, int slot, float v0, float v1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t p = pack_bf16(v0, v1);
+        o.f[i].w[slot / 2] = p;
+        if (i + 1 < N) {
+            v0 = minus_low(p, v0);
+            v1 = minus_high(p, v1);
+        }
+    }
+}
+
+// base (uniform) plus a lane's offset in elements, as a 32-bit byte offset.
+// The empty statement keeps the base in scalar registers: rows a stride apart
+// would otherwise become a chain of 64-bit vector additions.
+template <typename T>
+__device__ __forceinline__ T *lane_at(T *base, uint32_t elements) {
+    typedef __attribute__((address_space(1))) char global_char;
+    uint64_t at = reinterpret_cast<uint64_t>(base);
+    asm("" : "+s"(at));
+    return (T *)((global_char *)at + elements * static_cast<uint32_t>(sizeof(T)));
 }
 
 // c += A B over the parts' products whose orders add up to less than ORD
@@ -224,7 +265,7 @@ template <> struct lanevec<bf16_t, 2> {
     __device__ __forceinline__ void zero() { u = 0; }
     __device__ __forceinline__ float get(int c) const { return __uint_as_float(c ? (u & 0xffff0000u) : (u << 16)); }
     __device__ __forceinline__ static void st(bf16_t *p, const float (&v)[2]) {
-        *reinterpret_cast<uint32_t *>(p) = static_cast<uint32_t>(f32_to_bf16(v[0])) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
+        *reinterpret_cast<uint32_t *>(p) = pack_bf16(v[0], v[1]);
     }
 };
 template <> struct lanevec<float, 1> {
