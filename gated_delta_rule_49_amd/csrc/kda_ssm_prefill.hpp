@@ -45,8 +45,9 @@ struct ScanCfg {
     static constexpr size_t BYTES = sizeof(bf16_t) * NBUF * BUF + sizeof(float) * NW * WV;
 };
 
+// at most two waves a SIMD (the LDS holds one workgroup): all registers of two
 template <typename TI, typename TO, int NS, int PW, int NW, int MODE>
-__global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks_per_group, int phase) {
+__global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) ssm_scan_kernel(SsmScan q, int blocks_per_group, int phase) {
     using Cf = ScanCfg<TI, TO, NS, PW, NW, MODE>;
     constexpr int EX = Cf::EX, L = Cf::L, ORD = Cf::ORD, XP = Cf::XP, GP = Cf::GP, SP = Cf::SP, NT = Cf::NT, KS = Cf::KS;
     constexpr int CT = Cf::CT, ST = Cf::ST, TK = Cf::TK, RN = Cf::RN, RB = Cf::RB, RT = Cf::RT, NBUF = Cf::NBUF;
@@ -151,30 +152,30 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
     constexpr int BLOCKS = (L / 4) * (NS / 4), PER = (BLOCKS + 64 * NW - 1) / (64 * NW);
     constexpr int AHEAD = FULL ? 1 : 2;  // chunks between a request and its use: the states alone are a short iteration
     quad<TI> rawB[AHEAD][PER], rawC[FULL ? PER : 1];
-    auto fetch_rows = [&](quad<TI> (&raw)[PER], const TI *base, int64_t stride, int c) {
-        const int rem = min(sg.len - c * L, L);
-        const TI *cbase = base + c * L * stride;
-        const uint32_t st = static_cast<uint32_t>(stride);
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            const int i = tid + k * 64 * NW;
-            const uint32_t tq = i / (NS / 4), nq = i % (NS / 4);
-            if (BLOCKS % (64 * NW) == 0 || i < BLOCKS) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    if (rem == L) {
-                        raw[k].ld(r, lane_at(cbase + r * stride, 4 * tq * st + 4 * nq));
-                    } else {
-                        raw[k].ld(r, lane_at(cbase, min(4 * tq + r, rem - 1u) * st + 4 * nq));
-                        asm volatile("");
-                    }
-                }
-            }
-        }
-    };
     auto fetch = [&](int c, quad<TI> (&raw)[PER]) {
-        fetch_rows(raw, bb, p.b_st, c);
-        if constexpr (FULL) fetch_rows(rawC, cb, p.c_st, c);
+        const int rem = min(sg.len - c * L, L);
+        const TI *b0 = bb + static_cast<int64_t>(c) * L * p.b_st, *c0 = cb + static_cast<int64_t>(c) * L * p.c_st;
+        const uint32_t bs = static_cast<uint32_t>(p.b_st), cs = static_cast<uint32_t>(p.c_st);
+        auto each = [&](auto &&row) {
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const uint32_t i = min(tid + k * 64 * NW, BLOCKS - 1);  // the threads to spare repeat the last block
+#pragma unroll
+                for (int r = 0; r < 4; ++r) row(k, r, 4 * (i / (NS / 4)), 4 * (i % (NS / 4)));
+            }
+        };
+        if (rem == L) {
+            each([&](int k, int r, uint32_t t, uint32_t n) {
+                raw[k].ld(r, lane_at(b0 + r * p.b_st, t * bs + n));
+                if constexpr (FULL) rawC[k].ld(r, lane_at(c0 + r * p.c_st, t * cs + n));
+            });
+        } else {
+            each([&](int k, int r, uint32_t t, uint32_t n) {
+                raw[k].ld(r, lane_at(b0, min(t + r, rem - 1u) * bs + n));
+                if constexpr (FULL) rawC[k].ld(r, lane_at(c0, min(t + r, rem - 1u) * cs + n));
+            });
+            asm volatile("");  // keeps the two branches' requests apart, each with its own addresses
+        }
     };
     auto stage = [&](int b, const quad<TI> (&raw)[PER]) {
 #pragma unroll
@@ -227,9 +228,11 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
     // its own number in the reverse mode (sums from the chunk's start are
     // wanted), else counted from the chunk's end
     lanevec<TI, CT> xs[AHEAD][TK][8];
-    TI dts[AHEAD];
+    // held in 32 bits: a 16-bit one would be copied, and waited for, at its load
+    typedef typename std::conditional<Cf::BF, uint32_t, float>::type Step;
+    Step dts[AHEAD];
     auto token = [&] { return REV ? tid & 63 : L - 1 - (tid & 63); };
-    auto fetch_x = [&](int c, lanevec<TI, CT> (&xv)[TK][8], TI &d) {
+    auto fetch_x = [&](int c, lanevec<TI, CT> (&xv)[TK][8], Step &d) {
         const int rem = min(sg.len - c * L, L);
         const TI *base = xb + static_cast<int64_t>(c) * L * p.x_st;
         if (rem == L) {
@@ -243,24 +246,26 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
             for (int ks = 0; ks < TK; ++ks)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) xv[ks][j].ld(lane_at(base, min(32 * ks + kperm(g, j), rem - 1) * x_st + c16 * CT));
-            asm volatile("");  // keeps the two branches' loads apart, each with its own addresses
+            asm volatile("");
         }
         d = *lane_at(dtb + static_cast<int64_t>(c) * L * p.H, max(0, min(token(), rem - 1)) * p.H);
     };
 
     const int chunks = (sg.len + L - 1) / L;
     float seg_log = 0.f;
-    auto order = [&](int i) { return REV ? chunks - 1 - i : i; };
-    auto body = [&](int i, lanevec<TI, CT> (&xr)[TK][8], TI &dtr, quad<TI> (&raw)[PER]) {
+    // the i-th chunk of the walk; past the end the last one again: requests are
+    // made on every path, so that a wait can count those made after it
+    auto order = [&](int i) { return REV ? max(chunks - 1 - i, 0) : min(i, chunks - 1); };
+    auto body = [&](int i, lanevec<TI, CT> (&xr)[TK][8], Step &dtr, quad<TI> (&raw)[PER]) {
         const int b = NBUF == 2 ? i & 1 : 0;
         const int t0 = order(i) * L, rem = min(sg.len - t0, L);
         // what follows from the lane's place is computed again in every
         // iteration: kept over the loop it would push the tiles out of the
         // registers, and every spill waits for all loads in flight
         asm volatile("" : "+v"(g), "+v"(c16), "+v"(tid));
-        if (NBUF == 2 && i + 1 < chunks) {  // the next chunk into the other buffer
+        if (NBUF == 2) {  // the next chunk into the other buffer
             stage(b ^ 1, raw);
-            if (i + 1 + AHEAD < chunks) fetch(order(i + 1 + AHEAD), raw);
+            fetch(order(i + 1 + AHEAD), raw);
         }
         float dec = 1.f;
         bool fast = true, late = false;
@@ -271,7 +276,9 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                 store_state(p.chunk_states + ((static_cast<int64_t>(sg.chunk + t0 / 64) * (64 / q.state_chunk) + t0 % 64 / q.state_chunk) * p.H + h) * per_head + pw0);
             // decays, one token a lane
             const int tok = token(), lane = tid & 63;
-            float dt = io<TI>::ld(&dtr, 0) + bias;
+            float dt;
+            if constexpr (Cf::BF) dt = __uint_as_float(dtr << 16) + bias;
+            else dt = dtr + bias;
             if (p.softplus) dt = softplus_rel(dt);
             if (tok < 0 || tok >= rem) dt = 0.f;
             const float la = A2 * dt;
@@ -417,12 +424,24 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                             mfma_tiles<GP, XP, ORD, CT>(acc[s], a, xw);
                         }
                 }
+                // several tiles' operands requested together, and their products
+                // taken part by part: no instruction waits for the one before
+                constexpr int NG = EX == 1 ? (NT < 8 ? NT : 8) : 1;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    parts8<EX> a;
+                for (int n0 = 0; n0 < NT; n0 += NG) {
+                    parts8<EX> a[NG];
 #pragma unroll
-                    for (int part = 0; part < EX; ++part) load_cols(a.f[part], Bn(b, part), RB, 32 * ks, 16 * nt, g, c16);
-                    mfma_tiles<EX, XP, 3, CT>(S[nt], a, xw);
+                    for (int k = 0; k < NG; ++k)
+#pragma unroll
+                        for (int part = 0; part < EX; ++part) load_cols(a[k].f[part], Bn(b, part), RB, 32 * ks, 16 * (n0 + k), g, c16);
+#pragma unroll
+                    for (int i0 = 0; i0 < EX; ++i0)
+#pragma unroll
+                        for (int j0 = 0; i0 + j0 < 3 && j0 < XP; ++j0)
+#pragma unroll
+                            for (int k = 0; k < NG; ++k)
+#pragma unroll
+                                for (int ct = 0; ct < CT; ++ct) S[n0 + k][ct] = mfma16(a[k].f[i0].v, xw[ct].f[j0].v, S[n0 + k][ct]);
                 }
             }
             if constexpr (FULL) {  // y: slot (s % 2) 4 + r of x's step s / 2 is the same row
@@ -442,11 +461,11 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
                 }
             }
         }
-        if (i + AHEAD < chunks) fetch_x(order(i + AHEAD), xr, dtr);
+        fetch_x(order(i + AHEAD), xr, dtr);
         lds_barrier();
         if (NBUF == 1 && i + 1 < chunks) {
             stage(0, raw);
-            if (i + 1 + AHEAD < chunks) fetch(order(i + 1 + AHEAD), raw);
+            fetch(order(i + 1 + AHEAD), raw);
             lds_barrier();
             if (FULL) {
                 scores(0);
@@ -459,9 +478,9 @@ __global__ void __launch_bounds__(64 * NW) ssm_scan_kernel(SsmScan q, int blocks
         fetch_x(order(0), xs[0], dts[0]);
         stage(0, rawB[0]);
         // chunk c's B and C wait in set c % AHEAD
-        if (chunks > 1) fetch(order(1), rawB[1 % AHEAD]);
-        if (AHEAD == 2 && chunks > 2) fetch(order(2), rawB[0]);
-        if (AHEAD == 2 && chunks > 1) fetch_x(order(1), xs[AHEAD - 1], dts[AHEAD - 1]);
+        fetch(order(1), rawB[1 % AHEAD]);
+        if (AHEAD == 2) fetch(order(2), rawB[0]);
+        if (AHEAD == 2) fetch_x(order(1), xs[AHEAD - 1], dts[AHEAD - 1]);
         lds_barrier();
         if (FULL) {
             scores(0);
