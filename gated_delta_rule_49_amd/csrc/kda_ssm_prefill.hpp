@@ -148,7 +148,9 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
 
     // Staging of a chunk's B and C: a thread takes 4 tokens by 4 channels.
     // Rows past the segment repeat its last one: their step size is 0, so
-    // whatever they hold meets a factor of 0 or a row that is not stored.
+    // whatever they hold meets a factor of 0 or a row that is not stored.  Rows
+    // are clamped rather than branched on: a wait behind a branch counts no
+    // request made inside.  Strides are below 2^23: a 24-bit product.
     constexpr int BLOCKS = (L / 4) * (NS / 4), PER = (BLOCKS + 64 * NW - 1) / (64 * NW);
     constexpr int AHEAD = FULL ? 1 : 2;  // chunks between a request and its use: the states alone are a short iteration
     quad<TI> rawB[AHEAD][PER], rawC[FULL ? PER : 1];
@@ -156,25 +158,16 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
         const int rem = min(sg.len - c * L, L);
         const TI *b0 = bb + static_cast<int64_t>(c) * L * p.b_st, *c0 = cb + static_cast<int64_t>(c) * L * p.c_st;
         const uint32_t bs = static_cast<uint32_t>(p.b_st), cs = static_cast<uint32_t>(p.c_st);
-        auto each = [&](auto &&row) {
 #pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                const uint32_t i = min(tid + k * 64 * NW, BLOCKS - 1);  // the threads to spare repeat the last block
+        for (int k = 0; k < PER; ++k) {
+            const uint32_t i = min(tid + k * 64 * NW, BLOCKS - 1);  // the threads to spare repeat the last block
+            const uint32_t t = 4 * (i / (NS / 4)), n = 4 * (i % (NS / 4));
 #pragma unroll
-                for (int r = 0; r < 4; ++r) row(k, r, 4 * (i / (NS / 4)), 4 * (i % (NS / 4)));
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t row = min(t + r, rem - 1u);
+                raw[k].ld(r, lane_at(b0, __umul24(row, bs) + n));
+                if constexpr (FULL) rawC[k].ld(r, lane_at(c0, __umul24(row, cs) + n));
             }
-        };
-        if (rem == L) {
-            each([&](int k, int r, uint32_t t, uint32_t n) {
-                raw[k].ld(r, lane_at(b0 + r * p.b_st, t * bs + n));
-                if constexpr (FULL) rawC[k].ld(r, lane_at(c0 + r * p.c_st, t * cs + n));
-            });
-        } else {
-            each([&](int k, int r, uint32_t t, uint32_t n) {
-                raw[k].ld(r, lane_at(b0, min(t + r, rem - 1u) * bs + n));
-                if constexpr (FULL) rawC[k].ld(r, lane_at(c0, min(t + r, rem - 1u) * cs + n));
-            });
-            asm volatile("");  // keeps the two branches' requests apart, each with its own addresses
         }
     };
     auto stage = [&](int b, const quad<TI> (&raw)[PER]) {
@@ -228,49 +221,69 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
     // its own number in the reverse mode (sums from the chunk's start are
     // wanted), else counted from the chunk's end
     lanevec<TI, CT> xs[AHEAD][TK][8];
-    // held in 32 bits: a 16-bit one would be copied, and waited for, at its load
     typedef typename std::conditional<Cf::BF, uint32_t, float>::type Step;
-    Step dts[AHEAD];
+    Step dts[AHEAD] = {};
     auto token = [&] { return REV ? tid & 63 : L - 1 - (tid & 63); };
-    auto fetch_x = [&](int c, lanevec<TI, CT> (&xv)[TK][8], Step &d) {
+    auto fetch_dt = [&](int c, Step &d) {
         const int rem = min(sg.len - c * L, L);
-        const TI *base = xb + static_cast<int64_t>(c) * L * p.x_st;
-        if (rem == L) {
-            const uint32_t off = 4 * g * x_st + c16 * CT;
-#pragma unroll
-            for (int ks = 0; ks < TK; ++ks)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) xv[ks][j].ld(lane_at(base + (32 * ks + kperm(0, j)) * static_cast<int64_t>(x_st), off));
-        } else {
-#pragma unroll
-            for (int ks = 0; ks < TK; ++ks)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) xv[ks][j].ld(lane_at(base, min(32 * ks + kperm(g, j), rem - 1) * x_st + c16 * CT));
-            asm volatile("");
-        }
         d = *lane_at(dtb + static_cast<int64_t>(c) * L * p.H, max(0, min(token(), rem - 1)) * p.H);
     };
+    auto fetch_x = [&](int c, lanevec<TI, CT> (&xv)[TK][8]) {
+        const int rem = min(sg.len - c * L, L);
+        const TI *base = xb + static_cast<int64_t>(c) * L * p.x_st;
+#pragma unroll
+        for (int ks = 0; ks < TK; ++ks)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) xv[ks][j].ld(lane_at(base, __umul24(min(32 * ks + kperm(g, j), rem - 1), x_st) + c16 * CT));
+    };
 
-    const int chunks = (sg.len + L - 1) / L;
+    const int chunks = __builtin_amdgcn_readfirstlane((sg.len + L - 1) / L);
     float seg_log = 0.f;
     // the i-th chunk of the walk; past the end the last one again: requests are
     // made on every path, so that a wait can count those made after it
     auto order = [&](int i) { return REV ? max(chunks - 1 - i, 0) : min(i, chunks - 1); };
-    auto body = [&](int i, lanevec<TI, CT> (&xr)[TK][8], Step &dtr, quad<TI> (&raw)[PER]) {
-        const int b = NBUF == 2 ? i & 1 : 0;
-        const int t0 = order(i) * L, rem = min(sg.len - t0, L);
+    // the shared part of a chunk's step, before and after a wave's own: all
+    // waves stage B and C and take a part of the scores
+    auto request = [&](int i, quad<TI> (&raw)[PER]) {
         // what follows from the lane's place is computed again in every
         // iteration: kept over the loop it would push the tiles out of the
         // registers, and every spill waits for all loads in flight
         asm volatile("" : "+v"(g), "+v"(c16), "+v"(tid));
         if (NBUF == 2) {  // the next chunk into the other buffer
-            stage(b ^ 1, raw);
+            stage((i & 1) ^ 1, raw);
             fetch(order(i + 1 + AHEAD), raw);
         }
+    };
+    auto score = [&](int i) {
+        if (FULL && NBUF == 2) {  // the next chunk is staged: its scores, beside this chunk's products
+            lds_barrier();
+            if (i + 1 < chunks) scores((i & 1) ^ 1);
+        }
+    };
+    auto finish = [&](int i, quad<TI> (&raw)[PER]) {
+        lds_barrier();
+        if (NBUF == 1 && i + 1 < chunks) {
+            stage(0, raw);
+            fetch(order(i + 1 + AHEAD), raw);
+            lds_barrier();
+            if (FULL) {
+                scores(0);
+                lds_barrier();
+            }
+        }
+    };
+    // Whole chunks (WHOLE) take no branch around a store: behind one, a wait for
+    // an older load would have to count on the stores not having been made, and
+    // so wait for them too.
+    auto body = [&](auto whole, int i, lanevec<TI, CT> (&xr)[TK][8], Step &dtr, quad<TI> (&raw)[PER]) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        const int b = NBUF == 2 ? i & 1 : 0;
+        const int t0 = order(i) * L, rem = WHOLE ? L : min(sg.len - t0, L);
+        request(i, raw);
         float dec = 1.f;
         bool fast = true, late = false;
         f32x4 acc[FULL ? ST : 1][CT];
-        if (on) {
+        {
             // the state entering the chunk (from the right in the reverse order)
             if (phase == 2 && p.chunk_states && t0 % q.state_chunk == 0)
                 store_state(p.chunk_states + ((static_cast<int64_t>(sg.chunk + t0 / 64) * (64 / q.state_chunk) + t0 % 64 / q.state_chunk) * p.H + h) * per_head + pw0);
@@ -279,6 +292,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
             float dt;
             if constexpr (Cf::BF) dt = __uint_as_float(dtr << 16) + bias;
             else dt = dtr + bias;
+            fetch_dt(order(i + AHEAD), dtr);
             if (p.softplus) dt = softplus_rel(dt);
             if (tok < 0 || tok >= rem) dt = 0.f;
             const float la = A2 * dt;
@@ -350,11 +364,8 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
                 if (late) scale_state(dec);
             }
         }
-        if (FULL && NBUF == 2) {  // the next chunk is staged: its scores, beside this chunk's products
-            lds_barrier();
-            if (i + 1 < chunks) scores(b ^ 1);
-        }
-        if (on) {
+        score(i);
+        {
             if constexpr (FULL) {
                 if (!fast) {  // the second form's intra-chunk part
 #pragma unroll
@@ -455,43 +466,65 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
                         float v[CT];
 #pragma unroll
                         for (int ct = 0; ct < CT; ++ct) v[ct] = fmaf(Dh, xr[s / 2][(s % 2) * 4 + r].get(ct), acc[s][ct][r] * f[r]);
-                        if (rem == L || 16 * s + 4 * g + r < rem)
+                        if (WHOLE || 16 * s + 4 * g + r < rem)
                             lanevec<TO, CT>::st(lane_at(yc + (16 * s + r) * static_cast<int64_t>(y_st), 4 * g * y_st + c16 * CT), v);
                     }
                 }
             }
         }
-        fetch_x(order(i + AHEAD), xr, dtr);
-        lds_barrier();
-        if (NBUF == 1 && i + 1 < chunks) {
-            stage(0, raw);
-            fetch(order(i + 1 + AHEAD), raw);
-            lds_barrier();
-            if (FULL) {
-                scores(0);
-                lds_barrier();
-            }
-        }
+        fetch_x(order(i + AHEAD), xr);
+        finish(i, raw);
     };
     if (chunks > 0) {
         fetch(order(0), rawB[0]);
-        fetch_x(order(0), xs[0], dts[0]);
+        fetch_dt(order(0), dts[0]);
+        fetch_x(order(0), xs[0]);
+        __builtin_amdgcn_sched_barrier(0);  // in the order of their use: a wait in the loop counts from the worse of both ways in
         stage(0, rawB[0]);
         // chunk c's B and C wait in set c % AHEAD
         fetch(order(1), rawB[1 % AHEAD]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (AHEAD == 2) {
+            fetch_dt(order(1), dts[AHEAD - 1]);
+            fetch_x(order(1), xs[AHEAD - 1]);
+        }
         if (AHEAD == 2) fetch(order(2), rawB[0]);
-        if (AHEAD == 2) fetch_x(order(1), xs[AHEAD - 1], dts[AHEAD - 1]);
         lds_barrier();
         if (FULL) {
             scores(0);
             lds_barrier();
         }
     }
-    for (int i = 0; i < chunks; i += AHEAD) {
-        body(i, xs[0], dts[0], rawB[AHEAD - 1]);
-        if (AHEAD == 2 && i + 1 < chunks) body(i + 1, xs[AHEAD - 1], dts[AHEAD - 1], rawB[0]);
+    // kept from the compiler that they too are extended 16-bit values: it would
+    // carry 16 bits around the loop, extend them at its end, and wait for the
+    // loads just made to do so
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) asm volatile("" : "+v"(dts[k]));
+    if (!on) {  // as many barriers as the others
+        auto step = [&](int i, quad<TI> (&raw)[PER]) {
+            request(i, raw);
+            score(i);
+            finish(i, raw);
+        };
+        for (int i = 0; i < chunks; i += AHEAD) {
+            step(i, rawB[AHEAD - 1]);
+            if (AHEAD == 2 && i + 1 < chunks) step(i + 1, rawB[0]);
+        }
+        return;
     }
-    if (!on) return;
+    int i = 0;
+    if constexpr (FULL) {
+        for (const int whole = sg.len / L; i < whole; ++i) body(std::true_type{}, i, xs[0], dts[0], rawB[0]);
+        if (i < chunks) body(std::false_type{}, i, xs[0], dts[0], rawB[0]);
+    } else {
+        for (;;) {
+            if (i >= chunks) break;
+            body(std::false_type{}, i, xs[0], dts[0], rawB[AHEAD - 1]);
+            if (++i >= chunks) break;
+            body(std::false_type{}, i, xs[AHEAD - 1], dts[AHEAD - 1], rawB[0]);
+            ++i;
+        }
+    }
     if (phase == 1) {
         store_state(q.seg_state + (static_cast<int64_t>(x_seg) * p.H + h) * per_head + pw0);
         if (pc == 0 && g == 0) q.seg_log[static_cast<int64_t>(x_seg) * p.H + h] = seg_log;
