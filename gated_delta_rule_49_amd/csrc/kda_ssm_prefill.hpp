@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
     // Rows past the segment repeat its last one: their step size is 0, so
     // whatever they hold meets a factor of 0 or a row that is not stored.  Rows
     // are clamped rather than branched on: a wait behind a branch counts no
-    // request made inside.  Strides are below 2^23: a 24-bit product.
+    // request made inside.
     constexpr int BLOCKS = (L / 4) * (NS / 4), PER = (BLOCKS + 64 * NW - 1) / (64 * NW);
     constexpr int AHEAD = FULL ? 1 : 2;  // chunks between a request and its use: the states alone are a short iteration
     quad<TI> rawB[AHEAD][PER], rawC[FULL ? PER : 1];
@@ -161,12 +161,11 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const uint32_t i = min(tid + k * 64 * NW, BLOCKS - 1);  // the threads to spare repeat the last block
-            const uint32_t t = 4 * (i / (NS / 4)), n = 4 * (i % (NS / 4));
+            const uint32_t t = 4 * (i / (NS / 4)), n = 4 * (i % (NS / 4)), bt = t * bs, ct = t * cs;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const uint32_t row = min(t + r, rem - 1u);
-                raw[k].ld(r, lane_at(b0, __umul24(row, bs) + n));
-                if constexpr (FULL) rawC[k].ld(r, lane_at(c0, __umul24(row, cs) + n));
+                raw[k].ld(r, lane_at(b0, min(bt + r * bs, (rem - 1) * bs) + n));
+                if constexpr (FULL) rawC[k].ld(r, lane_at(c0, min(ct + r * cs, (rem - 1) * cs) + n));
             }
         }
     };
@@ -222,19 +221,28 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
     // wanted), else counted from the chunk's end
     lanevec<TI, CT> xs[AHEAD][TK][8];
     typedef typename std::conditional<Cf::BF, uint32_t, float>::type Step;
-    Step dts[AHEAD] = {};
+    float dt_next;  // of the chunk to come
     auto token = [&] { return REV ? tid & 63 : L - 1 - (tid & 63); };
     auto fetch_dt = [&](int c, Step &d) {
         const int rem = min(sg.len - c * L, L);
         d = *lane_at(dtb + static_cast<int64_t>(c) * L * p.H, max(0, min(token(), rem - 1)) * p.H);
     };
+    // The step sizes requested at a chunk's start are taken up at its end: a
+    // 16-bit value carried into the next iteration would be widened, and waited
+    // for, wherever the compiler likes.
+    auto take_dt = [&](Step &d) {
+        asm volatile("" : "+v"(d));
+        if constexpr (Cf::BF) dt_next = __uint_as_float(d << 16);
+        else dt_next = d;
+    };
     auto fetch_x = [&](int c, lanevec<TI, CT> (&xv)[TK][8]) {
         const int rem = min(sg.len - c * L, L);
         const TI *base = xb + static_cast<int64_t>(c) * L * p.x_st;
+        const uint32_t row = 4 * g * x_st, last = (rem - 1) * x_st;
 #pragma unroll
         for (int ks = 0; ks < TK; ++ks)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) xv[ks][j].ld(lane_at(base, __umul24(min(32 * ks + kperm(g, j), rem - 1), x_st) + c16 * CT));
+            for (int j = 0; j < 8; ++j) xv[ks][j].ld(lane_at(base, min(row + (32 * ks + kperm(0, j)) * x_st, last) + c16 * CT));
     };
 
     const int chunks = __builtin_amdgcn_readfirstlane((sg.len + L - 1) / L);
@@ -275,24 +283,23 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
     // Whole chunks (WHOLE) take no branch around a store: behind one, a wait for
     // an older load would have to count on the stores not having been made, and
     // so wait for them too.
-    auto body = [&](auto whole, int i, lanevec<TI, CT> (&xr)[TK][8], Step &dtr, quad<TI> (&raw)[PER]) {
+    auto body = [&](auto whole, int i, lanevec<TI, CT> (&xr)[TK][8], quad<TI> (&raw)[PER]) {
         constexpr bool WHOLE = decltype(whole)::value;
         const int b = NBUF == 2 ? i & 1 : 0;
-        const int t0 = order(i) * L, rem = WHOLE ? L : min(sg.len - t0, L);
+        const int t0 = order(i) * L, rem = WHOLE ? L : i < chunks ? min(sg.len - t0, L) : 0;
+        Step d;
+        fetch_dt(order(i + 1), d);
         request(i, raw);
         float dec = 1.f;
         bool fast = true, late = false;
         f32x4 acc[FULL ? ST : 1][CT];
         {
             // the state entering the chunk (from the right in the reverse order)
-            if (phase == 2 && p.chunk_states && t0 % q.state_chunk == 0)
+            if (phase == 2 && p.chunk_states && i < chunks && t0 % q.state_chunk == 0)
                 store_state(p.chunk_states + ((static_cast<int64_t>(sg.chunk + t0 / 64) * (64 / q.state_chunk) + t0 % 64 / q.state_chunk) * p.H + h) * per_head + pw0);
             // decays, one token a lane
             const int tok = token(), lane = tid & 63;
-            float dt;
-            if constexpr (Cf::BF) dt = __uint_as_float(dtr << 16) + bias;
-            else dt = dtr + bias;
-            fetch_dt(order(i + AHEAD), dtr);
+            float dt = dt_next + bias;
             if (p.softplus) dt = softplus_rel(dt);
             if (tok < 0 || tok >= rem) dt = 0.f;
             const float la = A2 * dt;
@@ -472,22 +479,20 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
                 }
             }
         }
+        take_dt(d);
         fetch_x(order(i + AHEAD), xr);
         finish(i, raw);
     };
     if (chunks > 0) {
         fetch(order(0), rawB[0]);
-        fetch_dt(order(0), dts[0]);
+        Step d;
+        fetch_dt(order(0), d);
+        take_dt(d);
         fetch_x(order(0), xs[0]);
-        __builtin_amdgcn_sched_barrier(0);  // in the order of their use: a wait in the loop counts from the worse of both ways in
         stage(0, rawB[0]);
         // chunk c's B and C wait in set c % AHEAD
         fetch(order(1), rawB[1 % AHEAD]);
-        __builtin_amdgcn_sched_barrier(0);
-        if (AHEAD == 2) {
-            fetch_dt(order(1), dts[AHEAD - 1]);
-            fetch_x(order(1), xs[AHEAD - 1]);
-        }
+        if (AHEAD == 2) fetch_x(order(1), xs[AHEAD - 1]);
         if (AHEAD == 2) fetch(order(2), rawB[0]);
         lds_barrier();
         if (FULL) {
@@ -495,11 +500,14 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
             lds_barrier();
         }
     }
-    // kept from the compiler that they too are extended 16-bit values: it would
-    // carry 16 bits around the loop, extend them at its end, and wait for the
-    // loads just made to do so
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k) asm volatile("" : "+v"(dts[k]));
+    // nothing is in flight where the loops are entered: their waits count from
+    // the worst of all the ways in
+    auto settle = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    settle();
     if (!on) {  // as many barriers as the others
         auto step = [&](int i, quad<TI> (&raw)[PER]) {
             request(i, raw);
@@ -508,21 +516,21 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
         };
         for (int i = 0; i < chunks; i += AHEAD) {
             step(i, rawB[AHEAD - 1]);
-            if (AHEAD == 2 && i + 1 < chunks) step(i + 1, rawB[0]);
+            if (AHEAD == 2) step(i + 1, rawB[0]);
         }
+        settle();
         return;
     }
     int i = 0;
     if constexpr (FULL) {
-        for (const int whole = sg.len / L; i < whole; ++i) body(std::true_type{}, i, xs[0], dts[0], rawB[0]);
-        if (i < chunks) body(std::false_type{}, i, xs[0], dts[0], rawB[0]);
+        for (const int whole = sg.len / L; i < whole; ++i) body(std::true_type{}, i, xs[0], rawB[0]);
+        if (i < chunks) body(std::false_type{}, i, xs[0], rawB[0]);
     } else {
-        for (;;) {
-            if (i >= chunks) break;
-            body(std::false_type{}, i, xs[0], dts[0], rawB[AHEAD - 1]);
-            if (++i >= chunks) break;
-            body(std::false_type{}, i, xs[AHEAD - 1], dts[AHEAD - 1], rawB[0]);
-            ++i;
+        // two at a time, with no exit between them that a wait would have to
+        // allow for; an odd last chunk is followed by one of no tokens
+        for (; i < chunks; i += 2) {
+            body(std::false_type{}, i, xs[0], rawB[AHEAD - 1]);
+            body(std::false_type{}, i + 1, xs[AHEAD - 1], rawB[0]);
         }
     }
     if (phase == 1) {
