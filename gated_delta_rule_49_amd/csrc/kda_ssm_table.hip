@@ -119,11 +119,15 @@ SsmPlan ssm_plan(const SsmParams &p, bool packed) {
     const int items = p.H / p.G * (p.P / pw);  // waves of a group
     r.waves = items > 4 ? 8 : 4;
     r.blocks_per_group = (items + r.waves - 1) / r.waves;
-    // About 512 workgroups, two for each CU: the second's phases fill the
-    // first's waits.  A segment has at least 4 chunks: its state is written
-    // and read once, which is the traffic of 2 chunks (d_state 128).
+    // Equal sequences: one workgroup for each of the 256 CUs, all of one length
+    // (32768 tokens, 64 heads of 64 channels, d_state 128: 121 us for phase 1 and
+    // 13 us for the chain, against 131 and 24 with 512 workgroups).  Packed ones
+    // end in segments of any length: shorter segments level them (8 sequences of
+    // 1 to 7001 tokens, d_state 64: 177 + 80 us with 512, 220 + 97 with 256).  A
+    // segment has at least 4 chunks: its state is written and read once, which
+    // is the traffic of 2 chunks (d_state 128).
     const int64_t per_seg = static_cast<int64_t>(p.G) * r.blocks_per_group;
-    int64_t k = r.chunks_bound * per_seg / 512;
+    int64_t k = packed ? r.chunks_bound * per_seg / 512 : (r.chunks_bound * per_seg + 255) / 256;
     k = std::max<int64_t>(k, 4);
     k = std::min<int64_t>(k, std::max(1, r.chunks_per_seq));
     r.seg_chunks = static_cast<int32_t>(k);
