@@ -5,67 +5,55 @@
 //     d_initial: the same sum as dx at the W - 1 places before the sequence.
 // act'(pre) = s + pre s (1 - s) with s = sigmoid(pre); pre is recomputed.
 //
-// HBM-bound: x and dy are read once and dx written once.  A thread owns CPT
-// consecutive channels (8, or 4 for W > 4 where the windows would not fit the
-// registers) and walks TT consecutive tokens with the last W - 1 inputs and
-// the W unfinished sums of dx in registers: g_t adds w_j g_t to the sum of
-// the token W - 1 - j places back, and the oldest sum is complete.  It walks
-// W - 1 tokens past its tile to finish the tile's sums (x and dy of those
-// come from L2: the neighbouring thread reads them too).  The sums over
+// HBM-bound: x and dy are read once and dx written once.  A thread owns 4
+// neighbouring channels and walks a tile of consecutive tokens with the last
+// W - 1 inputs and the W unfinished sums of dx in registers: g_t adds w_j g_t
+// to the sum of the token W - 1 - j places back, and the oldest sum is
+// complete.  It walks W - 1 tokens past its tile to finish the tile's sums (x
+// and dy of those come from L2: the neighbouring thread reads them too).  Four
+// tokens are requested while the four before are worked on, and tokens whose
+// windows lie inside one sequence take a path without branches.  The sums over
 // tokens of dw and dbias stay in registers, the threads of a workgroup that
-// share channels add theirs through LDS, and every workgroup writes one
-// row of partial sums; a second kernel adds the rows in order.
+// share channels add theirs through LDS, and every workgroup writes one row of
+// partial sums; a second kernel adds the rows in order.
+//
+// 2 x 4096 tokens of 4096 bf16 channels, W = 4, SiLU: 53 us for this kernel
+// (3.8 TB/s; a copy of the same bytes takes 39), 61 in all.  8 channels a
+// thread with 16-byte requests took 68 (229 registers, 2 waves a SIMD; 4
+// channels need 144), tiles of 32 tokens 60; held to 128 registers it spills
+// (120).  What is left is the issue rate: about 30 instructions a value.
 #include "kda_launch.hpp"
 
 namespace kda {
 
 namespace {
 
-constexpr int CG_THREADS = 256;
+constexpr int CG_THREADS = 256, CPT = 4;
 
-template <typename T, int CPT> struct chvec;
-template <int CPT> struct chvec<bf16_t, CPT> {
-    uint32_t u[CPT / 2];
-    __device__ __forceinline__ void ld(const bf16_t *p) {
-        if constexpr (CPT == 8) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p);
-            u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
-        } else {
-            const uint2 v = *reinterpret_cast<const uint2 *>(p);
-            u[0] = v.x; u[1] = v.y;
-        }
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < CPT / 2; ++i) u[i] = 0;
-    }
+template <typename T> struct chvec;  // CPT channels
+template <> struct chvec<bf16_t> {
+    uint2 u;
+    __device__ __forceinline__ void ld(const bf16_t *p) { u = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
     __device__ __forceinline__ float get(int c) const {
-        return __uint_as_float((c & 1) ? (u[c / 2] & 0xffff0000u) : (u[c / 2] << 16));
+        const uint32_t w = c < 2 ? u.x : u.y;
+        return __uint_as_float((c & 1) ? (w & 0xffff0000u) : (w << 16));
     }
     __device__ __forceinline__ static void st(bf16_t *p, const float (&v)[CPT]) {
-        uint32_t w[CPT / 2];
+        uint32_t w[2];
 #pragma unroll
-        for (int i = 0; i < CPT / 2; ++i)
+        for (int i = 0; i < 2; ++i)
             w[i] = static_cast<uint32_t>(f32_to_bf16(v[2 * i])) | (static_cast<uint32_t>(f32_to_bf16(v[2 * i + 1])) << 16);
-        if constexpr (CPT == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     }
 };
-template <int CPT> struct chvec<float, CPT> {
-    f32x4 u[CPT / 4];
-    __device__ __forceinline__ void ld(const float *p) {
-#pragma unroll
-        for (int i = 0; i < CPT / 4; ++i) u[i] = reinterpret_cast<const f32x4 *>(p)[i];
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < CPT / 4; ++i) u[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    __device__ __forceinline__ float get(int c) const { return u[c / 4][c % 4]; }
+template <> struct chvec<float> {
+    f32x4 u;
+    __device__ __forceinline__ void ld(const float *p) { u = *reinterpret_cast<const f32x4 *>(p); }
+    __device__ __forceinline__ void zero() { u = f32x4{0.f, 0.f, 0.f, 0.f}; }
+    __device__ __forceinline__ float get(int c) const { return u[c]; }
     __device__ __forceinline__ static void st(float *p, const float (&v)[CPT]) {
-#pragma unroll
-        for (int i = 0; i < CPT / 4; ++i)
-            reinterpret_cast<f32x4 *>(p)[i] = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+        *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
     }
 };
 
@@ -107,7 +95,7 @@ __device__ __forceinline__ float before_start(const ConvGradParams &p, int n, in
 
 // LG threads side by side on channel vectors, CG_THREADS / LG tiles of tt
 // tokens one below the other.
-template <typename TI, typename TG, int W, int CPT>
+template <typename TI, typename TG, int W>
 __global__ void __launch_bounds__(CG_THREADS) conv_grad_kernel(ConvGradParams p, int LG, int tt, int cols) {
     constexpr int HW = W - 1;
     extern __shared__ float red[];  // [waves][CPT (W + 1)][LG] at the end
@@ -135,7 +123,7 @@ __global__ void __launch_bounds__(CG_THREADS) conv_grad_kernel(ConvGradParams p,
 #pragma unroll
         for (int j = 0; j < HW; ++j) {
             const int pos = t0 - HW + j;
-            chvec<TI, CPT> v;
+            chvec<TI> v;
             v.zero();
             if (pos >= sq.start) v.ld(x + static_cast<int64_t>(pos) * p.C + c0);
 #pragma unroll
@@ -146,18 +134,56 @@ __global__ void __launch_bounds__(CG_THREADS) conv_grad_kernel(ConvGradParams p,
 #pragma unroll
             for (int j = 0; j < W; ++j) acc[c][j] = 0.f;
         const int t_end = t1 + HW;  // the last W - 1 steps only finish sums
-        constexpr int U = 4;        // tokens whose x and dy are requested together
-        for (int tb = t0; tb < t_end; tb += U) {
-            chvec<TI, CPT> xv[U];
-            chvec<TG, CPT> gv[U];
+        constexpr int U = 4;        // tokens whose x and dy are requested together, ahead of their use
+        chvec<TI> xv[U], xn[U];
+        chvec<TG> gv[U], gn[U];
+        auto request = [&](int tb, chvec<TI> (&xq)[U], chvec<TG> (&gq)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                xv[u].zero(); gv[u].zero();
-                if (tb + u < min(t_end, ntok)) {
-                    xv[u].ld(x + static_cast<int64_t>(tb + u) * p.C + c0);
-                    gv[u].ld(dy + static_cast<int64_t>(tb + u) * p.C + c0);
-                }
+                const int64_t at = static_cast<int64_t>(min(tb + u, ntok - 1)) * p.C + c0;  // past the end g is set to 0
+                xq[u].ld(x + at);
+                gq[u].ld(dy + at);
             }
+        };
+        request(t0, xv, gv);
+        for (int tb = t0; tb < t_end; tb += U) {
+            request(tb + U, xn, gn);
+            if (tb + U <= min(t1, sq.end) && tb - sq.start >= HW) {
+                // own tokens of one sequence, whose windows lie inside it; its
+                // end, where d_final is added, is W - 1 tokens off
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+#pragma unroll
+                    for (int c = 0; c < CPT; ++c) {
+                        xs[c][HW] = xv[u].get(c);
+                        float pre = bias[c];
+#pragma unroll
+                        for (int j = 0; j < W; ++j) pre = fmaf(w[c][j], xs[c][j], pre);
+                        const float g = through_act(pre, gv[u].get(c), p.silu);
+                        db[c] += g;
+#pragma unroll
+                        for (int j = 0; j < W; ++j) {
+                            dw[c][j] = fmaf(g, xs[c][j], dw[c][j]);
+                            acc[c][j] = fmaf(w[c][j], g, acc[c][j]);
+                        }
+                    }
+                    if (tb + u - HW >= t0) {
+                        float out[CPT];
+#pragma unroll
+                        for (int c = 0; c < CPT; ++c) out[c] = acc[c][0];
+                        chvec<TI>::st(dx + static_cast<int64_t>(tb + u - HW) * p.C + c0, out);
+                    }
+#pragma unroll
+                    for (int c = 0; c < CPT; ++c) {
+#pragma unroll
+                        for (int j = 0; j < HW; ++j) {
+                            xs[c][j] = xs[c][j + 1];
+                            acc[c][j] = acc[c][j + 1];
+                        }
+                        acc[c][HW] = 0.f;
+                    }
+                }
+            } else
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int t = tb + u;
@@ -210,7 +236,7 @@ __global__ void __launch_bounds__(CG_THREADS) conv_grad_kernel(ConvGradParams p,
 #pragma unroll
                             for (int c = 0; c < CPT; ++c) out[c] += p.d_final[(static_cast<int64_t>(ds.n) * p.C + c0 + c) * HW + k];
                     }
-                    chvec<TI, CPT>::st(dx + static_cast<int64_t>(done) * p.C + c0, out);
+                    chvec<TI>::st(dx + static_cast<int64_t>(done) * p.C + c0, out);
                 }
 #pragma unroll
                 for (int c = 0; c < CPT; ++c) {
@@ -222,6 +248,8 @@ __global__ void __launch_bounds__(CG_THREADS) conv_grad_kernel(ConvGradParams p,
                     acc[c][HW] = 0.f;
                 }
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) { xv[u] = xn[u]; gv[u] = gn[u]; }
         }
     }
     // one row of partial sums per workgroup, [dw C W | dbias C]: lanes of a
@@ -311,11 +339,11 @@ struct ConvGrid { int lg, tt, rows, cols; };
 // Channel vectors side by side: the most of {64, 32, 16, 8} that wastes at
 // most an eighth of the lanes (8 lanes still make 64- or 128-byte pieces),
 // fewer only where there are fewer.
-// Tokens per thread: 32, fewer while that leaves CUs without a workgroup (the
+// Tokens per thread: 64, fewer while that leaves CUs without a workgroup (the
 // walk past the tile then costs more of it).
-ConvGrid conv_grid(const ConvGradParams &p, int cpt) {
+ConvGrid conv_grid(const ConvGradParams &p) {
     ConvGrid g;
-    const int vecs = p.C / cpt;
+    const int vecs = p.C / CPT;
     for (g.lg = 1; g.lg < 8 && g.lg < vecs;) g.lg *= 2;
     for (int lg : {64, 32, 16}) {
         const int padded = (vecs + lg - 1) / lg * lg;
@@ -324,19 +352,17 @@ ConvGrid conv_grid(const ConvGradParams &p, int cpt) {
     g.cols = (vecs + g.lg - 1) / g.lg;
     const int subs = CG_THREADS / g.lg;
     const int64_t ntok = static_cast<int64_t>(p.B) * p.T;
-    g.tt = 32;
+    g.tt = 64;
     while (g.tt > 8 && (ntok + static_cast<int64_t>(subs) * g.tt - 1) / (static_cast<int64_t>(subs) * g.tt) * g.cols < 512) g.tt /= 2;
     g.rows = static_cast<int>((ntok + static_cast<int64_t>(subs) * g.tt - 1) / (static_cast<int64_t>(subs) * g.tt));
     return g;
 }
-int conv_cpt(int W) { return W <= 4 ? 8 : 4; }
 
 template <typename TI, typename TG, int W>
 hipError_t run(const ConvGradParams &p, hipStream_t s) {
-    constexpr int CPT = W <= 4 ? 8 : 4;
-    const ConvGrid g = conv_grid(p, CPT);
+    const ConvGrid g = conv_grid(p);
     if (g.rows > 0) {
-        hipLaunchKernelGGL((conv_grad_kernel<TI, TG, W, CPT>), dim3(static_cast<unsigned>(g.cols) * g.rows), dim3(CG_THREADS),
+        hipLaunchKernelGGL((conv_grad_kernel<TI, TG, W>), dim3(static_cast<unsigned>(g.cols) * g.rows), dim3(CG_THREADS),
                            sizeof(float) * (CG_THREADS / 64) * CPT * (W + 1) * g.lg, s, p, g.lg, g.tt, g.cols);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -367,7 +393,7 @@ hipError_t run_w(const ConvGradParams &p, hipStream_t s) {
 }  // namespace
 
 size_t conv_grad_bytes(const ConvGradParams &p) {
-    const int64_t rows = conv_grid(p, conv_cpt(p.W)).rows;
+    const int64_t rows = conv_grid(p).rows;
     return align_up(sizeof(float) * static_cast<size_t>(rows < 1 ? 1 : rows) * p.C * (p.W + 1));
 }
 
