@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
     }
     // The state is kept as S 2^level: a chunk adds its tot to the level (in 64
     // bits) and scales its own w x to match, and S is multiplied out only when
-    // the level has gone far, or before a store.
+    // the level has gone far, or before a store.  A chunk of a wide decay takes
+    // half of it as the level, so that its own factors lie around 1.
     double level = 0.0;
     auto scale_state = [&](float f) {
 #pragma unroll
@@ -308,9 +309,11 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
             fast = !FULL || fabsf(tot) < kFastTot;
             const float from = static_cast<float>(level);
             double next = level + tot;
-            const bool out = __builtin_amdgcn_readfirstlane(!(fabs(next) <= kLevel));
-            dec = fast_exp2(static_cast<float>(next));
-            if (out) next = 0.0;
+            const bool wide = FULL && fast && fabsf(tot) > kFastTot / 2;
+            const bool out = __builtin_amdgcn_readfirstlane(wide || !(fabs(next) <= kLevel));
+            const double to = wide ? 0.5 * tot : 0.0;
+            dec = fast_exp2(static_cast<float>(next - to));
+            if (out) next = to;
             level = next;
             if (fast && out) scale_state(dec);  // the second form reads the state before this chunk's decay
             const float hi = static_cast<float>(next), lo = static_cast<float>(next - hi);

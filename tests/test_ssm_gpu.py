@@ -158,3 +158,11 @@ def test_decode_steps_follow_a_prompt(B):
     y_r, S_r, _, _ = R.ssm_scan(r["x"], r["dt"], r["A"], r["B"], r["C"], r["D"], r["dt_bias"], True)
     check("prompt and steps y", torch.cat(ys, 1), y_r, TOL[BF])
     check("prompt and steps S", S, S_r, TOL_SPLIT)
+
+
+@pytest.mark.parametrize("dtype,steps", [(BF, (0.1, 0.2)), (F32, (0.2, 0.4))])
+def test_chunks_of_wide_decays(dtype, steps):
+    """Heads whose logs add up to -10 .. -230 (base 2) over a chunk: around the
+    limits at which the state's scale is centred and the second form taken."""
+    prefill(95, 2, 300, 24, 2, 32, 64, dtype, steps=steps, name=f"{dtype}")
+    prefill(96, 1, 0, 24, 2, 64, 128, dtype, lens=[65, 130, 1, 200], steps=steps, out_dtype=F32, name=f"{dtype} packed")
