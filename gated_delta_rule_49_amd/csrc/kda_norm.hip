@@ -19,6 +19,10 @@
 // cost no second read.  Teams walk the rows with a grid stride: the weights
 // stay in registers, and the next row's vectors are requested before this
 // row's reductions wait.
+//
+// 8192 rows of 4096 bf16 channels, residual, scale and both norms: forward
+// 65 us (4.1 TB/s; a copy of the same bytes takes 52), gradients 132 us (a copy:
+// 104), of which 8 are the column sums of the three weights' partial rows.
 #include "kda_launch.hpp"
 
 namespace kda {
@@ -563,7 +567,7 @@ int group_mode(const NormParams &p, int vec) {
 // Channels per vector, vectors per thread, threads per row.  Forward: 8
 // channels a thread.  Gradients: about 24 live values per channel, so 4
 // channels a thread, whatever the threads (8192 rows of 4096 channels: 897 us
-// with 256 threads of 16 channels, which spill, against XXX us).
+// with 256 threads of 16 channels, which spill, against 132 us).
 struct Shape { int vec, cpt, ts; };
 Shape pick(const NormParams &p, bool vec, bool grad) {
     if (!vec) {

@@ -9,19 +9,19 @@ hipError_t ssm_grad_bf16(const SsmGrad &a, hipStream_t s) { return grad_n<bf16_t
 namespace {
 // dA, dD and ddt_bias of a head: its chunks' shares in a fixed order
 __global__ void __launch_bounds__(256) ssm_scalar_kernel(SsmGrad a, int64_t items, int sub, float *dA, float *dD, float *dbias) {
-    __shared__ float s[4];
+    __shared__ double s[4];  // sums of either sign over all chunks: their own rounding would add up
     const int which = blockIdx.x / a.q.p.H, h = blockIdx.x % a.q.p.H;
     float *to = which == 0 ? dA : which == 1 ? dD : dbias;
     if (!to || (a.q.p.cu_seqlens && *a.q.status != 0)) return;  // the whole workgroup
     const int64_t n = a.q.p.cu_seqlens ? static_cast<int64_t>(a.q.chunk_off[a.q.p.N]) * sub : items;
     const float *src = a.scalars + (static_cast<int64_t>(which) * a.q.p.H + h) * items;
-    float v = 0.f;
+    double v = 0.0;
     for (int64_t i = threadIdx.x; i < n; i += 256) v += src[i];
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
     __syncthreads();
-    if (threadIdx.x == 0) to[h] = (s[0] + s[1]) + (s[2] + s[3]);
+    if (threadIdx.x == 0) to[h] = static_cast<float>((s[0] + s[1]) + (s[2] + s[3]));
 }
 }  // namespace
 

@@ -20,6 +20,14 @@
 // other; wave w owns 16 rows n of the states and the same 16 columns of dB and
 // dC, whose sums over the heads stay in its accumulators.  Each head's states
 // are read once, straight into operand order.
+//
+// 2 x 4096 tokens, 32 heads of 64 channels, one group, d_state 128, bf16: 208 us,
+// after 160 us for the four passes over the states and 27 for their chains, and
+// before 18 for the sums.  One workgroup fits a CU (127 KB of LDS); vector
+// instructions take 32 % of the cycles, LDS 31 % (14 % conflicts), matrix
+// instructions 11 %: it waits at the three barriers of a head.  Rows 16 banks
+// apart for what is only read by columns cost more in the writes than they
+// gained (4 % slower).
 #pragma once
 #include "kda_ssm_scan.hpp"
 
@@ -36,19 +44,25 @@ __device__ __forceinline__ float lane_xor(float v) {
     else if constexpr (BIT == 8) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, x, 0x128, 0xf, 0xf, true)); // row_ror:8
     else return __shfl_xor(v, BIT);
 }
+template <int BIT>
+__device__ __forceinline__ double lane_xor(double v) {
+    const int2 x = __builtin_bit_cast(int2, v);
+    return __builtin_bit_cast(double, make_int2(__builtin_bit_cast(int, lane_xor<BIT>(__builtin_bit_cast(float, x.x))),
+                                                __builtin_bit_cast(int, lane_xor<BIT>(__builtin_bit_cast(float, x.y)))));
+}
 // Sums of V = 4, 8 or 16 values over the 16 lanes of a lane group: each
 // exchange halves the values a lane carries; lane c ends with the sum of value
 // c / (16 / V).
-template <int V, int BIT>
-__device__ __forceinline__ float sum16(const float *v, int c16) {
+template <int V, int BIT, typename T>
+__device__ __forceinline__ T sum16(const T *v, int c16) {
     if constexpr (V > 1) {
         const bool up = c16 & BIT;
-        float next[V / 2];
+        T next[V / 2];
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) next[i] = (up ? v[i + V / 2] : v[i]) + lane_xor<BIT>(up ? v[i] : v[i + V / 2]);
         return sum16<V / 2, BIT / 2>(next, c16);
     } else if constexpr (BIT > 0) {
-        const float next = v[0] + lane_xor<BIT>(v[0]);
+        const T next = v[0] + lane_xor<BIT>(v[0]);
         return sum16<1, BIT / 2>(&next, c16);
     } else {
         return v[0];
@@ -67,12 +81,13 @@ struct GradCfg {
     // LDS, in bf16 elements
     static constexpr int BN = 0, CN = BN + EX * L * RN, XN = CN + EX * L * RN, YN = XN + EX * L * RP;
     static constexpr int M1 = YN + EX * L * RP, M2 = M1 + XP * L * RL, GN = M2 + XP * L * RL;
-    // then floats: dt, suf, 2^cum, 2^suf, diagonals of Q and E, suf's rounding; row and column sums per tile; inter and outer per wave; <G, S> per wave
-    static constexpr int FDT = 0, FSUF = L, FCUM = 2 * L, FWS = 3 * L, FQD = 4 * L, FED = 5 * L, FLO = 6 * L, FR = 7 * L, FC = FR + ST * L,
-                         FI = FC + ST * L, FO = FI + NT * L, FX = FO + NT * L, FEND = FX + 8;
+    // then floats: dt, suf, 2^cum, 2^suf, diagonals of Q and E, suf's rounding; row and column sums per tile (64 bits); inter and outer per wave; <G, S> per wave
+    static constexpr int FDT = 0, FSUF = L, FCUM = 2 * L, FWS = 3 * L, FQD = 4 * L, FED = 5 * L, FLO = 6 * L, FR = 7 * L, FC = FR + 2 * ST * L,
+                         FI = FC + 2 * ST * L, FO = FI + NT * L, FX = FO + NT * L, FEND = FX + 8;
     // G by rows, for du: through LDS where it fits, else read a second time
     static constexpr bool GLDS = sizeof(bf16_t) * (GN + XP * NS * RP) + sizeof(float) * FEND <= 160 * 1024;
     static constexpr int END = GN + (GLDS ? XP * NS * RP : 0);
+    static_assert(END % 4 == 0 && FR % 2 == 0, "64-bit sums are aligned");
     static constexpr size_t BYTES = sizeof(bf16_t) * END + sizeof(float) * FEND;
 };
 
@@ -84,6 +99,7 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
     __shared__ __attribute__((aligned(16))) char smem[Cf::BYTES];
     bf16_t *lds = reinterpret_cast<bf16_t *>(smem);
     float *fl = reinterpret_cast<float *>(smem + sizeof(bf16_t) * Cf::END);
+    double *rsum = reinterpret_cast<double *>(fl + Cf::FR), *csum = reinterpret_cast<double *>(fl + Cf::FC);
     const SsmParams &p = a.q.p;
     int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -304,21 +320,21 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
             const float lo_t = fl[Cf::FLO + t];
             const f32x4 lo_s = *reinterpret_cast<const f32x4 *>(fl + Cf::FLO + s0);
             const f32x4 dt_s = *reinterpret_cast<const f32x4 *>(fl + Cf::FDT + s0);
-            float rowsum = 0.f, E[4];
+            double rowsum = 0.0, E[4];  // the sums' difference is wanted: their own rounding would show
             granule m1[XP], m2[XP];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const float d = s0 + r <= t ? fast_exp2((suf_s[r] - suf_t) + (lo_s[r] - lo_t)) : 0.f;
                 const float qd = q[r] * d, kd = K[m][r] * d;
-                E[r] = q[r] * kd;
+                E[r] = static_cast<double>(q[r]) * kd;
                 // the diagonal passes through no token's decay: kept apart, it
                 // would only leave its rounding in the difference of the sums
                 if (s0 + r == t) {
                     fl[Cf::FQD + t] = q[r];
-                    fl[Cf::FED + t] = E[r];
-                    E[r] = 0.f;
+                    fl[Cf::FED + t] = static_cast<float>(E[r]);
+                    E[r] = 0.0;
                 }
-                rowsum = fmaf(E[r], dt_s[r], rowsum);
+                rowsum = fma(E[r], static_cast<double>(dt_s[r]), rowsum);
                 float v1 = qd * dt_s[r], v2 = kd;
 #pragma unroll
                 for (int part = 0; part < XP; ++part) {
@@ -335,9 +351,9 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
             }
             rowsum += __shfl_xor(rowsum, 16);
             rowsum += __shfl_xor(rowsum, 32);
-            if (g == 0) fl[Cf::FR + tj * L + t] = rowsum;
-            const float colsum = sum16<4, 8>(E, c16);
-            if (c16 % 4 == 0) fl[Cf::FC + ti * L + s0 + c16 / 4] = colsum;
+            if (g == 0) rsum[tj * L + t] = rowsum;
+            const double colsum = sum16<4, 8>(E, c16);
+            if (c16 % 4 == 0) csum[ti * L + s0 + c16 / 4] = colsum;
         }
 
         // ---- the states' shares of dC and dB, and their sums with C and B
@@ -472,12 +488,13 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
         }
         // ---- the step sizes: one token a lane
         if (wave == 7) {
-            float R = 0.f, Cs = 0.f, in = 0.f, out = 0.f, X = 0.f;
+            double R = 0.0, Cs = 0.0;
+            float in = 0.f, out = 0.f, X = 0.f;
             if (lane < L) {
 #pragma unroll
                 for (int k = 0; k < ST; ++k) {
-                    R += fl[Cf::FR + k * L + lane];
-                    Cs += fl[Cf::FC + k * L + lane];
+                    R += rsum[k * L + lane];
+                    Cs += csum[k * L + lane];
                 }
 #pragma unroll
                 for (int k = 0; k < NT; ++k) {
@@ -488,12 +505,21 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
 #pragma unroll
             for (int k = 0; k < NT; ++k) X += fl[Cf::FX + k];
             const float o = dt * out;
-            const float dlog = suffix_sum(R - dt * Cs + in, lane) + lane_shift(lane_scan(o)) + fast_exp2(tot) * X;
-            float dd = Cs + (lane < L ? fl[Cf::FED + lane] : 0.f) + out + A * dlog;
+            double left = R - dt * Cs + in, right = o;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const double l = __shfl_down(left, d), r = __shfl_up(right, d);
+                if (lane + d < 64) left += l;
+                if (lane >= d) right += r;
+            }
+            right = __shfl_up(right, 1);
+            if (lane == 0) right = 0.0;
+            const double dlog = left + right + static_cast<double>(fast_exp2(tot)) * X;
+            float dd = static_cast<float>(Cs + (lane < L ? fl[Cf::FED + lane] : 0.f) + out + A * dlog);
             if (p.softplus) dd *= sigmoid_f32(raw_dt);
             if (lane >= len) dd = 0.f;
             if (lane < len) io<TI>::st(static_cast<TI *>(a.ddt), (flat0 + lane) * p.H + h, dd);
-            const float sa = lane_scan(dt * dlog), sd = lane_scan(lane < L ? fl[Cf::FQD + lane] : 0.f);
+            const float sa = lane_scan(static_cast<float>(dt * dlog)), sd = lane_scan(lane < L ? fl[Cf::FQD + lane] : 0.f);
             const float sb = lane_scan(dd);
             if (lane == 63) {
                 a.scalars[(0 * static_cast<int64_t>(p.H) + h) * items + item] = sa;

@@ -13,6 +13,15 @@
 // Phase 1 runs the state part alone over every segment but the last, from
 // zero; a small kernel chains the segments' end states; phase 2 runs the full
 // scan over all segments at once.
+//
+// 32768 tokens, 64 heads of 64 channels in 8 groups, d_state 128, bf16: phase 1
+// 121 us, the chain 13, phase 2 302 (257 where no head's decay is wide); the
+// bytes alone would take 131.  Phase 2 spends 47 % of its cycles issuing vector
+// instructions (splitting fp32 values into bf16 parts, scaling, rounding) and
+// 33 % in matrix instructions; the two overlap only between the two waves of a
+// SIMD, which the barriers hold at the same place.  Workgroups of 4 waves, twice
+// as many to a CU, move B twice and gain nothing (140 against 131 us for phase
+// 1); 16 waves of 16 channels spill (520 us for phase 2).
 #pragma once
 #include "kda_ssm_scan.hpp"
 

@@ -309,22 +309,6 @@ __device__ __forceinline__ float lane_shift(float v) {
 }
 
 // inclusive sums over the lanes at and below / above each lane
-__device__ __forceinline__ float prefix_sum(float v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const float o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
-}
-__device__ __forceinline__ float suffix_sum(float v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const float o = __shfl_down(v, d);
-        if (lane + d < 64) v += o;
-    }
-    return v;
-}
 
 // Workspace layout, the tables of packed sequences and how a scan is split
 // (host).  bytes: of the whole layout; the state and log arrays are there
