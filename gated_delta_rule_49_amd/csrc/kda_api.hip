@@ -615,11 +615,11 @@ SsmParams ssm_params(const kda_ssm_args *a) {
 }  // namespace
 
 int64_t kda_ssm_max_chunks(const kda_ssm_args *a) {
-    return check_ssm_prefill(a, false) == KDA_OK ? ssm_plan(ssm_params(a), a->cu_seqlens != nullptr).chunks_bound : 0;
+    return check_ssm_prefill(a, false) == KDA_OK ? ssm_plan(ssm_params(a), a->cu_seqlens != nullptr, 1).chunks_bound : 0;
 }
 
 size_t kda_ssm_workspace_bytes(const kda_ssm_args *a) {
-    return check_ssm_prefill(a, false) == KDA_OK ? ssm_plan(ssm_params(a), a->cu_seqlens != nullptr).bytes() : 0;
+    return check_ssm_prefill(a, false) == KDA_OK ? ssm_plan(ssm_params(a), a->cu_seqlens != nullptr, 1).bytes() : 0;
 }
 
 kda_status kda_ssm_prefill(const kda_ssm_args *a, void *hip_stream) {
@@ -629,13 +629,13 @@ kda_status kda_ssm_prefill(const kda_ssm_args *a, void *hip_stream) {
     if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign) return KDA_ERR_BAD_SHAPE;
     SsmScan q{};
     q.p = ssm_params(a);
-    const SsmPlan plan = ssm_plan(q.p, a->cu_seqlens != nullptr);
+    const SsmPlan plan = ssm_plan(q.p, a->cu_seqlens != nullptr, 1);
     if (a->workspace_bytes < plan.bytes()) return KDA_ERR_WORKSPACE_TOO_SMALL;
     ssm_layout(q, plan, static_cast<char *>(a->workspace));
     q.user_status = a->device_status;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     hipError_t e = a->cu_seqlens ? launch_ssm_table(q, s) : hipSuccess;
-    if (e == hipSuccess) e = launch_ssm_scan(q, plan, SSM_FULL, a->in_dtype, a->out_dtype, s);
+    if (e == hipSuccess) e = launch_ssm_scan(q, plan, a->in_dtype, a->out_dtype, s);
     return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 

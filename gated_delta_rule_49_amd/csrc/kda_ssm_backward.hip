@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(256) ssm_scalar_kernel(SsmGrad a, int64_t item
 
 SsmGradPlan ssm_grad_plan(const SsmParams &p, bool packed, int in_dtype) {
     SsmGradPlan r{};
-    r.scan = ssm_plan(p, packed);
+    r.scan = ssm_plan(p, packed, 2);
     r.sub = in_dtype == 0 ? 2 : 1;
     r.items = r.scan.chunks_bound * r.sub;
     // A block walks several heads of a group, keeping the sums of dB and dC;
@@ -50,7 +50,8 @@ hipError_t launch_ssm_backward(const SsmParams &p, const SsmGradOut &o, char *ws
     a.q.p = p;
     ssm_layout(a.q, plan.scan, ws);
     a.q.state_chunk = 64 / plan.sub;
-    char *at = ws + plan.scan.bytes();
+    char *at = ws + plan.scan.bytes(), *other = at;  // segment states of the walk from the right
+    at += plan.scan.state_bytes + plan.scan.log_bytes;
     float *states = reinterpret_cast<float *>(at), *gstates = reinterpret_cast<float *>(at + plan.state_bytes);
     at += 2 * plan.state_bytes;
     if (plan.splits > 1) {
@@ -66,14 +67,16 @@ hipError_t launch_ssm_backward(const SsmParams &p, const SsmGradOut &o, char *ws
     // the states entering the chunks from the left ...
     SsmScan f = a.q;
     f.p.final_state = nullptr; f.p.chunk_states = states; f.p.y = nullptr;
-    e = launch_ssm_scan(f, plan.scan, SSM_STATES, in_dtype, 0, s);
-    if (e != hipSuccess) return e;
     // ... and their gradients from the right: C in B's place, dy in x's
     SsmScan r = a.q;
     r.p.Bm = p.Cm; r.p.b_sb = p.c_sb; r.p.b_st = p.c_st;
     r.p.x = o.d_y; r.p.x_st = static_cast<int64_t>(p.H) * p.P; r.p.x_sb = r.p.x_st * p.T;
     r.p.initial_state = o.d_final; r.p.final_state = o.d_initial; r.p.chunk_states = gstates; r.p.y = nullptr;
-    e = launch_ssm_scan(r, plan.scan, SSM_REVERSE, in_dtype, 0, s);
+    if (plan.scan.split) {
+        r.seg_state = reinterpret_cast<float *>(other);
+        r.seg_log = reinterpret_cast<float *>(other + plan.scan.state_bytes);
+    }
+    e = launch_ssm_both(f, r, plan.scan, in_dtype, s);
     if (e != hipSuccess) return e;
     e = in_dtype == 0 ? ssm_grad_f32(a, s) : ssm_grad_bf16(a, s);
     if (e != hipSuccess) return e;

@@ -54,17 +54,16 @@ struct ScanCfg {
     static constexpr size_t BYTES = sizeof(bf16_t) * NBUF * BUF + sizeof(float) * NW * WV;
 };
 
-// at most two waves a SIMD (the LDS holds one workgroup): all registers of two
+// number: this workgroup's, among `blocks`
 template <typename TI, typename TO, int NS, int PW, int NW, int MODE>
-__global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) ssm_scan_kernel(SsmScan q, int blocks_per_group, int phase) {
+__device__ __forceinline__ void ssm_scan(char *smem, const SsmScan &q, int number, int blocks, int blocks_per_group, int phase) {
     using Cf = ScanCfg<TI, TO, NS, PW, NW, MODE>;
     constexpr int EX = Cf::EX, L = Cf::L, ORD = Cf::ORD, XP = Cf::XP, GP = Cf::GP, SP = Cf::SP, NT = Cf::NT, KS = Cf::KS;
     constexpr int CT = Cf::CT, ST = Cf::ST, TK = Cf::TK, RN = Cf::RN, RB = Cf::RB, RT = Cf::RT, NBUF = Cf::NBUF;
     constexpr bool FULL = MODE == SSM_FULL, REV = MODE == SSM_REVERSE;
-    __shared__ __attribute__((aligned(16))) char smem[Cf::BYTES];
     const SsmParams &p = q.p;
-    if (q.user_status && !p.cu_seqlens && phase == 2 && blockIdx.x == 0 && threadIdx.x == 0) *q.user_status = 0;
-    const int block = xcd_order(blockIdx.x, gridDim.x);
+    if (q.user_status && !p.cu_seqlens && phase == 2 && number == 0 && threadIdx.x == 0) *q.user_status = 0;
+    const int block = xcd_order(number, blocks);
     const int x_seg = block / (p.G * blocks_per_group);
     if (x_seg >= q.segs_bound) return;
     const SsmSeg sg = ssm_seg(q, x_seg);
@@ -553,36 +552,73 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
     }
 }
 
+// at most two waves a SIMD (the LDS holds one workgroup): all registers of two
+template <typename TI, typename TO, int NS, int PW, int NW, int MODE>
+__global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4)))
+ssm_scan_kernel(SsmScan q, int blocks_per_group, int phase) {
+    __shared__ __attribute__((aligned(16))) char smem[ScanCfg<TI, TO, NS, PW, NW, MODE>::BYTES];
+    ssm_scan<TI, TO, NS, PW, NW, MODE>(smem, q, blockIdx.x, gridDim.x, blocks_per_group, phase);
+}
+// the states from the left, and with the second half of the grid from the right
+template <typename TI, int NS, int PW, int NW>
+__global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4)))
+ssm_states_kernel(SsmScan f, SsmScan r, int blocks_per_group, int phase) {
+    __shared__ __attribute__((aligned(16))) char smem[ScanCfg<TI, float, NS, PW, NW, SSM_STATES>::BYTES];
+    const int half = gridDim.x / 2;
+    if (blockIdx.x < half) ssm_scan<TI, float, NS, PW, NW, SSM_STATES>(smem, f, blockIdx.x, half, blocks_per_group, phase);
+    else ssm_scan<TI, float, NS, PW, NW, SSM_REVERSE>(smem, r, blockIdx.x - half, half, blocks_per_group, phase);
+}
+
+inline unsigned scan_grid(const SsmScan &q, const SsmPlan &plan) {
+    const int64_t want = static_cast<int64_t>(plan.segs_bound) * q.p.G * plan.blocks_per_group;
+    return static_cast<unsigned>((want + 7) / 8 * 8);
+}
 template <typename TI, typename TO, int NS, int PW, int MODE>
 hipError_t run(const SsmScan &q, const SsmPlan &plan, int phase, hipStream_t s) {
-    const int64_t want = static_cast<int64_t>(plan.segs_bound) * q.p.G * plan.blocks_per_group;
-    const unsigned grid = static_cast<unsigned>((want + 7) / 8 * 8);
+    const unsigned grid = scan_grid(q, plan);
     if (plan.waves == 8)
         hipLaunchKernelGGL((ssm_scan_kernel<TI, TO, NS, PW, 8, MODE>), dim3(grid), dim3(512), 0, s, q, plan.blocks_per_group, phase);
     else
         hipLaunchKernelGGL((ssm_scan_kernel<TI, TO, NS, PW, 4, MODE>), dim3(grid), dim3(256), 0, s, q, plan.blocks_per_group, phase);
     return hipGetLastError();
 }
+template <typename TI, int NS, int PW>
+hipError_t run_states(const SsmScan &f, const SsmScan &r, const SsmPlan &plan, int phase, hipStream_t s) {
+    const unsigned grid = 2 * scan_grid(f, plan);
+    if (plan.waves == 8)
+        hipLaunchKernelGGL((ssm_states_kernel<TI, NS, PW, 8>), dim3(grid), dim3(512), 0, s, f, r, plan.blocks_per_group, phase);
+    else
+        hipLaunchKernelGGL((ssm_states_kernel<TI, NS, PW, 4>), dim3(grid), dim3(256), 0, s, f, r, plan.blocks_per_group, phase);
+    return hipGetLastError();
+}
 template <typename TI, typename TO, int NS>
-hipError_t run_p(const SsmScan &q, const SsmPlan &plan, int mode, int phase, hipStream_t s) {
-    if (q.p.P == 16) {
-        if (mode == SSM_FULL) return run<TI, TO, NS, 16, SSM_FULL>(q, plan, phase, s);
-        if (mode == SSM_STATES) return run<TI, float, NS, 16, SSM_STATES>(q, plan, phase, s);
-        return run<TI, float, NS, 16, SSM_REVERSE>(q, plan, phase, s);
-    }
-    if (mode == SSM_FULL) return run<TI, TO, NS, 32, SSM_FULL>(q, plan, phase, s);
-    if (mode == SSM_STATES) return run<TI, float, NS, 32, SSM_STATES>(q, plan, phase, s);
-    return run<TI, float, NS, 32, SSM_REVERSE>(q, plan, phase, s);
+hipError_t run_p(const SsmScan &q, const SsmPlan &plan, int phase, hipStream_t s) {
+    if (q.p.P == 16)
+        return phase == 2 ? run<TI, TO, NS, 16, SSM_FULL>(q, plan, phase, s) : run<TI, float, NS, 16, SSM_STATES>(q, plan, phase, s);
+    return phase == 2 ? run<TI, TO, NS, 32, SSM_FULL>(q, plan, phase, s) : run<TI, float, NS, 32, SSM_STATES>(q, plan, phase, s);
+}
+template <typename TI, int NS>
+hipError_t run_states_p(const SsmScan &f, const SsmScan &r, const SsmPlan &plan, int phase, hipStream_t s) {
+    return f.p.P == 16 ? run_states<TI, NS, 16>(f, r, plan, phase, s) : run_states<TI, NS, 32>(f, r, plan, phase, s);
 }
 }  // namespace
 
 template <typename TI, typename TO>
-hipError_t ssm_phase(const SsmScan &q, const SsmPlan &plan, int mode, int phase, hipStream_t s) {
+hipError_t ssm_phase(const SsmScan &q, const SsmPlan &plan, int phase, hipStream_t s) {
     switch (q.p.Ns) {
-        case 16: return run_p<TI, TO, 16>(q, plan, mode, phase, s);
-        case 32: return run_p<TI, TO, 32>(q, plan, mode, phase, s);
-        case 64: return run_p<TI, TO, 64>(q, plan, mode, phase, s);
-        default: return run_p<TI, TO, 128>(q, plan, mode, phase, s);
+        case 16: return run_p<TI, TO, 16>(q, plan, phase, s);
+        case 32: return run_p<TI, TO, 32>(q, plan, phase, s);
+        case 64: return run_p<TI, TO, 64>(q, plan, phase, s);
+        default: return run_p<TI, TO, 128>(q, plan, phase, s);
+    }
+}
+template <typename TI>
+hipError_t ssm_states(const SsmScan &f, const SsmScan &r, const SsmPlan &plan, int phase, hipStream_t s) {
+    switch (f.p.Ns) {
+        case 16: return run_states_p<TI, 16>(f, r, plan, phase, s);
+        case 32: return run_states_p<TI, 32>(f, r, plan, phase, s);
+        case 64: return run_states_p<TI, 64>(f, r, plan, phase, s);
+        default: return run_states_p<TI, 128>(f, r, plan, phase, s);
     }
 }
 

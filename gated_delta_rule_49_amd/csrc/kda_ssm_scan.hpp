@@ -308,8 +308,6 @@ __device__ __forceinline__ float lane_shift(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x138, 0xf, 0xf, true));  // wave_shr:1
 }
 
-// inclusive sums over the lanes at and below / above each lane
-
 // Workspace layout, the tables of packed sequences and how a scan is split
 // (host).  bytes: of the whole layout; the state and log arrays are there
 // only where the scan may be split.
@@ -321,7 +319,8 @@ struct SsmPlan {
     size_t table_bytes, state_bytes, log_bytes;
     size_t bytes() const { return table_bytes + state_bytes + log_bytes; }
 };
-SsmPlan ssm_plan(const SsmParams &p, bool packed);
+// walks: 1, or 2 for a pass from both ends at once
+SsmPlan ssm_plan(const SsmParams &p, bool packed, int walks);
 // fills the tables' pointers of q from a workspace laid out by the plan
 void ssm_layout(SsmScan &q, const SsmPlan &plan, char *ws);
 // the same without the lane's own value (taken from the neighbour's sum, not
@@ -339,14 +338,12 @@ __device__ __forceinline__ float after(float inclusive, int lane) {
 hipError_t launch_ssm_table(const SsmScan &q, hipStream_t s);
 // the status word where there are no offsets to check
 hipError_t launch_ssm_status(const SsmScan &q, hipStream_t s);
-// chains the segments' end states into the states entering each, in place;
-// reverse: from the last segment to the first
-hipError_t launch_ssm_combine(const SsmScan &q, const float *first, bool reverse, hipStream_t s);
 // one phase of a scan; FULL writes y, the others only states.  phase 1: from
 // zero, the end state and log decay of every segment but the last (reverse:
 // but the first); phase 2: from the entering states.
 enum { SSM_FULL = 0, SSM_STATES = 1, SSM_REVERSE = 2 };
-hipError_t launch_ssm_phase(const SsmScan &q, const SsmPlan &plan, int mode, int phase, int in_dtype, int out_dtype, hipStream_t s);
+hipError_t launch_ssm_phase(const SsmScan &q, const SsmPlan &plan, int phase, int in_dtype, int out_dtype, hipStream_t s);
+hipError_t launch_ssm_states(const SsmScan &f, const SsmScan &r, const SsmPlan &plan, int phase, int in_dtype, hipStream_t s);
 // Gradients (kda_ssm_backward.hpp)
 struct SsmGrad {
     SsmScan q;                  // p.x, p.Bm, p.Cm, p.dt as in the forward
@@ -365,7 +362,7 @@ struct SsmGradPlan {
     int32_t sub, splits, heads_per_block;
     int64_t items;  // bound on the chunks (parts of 64 tokens in fp32)
     size_t state_bytes, part_bytes, scalar_bytes;
-    size_t bytes() const { return scan.bytes() + 2 * state_bytes + 2 * part_bytes + scalar_bytes; }
+    size_t bytes() const { return scan.bytes() + scan.state_bytes + scan.log_bytes + 2 * state_bytes + 2 * part_bytes + scalar_bytes; }
 };
 SsmGradPlan ssm_grad_plan(const SsmParams &p, bool packed, int in_dtype);
 struct SsmGradOut {
@@ -375,7 +372,10 @@ struct SsmGradOut {
     float *dA, *dD, *ddt_bias, *d_initial;
 };
 hipError_t launch_ssm_backward(const SsmParams &p, const SsmGradOut &o, char *ws, int in_dtype, hipStream_t s);
-// a whole scan: phases and combination
-hipError_t launch_ssm_scan(const SsmScan &q, const SsmPlan &plan, int mode, int in_dtype, int out_dtype, hipStream_t s);
+// a whole scan: phases and the chain of segments between them
+hipError_t launch_ssm_scan(const SsmScan &q, const SsmPlan &plan, int in_dtype, int out_dtype, hipStream_t s);
+// the states alone, f from the left and r from the right (with segment states
+// of its own), side by side
+hipError_t launch_ssm_both(const SsmScan &f, const SsmScan &r, const SsmPlan &plan, int in_dtype, hipStream_t s);
 
 }  // namespace kda

@@ -73,11 +73,11 @@ __global__ void __launch_bounds__(1024) ssm_table_kernel(SsmScan q, int32_t *seg
 
 // One thread per 4 state elements of a (sequence, head), walking the
 // sequence's segments; four segments' end states are requested together.
-__global__ void __launch_bounds__(256) ssm_combine_kernel(SsmScan q, const float *first, int reverse) {
+__device__ __forceinline__ void combine(const SsmScan &q, const float *first, int block, bool reverse) {
     const int H = q.p.H, per = q.p.Ns * q.p.P;
     const int blocks = (per / 4 + 255) / 256;
-    const int e = ((blockIdx.x % blocks) * 256 + threadIdx.x) * 4;
-    const int nh = blockIdx.x / blocks, n = nh / H, h = nh % H;
+    const int e = ((block % blocks) * 256 + threadIdx.x) * 4;
+    const int nh = block / blocks, n = nh / H, h = nh % H;
     if (e >= per) return;
     int x0 = n * q.segs_per_seq, count = q.segs_per_seq;
     if (q.p.cu_seqlens) {
@@ -108,10 +108,16 @@ __global__ void __launch_bounds__(256) ssm_combine_kernel(SsmScan q, const float
             }
     }
 }
+// f from the first segment to the last, and with a grid twice as large r from
+// the last to the first
+__global__ void __launch_bounds__(256) ssm_combine_kernel(SsmScan f, SsmScan r, int blocks) {
+    if (blockIdx.x < blocks) combine(f, f.p.initial_state, blockIdx.x, false);
+    else combine(r, r.p.initial_state, blockIdx.x - blocks, true);
+}
 
 }  // namespace
 
-SsmPlan ssm_plan(const SsmParams &p, bool packed) {
+SsmPlan ssm_plan(const SsmParams &p, bool packed, int walks) {
     SsmPlan r{};
     r.chunks_per_seq = static_cast<int32_t>((static_cast<int64_t>(p.T) + 63) / 64);
     r.chunks_bound = packed ? static_cast<int64_t>(r.chunks_per_seq) + p.N : static_cast<int64_t>(r.chunks_per_seq) * p.N;
@@ -126,7 +132,7 @@ SsmPlan ssm_plan(const SsmParams &p, bool packed) {
     // 1 to 7001 tokens, d_state 64: 177 + 80 us with 512, 220 + 97 with 256).  A
     // segment has at least 4 chunks: its state is written and read once, which
     // is the traffic of 2 chunks (d_state 128).
-    const int64_t per_seg = static_cast<int64_t>(p.G) * r.blocks_per_group;
+    const int64_t per_seg = static_cast<int64_t>(p.G) * r.blocks_per_group * walks;
     int64_t k = packed ? r.chunks_bound * per_seg / 512 : (r.chunks_bound * per_seg + 255) / 256;
     k = std::max<int64_t>(k, 4);
     k = std::min<int64_t>(k, std::max(1, r.chunks_per_seq));
@@ -169,19 +175,30 @@ hipError_t launch_ssm_status(const SsmScan &q, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_ssm_combine(const SsmScan &q, const float *first, bool reverse, hipStream_t s) {
-    const unsigned blocks = (q.p.Ns * q.p.P / 4 + 255) / 256;
-    hipLaunchKernelGGL(ssm_combine_kernel, dim3(blocks * q.p.N * q.p.H), dim3(256), 0, s, q, first, reverse ? 1 : 0);
+namespace {
+hipError_t launch_combine(const SsmScan &f, const SsmScan &r, int walks, hipStream_t s) {
+    const int blocks = (f.p.Ns * f.p.P / 4 + 255) / 256 * f.p.N * f.p.H;
+    hipLaunchKernelGGL(ssm_combine_kernel, dim3(static_cast<unsigned>(blocks) * walks), dim3(256), 0, s, f, r, blocks);
     return hipGetLastError();
 }
+}  // namespace
 
-hipError_t launch_ssm_scan(const SsmScan &q, const SsmPlan &plan, int mode, int in_dtype, int out_dtype, hipStream_t s) {
+hipError_t launch_ssm_scan(const SsmScan &q, const SsmPlan &plan, int in_dtype, int out_dtype, hipStream_t s) {
     if (plan.split) {
-        hipError_t e = launch_ssm_phase(q, plan, mode == SSM_FULL ? SSM_STATES : mode, 1, in_dtype, out_dtype, s);
-        if (e == hipSuccess) e = launch_ssm_combine(q, q.p.initial_state, mode == SSM_REVERSE, s);
+        hipError_t e = launch_ssm_phase(q, plan, 1, in_dtype, out_dtype, s);
+        if (e == hipSuccess) e = launch_combine(q, q, 1, s);
         if (e != hipSuccess) return e;
     }
-    return launch_ssm_phase(q, plan, mode, 2, in_dtype, out_dtype, s);
+    return launch_ssm_phase(q, plan, 2, in_dtype, out_dtype, s);
+}
+
+hipError_t launch_ssm_both(const SsmScan &f, const SsmScan &r, const SsmPlan &plan, int in_dtype, hipStream_t s) {
+    if (plan.split) {
+        hipError_t e = launch_ssm_states(f, r, plan, 1, in_dtype, s);
+        if (e == hipSuccess) e = launch_combine(f, r, 2, s);
+        if (e != hipSuccess) return e;
+    }
+    return launch_ssm_states(f, r, plan, 2, in_dtype, s);
 }
 
 }  // namespace kda

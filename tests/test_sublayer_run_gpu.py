@@ -371,3 +371,30 @@ def test_refusals_of_the_binding():
     with pytest.raises((TypeError, ValueError)):
         kda.short_conv_backward(d["mixed"], d["w"], d["gate"])
     torch.cuda.synchronize()
+
+
+def test_offsets_past_32_bits():
+    """Slices of tokens so wide that the last ones lie past 2^31 elements: the
+    same results, bit for bit, as from dense copies."""
+    B, T, width, h, g, p, n = 2, 140000, 8192, 2, 1, 64, 64
+    base = torch.empty(B, T, width, dtype=BF, device="cuda")
+    assert base.numel() > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    used = h * p + 2 * g * n
+    base[..., -used:] = torch.randn(B, T, used, generator=gen, device="cuda").to(BF)
+    cols = base[..., -used:]
+    x, b, c = cols[..., :h * p].unflatten(-1, (h, p)), cols[..., h * p:h * p + g * n].unflatten(-1, (g, n)), cols[..., h * p + g * n:].unflatten(-1, (g, n))
+    dt = torch.randn(B, T, h, generator=gen, device="cuda").to(BF)
+    A, bias = torch.tensor([-1.0, -4.0], device="cuda"), torch.full((h,), -3.0, device="cuda")
+    kw = dict(dt_bias=bias, dt_softplus=True)
+    y, S = kda.ssm_prefill(x, dt, A, b, c, **kw)
+    grads = kda.ssm_backward(x, dt, A, b, c, y, **kw)
+    dense = [v.contiguous() for v in (x, b, c)]
+    y2, S2 = kda.ssm_prefill(dense[0], dt, A, *dense[1:], **kw)
+    grads2 = kda.ssm_backward(dense[0], dt, A, *dense[1:], y, **kw)
+    for a, e in zip((y, S, *grads), (y2, S2, *grads2)):
+        assert a is e is None or torch.equal(a, e)
+    w = torch.rand(used, generator=gen, device="cuda")
+    out, normed = kda.block_norm(cols, post_weight=w, pre_weight=w, group_size=64)
+    out2, normed2 = kda.block_norm(cols.contiguous(), post_weight=w, pre_weight=w, group_size=64)
+    assert torch.equal(out, out2) and torch.equal(normed, normed2)
