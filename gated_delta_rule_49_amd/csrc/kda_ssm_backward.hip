@@ -10,6 +10,8 @@ namespace {
 // dA, dD and ddt_bias of a head: its chunks' shares in a fixed order
 __global__ void __launch_bounds__(256) ssm_scalar_kernel(SsmGrad a, int64_t items, int sub, float *dA, float *dD, float *dbias) {
     __shared__ double s[4];  // sums of either sign over all chunks: their own rounding would add up
+    // without offsets to check, nothing has written the call's status yet
+    if (!a.q.p.cu_seqlens && blockIdx.x == 0 && threadIdx.x == 0) *const_cast<int32_t *>(a.q.status) = 0;
     const int which = blockIdx.x / a.q.p.H, h = blockIdx.x % a.q.p.H;
     float *to = which == 0 ? dA : which == 1 ? dD : dbias;
     if (!to || (a.q.p.cu_seqlens && *a.q.status != 0)) return;  // the whole workgroup
@@ -62,7 +64,7 @@ hipError_t launch_ssm_backward(const SsmParams &p, const SsmGradOut &o, char *ws
     a.states = states; a.gstates = gstates;
     a.d_y = o.d_y; a.dx = o.dx; a.ddt = o.ddt; a.dB = o.dB; a.dC = o.dC;
     a.heads_per_block = plan.heads_per_block; a.splits = plan.splits;
-    hipError_t e = p.cu_seqlens ? launch_ssm_table(a.q, s) : launch_ssm_status(a.q, s);
+    hipError_t e = p.cu_seqlens ? launch_ssm_table(a.q, s) : hipSuccess;
     if (e != hipSuccess) return e;
     // the states entering the chunks from the left ...
     SsmScan f = a.q;

@@ -325,19 +325,9 @@ SsmPlan ssm_plan(const SsmParams &p, bool packed, int walks);
 void ssm_layout(SsmScan &q, const SsmPlan &plan, char *ws);
 // the same without the lane's own value (taken from the neighbour's sum, not
 // by subtracting: the own value may be far larger than the sum)
-__device__ __forceinline__ float before(float inclusive, int lane) {
-    const float o = __shfl_up(inclusive, 1);
-    return lane > 0 ? o : 0.f;
-}
-__device__ __forceinline__ float after(float inclusive, int lane) {
-    const float o = __shfl_down(inclusive, 1);
-    return lane < 63 ? o : 0.f;
-}
 
 // segment and chunk tables of packed sequences; checks the offsets
 hipError_t launch_ssm_table(const SsmScan &q, hipStream_t s);
-// the status word where there are no offsets to check
-hipError_t launch_ssm_status(const SsmScan &q, hipStream_t s);
 // one phase of a scan; FULL writes y, the others only states.  phase 1: from
 // zero, the end state and log decay of every segment but the last (reverse:
 // but the first); phase 2: from the entering states.

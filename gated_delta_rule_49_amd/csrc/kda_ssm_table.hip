@@ -168,13 +168,6 @@ hipError_t launch_ssm_table(const SsmScan &q, hipStream_t s) {
     return hipGetLastError();
 }
 
-__global__ void ssm_status_kernel(int32_t *status) { *status = 0; }
-
-hipError_t launch_ssm_status(const SsmScan &q, hipStream_t s) {
-    hipLaunchKernelGGL(ssm_status_kernel, dim3(1), dim3(1), 0, s, const_cast<int32_t *>(q.status));
-    return hipGetLastError();
-}
-
 namespace {
 hipError_t launch_combine(const SsmScan &f, const SsmScan &r, int walks, hipStream_t s) {
     const int blocks = (f.p.Ns * f.p.P / 4 + 255) / 256 * f.p.N * f.p.H;

@@ -398,3 +398,15 @@ def test_offsets_past_32_bits():
     out, normed = kda.block_norm(cols, post_weight=w, pre_weight=w, group_size=64)
     out2, normed2 = kda.block_norm(cols.contiguous(), post_weight=w, pre_weight=w, group_size=64)
     assert torch.equal(out, out2) and torch.equal(normed, normed2)
+
+
+@pytest.mark.parametrize("lens", [None, [70, 1, 0, 129]])
+def test_the_gradients_report_their_status(lens):
+    _, dcu = offsets(lens)
+    L = Layer(80, 1 if lens else 2, 200 if lens else 150, F32, len(lens) if lens else None)
+    d = L.dev
+    x, b, c = cut(d["mixed"])
+    status = torch.full((1,), 77, dtype=torch.int32, device="cuda")
+    dy = torch.ones(L.B, L.T, H, P, device="cuda")
+    kda.ssm_backward(x, d["dt"], d["A"], b, c, dy, initial_state=d["state"], cu_seqlens=dcu, device_status=status)
+    assert int(status) == 0
