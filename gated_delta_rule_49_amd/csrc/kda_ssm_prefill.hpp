@@ -15,7 +15,7 @@
 // scan over all segments at once.
 //
 // 32768 tokens, 64 heads of 64 channels in 8 groups, d_state 128, bf16: phase 1
-// 121 us, the chain 13, phase 2 302 (257 where no head's decay is wide); the
+// 121 to 142 us, the chain 14, phase 2 302 (257 where no head's decay is wide); the
 // bytes alone would take 131.  Phase 2 spends 47 % of its cycles issuing vector
 // instructions (splitting fp32 values into bf16 parts, scaling, rounding) and
 // 33 % in matrix instructions; the two overlap only between the two waves of a

@@ -323,8 +323,6 @@ struct SsmPlan {
 SsmPlan ssm_plan(const SsmParams &p, bool packed, int walks);
 // fills the tables' pointers of q from a workspace laid out by the plan
 void ssm_layout(SsmScan &q, const SsmPlan &plan, char *ws);
-// the same without the lane's own value (taken from the neighbour's sum, not
-// by subtracting: the own value may be far larger than the sum)
 
 // segment and chunk tables of packed sequences; checks the offsets
 hipError_t launch_ssm_table(const SsmScan &q, hipStream_t s);
