@@ -37,10 +37,10 @@ struct ScanCfg {
     static constexpr int ORD = BF ? 2 : 3;
     static constexpr int XP = 3;                          // parts of w x: the state keeps fp32 accuracy
     static constexpr int GP = BF ? 2 : 3;                 // parts of the scores
-    // the state as an operand of C S: a bf16 y carries a rounding of up to
-    // 2^-9 of its own; one part of S adds an error of that size only to what
-    // the state contributes
-    static constexpr int SP = !BF ? 3 : std::is_same<TO, bf16_t>::value ? 1 : 2;
+    // parts of the state in C S, also behind a bf16 y: with one part each of the
+    // sum's d_state terms is off by up to 2^-8 of itself, and where they cancel y
+    // by several of its own steps
+    static constexpr int SP = BF ? 2 : 3;
     static constexpr int NT = NS / 16, KS = (NS + 31) / 32, NK = KS * 32;
     static constexpr int CT = PW / 16, ST = L / 16, TK = L / 32;
     // LDS row strides: 16-byte pieces of 16 rows hit all banks (C, scores);
