@@ -28,12 +28,15 @@ namespace kda {
 //            against both halves of log2 e, |r| <= 1/2
 //   log(1 + y) = 2 atanh(y / (2 + y)), |y / (2 + y)| <= 1/3: seven odd terms
 //            leave less than (1/9)^7 / 15 = 1.4e-8 of it
+// e^-200 is below the smallest float, so |x| counts no further than 200: r would
+// not stay small, and a step masked by the lowest value or -inf (a step of 0)
+// would become NaN.
 __device__ __forceinline__ float softplus_rel(float x) {
     constexpr float kLog2eLo = 1.92596299e-08f;  // log2 e - kLog2e
-    const float m = -fabsf(x);
+    const float m = fmaxf(-fabsf(x), -200.f);
     const float n = rintf(m * kLog2e);
     const float r = fmaf(m, kLog2eLo, fmaf(m, kLog2e, -n));
-    const float y = ldexpf(fast_exp2(r), static_cast<int>(fmaxf(n, -200.f)));
+    const float y = ldexpf(fast_exp2(r), static_cast<int>(n));
     const float s = y / (2.f + y), q = s * s;
     float p = 1.f / 13.f;
     p = fmaf(p, q, 1.f / 11.f);
