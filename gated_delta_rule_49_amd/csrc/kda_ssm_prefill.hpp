@@ -50,7 +50,7 @@ struct ScanCfg {
     static constexpr int BN = EX * L * RB, CN = EX * L * RN;
     static constexpr int GT = FULL ? GP * L * RT : 0;     // causal scores
     static constexpr int BUF = BN + (FULL ? CN : 0) + GT;
-    static constexpr int WV = (FULL ? 4 : 1) * L;         // per wave: w, row factor, suf, dt
+    static constexpr int WV = (FULL ? 5 : 1) * L;         // per wave: w, row factor, suf, dt, suf's rounding
     static constexpr size_t BYTES = sizeof(bf16_t) * NBUF * BUF + sizeof(float) * NW * WV;
 };
 
@@ -83,7 +83,7 @@ __device__ __forceinline__ void ssm_scan(char *smem, const SsmScan &q, int numbe
 
     bf16_t *lds = reinterpret_cast<bf16_t *>(smem);
     float *wv = reinterpret_cast<float *>(smem + sizeof(bf16_t) * NBUF * Cf::BUF) + wave * Cf::WV;
-    float *fv = wv + L, *sv = wv + 2 * L, *dv = wv + 3 * L;
+    float *fv = wv + L, *sv = wv + 2 * L, *dv = wv + 3 * L, *sl = wv + 4 * L;
     auto Bn = [&](int b, int part) { return lds + b * Cf::BUF + part * L * RB; };
     auto Cn = [&](int b, int part) { return lds + b * Cf::BUF + Cf::BN + part * L * RN; };
     auto Gt = [&](int b, int part) { return lds + b * Cf::BUF + Cf::BN + Cf::CN + part * L * RT; };
@@ -311,13 +311,18 @@ __device__ __forceinline__ void ssm_scan(char *smem, const SsmScan &q, int numbe
             float dt = dt_next + bias;
             if (p.softplus) dt = softplus_rel(dt);
             if (tok < 0 || tok >= rem) dt = 0.f;
-            const float la = A2 * dt;
-            const float incl = lane_scan(la);  // from the chunk's end (reverse: its start) to the token
-            const float tot = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, incl), 63));
-            fast = !FULL || fabsf(tot) < kFastTot;
+            float la = A2 * dt;
+            if (la < kGone) la = kGone;
+            // from the chunk's end (reverse: its start) to the token.  The states
+            // alone take no difference of two sums: a sum large enough to be coarse
+            // has left nothing
+            typedef typename std::conditional<FULL, double, float>::type Sum;
+            const Sum incl = lane_scan(static_cast<Sum>(la));
+            const Sum tot = last_lane(incl);
+            fast = !FULL || fabs(tot) < kFastTot;
             const float from = static_cast<float>(level);
             double next = level + tot;
-            const bool wide = FULL && fast && fabsf(tot) > kFastTot / 2;
+            const bool wide = FULL && fast && fabs(tot) > kFastTot / 2;
             const bool out = __builtin_amdgcn_readfirstlane(wide || !(fabs(next) <= kLevel));
             const double to = wide ? 0.5 * tot : 0.0;
             dec = fast_exp2(static_cast<float>(next - to));
@@ -328,13 +333,16 @@ __device__ __forceinline__ void ssm_scan(char *smem, const SsmScan &q, int numbe
             if (REV) {
                 if (lane < L) wv[lane] = lane < rem ? fast_exp2((incl - hi) - lo) : 0.f;
             } else {
-                const float suf = lane_shift(incl);
+                const Sum suf = lane_shift(incl);
                 if (tok >= 0) {
-                    wv[tok] = dt * fast_exp2((suf - hi) - lo);
-                    if (FULL) {
-                        fv[tok] = fast ? fast_exp2((hi - suf) + lo) : la;
-                        sv[tok] = suf;
+                    if constexpr (FULL) {
+                        wv[tok] = dt * fast_exp2(static_cast<float>(suf - next));
+                        fv[tok] = fast ? fast_exp2(static_cast<float>(next - suf)) : la;
+                        sv[tok] = static_cast<float>(suf);
+                        sl[tok] = static_cast<float>(suf - static_cast<float>(suf));
                         dv[tok] = dt;
+                    } else {
+                        wv[tok] = dt * fast_exp2((suf - hi) - lo);
                     }
                 }
                 if (FULL && !fast) {  // the sums from the chunk's start
@@ -344,7 +352,7 @@ __device__ __forceinline__ void ssm_scan(char *smem, const SsmScan &q, int numbe
                     if (lane < L) fv[lane] = fast_exp2(cum + from);
                 }
             }
-            seg_log += tot;
+            seg_log += static_cast<float>(tot);
             late = !fast && out;
             wave_lds_fence();
             if constexpr (FULL) {  // C S
@@ -389,7 +397,7 @@ __device__ __forceinline__ void ssm_scan(char *smem, const SsmScan &q, int numbe
 #pragma unroll
                     for (int s = 0; s < ST; ++s) {
                         const int row = 16 * s + c16;
-                        const float suf_row = sv[row];
+                        const float suf_row = sv[row], low_row = sl[row];
 #pragma unroll
                         for (int ks = 0; ks <= s / 2; ++ks) {
                             asm volatile("" ::: "memory");  // the factors are read again, not kept over the strips
@@ -408,10 +416,11 @@ __device__ __forceinline__ void ssm_scan(char *smem, const SsmScan &q, int numbe
                             for (int hq = 0; hq < 2; ++hq) {
                                 const int col = 32 * ks + 16 * hq + 4 * g;
                                 const f32x4 sc = *reinterpret_cast<const f32x4 *>(sv + col);
+                                const f32x4 lc = *reinterpret_cast<const f32x4 *>(sl + col);
                                 const f32x4 dc = *reinterpret_cast<const f32x4 *>(dv + col);
 #pragma unroll
                                 for (int r = 0; r < 4; ++r) {
-                                    const float k = col + r <= row ? dc[r] * fast_exp2(sc[r] - suf_row) : 0.f;
+                                    const float k = col + r <= row ? dc[r] * fast_exp2((sc[r] - suf_row) + (lc[r] - low_row)) : 0.f;
                                     split_to<GP>(m, 4 * hq + r, mv[4 * hq + r] * k);
                                 }
                             }

@@ -11,7 +11,9 @@
 // exact while 2^tot stays a normal number with room for its low-order parts;
 // a chunk that decays by more than kFastTot takes the second form,
 //     y_t = 2^(cum_t) C_t^T S_in + sum_{s <= t} (C_t . B_s) 2^(suf_s - suf_t) dt_s x_s ,
-// every exponent <= 0.
+// every exponent <= 0.  suf_s - suf_t may be one token's small log beside sums of
+// thousands (steps of mixed sizes in one head): where y is made the sums are in 64
+// bits, kept as two floats for the second form.
 //
 // Precision: bf16 inputs enter the matrix cores as they are; the state, the
 // scores and the scaled inputs are fp32 values split into bf16 parts (2 parts:
@@ -57,6 +59,10 @@ __device__ __forceinline__ float softplus_rel(float x) {
 // 32768 tokens of 64 such heads took 334 us in phase 2, 302 so; inputs
 // without wide decays take 257.)
 constexpr float kFastTot = 112.f;
+// A token whose own log is below this ends everything before it: 2^-256 is 0 in
+// fp32 whatever it multiplies.  The log is taken as -256 then, so that sums over a
+// chunk keep the small logs beside it.
+constexpr float kGone = -256.f;
 // how far a kept state's scale may go from 1 (log2) before it is multiplied out
 constexpr double kLevel = 24.0;
 
@@ -297,7 +303,17 @@ template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp_add(float v) {
     return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, true));
 }
-__device__ __forceinline__ float lane_scan(float v) {
+// the same of both halves of a 64-bit value
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_moved(double v) {
+    const int2 x = __builtin_bit_cast(int2, v);
+    return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_update_dpp(0, x.x, CTRL, ROWS, 0xf, true),
+                                                __builtin_amdgcn_update_dpp(0, x.y, CTRL, ROWS, 0xf, true)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) { return v + dpp_moved<CTRL, ROWS>(v); }
+template <typename T>
+__device__ __forceinline__ T lane_scan(T v) {
     v = dpp_add<0x111, 0xf>(v);  // row_shr:1, 2, 4, 8
     v = dpp_add<0x112, 0xf>(v);
     v = dpp_add<0x114, 0xf>(v);
@@ -309,6 +325,15 @@ __device__ __forceinline__ float lane_scan(float v) {
 // the value of the lane below, 0 for lane 0
 __device__ __forceinline__ float lane_shift(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x138, 0xf, 0xf, true));  // wave_shr:1
+}
+__device__ __forceinline__ double lane_shift(double v) { return dpp_moved<0x138, 0xf>(v); }
+// the last lane's value, uniform
+__device__ __forceinline__ float last_lane(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+__device__ __forceinline__ double last_lane(double v) {
+    const int2 x = __builtin_bit_cast(int2, v);
+    return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_readlane(x.x, 63), __builtin_amdgcn_readlane(x.y, 63)));
 }
 
 // Workspace layout, the tables of packed sequences and how a scan is split
