@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
         store_xy();
         const float A = p.A[h];
         float raw_dt = 0.f, dt = 0.f, tot = 0.f;
+        bool gone = false;  // the token ends everything before it (kGone)
         if (wave == 7) {
             raw_dt = rawdt + (p.dt_bias ? p.dt_bias[h] : 0.f);
             dt = p.softplus ? softplus_rel(raw_dt) : raw_dt;
@@ -274,6 +275,9 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
             // D compares sums over the rest of the chunk whose difference may
             // be one token's log: kept in 64 bits, as two floats in LDS
             double sum = static_cast<double>(A) * 1.4426950408889634 * dt;
+            gone = sum < kGone;
+            if (gone) sum = kGone;
+            const float la = static_cast<float>(sum);
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
                 const double o = __shfl_down(sum, d);
@@ -283,7 +287,7 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
             double rest = __shfl_down(sum, 1);
             if (lane == 63) rest = 0.0;
             const float suf = static_cast<float>(rest);
-            const float ecum = fast_exp2(lane_scan(A * kLog2e * dt));
+            const float ecum = fast_exp2(lane_scan(la));
             if (lane < L) {
                 fl[Cf::FDT + lane] = dt;
                 fl[Cf::FSUF + lane] = suf;
@@ -514,7 +518,9 @@ __global__ void __launch_bounds__(512) ssm_grad_kernel(SsmGrad a) {
             }
             right = __shfl_up(right, 1);
             if (lane == 0) right = 0.0;
-            const double dlog = left + right + static_cast<double>(fast_exp2(tot)) * X;
+            // nothing passes through a token that is gone; what its sums leave is
+            // their rounding, and it would meet the huge step in dA
+            const double dlog = gone ? 0.0 : left + right + static_cast<double>(fast_exp2(tot)) * X;
             float dd = static_cast<float>(Cs + (lane < L ? fl[Cf::FED + lane] : 0.f) + out + A * dlog);
             if (p.softplus) dd *= sigmoid_f32(raw_dt);
             if (lane >= len) dd = 0.f;
