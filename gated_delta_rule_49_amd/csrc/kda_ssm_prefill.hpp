@@ -34,13 +34,16 @@ struct ScanCfg {
     static constexpr bool BF = std::is_same<TI, bf16_t>::value, FULL = MODE == SSM_FULL;
     static constexpr int EX = quad<TI>::PARTS;            // parts of an input
     static constexpr int L = BF ? 64 : 32;                // tokens of a chunk
-    static constexpr int ORD = BF ? 2 : 3;
+    // Parts of an fp32 operand of y's products, and the products of parts that are
+    // kept (orders adding up to less than ORD).  Three hold all 24 bits and leave
+    // 2^-20 of a term out: for fp32 inputs or an fp32 y.  A bf16 y between bf16
+    // inputs takes two: cut off after 16 bits, a term is off by at most 2^-14, a
+    // 64th of y's own half step.  (One part of the state is not enough: each of
+    // d_state terms is then off by up to 2^-8, and where they cancel y is off by
+    // several of its steps.)
+    static constexpr int ORD = BF && std::is_same<TO, bf16_t>::value ? 2 : 3;
     static constexpr int XP = 3;                          // parts of w x: the state keeps fp32 accuracy
-    static constexpr int GP = BF ? 2 : 3;                 // parts of the scores
-    // parts of the state in C S, also behind a bf16 y: with one part each of the
-    // sum's d_state terms is off by up to 2^-8 of itself, and where they cancel y
-    // by several of its own steps
-    static constexpr int SP = BF ? 2 : 3;
+    static constexpr int GP = ORD, SP = ORD;              // parts of the scores, of the state in C S
     static constexpr int NT = NS / 16, KS = (NS + 31) / 32, NK = KS * 32;
     static constexpr int CT = PW / 16, ST = L / 16, TK = L / 32;
     // LDS row strides: 16-byte pieces of 16 rows hit all banks (C, scores);

@@ -63,3 +63,32 @@ def test_a_bf16_y(H, G, P, N, step):
     want = R.ssm_scan(*(r[k] for k in ("x", "dt", "A", "B", "C")), initial_state=r["state"])[0]
     mag = R.ssm_scan(np.abs(r["x"]), r["dt"], r["A"], np.abs(r["B"]), np.abs(r["C"]), initial_state=np.abs(r["state"]))[0]
     check_elements(f"H={H} {P}x{N} step {step}", y, want, 2.0 ** -8 * np.abs(want) + 2.0 ** -12 * mag)
+
+
+@pytest.mark.parametrize("N,P", [(16, 16), (32, 64), (64, 128), (128, 64)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_an_fp32_y_of_one_state_row(dtype, N, P):
+    # Steps of 0 and a C that picks one row: y is that row of the state, all 24
+    # bits of it (three bf16 parts hold them, and their sums are exact).
+    B, T, H, G = 2, 70, 4, 2
+    t, _ = inputs(3, B, T, H, G, P, N, dtype, 0.0)
+    row = torch.from_numpy(np.random.default_rng(4).integers(0, N, (B, T, G))).cuda()
+    C = torch.nn.functional.one_hot(row, N).to(dtype)
+    y, _ = kda.ssm_prefill(t["x"], t["dt"], t["A"], t["B"], C, initial_state=t["state"], out_dtype=F32)
+    rows = row.repeat_interleave(H // G, 2).permute(0, 2, 1)[..., None].expand(B, H, T, P)
+    assert torch.equal(y.transpose(1, 2), t["state"].gather(2, rows))
+
+
+@pytest.mark.parametrize("step", [0.01, 0.3])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_an_fp32_y(dtype, step):
+    # One chunk.  Relative to a term: products of parts left out 2^-20 + 2^-21,
+    # accumulators (6 products' sums for each 32 of d_state and of the tokens)
+    # 36 x 2^-24, logs and exponentials 2^-21: below 2^-18.
+    B, H, G, P, N = 2, 4, 2, 64, 128
+    T = 64 if dtype == BF else 32
+    t, r = inputs(5, B, T, H, G, P, N, dtype, step)
+    y, _ = kda.ssm_prefill(t["x"], t["dt"], t["A"], t["B"], t["C"], initial_state=t["state"], out_dtype=F32)
+    want = R.ssm_scan(*(r[k] for k in ("x", "dt", "A", "B", "C")), initial_state=r["state"])[0]
+    mag = R.ssm_scan(np.abs(r["x"]), r["dt"], r["A"], np.abs(r["B"]), np.abs(r["C"]), initial_state=np.abs(r["state"]))[0]
+    check_elements(f"{dtype} step {step}", y, want, 2.0 ** -18 * mag)
