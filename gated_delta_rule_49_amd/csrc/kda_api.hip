@@ -496,6 +496,23 @@ kda_status kda_short_conv_backward(const kda_conv_backward_args *a, void *hip_st
 
 // --------------------------------------------------------------- block norm
 namespace {
+// whether [p, p + n) and [q, q + m) share a byte
+bool overlap(const void *p, int64_t n, const void *q, int64_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + static_cast<uintptr_t>(m) && b < a + static_cast<uintptr_t>(n);
+}
+// out and normed apart from each other, and from each input or on its very rows
+bool block_norm_apart(const kda_block_norm_args *a) {
+    const int64_t e = a->dtype == KDA_F32 ? 4 : 2, row = a->dim * e, plane = a->rows * row;
+    if (overlap(a->out, plane, a->normed, plane)) return false;
+    struct In { const void *ptr; int64_t stride; };
+    for (const In &in : {In{a->x, a->x_stride}, In{a->gate, a->gate_stride}, In{a->residual, a->residual_stride}})
+        for (const void *to : {a->out, a->normed}) {
+            const bool same = to == in.ptr && (a->rows == 1 || in.stride == a->dim);
+            if (!same && overlap(to, plane, in.ptr, (a->rows - 1) * in.stride * e + row)) return false;
+        }
+    return true;
+}
 kda_status check_block_norm(const kda_block_norm_args *a, bool need_ptrs, bool need_out) {
     if (!a) return KDA_ERR_NULL_ARG;
     if (a->rows < 0 || a->dim < 1 || a->group < 1 || a->dim % a->group != 0) return KDA_ERR_BAD_SHAPE;
@@ -509,6 +526,7 @@ kda_status check_block_norm(const kda_block_norm_args *a, bool need_ptrs, bool n
     if (a->rows > 1)  // rows may repeat (stride 0) or be padded, not overlap in part
         for (const int64_t st : {a->x_stride, a->gate ? a->gate_stride : 0, a->residual ? a->residual_stride : 0})
             if (st < 0 || (st > 0 && st < a->dim)) return KDA_ERR_BAD_SHAPE;
+    if (need_out && !block_norm_apart(a)) return KDA_ERR_BAD_SHAPE;
     return KDA_OK;
 }
 NormParams norm_params(const kda_block_norm_args *a) {

@@ -338,8 +338,8 @@ def block_norm(x, residual=None, post_weight=None, gate=None, scale=None, pre_we
     size when group_size is None); ``scale`` and ``pre_weight`` float32 [dim];
     ``gate`` and ``residual`` like x (all three may be slices of wider rows);
     ``gate_activation`` "sigmoid" or "silu".  Returns (out, normed or None),
-    contiguous, x's dtype; ``out`` may be x's, the residual's or the gate's
-    own memory."""
+    contiguous, x's dtype; ``out`` and ``normed`` may each be x's, the
+    residual's or the gate's own memory (any other overlap is refused)."""
     a, dev, dim = _norm_args(x, residual, post_weight, gate, scale, pre_weight, gate_activation, gate_first, eps)
     _post_group(a, post_weight, group_size, dim)
     _dense(dev, out, normed)

@@ -602,7 +602,9 @@ kda_status kda_short_conv_backward(const kda_conv_backward_args *a, void *hip_st
  *   out          DEVICE [rows, dim] dtype, contiguous
  *   normed       DEVICE [rows, dim] dtype, contiguous; required with
  *                pre_weight, NULL without
- * out may alias x, residual or gate (contiguous), normed not out.
+ * out and normed may each be an input's own rows (contiguous); any other
+ * overlap, of each other or of part of an input, is refused
+ * (KDA_ERR_BAD_SHAPE).
  * Supported: 1 <= dim <= 16384, group divides dim, rows * dim < 2^40.  Rows
  * whose sizes, strides and addresses are multiples of 8 channels and 16 bytes
  * are moved as 128-bit vectors; any other row element by element.
