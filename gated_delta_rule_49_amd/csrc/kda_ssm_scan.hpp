@@ -222,17 +222,8 @@ template <> struct quad<bf16_t> {
     static constexpr int PARTS = 1;
     __device__ __forceinline__ void ld(int i, const bf16_t *p) { r[i] = *reinterpret_cast<const uint2 *>(p); }
     __device__ __forceinline__ void zero(int i) { r[i] = make_uint2(0, 0); }
-    // part `part` of the four channels of token i / the four tokens of channel i
+    // part `part` of the four channels of token i
     __device__ __forceinline__ granule row(int i, int) const { granule g; g.u = r[i]; return g; }
-    __device__ __forceinline__ granule col(int i, int) const {
-        granule g;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const uint32_t w = i < 2 ? r[t].x : r[t].y;
-            g.s[t] = static_cast<bf16_t>((i & 1) ? w >> 16 : w & 0xffffu);
-        }
-        return g;
-    }
 };
 template <> struct quad<float> {
     f32x4 r[4];
@@ -249,12 +240,6 @@ template <> struct quad<float> {
         for (int c = 0; c < 4; ++c) g.s[c] = part_of(r[i][c], part);
         return g;
     }
-    __device__ __forceinline__ granule col(int i, int part) const {
-        granule g;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) g.s[t] = part_of(r[t][i], part);
-        return g;
-    }
 };
 
 // PW / 16 neighbouring channels of one token, as a lane loads and stores them
@@ -262,14 +247,12 @@ template <typename T, int CT> struct lanevec;
 template <> struct lanevec<bf16_t, 1> {
     bf16_t u;
     __device__ __forceinline__ void ld(const bf16_t *p) { u = *p; }
-    __device__ __forceinline__ void zero() { u = 0; }
     __device__ __forceinline__ float get(int) const { return bf16_to_f32(u); }
     __device__ __forceinline__ static void st(bf16_t *p, const float (&v)[1]) { *p = f32_to_bf16(v[0]); }
 };
 template <> struct lanevec<bf16_t, 2> {
     uint32_t u;
     __device__ __forceinline__ void ld(const bf16_t *p) { u = *reinterpret_cast<const uint32_t *>(p); }
-    __device__ __forceinline__ void zero() { u = 0; }
     __device__ __forceinline__ float get(int c) const { return __uint_as_float(c ? (u & 0xffff0000u) : (u << 16)); }
     __device__ __forceinline__ static void st(bf16_t *p, const float (&v)[2]) {
         *reinterpret_cast<uint32_t *>(p) = pack_bf16(v[0], v[1]);
@@ -278,14 +261,12 @@ template <> struct lanevec<bf16_t, 2> {
 template <> struct lanevec<float, 1> {
     float u;
     __device__ __forceinline__ void ld(const float *p) { u = *p; }
-    __device__ __forceinline__ void zero() { u = 0.f; }
     __device__ __forceinline__ float get(int) const { return u; }
     __device__ __forceinline__ static void st(float *p, const float (&v)[1]) { *p = v[0]; }
 };
 template <> struct lanevec<float, 2> {
     float2 u;
     __device__ __forceinline__ void ld(const float *p) { u = *reinterpret_cast<const float2 *>(p); }
-    __device__ __forceinline__ void zero() { u = make_float2(0.f, 0.f); }
     __device__ __forceinline__ float get(int c) const { return c ? u.y : u.x; }
     __device__ __forceinline__ static void st(float *p, const float (&v)[2]) { *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]); }
 };
