@@ -21,7 +21,8 @@
 // (3.8 TB/s; a copy of the same bytes takes 39), 61 in all.  8 channels a
 // thread with 16-byte requests took 68 (229 registers, 2 waves a SIMD; 4
 // channels need 144), tiles of 32 tokens 60; held to 128 registers it spills
-// (120).  What is left is the issue rate: about 30 instructions a value.
+// (120).  About 36 vector instructions a value (counted) issue in 31 to
+// 36 us of it; the rest is waiting, at 3 waves a SIMD.
 #include "kda_launch.hpp"
 
 namespace kda {

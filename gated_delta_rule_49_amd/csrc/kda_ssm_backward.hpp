@@ -23,11 +23,13 @@
 //
 // 2 x 4096 tokens, 32 heads of 64 channels, one group, d_state 128, bf16: 208 us,
 // after 2 x 66 us for the states from both ends (each direction by itself took
-// 2 x 40) and 11 for their chains, and before 13 for the sums.  One workgroup fits a CU (127 KB of LDS); vector
+// 2 x 40) and 11 for their chains, and before 13 for the sums.  One workgroup fits a CU (145184 bytes of LDS); vector
 // instructions take 32 % of the cycles, LDS 31 % (14 % conflicts), matrix
 // instructions 11 %: it waits at the three barriers of a head.  Rows 16 banks
 // apart for what is only read by columns cost more in the writes than they
-// gained (4 % slower).
+// gained (4 % slower).  Other shapes are less well served: with 128 bf16 channels
+// 30 to 40 registers spill, and fp32 instances keep an operand of the du tiles in
+// 64 bytes of scratch a lane.
 #pragma once
 #include "kda_ssm_scan.hpp"
 
@@ -72,7 +74,10 @@ __device__ __forceinline__ T sum16(const T *v, int c16) {
 template <typename TI, int NS, int P>
 struct GradCfg {
     static constexpr bool BF = std::is_same<TI, bf16_t>::value;
-    static constexpr int EX = quad<TI>::PARTS, ORD = BF ? 2 : 3, XP = BF ? 2 : 3;
+    static constexpr int EX = quad<TI>::PARTS, ORD = BF ? 2 : 3;
+    // M1, M2 and, for du, G: they make dx, dB and dC alone, which are rounded to
+    // bf16 where the inputs are; two rounded parts are off by 2^-16
+    static constexpr int XP = BF ? 2 : 3;
     // the states' products also make the fp32 sums dA and ddt_bias: all three parts
     static constexpr int SP = 3;
     static constexpr int L = BF ? 64 : 32, SUB = 64 / L, ST = L / 16, TK = L / 32;

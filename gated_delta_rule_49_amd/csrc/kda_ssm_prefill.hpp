@@ -15,13 +15,16 @@
 // scan over all segments at once.
 //
 // 32768 tokens, 64 heads of 64 channels in 8 groups, d_state 128, bf16: phase 1
-// 121 to 142 us, the chain 14, phase 2 302 (257 where no head's decay is wide); the
-// bytes alone would take 131.  Phase 2 spends 47 % of its cycles issuing vector
-// instructions (splitting fp32 values into bf16 parts, scaling, rounding) and
-// 33 % in matrix instructions; the two overlap only between the two waves of a
-// SIMD, which the barriers hold at the same place.  Workgroups of 4 waves, twice
-// as many to a CU, move B twice and gain nothing (140 against 131 us for phase
-// 1); 16 waves of 16 channels spill (520 us for phase 2).
+// 133 to 142 us, the chain 14, phase 2 329 to 354 (315 to 330 where no head's decay
+// is wide); the bytes alone would take 131.  Phase 2 spends 51 % of its cycles
+// issuing vector instructions (splitting fp32 values into bf16 parts, scaling,
+// rounding) and 37 % in matrix instructions; the two overlap only between the two
+// waves of a SIMD, which the barriers hold at the same place.  It spills 24
+// registers.  One part of the state behind y and 32-bit sums of the logs took 293
+// to 308 us, and were wrong (ScanCfg, kda_ssm_scan.hpp).  An fp32 y takes 415 to
+// 425 us, fp32 inputs 1.7 times as long as bf16 ones in all.  Workgroups of 4
+// waves, twice as many to a CU, move B twice and gain nothing (140 against 131 us
+// for phase 1); 16 waves of 16 channels spill (520 us for phase 2).
 #pragma once
 #include "kda_ssm_scan.hpp"
 

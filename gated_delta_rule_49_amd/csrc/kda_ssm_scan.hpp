@@ -1,5 +1,6 @@
 // Selective state space scan in chunked form: shared by the prompt scan
-// (kda_ssm_prefill.hip) and the gradients (kda_ssm_backward.hip).
+// (kda_ssm_prefill.hpp) and the gradients (kda_ssm_backward.hpp); the step sizes'
+// softplus is the token step's too (kda_ssm_decode.hip).
 //
 // Over a chunk of L tokens, with la_t = A dt_t (all logs base 2 in the code),
 // suf_t = sum_{s > t} la_s, tot = sum la, w_t = dt_t 2^suf_t:
@@ -15,10 +16,13 @@
 // thousands (steps of mixed sizes in one head): where y is made the sums are in 64
 // bits, kept as two floats for the second form.
 //
-// Precision: bf16 inputs enter the matrix cores as they are; the state, the
-// scores and the scaled inputs are fp32 values split into bf16 parts (2 parts:
-// 2^-17 of the value).  fp32 inputs are split into 3 parts, and the products
-// of parts down to 2^-24 are kept.  Everything accumulates in fp32.
+// Precision: bf16 inputs enter the matrix cores as they are.  An fp32 operand is
+// split into bf16 parts, every part but the last cut off or rounded: two hold it
+// to 2^-15, three hold all 24 bits.  fp32 inputs take three; so does w x, which
+// makes the state; the scores and the state behind y as many as y's type needs
+// (ScanCfg), the operands of the gradients as theirs (GradCfg).  Products of two
+// later parts, below 2^-14 (2 parts) or 2^-20 (3) of the term, are left out.
+// Everything accumulates in fp32.
 #pragma once
 #include "kda_launch.hpp"
 
@@ -55,9 +59,9 @@ __device__ __forceinline__ float softplus_rel(float x) {
 // 2^(kFastTot / 2) for w, the inverse for the rows.  Low-order parts reach down
 // to about 2^(-kFastTot / 2 - 24), far above the smallest normal number 2^-126,
 // and values below 2^64 do not overflow.  (With the scale fixed at the chunk's
-// end the limit was 56: heads of A = -16 and steps of 0.1 passed it by far, and
-// 32768 tokens of 64 such heads took 334 us in phase 2, 302 so; inputs
-// without wide decays take 257.)
+// end the limit is 56: heads of A = -16 and steps of 0.1 pass it by far, and 32768
+// tokens of 64 such heads take 395 us in phase 2, 329 to 354 so; inputs
+// without wide decays take 315 to 330.)
 constexpr float kFastTot = 112.f;
 // A token whose own log is below this ends everything before it: 2^-256 is 0 in
 // fp32 whatever it multiplies.  The log is taken as -256 then, so that sums over a

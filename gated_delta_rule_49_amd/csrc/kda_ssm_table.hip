@@ -126,10 +126,10 @@ SsmPlan ssm_plan(const SsmParams &p, bool packed, int walks) {
     r.waves = items > 4 ? 8 : 4;
     r.blocks_per_group = (items + r.waves - 1) / r.waves;
     // Equal sequences: one workgroup for each of the 256 CUs, all of one length
-    // (32768 tokens, 64 heads of 64 channels, d_state 128: 121 us for phase 1 and
-    // 13 us for the chain, against 131 and 24 with 512 workgroups).  Packed ones
+    // (32768 tokens, 64 heads of 64 channels, d_state 128: 138 us for phase 1 and
+    // 14 us for the chain, against 150 and 25 with 512 workgroups).  Packed ones
     // end in segments of any length: shorter segments level them (8 sequences of
-    // 1 to 7001 tokens, d_state 64: 177 + 80 us with 512, 220 + 97 with 256).  A
+    // 1 to 7001 tokens, d_state 64: 184 + 83 us with 512, 227 + 99 with 256).  A
     // segment has at least 4 chunks: its state is written and read once, which
     // is the traffic of 2 chunks (d_state 128).
     const int64_t per_seg = static_cast<int64_t>(p.G) * r.blocks_per_group * walks;

@@ -143,7 +143,8 @@ def ssm_prefill(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=False, initial
     slices of a wider token are taken as they are), dt [B,T,H], all float32 or
     all bfloat16; A, D, dt_bias float32 [H].  Per token and head
     dt = softplus(dt + dt_bias) (with ``dt_softplus``, else dt + dt_bias),
-    S = exp(A dt) S + dt B x^T, y = S^T C + D x.  ``cu_seqlens`` (int32 [N+1],
+    S = exp(A dt) S + dt B x^T, y = S^T C + D x.  A step of 0 leaves the state
+    as it is; under the softplus the dtype's lowest value or -inf is one.  ``cu_seqlens`` (int32 [N+1],
     batch 1) packs N documents along T; ``initial_state`` fp32
     [N,H,d_state,d_head] or None (zeros).  Returns (y, final_state or None) or,
     with ``chunk_states``, (y, final_state, states entering every SSM_CHUNK

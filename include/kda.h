@@ -412,6 +412,10 @@ kda_status kda_backward(const kda_backward_args *a, void *hip_stream);
  *     a_t  = exp(A[h] dt_t)
  *     S_t  = a_t S_{t-1} + dt_t B_t x_t^T ,   y_t = S_t^T C_t (+ D[h] x_t)
  *
+ * A step of 0 leaves the state as it is; with dt_softplus a dt of the type's
+ * lowest value or -infinity is such a step (x, B and C finite there: a NaN or
+ * an infinity may reach all of its own sequence's chunk).
+ *
  * x, B and C may be slices of one wider tensor (the convolution's output):
  * their token and batch strides are given in elements, the last two axes are
  * contiguous.
