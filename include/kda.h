@@ -423,7 +423,7 @@ kda_status kda_backward(const kda_backward_args *a, void *hip_stream);
  *   x            DEVICE [B, T, H, d_head]   in_dtype, strides x_stride_*
  *   Bm, Cm       DEVICE [B, T, G, d_state]  in_dtype, strides b_/c_stride_*
  *   dt           DEVICE [B, T, H]           in_dtype, contiguous
- *   A            DEVICE fp32 [H], <= 0 (not checked)
+ *   A            DEVICE fp32 [H], <= 0, as every dt_t is >= 0 (not checked)
  *   D, dt_bias   DEVICE fp32 [H], NULL = none
  *   cu_seqlens   DEVICE int32 [num_seqs + 1], NULL = the B rows are the
  *                sequences; else B == 1 and documents are packed along T.
