@@ -23,6 +23,14 @@ The stages and the recurrence a hybrid model runs beside it (``sublayer.py``):
     out, normed = block_norm(x, residual, post_weight=w, gate=z, pre_weight=w2)
     dx, dres, dw, dz, ds, dw2 = block_norm_backward(x, d_out, d_normed, residual, ...)
 
+The full-attention layer beside them (``latent.py``):
+
+    q = rotary(q, freqs, positions, offset=d_nope)               # freqs from rotary_frequencies
+    rows = latent_append(kv, cache, page_table, lengths, d_latent, norm_weight=w, freqs=freqs, output_rows=True)
+    o, lse = latent_prefill(q, k_nope, k_rope, v)                # expanded form
+    dq, dk_nope, dk_rope, dv = latent_backward(q, k_nope, k_rope, v, o, lse, d_o)
+    o, lse = latent_decode(q_latent, cache, page_table, lengths, d_latent, scale)   # absorbed form
+
 ``prologue`` (prefill and decode) fuses the stages that precede the
 recurrence: PROLOGUE_GATE_SOFTPLUS (log_alpha holds x, log alpha =
 -softplus(x)), PROLOGUE_BETA_SIGMOID (beta holds x, beta = sigmoid(x)),
@@ -46,7 +54,9 @@ __all__ = ["prefill", "prefill_noalloc", "NOALLOC_SCRATCH_BYTES", "decode_step",
            "PROLOGUE_BETA_SIGMOID", "PROLOGUE_QK_L2NORM", "PROLOGUE_ALL",
            "short_conv_backward", "ssm_prefill", "ssm_decode", "ssm_backward", "block_norm", "block_norm_backward",
            "ConvBackwardArgs", "SsmArgs", "SsmDecodeArgs", "SsmBackwardArgs", "BlockNormArgs", "BlockNormBackwardArgs",
-           "GATE_SIGMOID", "GATE_SILU", "SSM_CHUNK"]
+           "GATE_SIGMOID", "GATE_SILU", "SSM_CHUNK",
+           "rotary_frequencies", "rotary", "rotary_backward", "latent_append", "latent_prefill", "latent_backward", "latent_decode",
+           "RotaryArgs", "LatentAppendArgs", "LatentPrefillArgs", "LatentBackwardArgs", "LatentDecodeArgs"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkda.so")
@@ -184,6 +194,51 @@ class BlockNormBackwardArgs(ctypes.Structure):
         z: workspace_bytes""")
 
 
+class RotaryArgs(ctypes.Structure):
+    """Mirror of ``kda_rotary_args`` (include/kda.h)."""
+    _fields_ = _fields("""
+        i: B T H D rotary_dim offset interleaved dtype
+        f: magnitude
+        l: x_stride_b x_stride_t x_stride_h out_stride_b out_stride_t out_stride_h pos_stride_b pos_stride_t
+        p: x positions freqs out""")
+
+
+class LatentAppendArgs(ctypes.Structure):
+    """Mirror of ``kda_latent_append_args`` (include/kda.h)."""
+    _fields_ = _fields("""
+        i: B T num_seqs d_latent d_rope interleaved dtype num_pages page_size max_pages
+        f: eps magnitude
+        l: kv_stride_b kv_stride_t page_stride row_stride table_stride
+        p: kv norm_weight freqs cu_seqlens lengths page_table cache rows device_status""")
+
+
+class LatentPrefillArgs(ctypes.Structure):
+    """Mirror of ``kda_latent_prefill_args`` (include/kda.h)."""
+    _fields_ = _fields("""
+        i: B T S H d_nope d_rope d_v num_seqs in_dtype out_dtype causal
+        f: scale
+        l: q_stride_b q_stride_t q_stride_h k_stride_b k_stride_t k_stride_h r_stride_b r_stride_t v_stride_b v_stride_t v_stride_h
+        p: q k_nope k_rope v cu_seqlens_q cu_seqlens_k o lse device_status workspace
+        z: workspace_bytes""")
+
+
+class LatentBackwardArgs(ctypes.Structure):
+    """Mirror of ``kda_latent_backward_args`` (include/kda.h)."""
+    _fields_ = [("f", LatentPrefillArgs)] + _fields("""
+        p: d_o dq dk_nope dk_rope dv workspace
+        z: workspace_bytes""")
+
+
+class LatentDecodeArgs(ctypes.Structure):
+    """Mirror of ``kda_latent_decode_args`` (include/kda.h)."""
+    _fields_ = _fields("""
+        i: B H n_tokens d_latent d_rope in_dtype out_dtype num_pages page_size max_pages
+        f: scale
+        l: q_stride_b q_stride_t q_stride_h page_stride row_stride table_stride
+        p: q cache page_table lengths o lse device_status workspace
+        z: workspace_bytes""")
+
+
 _lib = None
 
 
@@ -218,12 +273,18 @@ def lib():
         L.kda_backward.restype = I32
         for name, cls in (("kda_short_conv_backward", ConvBackwardArgs), ("kda_ssm_prefill", SsmArgs),
                           ("kda_ssm_decode", SsmDecodeArgs), ("kda_ssm_backward", SsmBackwardArgs),
-                          ("kda_block_norm", BlockNormArgs), ("kda_block_norm_backward", BlockNormBackwardArgs)):
+                          ("kda_block_norm", BlockNormArgs), ("kda_block_norm_backward", BlockNormBackwardArgs),
+                          ("kda_rotary", RotaryArgs), ("kda_rotary_backward", RotaryArgs), ("kda_latent_append", LatentAppendArgs),
+                          ("kda_latent_prefill", LatentPrefillArgs), ("kda_latent_backward", LatentBackwardArgs),
+                          ("kda_latent_decode", LatentDecodeArgs)):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = [ctypes.POINTER(cls), P], I32
         for name, cls in (("kda_short_conv_backward_workspace_bytes", ConvBackwardArgs), ("kda_ssm_workspace_bytes", SsmArgs),
                           ("kda_ssm_backward_workspace_bytes", SsmBackwardArgs),
-                          ("kda_block_norm_backward_workspace_bytes", BlockNormBackwardArgs)):
+                          ("kda_block_norm_backward_workspace_bytes", BlockNormBackwardArgs),
+                          ("kda_latent_prefill_workspace_bytes", LatentPrefillArgs),
+                          ("kda_latent_backward_workspace_bytes", LatentBackwardArgs),
+                          ("kda_latent_decode_workspace_bytes", LatentDecodeArgs)):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = [ctypes.POINTER(cls)], ctypes.c_size_t
         L.kda_ssm_max_chunks.argtypes, L.kda_ssm_max_chunks.restype = [ctypes.POINTER(SsmArgs)], ctypes.c_int64
@@ -635,3 +696,5 @@ def backward(q, k, v, beta, log_alpha, d_o, initial_state=None, d_final_state=No
 
 from .sublayer import (block_norm, block_norm_backward, short_conv_backward, ssm_backward,  # noqa: E402
                        ssm_decode, ssm_prefill)
+from .latent import (latent_append, latent_backward, latent_decode, latent_prefill, rotary, rotary_backward,  # noqa: E402
+                     rotary_frequencies)

@@ -120,6 +120,7 @@ const char *kda_status_string(int32_t s) {
         case KDA_ERR_BAD_SEQLENS: return "cu_seqlens malformed";
         case KDA_ERR_SCRATCH_LIMIT: return "needs more scratch than the allocation-free entry point holds";
         case KDA_ERR_DEVICE_WAIT: return "a hand-off between workgroups of the overlapped prefill failed";
+        case KDA_ERR_BAD_PAGES: return "a page table entry or a length points outside the cache";
         default: return "unknown status";
     }
 }

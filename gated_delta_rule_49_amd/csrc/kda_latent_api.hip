@@ -1,0 +1,329 @@
+// C ABI of latent attention, its positions and its cache (declared in
+// include/kda.h): host-side validation, workspace sizing and dispatch.  No
+// kernel is launched before every argument has been checked; nothing here
+// allocates or synchronises.
+#include "../../include/kda.h"
+#include "kda_latent.hpp"
+
+#include <initializer_list>
+
+using namespace kda;
+
+namespace {
+
+constexpr int64_t kMost31 = (static_cast<int64_t>(1) << 31) - 1;
+
+bool dtype_ok(int t) { return t == KDA_F32 || t == KDA_BF16; }
+int64_t size_of(int t) { return t == KDA_F32 ? 4 : 2; }
+bool flag_ok(int f) { return f == 0 || f == 1; }
+bool misaligned(std::initializer_list<const void *> ptrs) {
+    for (const void *p : ptrs)
+        if (reinterpret_cast<uintptr_t>(p) % 16) return true;
+    return false;
+}
+// strides that rows of 16-byte vectors can have
+kda_status check_strides(std::initializer_list<int64_t> strides) {
+    for (const int64_t st : strides) {
+        if (st < 0 || st > (static_cast<int64_t>(1) << 48)) return KDA_ERR_BAD_SHAPE;
+        if (st % 8) return KDA_ERR_UNSUPPORTED;
+    }
+    return KDA_OK;
+}
+// whether [p, p + n) and [q, q + m) share a byte
+bool overlap(const void *p, int64_t n, const void *q, int64_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && n > 0 && m > 0 && a < b + static_cast<uintptr_t>(m) && b < a + static_cast<uintptr_t>(n);
+}
+kda_status status_of(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
+
+// -------------------------------------------------------------- rotary ----
+// elements from the first to behind the last of a strided [B, T, H, D]
+int64_t extent(const kda_rotary_args *a, int64_t sb, int64_t st, int64_t sh) {
+    return (a->B - 1) * sb + (a->T - 1) * st + (a->H - 1) * sh + a->D;
+}
+// whether no two elements share memory: taken by size, each axis steps over
+// all that the smaller ones reach
+bool apart(const kda_rotary_args *a, int64_t sb, int64_t st, int64_t sh) {
+    struct Axis { int64_t n, s; } ax[3] = {{a->B, sb}, {a->T, st}, {a->H, sh}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (ax[j].s < ax[i].s) std::swap(ax[i], ax[j]);
+    int64_t reach = a->D;
+    for (const Axis &x : ax) {
+        if (x.n <= 1) continue;
+        if (x.s < reach) return false;
+        reach += (x.n - 1) * x.s;
+    }
+    return true;
+}
+kda_status rotary(const kda_rotary_args *a, bool back, void *hip_stream) {
+    if (!a) return KDA_ERR_NULL_ARG;
+    if (a->B < 0 || a->T < 0 || a->H < 1 || a->D < 1 || a->rotary_dim < 0 || a->rotary_dim % 2 || a->offset < 0 ||
+        static_cast<int64_t>(a->offset) + a->rotary_dim > a->D)
+        return KDA_ERR_BAD_SHAPE;
+    if (!dtype_ok(a->dtype) || !flag_ok(a->interleaved) || a->D > 4096 || a->rotary_dim > 1024) return KDA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(a->B) * a->T > kMost31 || static_cast<int64_t>(a->H) * a->D > kMost31) return KDA_ERR_UNSUPPORTED;
+    for (const int64_t st : {a->x_stride_b, a->x_stride_t, a->x_stride_h, a->out_stride_b, a->out_stride_t, a->out_stride_h})
+        if (st < 0 || st > (static_cast<int64_t>(1) << 48)) return KDA_ERR_BAD_SHAPE;
+    if (a->B == 0 || a->T == 0) return KDA_OK;
+    if (!a->x || !a->out || (a->rotary_dim && !a->freqs)) return KDA_ERR_NULL_ARG;
+    const int64_t e = size_of(a->dtype);
+    if (reinterpret_cast<uintptr_t>(a->x) % e || reinterpret_cast<uintptr_t>(a->out) % e) return KDA_ERR_UNSUPPORTED;
+    if (!apart(a, a->out_stride_b, a->out_stride_t, a->out_stride_h)) return KDA_ERR_BAD_SHAPE;
+    const bool same = a->x == a->out && (a->B == 1 || a->x_stride_b == a->out_stride_b) && (a->T == 1 || a->x_stride_t == a->out_stride_t) &&
+                      (a->H == 1 || a->x_stride_h == a->out_stride_h);
+    if (!same && overlap(a->x, extent(a, a->x_stride_b, a->x_stride_t, a->x_stride_h) * e, a->out,
+                         extent(a, a->out_stride_b, a->out_stride_t, a->out_stride_h) * e))
+        return KDA_ERR_BAD_SHAPE;
+    RotaryParams p{};
+    p.x = a->x; p.out = a->out; p.pos = a->positions; p.freqs = a->freqs;
+    p.x_sb = a->x_stride_b; p.x_st = a->x_stride_t; p.x_sh = a->x_stride_h;
+    p.o_sb = a->out_stride_b; p.o_st = a->out_stride_t; p.o_sh = a->out_stride_h;
+    p.p_sb = a->pos_stride_b; p.p_st = a->pos_stride_t;
+    p.B = a->B; p.T = a->T; p.H = a->H; p.D = a->D; p.rot = a->rotary_dim; p.offset = a->offset;
+    p.interleaved = a->interleaved; p.back = back; p.magnitude = a->magnitude;
+    return status_of(launch_rotary(p, a->dtype, static_cast<hipStream_t>(hip_stream)));
+}
+
+// ------------------------------------------------------------- prefill ----
+kda_status check_prefill(const kda_latent_prefill_args *a, bool need_ptrs, bool need_out) {
+    if (!a) return KDA_ERR_NULL_ARG;
+    if (a->B < 1 || a->T < 0 || a->S < 0 || a->H < 1 || a->num_seqs < 0 || a->d_nope < 1 || a->d_rope < 0 || a->d_v < 1) return KDA_ERR_BAD_SHAPE;
+    if (a->d_nope % 8 || a->d_rope % 8 || a->d_v % 8 || static_cast<int64_t>(a->d_nope) + a->d_rope > 192 || a->d_v > 128) return KDA_ERR_UNSUPPORTED;
+    if (!dtype_ok(a->in_dtype) || !dtype_ok(a->out_dtype) || !flag_ok(a->causal)) return KDA_ERR_UNSUPPORTED;
+    if (!a->cu_seqlens_q != !a->cu_seqlens_k) return KDA_ERR_BAD_SHAPE;
+    if (a->cu_seqlens_q ? a->B != 1 || a->num_seqs < 1 : a->num_seqs != a->B) return KDA_ERR_BAD_SHAPE;
+    if (static_cast<int64_t>(a->B) * a->H > (1 << 22) || a->num_seqs > (1 << 20)) return KDA_ERR_UNSUPPORTED;
+    // blocks of a launch: (tokens / 64 + sequences) heads
+    if ((static_cast<int64_t>(a->B) * (std::max(a->T, a->S) / 64 + 1) + a->num_seqs) * a->H > kMost31 / 2) return KDA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(a->B) * std::max(a->T, a->S) > kMost31) return KDA_ERR_UNSUPPORTED;
+    const kda_status st = check_strides({a->q_stride_b, a->q_stride_t, a->q_stride_h, a->k_stride_b, a->k_stride_t, a->k_stride_h, a->r_stride_b,
+                                         a->r_stride_t, a->v_stride_b, a->v_stride_t, a->v_stride_h});
+    if (st != KDA_OK) return st;
+    for (const int64_t t : {a->q_stride_t, a->k_stride_t, a->r_stride_t, a->v_stride_t, static_cast<int64_t>(a->H) * a->d_v})
+        if (t >= (1 << 23)) return KDA_ERR_UNSUPPORTED;  // 32-bit offsets inside a tile
+    if (!need_ptrs) return KDA_OK;
+    if (a->T > 0 && (!a->q || (need_out && (!a->o || !a->lse)))) return KDA_ERR_NULL_ARG;
+    if (a->S > 0 && (!a->k_nope || !a->v || (a->d_rope && !a->k_rope))) return KDA_ERR_NULL_ARG;
+    if (misaligned({a->q, a->k_nope, a->k_rope, a->v, a->o})) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+LatentParams latent_params(const kda_latent_prefill_args *a) {
+    LatentParams p{};
+    p.q = a->q; p.kn = a->k_nope; p.kr = a->k_rope; p.v = a->v;
+    p.q_sb = a->q_stride_b; p.q_st = a->q_stride_t; p.q_sh = a->q_stride_h;
+    p.k_sb = a->k_stride_b; p.k_st = a->k_stride_t; p.k_sh = a->k_stride_h;
+    p.r_sb = a->r_stride_b; p.r_st = a->r_stride_t;
+    p.v_sb = a->v_stride_b; p.v_st = a->v_stride_t; p.v_sh = a->v_stride_h;
+    p.cu_q = a->cu_seqlens_q; p.cu_k = a->cu_seqlens_k;
+    p.o = a->o; p.lse = a->lse;
+    p.B = a->B; p.T = a->T; p.S = a->S; p.H = a->H; p.dn = a->d_nope; p.dr = a->d_rope; p.dv = a->d_v; p.N = a->num_seqs;
+    p.causal = a->causal; p.scale = a->scale;
+    return p;
+}
+// status words, the table of the queries' tiles, of the keys' (gradients),
+// then the gradients' fp32 buffers
+struct Layout {
+    LatentTiles q, k;
+    size_t entry_q, entry_k, delta, part, bytes;
+};
+Layout latent_layout(const kda_latent_prefill_args *a, bool grad) {
+    Layout l{};
+    const bool packed = a->cu_seqlens_q != nullptr;
+    const int size_q = grad ? latent_grad_tile_q(a->in_dtype) : latent_tile_q(a->in_dtype), size_k = latent_grad_tile_k(a->in_dtype);
+    l.q.bound = l.q.per_seq = latent_tiles_bound(a->T, a->num_seqs, size_q, packed);
+    l.k.bound = l.k.per_seq = latent_tiles_bound(a->S, a->num_seqs, size_k, packed);
+    l.entry_q = kAlign;
+    l.entry_k = l.entry_q + (packed ? align_up(sizeof(int2) * l.q.bound) : 0);
+    l.delta = l.entry_k + (packed && grad ? align_up(sizeof(int2) * l.k.bound) : 0);
+    l.part = l.delta + (grad ? align_up(sizeof(float) * a->B * a->T * a->H) : 0);
+    l.bytes = l.part + (grad ? align_up(sizeof(float) * a->H * a->B * a->S * a->d_rope) : 0);
+    return l;
+}
+// the table of packed sequences; unpacked calls have their status set
+hipError_t prepare_tiles(const kda_latent_prefill_args *a, Layout &l, char *ws, bool grad, int32_t *user_status, hipStream_t s) {
+    l.q.entry = reinterpret_cast<int2 *>(ws + l.entry_q);
+    l.k.entry = reinterpret_cast<int2 *>(ws + l.entry_k);
+    int32_t *word = reinterpret_cast<int32_t *>(ws);
+    l.q.count = word + 1;
+    l.k.count = word + 2;
+    if (!a->cu_seqlens_q) return user_status ? launch_status_word(user_status, s) : hipSuccess;
+    LatentTable t{};
+    t.cu_q = a->cu_seqlens_q; t.cu_k = a->cu_seqlens_k;
+    t.T = a->T; t.S = a->S; t.N = a->num_seqs;
+    t.size_q = grad ? latent_grad_tile_q(a->in_dtype) : latent_tile_q(a->in_dtype);
+    t.size_k = latent_grad_tile_k(a->in_dtype);
+    t.bound_q = l.q.bound;
+    t.bound_k = l.k.bound;
+    t.entry_q = reinterpret_cast<int2 *>(ws + l.entry_q);
+    t.entry_k = grad ? reinterpret_cast<int2 *>(ws + l.entry_k) : nullptr;
+    t.word = word;
+    t.user_status = user_status;
+    return launch_latent_table(t, s);
+}
+kda_status check_backward(const kda_latent_backward_args *a, bool need_ptrs) {
+    if (!a) return KDA_ERR_NULL_ARG;
+    const kda_status st = check_prefill(&a->f, need_ptrs, true);
+    if (st != KDA_OK) return st;
+    if (!need_ptrs) return KDA_OK;
+    if (a->f.T > 0 && (!a->d_o || !a->dq)) return KDA_ERR_NULL_ARG;
+    if (a->f.S > 0 && (!a->dk_nope || !a->dv || (a->f.d_rope && !a->dk_rope))) return KDA_ERR_NULL_ARG;
+    if (!a->f.d_rope && a->dk_rope) return KDA_ERR_BAD_SHAPE;
+    if (misaligned({a->d_o, a->dq, a->dk_nope, a->dk_rope, a->dv})) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// -------------------------------------------------------------- decode ----
+kda_status check_pages(int32_t num_pages, int32_t page_size, int32_t max_pages, int64_t page_stride, int64_t row_stride, int64_t table_stride, int64_t d) {
+    if (num_pages < 1 || page_size < 1 || max_pages < 1 || table_stride < 0) return KDA_ERR_BAD_SHAPE;
+    if (static_cast<int64_t>(max_pages) * page_size > kMost31) return KDA_ERR_UNSUPPORTED;
+    const kda_status st = check_strides({page_stride, row_stride});
+    if (st != KDA_OK) return st;
+    // rows, and pages, that do not share memory
+    if ((page_size > 1 && row_stride < d) || (num_pages > 1 && page_stride < d)) return KDA_ERR_BAD_SHAPE;
+    return KDA_OK;
+}
+kda_status check_decode(const kda_latent_decode_args *a, bool need_ptrs) {
+    if (!a) return KDA_ERR_NULL_ARG;
+    if (a->B < 0 || a->H < 1 || a->n_tokens < 1 || a->d_latent < 1 || a->d_rope < 0) return KDA_ERR_BAD_SHAPE;
+    if (a->d_latent % 8 || a->d_rope % 8 || a->d_latent > 512 || static_cast<int64_t>(a->d_latent) + a->d_rope > 576) return KDA_ERR_UNSUPPORTED;
+    if (!dtype_ok(a->in_dtype) || !dtype_ok(a->out_dtype)) return KDA_ERR_UNSUPPORTED;
+    if (a->B > 65536 || static_cast<int64_t>(a->n_tokens) * a->H >= (1 << 24) || static_cast<int64_t>(a->B) * a->n_tokens * a->H >= (1 << 24))
+        return KDA_ERR_UNSUPPORTED;
+    kda_status st = check_pages(a->num_pages, a->page_size, a->max_pages, a->page_stride, a->row_stride, a->table_stride, a->d_latent + a->d_rope);
+    if (st != KDA_OK) return st;
+    st = check_strides({a->q_stride_b, a->q_stride_t, a->q_stride_h});
+    if (st != KDA_OK) return st;
+    if (!need_ptrs || a->B == 0) return KDA_OK;
+    if (!a->q || !a->cache || !a->page_table || !a->lengths || !a->o || !a->lse) return KDA_ERR_NULL_ARG;
+    if (misaligned({a->q, a->cache, a->o})) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+LatentDecodePlan decode_plan(const kda_latent_decode_args *a) {
+    return latent_decode_plan(a->B, a->H, a->n_tokens, a->d_latent, a->d_rope, static_cast<int64_t>(a->max_pages) * a->page_size, a->in_dtype);
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_rotary(const kda_rotary_args *a, void *hip_stream) { return rotary(a, false, hip_stream); }
+kda_status kda_rotary_backward(const kda_rotary_args *a, void *hip_stream) { return rotary(a, true, hip_stream); }
+
+kda_status kda_latent_append(const kda_latent_append_args *a, void *hip_stream) {
+    if (!a) return KDA_ERR_NULL_ARG;
+    if (a->B < 0 || a->T < 0 || a->num_seqs < 0 || a->d_latent < 1 || a->d_rope < 0) return KDA_ERR_BAD_SHAPE;
+    if (a->d_latent % 8 || a->d_rope % 8 || a->d_latent > 2048 || a->d_rope > 256) return KDA_ERR_UNSUPPORTED;
+    if (!dtype_ok(a->dtype) || !flag_ok(a->interleaved)) return KDA_ERR_UNSUPPORTED;
+    if (!(a->eps >= 0.f)) return KDA_ERR_BAD_SHAPE;
+    if (a->cu_seqlens ? a->B != 1 || a->num_seqs < 1 : a->num_seqs != a->B) return KDA_ERR_BAD_SHAPE;
+    if (static_cast<int64_t>(a->B) * a->T > kMost31) return KDA_ERR_UNSUPPORTED;
+    const int64_t d = a->d_latent + a->d_rope, e = size_of(a->dtype);
+    kda_status st = check_pages(a->num_pages, a->page_size, a->max_pages, a->page_stride, a->row_stride, a->table_stride, d);
+    if (st != KDA_OK) return st;
+    st = check_strides({a->kv_stride_b, a->kv_stride_t});
+    if (st != KDA_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    if (a->B > 0 && a->T > 0) {
+        if (!a->kv || !a->cache || !a->page_table || !a->lengths) return KDA_ERR_NULL_ARG;
+        if (misaligned({a->kv, a->cache, a->rows})) return KDA_ERR_UNSUPPORTED;
+        const int64_t kv = ((a->B - 1) * a->kv_stride_b + (a->T - 1) * a->kv_stride_t + d) * e;
+        const int64_t cache = ((a->num_pages - 1) * a->page_stride + (a->page_size - 1) * a->row_stride + d) * e;
+        const int64_t rows = static_cast<int64_t>(a->B) * a->T * d * e;
+        if (overlap(a->kv, kv, a->cache, cache) || overlap(a->rows, rows, a->kv, kv) || overlap(a->rows, rows, a->cache, cache)) return KDA_ERR_BAD_SHAPE;
+    }
+    if (a->device_status && launch_status_word(a->device_status, s) != hipSuccess) return KDA_ERR_HIP;
+    if (a->B == 0 || a->T == 0) return KDA_OK;
+    LatentAppendParams p{};
+    p.kv = a->kv; p.weight = a->norm_weight; p.freqs = a->freqs; p.cu = a->cu_seqlens; p.lengths = a->lengths; p.page_table = a->page_table;
+    p.cache = a->cache; p.rows = a->rows; p.status = a->device_status;
+    p.kv_sb = a->kv_stride_b; p.kv_st = a->kv_stride_t;
+    p.page_stride = a->page_stride; p.row_stride = a->row_stride; p.table_stride = a->table_stride;
+    p.B = a->B; p.T = a->T; p.N = a->num_seqs; p.dc = a->d_latent; p.dr = a->d_rope; p.interleaved = a->interleaved;
+    p.num_pages = a->num_pages; p.page_size = a->page_size; p.max_pages = a->max_pages;
+    p.eps = a->eps; p.magnitude = a->magnitude;
+    return status_of(launch_latent_append(p, a->dtype, s));
+}
+
+size_t kda_latent_prefill_workspace_bytes(const kda_latent_prefill_args *a) {
+    return check_prefill(a, false, false) == KDA_OK ? latent_layout(a, false).bytes : 0;
+}
+
+kda_status kda_latent_prefill(const kda_latent_prefill_args *a, void *hip_stream) {
+    const kda_status st = check_prefill(a, true, true);
+    if (st != KDA_OK) return st;
+    if (!a->workspace) return KDA_ERR_NULL_ARG;
+    if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign) return KDA_ERR_BAD_SHAPE;
+    Layout l = latent_layout(a, false);
+    if (a->workspace_bytes < l.bytes) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    char *ws = static_cast<char *>(a->workspace);
+    hipError_t e = prepare_tiles(a, l, ws, false, a->device_status, s);
+    if (e != hipSuccess) return KDA_ERR_HIP;
+    if (a->T == 0) return KDA_OK;
+    LatentParams p = latent_params(a);
+    p.tq = l.q;
+    p.status = reinterpret_cast<int32_t *>(ws);
+    return status_of(launch_latent_prefill(p, a->in_dtype, a->out_dtype, s));
+}
+
+size_t kda_latent_backward_workspace_bytes(const kda_latent_backward_args *a) {
+    return check_backward(a, false) == KDA_OK ? latent_layout(&a->f, true).bytes : 0;
+}
+
+kda_status kda_latent_backward(const kda_latent_backward_args *a, void *hip_stream) {
+    const kda_status st = check_backward(a, true);
+    if (st != KDA_OK) return st;
+    if (!a->workspace) return KDA_ERR_NULL_ARG;
+    if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign) return KDA_ERR_BAD_SHAPE;
+    Layout l = latent_layout(&a->f, true);
+    if (a->workspace_bytes < l.bytes) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    char *ws = static_cast<char *>(a->workspace);
+    hipError_t e = prepare_tiles(&a->f, l, ws, true, a->f.device_status, s);
+    if (e != hipSuccess) return KDA_ERR_HIP;
+    LatentGradParams g{};
+    g.f = latent_params(&a->f);
+    g.f.tq = l.q;
+    g.f.status = reinterpret_cast<int32_t *>(ws);
+    g.tk = l.k;
+    g.d_o = a->d_o;
+    g.o_dtype = a->f.out_dtype;
+    g.dq = a->dq; g.dkn = a->dk_nope; g.dkr = a->dk_rope; g.dv = a->dv;
+    g.delta = reinterpret_cast<float *>(ws + l.delta);
+    g.dkr_part = reinterpret_cast<float *>(ws + l.part);
+    return status_of(launch_latent_backward(g, a->f.in_dtype, s));
+}
+
+size_t kda_latent_decode_workspace_bytes(const kda_latent_decode_args *a) {
+    return check_decode(a, false) == KDA_OK ? decode_plan(a).bytes() + kAlign : 0;
+}
+
+kda_status kda_latent_decode(const kda_latent_decode_args *a, void *hip_stream) {
+    const kda_status st = check_decode(a, true);
+    if (st != KDA_OK) return st;
+    if (!a->workspace) return KDA_ERR_NULL_ARG;
+    if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign) return KDA_ERR_BAD_SHAPE;
+    if (a->workspace_bytes < kda_latent_decode_workspace_bytes(a)) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    if (a->device_status && launch_status_word(a->device_status, s) != hipSuccess) return KDA_ERR_HIP;
+    if (a->B == 0) return KDA_OK;
+    const LatentDecodePlan plan = decode_plan(a);
+    LatentDecodeParams p{};
+    p.q = a->q; p.cache = a->cache;
+    p.q_sb = a->q_stride_b; p.q_st = a->q_stride_t; p.q_sh = a->q_stride_h;
+    p.page_stride = a->page_stride; p.row_stride = a->row_stride; p.table_stride = a->table_stride;
+    p.page_table = a->page_table; p.lengths = a->lengths;
+    p.o = a->o; p.lse = a->lse; p.status = a->device_status;
+    char *ws = static_cast<char *>(a->workspace);
+    p.part_o = reinterpret_cast<float *>(ws);
+    p.part_lse = reinterpret_cast<float *>(ws + plan.o_bytes);
+    p.info = reinterpret_cast<int2 *>(ws + plan.o_bytes + plan.lse_bytes);
+    p.B = a->B; p.H = a->H; p.m = a->n_tokens; p.dc = a->d_latent; p.dr = a->d_rope;
+    p.num_pages = a->num_pages; p.page_size = a->page_size; p.max_pages = a->max_pages;
+    p.workers = plan.workers;
+    p.scale = a->scale;
+    return status_of(launch_latent_decode(p, plan, a->in_dtype, a->out_dtype, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,377 @@
+// Latent attention's expanded form on the fp32 matrix cores: forward and
+// gradients for fp32 inputs.
+//
+// Everything is written with the operand that a wave owns along the COLUMNS of
+// the products (v_mfma_f32_16x16x4_f32: A is 16 x 4, lane l holds row l % 16,
+// k = l / 16; B likewise by columns; C/D: lane l holds column l % 16, rows
+// 4 (l / 16) + j).  The forward and the queries' gradient own 16 queries,
+//     S^T = K Q^T,   O^T += V^T P^T,   dP^T = V dO^T,   dQ^T += K^T dS^T,
+// the keys' gradient 16 keys,
+//     S = Q K^T,     dV^T += dO^T P,   dP = dO V^T,     dK^T += Q^T dS.
+// A C tile's register j is then row 4 g + j (g = l / 16) of the wave's column,
+// which is what the next product's B operand wants when its contraction takes
+// rows {4 g + j : g = 0..3} in step j: P and dS go from accumulator to operand
+// without leaving their registers, and the shared operand is read from its
+// row-major LDS tile by rows (16 bytes, four steps) or by columns (4 bytes).
+// Rows of LDS tiles are 4 floats longer than their channels: 8 rows of a
+// 16-byte read then fall on 32 different banks.
+//
+// Softmax: running maximum and sum per query in fp32; a lane sees the query of
+// its column and a quarter of the tile's keys.
+#include "kda_latent.hpp"
+
+namespace kda {
+
+namespace {
+
+constexpr int kTileQ = 64, kTileK = 64;  // four waves of 16
+constexpr int kStep = 32;                // tokens of the other side per step
+
+__device__ __forceinline__ f32x4 mfma_f32(float a, float b, const f32x4 &c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x4 load4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
+__device__ __forceinline__ f32x4 load4(const bf16_t *p) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)};
+}
+__device__ __forceinline__ void store4(float *p, const f32x4 &v) { *reinterpret_cast<f32x4 *>(p) = v; }
+__device__ __forceinline__ void store4(bf16_t *p, const f32x4 &v) {
+    const uint32_t a = static_cast<uint32_t>(f32_to_bf16(v[0])) | static_cast<uint32_t>(f32_to_bf16(v[1])) << 16;
+    const uint32_t b = static_cast<uint32_t>(f32_to_bf16(v[2])) | static_cast<uint32_t>(f32_to_bf16(v[3])) << 16;
+    *reinterpret_cast<uint2 *>(p) = make_uint2(a, b);
+}
+
+// four channels from `c` of a key: its own part, the shared part, zeros behind
+template <typename T>
+__device__ __forceinline__ f32x4 key4(const LatentParams &p, const T *kn, const T *kr, int64_t token, int c) {
+    if (c < p.dn) return load4(kn + token * p.k_st + c);
+    if (c < p.dn + p.dr) return load4(kr + token * p.r_st + c - p.dn);
+    return f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
+// rows [r0, r0 + kStep) of `n` tokens into an LDS tile; zeros outside
+template <int D, typename F>
+__device__ __forceinline__ void stage(float *tile, int r0, int n, F &&row4) {
+    for (int i = threadIdx.x; i < kStep * (D / 4); i += 256) {
+        const int r = i / (D / 4), c = 4 * (i % (D / 4));
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        if (r0 + r < n) v = row4(r0 + r, c);
+        *reinterpret_cast<f32x4 *>(tile + r * (D + 4) + c) = v;
+    }
+}
+
+// C tile of 16 rows of an LDS tile (from `row`) by the wave's 16 columns
+template <int D>
+__device__ __forceinline__ f32x4 by_rows(const float *tile, int row, const f32x4 (&own)[D / 16], int g, int c16) {
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+        const f32x4 a = *reinterpret_cast<const f32x4 *>(tile + (row + c16) * (D + 4) + 16 * s + 4 * g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc = mfma_f32(a[j], own[s][j], acc);
+    }
+    return acc;
+}
+// acc (channels by the wave's columns) += tile^T w, w a C tile over rows [row, row + 16)
+template <int D>
+__device__ __forceinline__ void by_cols(f32x4 (&acc)[D / 16], const float *tile, int row, const f32x4 &w, int g, int c16) {
+#pragma unroll
+    for (int b = 0; b < D / 16; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[b] = mfma_f32(tile[(row + 4 * g + j) * (D + 4) + 16 * b + c16], w[j], acc[b]);
+}
+
+__device__ __forceinline__ float quarter_max(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float quarter_sum(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+template <typename T, typename O, int DK, int DV>
+__global__ void __launch_bounds__(256) prefill_f32_kernel(LatentParams p) {
+    __shared__ float s_k[kStep * (DK + 4)], s_v[kStep * (DV + 4)];
+    const LatentPlace a = latent_place(p, p.tq, blockIdx.x, p.causal);
+    if (!a.valid) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c16 = lane & 15;
+    const T *kn = static_cast<const T *>(p.kn) + a.b * p.k_sb + a.h * p.k_sh + a.k0 * p.k_st;
+    const T *kr = static_cast<const T *>(p.kr) + a.b * p.r_sb + a.k0 * p.r_st;
+    const T *v = static_cast<const T *>(p.v) + a.b * p.v_sb + a.h * p.v_sh + a.k0 * p.v_st;
+    const int qi = a.tile * kTileQ + wave * 16 + c16;  // the lane's query
+    const T *q = static_cast<const T *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + (static_cast<int64_t>(a.q0) + qi) * p.q_st;
+    f32x4 qf[DK / 16];
+#pragma unroll
+    for (int s = 0; s < DK / 16; ++s) {
+        const int c = 16 * s + 4 * g;
+        qf[s] = qi < a.tq && c < p.dn + p.dr ? load4(q + c) : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    const int last_q = min(a.tq, (a.tile + 1) * kTileQ) - 1;
+    const int shift = a.tk - a.tq;                        // query i sees keys up to i + shift
+    const int n = p.causal ? min(a.tk, last_q + shift + 1) : a.tk;
+    const int limit = p.causal ? min(n, qi + shift + 1) : n;  // the lane's own
+    const float c = p.scale * kLog2e;
+    f32x4 acc[DV / 16];
+#pragma unroll
+    for (int b = 0; b < DV / 16; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float top = -INFINITY, sum = 0.f;
+    for (int k0 = 0; k0 < n; k0 += kStep) {
+        __syncthreads();
+        stage<DK>(s_k, k0, n, [&](int r, int ch) { return key4<T>(p, kn, kr, r, ch); });
+        stage<DV>(s_v, k0, n, [&](int r, int ch) { return ch < p.dv ? load4(v + static_cast<int64_t>(r) * p.v_st + ch) : f32x4{0.f, 0.f, 0.f, 0.f}; });
+        __syncthreads();
+        f32x4 s[2];
+        float most = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s[t] = by_rows<DK>(s_k, 16 * t, qf, g, c16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[t][j] = k0 + 16 * t + 4 * g + j < limit ? s[t][j] * c : -INFINITY;
+                most = fmaxf(most, s[t][j]);
+            }
+        }
+        most = fmaxf(top, quarter_max(most));
+        const float base = most == -INFINITY ? 0.f : most;  // nothing seen yet
+        const float keep = fast_exp2(top - base);
+        top = most;
+        sum *= keep;
+#pragma unroll
+        for (int b = 0; b < DV / 16; ++b) acc[b] *= keep;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[t][j] = fast_exp2(s[t][j] - base);
+                sum += s[t][j];
+            }
+            by_cols<DV>(acc, s_v, 16 * t, s[t], g, c16);
+        }
+    }
+    sum = quarter_sum(sum);
+    if (qi >= a.tq) return;
+    const int64_t row = (a.q_row + qi) * p.H + a.h;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    O *o = static_cast<O *>(p.o) + row * p.dv;
+#pragma unroll
+    for (int b = 0; b < DV / 16; ++b)
+        if (16 * b + 4 * g < p.dv) store4(o + 16 * b + 4 * g, acc[b] * inv);
+    if (g == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+// delta = rowsum(d_o o), one wave a (token, head); o may be kept in fp32
+template <typename T, typename O>
+__global__ void __launch_bounds__(256) delta_f32_kernel(LatentGradParams g) {
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (row >= static_cast<int64_t>(g.f.B) * g.f.T * g.f.H) return;
+    const O *o = static_cast<const O *>(g.f.o) + row * g.f.dv;
+    const T *d = static_cast<const T *>(g.d_o) + row * g.f.dv;
+    float s = 0.f;
+    for (int c = lane; c < g.f.dv; c += 64) s = fmaf(io<O>::ld(o, c), io<T>::ld(d, c), s);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) s += __shfl_xor(s, x);
+    if (lane == 0) g.delta[row] = s;
+}
+
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(256) grad_q_f32_kernel(LatentGradParams gp) {
+    __shared__ float s_k[kStep * (DK + 4)], s_v[kStep * (DV + 4)];
+    const LatentParams &p = gp.f;
+    const LatentPlace a = latent_place(p, p.tq, blockIdx.x, p.causal);
+    if (!a.valid) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c16 = lane & 15;
+    const T *kn = static_cast<const T *>(p.kn) + a.b * p.k_sb + a.h * p.k_sh + a.k0 * p.k_st;
+    const T *kr = static_cast<const T *>(p.kr) + a.b * p.r_sb + a.k0 * p.r_st;
+    const T *v = static_cast<const T *>(p.v) + a.b * p.v_sb + a.h * p.v_sh + a.k0 * p.v_st;
+    const int qi = a.tile * kTileQ + wave * 16 + c16;
+    const bool inside = qi < a.tq;
+    const int64_t row = (a.q_row + qi) * p.H + a.h;
+    const T *q = static_cast<const T *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + (static_cast<int64_t>(a.q0) + qi) * p.q_st;
+    const T *d_o = static_cast<const T *>(gp.d_o) + row * p.dv;
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    f32x4 qf[DK / 16], df[DV / 16], acc[DK / 16];
+#pragma unroll
+    for (int s = 0; s < DK / 16; ++s) {
+        const int c = 16 * s + 4 * g;
+        qf[s] = inside && c < p.dn + p.dr ? load4(q + c) : zero;
+        acc[s] = zero;
+    }
+#pragma unroll
+    for (int s = 0; s < DV / 16; ++s) {
+        const int c = 16 * s + 4 * g;
+        df[s] = inside && c < p.dv ? load4(d_o + c) : zero;
+    }
+    const float lse2 = inside ? p.lse[row] * kLog2e : 0.f, delta = inside ? gp.delta[row] : 0.f;
+    const int last_q = min(a.tq, (a.tile + 1) * kTileQ) - 1, shift = a.tk - a.tq;
+    const int n = p.causal ? min(a.tk, last_q + shift + 1) : a.tk;
+    const int limit = inside ? (p.causal ? min(n, qi + shift + 1) : n) : 0;
+    const float c = p.scale * kLog2e;
+    for (int k0 = 0; k0 < n; k0 += kStep) {
+        __syncthreads();
+        stage<DK>(s_k, k0, n, [&](int r, int ch) { return key4<T>(p, kn, kr, r, ch); });
+        stage<DV>(s_v, k0, n, [&](int r, int ch) { return ch < p.dv ? load4(v + static_cast<int64_t>(r) * p.v_st + ch) : f32x4{0.f, 0.f, 0.f, 0.f}; });
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const f32x4 s = by_rows<DK>(s_k, 16 * t, qf, g, c16);
+            f32x4 dp = by_rows<DV>(s_v, 16 * t, df, g, c16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                dp[j] = k0 + 16 * t + 4 * g + j < limit ? fast_exp2(s[j] * c - lse2) * (dp[j] - delta) * p.scale : 0.f;
+            by_cols<DK>(acc, s_k, 16 * t, dp, g, c16);
+        }
+    }
+    if (!inside) return;
+    T *dq = static_cast<T *>(gp.dq) + row * (p.dn + p.dr);
+#pragma unroll
+    for (int b = 0; b < DK / 16; ++b)
+        if (16 * b + 4 * g < p.dn + p.dr) store4(dq + 16 * b + 4 * g, acc[b]);
+}
+
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
+    __shared__ float s_q[kStep * (DK + 4)], s_d[kStep * (DV + 4)];
+    __shared__ float s_lse[kStep], s_delta[kStep];
+    const LatentParams &p = gp.f;
+    const LatentPlace a = latent_place(p, gp.tk, blockIdx.x, false);  // early keys are seen by more queries
+    if (!a.valid) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c16 = lane & 15;
+    const int ki = a.tile * kTileK + wave * 16 + c16;  // the lane's key
+    const bool inside = ki < a.tk;
+    const int64_t token = static_cast<int64_t>(a.k0) + ki;
+    const T *kn = static_cast<const T *>(p.kn) + a.b * p.k_sb + a.h * p.k_sh;
+    const T *kr = static_cast<const T *>(p.kr) + a.b * p.r_sb;
+    const T *v = static_cast<const T *>(p.v) + a.b * p.v_sb + a.h * p.v_sh + token * p.v_st;
+    const T *q = static_cast<const T *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + a.q0 * p.q_st;
+    const T *d_o = static_cast<const T *>(gp.d_o) + (a.q_row * p.H + a.h) * p.dv;
+    const int64_t d_st = static_cast<int64_t>(p.H) * p.dv;
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    f32x4 kf[DK / 16], vf[DV / 16], dk[DK / 16], dv[DV / 16];
+#pragma unroll
+    for (int s = 0; s < DK / 16; ++s) {
+        kf[s] = inside ? key4<T>(p, kn, kr, token, 16 * s + 4 * g) : zero;
+        dk[s] = zero;
+    }
+#pragma unroll
+    for (int s = 0; s < DV / 16; ++s) {
+        vf[s] = inside && 16 * s + 4 * g < p.dv ? load4(v + 16 * s + 4 * g) : zero;
+        dv[s] = zero;
+    }
+    const int shift = a.tk - a.tq;
+    const float c = p.scale * kLog2e;
+    // the first query that sees the tile's first key
+    int i0 = p.causal ? max(0, a.tile * kTileK - shift) : 0;
+    i0 = i0 / kStep * kStep;
+    for (; i0 < a.tq; i0 += kStep) {
+        __syncthreads();
+        stage<DK>(s_q, i0, a.tq, [&](int r, int ch) { return ch < p.dn + p.dr ? load4(q + static_cast<int64_t>(r) * p.q_st + ch) : f32x4{0.f, 0.f, 0.f, 0.f}; });
+        stage<DV>(s_d, i0, a.tq, [&](int r, int ch) { return ch < p.dv ? load4(d_o + r * d_st + ch) : f32x4{0.f, 0.f, 0.f, 0.f}; });
+        if (threadIdx.x < kStep) {
+            const int i = i0 + threadIdx.x;
+            const int64_t row = (a.q_row + i) * p.H + a.h;
+            s_lse[threadIdx.x] = i < a.tq ? p.lse[row] * kLog2e : 0.f;
+            s_delta[threadIdx.x] = i < a.tq ? gp.delta[row] : 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            f32x4 s = by_rows<DK>(s_q, 16 * t, kf, g, c16);
+            f32x4 dp = by_rows<DV>(s_d, 16 * t, vf, g, c16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 16 * t + 4 * g + j, i = i0 + r;
+                const bool sees = inside && i < a.tq && (!p.causal || ki <= i + shift);
+                s[j] = sees ? fast_exp2(s[j] * c - s_lse[r]) : 0.f;
+                dp[j] = sees ? s[j] * (dp[j] - s_delta[r]) * p.scale : 0.f;
+            }
+            by_cols<DV>(dv, s_d, 16 * t, s, g, c16);
+            by_cols<DK>(dk, s_q, 16 * t, dp, g, c16);
+        }
+    }
+    if (!inside) return;
+    const int64_t key = a.k_row + ki;
+    T *dkn = static_cast<T *>(gp.dkn) + (key * p.H + a.h) * p.dn;
+    T *dvp = static_cast<T *>(gp.dv) + (key * p.H + a.h) * p.dv;
+    float *part = gp.dkr_part + (static_cast<int64_t>(a.h) * p.B * p.S + key) * p.dr;
+#pragma unroll
+    for (int b = 0; b < DK / 16; ++b) {
+        const int ch = 16 * b + 4 * g;
+        if (ch < p.dn) store4(dkn + ch, dk[b]);
+        else if (ch < p.dn + p.dr) store4(part + ch - p.dn, dk[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < DV / 16; ++b)
+        if (16 * b + 4 * g < p.dv) store4(dvp + 16 * b + 4 * g, dv[b]);
+}
+
+// dk_rope: the heads' shares added in order
+template <typename T>
+__global__ void __launch_bounds__(256) grad_rope_f32_kernel(LatentGradParams g) {
+    if (g.f.cu_q && *g.f.status != 0) return;
+    const int64_t plane = static_cast<int64_t>(g.f.B) * g.f.S * g.f.dr;
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (at >= plane) return;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    for (int h = 0; h < g.f.H; ++h) sum += load4(g.dkr_part + h * plane + at);
+    store4(static_cast<T *>(g.dkr) + at, sum);
+}
+
+template <typename T, typename O, int DK, int DV>
+hipError_t run_prefill(const LatentParams &p, hipStream_t s) {
+    const int grid = p.cu_q ? p.H * p.tq.bound : p.H * p.N * p.tq.per_seq;
+    prefill_f32_kernel<T, O, DK, DV><<<grid, 256, 0, s>>>(p);
+    return hipGetLastError();
+}
+template <typename T, typename O>
+hipError_t pick_prefill(const LatentParams &p, hipStream_t s) {
+    const int dk = p.dn + p.dr;
+    if (dk <= 64 && p.dv <= 64) return run_prefill<T, O, 64, 64>(p, s);
+    if (dk <= 128) return run_prefill<T, O, 128, 128>(p, s);
+    return run_prefill<T, O, 192, 128>(p, s);
+}
+
+template <typename T, int DK, int DV>
+hipError_t run_grad(const LatentGradParams &g, hipStream_t s) {
+    const LatentParams &p = g.f;
+    const int64_t rows = static_cast<int64_t>(p.B) * p.T * p.H, keys = static_cast<int64_t>(p.B) * p.S;
+    const unsigned grid_d = static_cast<unsigned>((rows + 3) / 4);
+    if (rows && g.o_dtype == 0) delta_f32_kernel<T, float><<<grid_d, 256, 0, s>>>(g);
+    if (rows && g.o_dtype != 0) delta_f32_kernel<T, bf16_t><<<grid_d, 256, 0, s>>>(g);
+    const int grid_q = p.cu_q ? p.H * p.tq.bound : p.H * p.N * p.tq.per_seq;
+    const int grid_k = p.cu_q ? p.H * g.tk.bound : p.H * p.N * g.tk.per_seq;
+    if (rows) grad_q_f32_kernel<T, DK, DV><<<grid_q, 256, 0, s>>>(g);
+    if (keys) {
+        grad_k_f32_kernel<T, DK, DV><<<grid_k, 256, 0, s>>>(g);
+        if (p.dr) grad_rope_f32_kernel<T><<<static_cast<unsigned>((keys * p.dr / 4 + 255) / 256), 256, 0, s>>>(g);
+    }
+    return hipGetLastError();
+}
+template <typename T>
+hipError_t pick_grad(const LatentGradParams &g, hipStream_t s) {
+    const int dk = g.f.dn + g.f.dr;
+    if (dk <= 64 && g.f.dv <= 64) return run_grad<T, 64, 64>(g, s);
+    if (dk <= 128) return run_grad<T, 128, 128>(g, s);
+    return run_grad<T, 192, 128>(g, s);
+}
+
+}  // namespace
+
+int latent_tile_q(int dtype) { return kTileQ; }
+int latent_grad_tile_q(int dtype) { return kTileQ; }
+int latent_grad_tile_k(int dtype) { return kTileK; }
+
+hipError_t latent_prefill_f32(const LatentParams &p, int in_dtype, int out_dtype, hipStream_t s) {
+    if (in_dtype == 0) return out_dtype == 0 ? pick_prefill<float, float>(p, s) : pick_prefill<float, bf16_t>(p, s);
+    return out_dtype == 0 ? pick_prefill<bf16_t, float>(p, s) : pick_prefill<bf16_t, bf16_t>(p, s);
+}
+hipError_t latent_backward_f32(const LatentGradParams &g, int in_dtype, hipStream_t s) {
+    return in_dtype == 0 ? pick_grad<float>(g, s) : pick_grad<bf16_t>(g, s);
+}
+hipError_t launch_latent_prefill(const LatentParams &p, int in_dtype, int out_dtype, hipStream_t s) { return latent_prefill_f32(p, in_dtype, out_dtype, s); }
+hipError_t launch_latent_backward(const LatentGradParams &g, int in_dtype, hipStream_t s) { return latent_backward_f32(g, in_dtype, s); }
+
+}  // namespace kda

@@ -82,10 +82,13 @@ typedef enum {
     KDA_ERR_BAD_SEQLENS = 6,        /* host-visible cu_seqlens are malformed      */
     KDA_ERR_SCRATCH_LIMIT = 7,      /* needs more than the fixed scratch of
                                        kda_prefill_chunked_noalloc             */
-    KDA_ERR_DEVICE_WAIT = 8         /* device-side only (*device_status): a
+    KDA_ERR_DEVICE_WAIT = 8,        /* device-side only (*device_status): a
                                        hand-off between workgroups of the
                                        overlapped prefill failed; the call's
                                        results are undefined                  */
+    KDA_ERR_BAD_PAGES = 9           /* device-side only (*device_status): a page
+                                       table entry or a length points outside
+                                       the cache                              */
 } kda_status;
 
 typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
@@ -657,6 +660,252 @@ typedef struct kda_block_norm_backward_args {
 } kda_block_norm_backward_args;
 size_t kda_block_norm_backward_workspace_bytes(const kda_block_norm_backward_args *a);
 kda_status kda_block_norm_backward(const kda_block_norm_backward_args *a, void *hip_stream);
+
+/*
+ * The layer of full attention that a hybrid model runs after every few
+ * recurrent ones (the course index's schedule KDA, KDA, KDA, MLA): latent
+ * attention.  One latent vector c a token (d_latent) is shared by all heads;
+ * beside it a token has one key that carries its position (d_rope).  The next
+ * five calls are the rotation of positions, the write of a token's row
+ * [c, k_rope] into a paged cache, the attention in its expanded form (prompts,
+ * training) with its gradients, and in its absorbed form over the cache.
+ *
+ * Rotary positions on part of each head.  With p the token's position, f_i
+ * the frequency of pair i and m the magnitude, the pair (a, b) of channels
+ * becomes
+ *
+ *     m (a cos(p f_i) - b sin(p f_i)),   m (a sin(p f_i) + b cos(p f_i)).
+ *
+ * The pairs are (2i, 2i + 1) with interleaved, else (i, i + rotary_dim / 2),
+ * counted from channel `offset`; the other channels are copied.  Angles are
+ * computed in 64 bits (no loss at far positions), the products in fp32.
+ * kda_rotary_backward is the gradient: x holds d_out, out receives dx (the
+ * pairs turn back, with the same magnitude).
+ *
+ *   x, out       DEVICE [B, T, H, D] dtype, strides in elements, channels
+ *                contiguous.  out may be x with the same strides; any other
+ *                overlap of their address ranges is refused
+ *                (KDA_ERR_BAD_SHAPE), as are strides of out by which two of
+ *                its elements could share memory
+ *   positions    DEVICE int32, [b * pos_stride_b + t * pos_stride_t], NULL =
+ *                0 .. T - 1 in every row
+ *   freqs        DEVICE double [rotary_dim / 2], radians per position
+ * Supported: D <= 4096, rotary_dim even and <= 1024, offset + rotary_dim <= D;
+ * B * T < 2^31.  Heads whose sizes, strides and addresses are multiples of
+ * 16 bytes are moved as 128-bit vectors; any other element by element.
+ */
+typedef struct kda_rotary_args {
+    int32_t B, T, H, D;
+    int32_t rotary_dim, offset;
+    int32_t interleaved;           /* 0 or 1 */
+    int32_t dtype;                 /* kda_dtype */
+    float magnitude;
+    int64_t x_stride_b, x_stride_t, x_stride_h;
+    int64_t out_stride_b, out_stride_t, out_stride_h;
+    int64_t pos_stride_b, pos_stride_t;
+    const void *x;
+    const int32_t *positions;
+    const double *freqs;
+    void *out;
+} kda_rotary_args;
+kda_status kda_rotary(const kda_rotary_args *a, void *hip_stream);
+kda_status kda_rotary_backward(const kda_rotary_args *a, void *hip_stream);
+
+/*
+ * Write of new tokens' rows into a paged latent cache.  Token t of sequence n
+ * stands at position p = lengths[n] + t; its row [c, k_rope] goes to row
+ * p % page_size of page page_table[n][p / page_size]:
+ *
+ *     c      <- c / sqrt(mean(c^2) + eps) * norm_weight   (as it is when
+ *               norm_weight is NULL)
+ *     k_rope <- turned by its position as by kda_rotary (as it is when freqs
+ *               is NULL)
+ *
+ *   kv           DEVICE [B, T, d_latent + d_rope] dtype, strides in elements
+ *   norm_weight  DEVICE fp32 [d_latent], NULL = no norm
+ *   freqs        DEVICE double [d_rope / 2], NULL = no rotation
+ *   cu_seqlens   DEVICE int32 [num_seqs + 1], NULL = the B rows are the
+ *                sequences; else B == 1 and sequences are packed along T
+ *                (malformed offsets give unspecified values in the sequences'
+ *                own pages, never an out-of-range access)
+ *   lengths      DEVICE int32 [num_seqs]: tokens each sequence has in the
+ *                cache already.  Not changed
+ *   page_table   DEVICE int32 [num_seqs, max_pages], rows table_stride apart
+ *   cache        DEVICE [num_pages, page_size, d_latent + d_rope] dtype, pages
+ *                page_stride and rows row_stride elements apart
+ *   rows         DEVICE [B, T, d_latent + d_rope] dtype, contiguous, NULL =
+ *                not written: the rows as they are written to the cache (a
+ *                token that finds no page has its row here too)
+ *   device_status DEVICE int32, NULL = not reported; written 0 or
+ *                KDA_ERR_BAD_PAGES
+ * A token whose position lies outside [0, max_pages * page_size) or whose
+ * page is not in [0, num_pages) is not written to the cache and reported in
+ * *device_status.  Rows that no token goes to keep their contents.  Sequences
+ * that share the page they append to give that page undefined contents.  kv,
+ * rows and cache must not overlap (KDA_ERR_BAD_SHAPE).
+ * Supported: d_latent, d_rope multiples of 8 (d_rope may be 0), d_latent <=
+ * 2048, d_rope <= 256; strides multiples of 8; kv, cache and rows 16-byte
+ * aligned; B * T < 2^31.
+ */
+typedef struct kda_latent_append_args {
+    int32_t B, T;
+    int32_t num_seqs;
+    int32_t d_latent, d_rope;
+    int32_t interleaved;           /* 0 or 1 */
+    int32_t dtype;                 /* kda_dtype */
+    int32_t num_pages, page_size, max_pages;
+    float eps, magnitude;
+    int64_t kv_stride_b, kv_stride_t;
+    int64_t page_stride, row_stride, table_stride;
+    const void *kv;
+    const float *norm_weight;
+    const double *freqs;
+    const int32_t *cu_seqlens;
+    const int32_t *lengths;
+    const int32_t *page_table;
+    void *cache;
+    void *rows;
+    int32_t *device_status;
+} kda_latent_append_args;
+kda_status kda_latent_append(const kda_latent_append_args *a, void *hip_stream);
+
+/*
+ * Latent attention in its expanded form: every head has its own keys k_nope
+ * and values v (expanded from the latent vectors by the caller's projection)
+ * and all heads share k_rope.  For query i of a sequence with tq queries and
+ * tk keys, which stand at the end of the keys:
+ *
+ *     s_ij = scale (q_i[0, d_nope) . k_nope_j + q_i[d_nope, ..) . k_rope_j),
+ *            j < tk, with causal j <= i + tk - tq
+ *     o_i  = sum_j e^{s_ij - lse_i} v_j,   lse_i = log sum_j e^{s_ij}
+ *
+ * A query that sees no key has o = 0 and lse = -infinity.
+ *
+ *   q            DEVICE [B, T, H, d_nope + d_rope]  in_dtype
+ *   k_nope       DEVICE [B, S, H, d_nope]           in_dtype
+ *   k_rope       DEVICE [B, S, d_rope]              in_dtype, NULL with d_rope 0
+ *   v            DEVICE [B, S, H, d_v]              in_dtype
+ *                Strides of batch, token and head in elements, channels
+ *                contiguous (k_nope and v may be slices of one tensor).
+ *   cu_seqlens_q, cu_seqlens_k  DEVICE int32 [num_seqs + 1], both NULL = the B
+ *                rows are the sequences (tq = T, tk = S); else B == 1 and
+ *                sequences are packed along T and along S.  Checked on the
+ *                device before any other kernel reads them: if malformed,
+ *                nothing is written but the status
+ *   o            DEVICE [B, T, H, d_v] out_dtype, contiguous
+ *   lse          DEVICE fp32 [B, T, H], contiguous
+ *   device_status DEVICE int32, NULL = not reported; written 0 or an error
+ *   workspace    DEVICE, >= kda_latent_prefill_workspace_bytes(args), 256-byte
+ *                aligned
+ *
+ * Inputs are finite: a NaN or an infinity may reach every row of its own
+ * sequence, never another sequence.  Precision: bf16 inputs enter the matrix
+ * cores as they are, the probabilities rounded to bf16; statistics and sums
+ * are fp32.  fp32 inputs run on fp32 matrix cores.
+ * Supported: d_nope, d_rope, d_v multiples of 8, d_nope >= 8, d_nope + d_rope
+ * <= 192, d_v <= 128; strides multiples of 8, token strides below 2^23; q,
+ * k_nope, k_rope, v, o 16-byte aligned (else KDA_ERR_UNSUPPORTED).
+ */
+typedef struct kda_latent_prefill_args {
+    int32_t B, T, S, H;
+    int32_t d_nope, d_rope, d_v;
+    int32_t num_seqs;
+    int32_t in_dtype;              /* kda_dtype */
+    int32_t out_dtype;             /* kda_dtype */
+    int32_t causal;                /* 0 or 1 */
+    float scale;
+    int64_t q_stride_b, q_stride_t, q_stride_h;
+    int64_t k_stride_b, k_stride_t, k_stride_h;    /* k_nope */
+    int64_t r_stride_b, r_stride_t;                /* k_rope */
+    int64_t v_stride_b, v_stride_t, v_stride_h;
+    const void *q, *k_nope, *k_rope, *v;
+    const int32_t *cu_seqlens_q, *cu_seqlens_k;
+    void *o;
+    float *lse;
+    int32_t *device_status;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_latent_prefill_args;
+size_t kda_latent_prefill_workspace_bytes(const kda_latent_prefill_args *a);
+kda_status kda_latent_prefill(const kda_latent_prefill_args *a, void *hip_stream);
+
+/*
+ * Gradients of kda_latent_prefill: of q, k_nope, k_rope (summed over the heads
+ * that share it) and v, from the gradient of o; o and lse are the forward's.
+ *   f            the forward's arguments: f.o (out_dtype) and f.lse are read,
+ *                f.workspace is not used.  The gradient of a score is
+ *                p (d_o . v - rowsum(d_o o)): an o in bf16 brings its rounding
+ *                into that difference, one in fp32 does not
+ *   d_o          DEVICE [B, T, H, d_v] in_dtype, contiguous
+ *   dq, dk_nope, dk_rope, dv  DEVICE, shapes of q, k_nope, k_rope and v,
+ *                contiguous, in_dtype; dk_rope NULL with d_rope 0
+ *   workspace    DEVICE, >= kda_latent_backward_workspace_bytes(args), 256-byte
+ *                aligned
+ * f.device_status reports as in the forward; with malformed offsets nothing
+ * else is written.  The workspace holds an fp32 row of d_rope per key and head.  Results are the
+ * same from run to run (no floating-point atomics).
+ */
+typedef struct kda_latent_backward_args {
+    kda_latent_prefill_args f;
+    const void *d_o;
+    void *dq, *dk_nope, *dk_rope, *dv;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_latent_backward_args;
+size_t kda_latent_backward_workspace_bytes(const kda_latent_backward_args *a);
+kda_status kda_latent_backward(const kda_latent_backward_args *a, void *hip_stream);
+
+/*
+ * Latent attention in its absorbed form, over a paged cache (written by
+ * kda_latent_append): the queries have been carried into the latent space (the
+ * keys' up-projection absorbed), a cache row [c, k_rope] is the key of every
+ * head and c its value; the result stays in the latent space.  n_tokens m >= 1
+ * tokens of each of B sequences: the last m of its `lengths` rows are theirs,
+ * token j sees the rows before lengths[b] - m + 1 + j.
+ *
+ *   q            DEVICE [B, m, H, d_latent + d_rope] in_dtype, strides in
+ *                elements
+ *   cache        DEVICE [num_pages, page_size, d_latent + d_rope] in_dtype,
+ *                pages page_stride and rows row_stride elements apart
+ *   page_table   DEVICE int32 [B, max_pages], rows table_stride apart
+ *   lengths      DEVICE int32 [B]: rows of each sequence, its m tokens among
+ *                them; 0 = an empty slot (o = 0, lse = -infinity)
+ *   o            DEVICE [B, m, H, d_latent] out_dtype, contiguous
+ *   lse          DEVICE fp32 [B, m, H], contiguous
+ *   device_status DEVICE int32, NULL = not reported; written 0 or
+ *                KDA_ERR_BAD_PAGES
+ *   workspace    DEVICE, >= kda_latent_decode_workspace_bytes(args), 256-byte
+ *                aligned
+ * Cache rows behind a sequence's length are never read.  A length below 0
+ * counts as 0, one above max_pages * page_size as that; such a length, or an
+ * entry of the table outside [0, num_pages) within the length, is reported in
+ * *device_status, the results of that sequence are undefined, others are not
+ * touched by it, and no access is out of range.  Results are the same from run
+ * to run.
+ * Supported: d_latent, d_rope multiples of 8, 8 <= d_latent <= 512, d_latent +
+ * d_rope <= 576; page_size, max_pages, num_pages >= 1, max_pages * page_size <
+ * 2^31; B <= 65536, B * m * H < 2^24; strides multiples of 8; q, cache, o
+ * 16-byte aligned.
+ */
+typedef struct kda_latent_decode_args {
+    int32_t B, H, n_tokens;
+    int32_t d_latent, d_rope;
+    int32_t in_dtype;              /* kda_dtype */
+    int32_t out_dtype;             /* kda_dtype */
+    int32_t num_pages, page_size, max_pages;
+    float scale;
+    int64_t q_stride_b, q_stride_t, q_stride_h;
+    int64_t page_stride, row_stride, table_stride;
+    const void *q, *cache;
+    const int32_t *page_table, *lengths;
+    void *o;
+    float *lse;
+    int32_t *device_status;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_latent_decode_args;
+size_t kda_latent_decode_workspace_bytes(const kda_latent_decode_args *a);
+kda_status kda_latent_decode(const kda_latent_decode_args *a, void *hip_stream);
 
 /* Static description of a status code (never NULL). */
 const char *kda_status_string(int32_t status);
