@@ -225,6 +225,7 @@ class LatentPrefillArgs(ctypes.Structure):
 class LatentBackwardArgs(ctypes.Structure):
     """Mirror of ``kda_latent_backward_args`` (include/kda.h)."""
     _fields_ = [("f", LatentPrefillArgs)] + _fields("""
+        l: o_stride_b o_stride_t o_stride_h lse_stride_b lse_stride_t lse_stride_h d_o_stride_b d_o_stride_t d_o_stride_h
         p: d_o dq dk_nope dk_rope dv workspace
         z: workspace_bytes""")
 

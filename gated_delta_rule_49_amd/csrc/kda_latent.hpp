@@ -33,8 +33,9 @@ struct LatentParams {
 struct LatentGradParams {
     LatentParams f;             // f.o, f.lse are read
     const void *d_o;
+    int64_t o_sb, o_st, o_sh, l_sb, l_st, l_sh, d_sb, d_st, d_sh;  // strides of o, lse, d_o
     void *dq, *dkn, *dkr, *dv;
-    float *delta;               // [B, T, H]: rowsum(d_o o)
+    float2 *stats;              // [H, B T]: (lse log2 e, rowsum(d_o o))
     float *dkr_part;            // [H, B S, dr]: each head's share of dk_rope
     LatentTiles tk;
     int32_t o_dtype;

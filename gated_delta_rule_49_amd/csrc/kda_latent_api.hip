@@ -125,7 +125,7 @@ LatentParams latent_params(const kda_latent_prefill_args *a) {
 // then the gradients' fp32 buffers
 struct Layout {
     LatentTiles q, k;
-    size_t entry_q, entry_k, delta, part, bytes;
+    size_t entry_q, entry_k, stats, part, bytes;
 };
 Layout latent_layout(const kda_latent_prefill_args *a, bool grad) {
     Layout l{};
@@ -135,8 +135,8 @@ Layout latent_layout(const kda_latent_prefill_args *a, bool grad) {
     l.k.bound = l.k.per_seq = latent_tiles_bound(a->S, a->num_seqs, size_k, packed);
     l.entry_q = kAlign;
     l.entry_k = l.entry_q + (packed ? align_up(sizeof(int2) * l.q.bound) : 0);
-    l.delta = l.entry_k + (packed && grad ? align_up(sizeof(int2) * l.k.bound) : 0);
-    l.part = l.delta + (grad ? align_up(sizeof(float) * a->B * a->T * a->H) : 0);
+    l.stats = l.entry_k + (packed && grad ? align_up(sizeof(int2) * l.k.bound) : 0);
+    l.part = l.stats + (grad ? align_up(sizeof(float2) * a->B * a->T * a->H) : 0);
     l.bytes = l.part + (grad ? align_up(sizeof(float) * a->H * a->B * a->S * a->d_rope) : 0);
     return l;
 }
@@ -163,8 +163,13 @@ hipError_t prepare_tiles(const kda_latent_prefill_args *a, Layout &l, char *ws, 
 }
 kda_status check_backward(const kda_latent_backward_args *a, bool need_ptrs) {
     if (!a) return KDA_ERR_NULL_ARG;
-    const kda_status st = check_prefill(&a->f, need_ptrs, true);
+    kda_status st = check_prefill(&a->f, need_ptrs, true);
     if (st != KDA_OK) return st;
+    st = check_strides({a->o_stride_b, a->o_stride_t, a->o_stride_h, a->d_o_stride_b, a->d_o_stride_t, a->d_o_stride_h});
+    if (st != KDA_OK) return st;
+    if (a->d_o_stride_t >= (1 << 23)) return KDA_ERR_UNSUPPORTED;
+    for (const int64_t s : {a->lse_stride_b, a->lse_stride_t, a->lse_stride_h})
+        if (s < 0 || s > (static_cast<int64_t>(1) << 48)) return KDA_ERR_BAD_SHAPE;
     if (!need_ptrs) return KDA_OK;
     if (a->f.T > 0 && (!a->d_o || !a->dq)) return KDA_ERR_NULL_ARG;
     if (a->f.S > 0 && (!a->dk_nope || !a->dv || (a->f.d_rope && !a->dk_rope))) return KDA_ERR_NULL_ARG;
@@ -290,7 +295,10 @@ kda_status kda_latent_backward(const kda_latent_backward_args *a, void *hip_stre
     g.d_o = a->d_o;
     g.o_dtype = a->f.out_dtype;
     g.dq = a->dq; g.dkn = a->dk_nope; g.dkr = a->dk_rope; g.dv = a->dv;
-    g.delta = reinterpret_cast<float *>(ws + l.delta);
+    g.o_sb = a->o_stride_b; g.o_st = a->o_stride_t; g.o_sh = a->o_stride_h;
+    g.l_sb = a->lse_stride_b; g.l_st = a->lse_stride_t; g.l_sh = a->lse_stride_h;
+    g.d_sb = a->d_o_stride_b; g.d_st = a->d_o_stride_t; g.d_sh = a->d_o_stride_h;
+    g.stats = reinterpret_cast<float2 *>(ws + l.stats);
     g.dkr_part = reinterpret_cast<float *>(ws + l.part);
     return status_of(launch_latent_backward(g, a->f.in_dtype, s));
 }

@@ -162,19 +162,24 @@ __global__ void __launch_bounds__(256) prefill_f32_kernel(LatentParams p) {
     if (g == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
-// delta = rowsum(d_o o), one wave a (token, head); o may be kept in fp32
+// (lse log2 e, rowsum(d_o o)) of every (head, token), one wave each; a query
+// without a key has +infinity for its lse, by which its probabilities are 0
 template <typename T, typename O>
-__global__ void __launch_bounds__(256) delta_f32_kernel(LatentGradParams g) {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+__global__ void __launch_bounds__(256) stats_kernel(LatentGradParams g) {
+    const int64_t rows = static_cast<int64_t>(g.f.B) * g.f.T;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    if (row >= static_cast<int64_t>(g.f.B) * g.f.T * g.f.H) return;
-    const O *o = static_cast<const O *>(g.f.o) + row * g.f.dv;
-    const T *d = static_cast<const T *>(g.d_o) + row * g.f.dv;
+    if (id >= rows * g.f.H) return;
+    const int64_t row = id / g.f.H;
+    const int h = static_cast<int>(id - row * g.f.H), b = static_cast<int>(row / g.f.T), t = static_cast<int>(row - static_cast<int64_t>(b) * g.f.T);
+    const O *o = static_cast<const O *>(g.f.o) + b * g.o_sb + t * g.o_st + h * g.o_sh;
+    const T *d = static_cast<const T *>(g.d_o) + b * g.d_sb + t * g.d_st + h * g.d_sh;
     float s = 0.f;
     for (int c = lane; c < g.f.dv; c += 64) s = fmaf(io<O>::ld(o, c), io<T>::ld(d, c), s);
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) s += __shfl_xor(s, x);
-    if (lane == 0) g.delta[row] = s;
+    const float lse = g.f.lse[b * g.l_sb + t * g.l_st + h * g.l_sh];
+    if (lane == 0) g.stats[h * rows + row] = make_float2(lse == -INFINITY ? INFINITY : lse * kLog2e, s);
 }
 
 template <typename T, int DK, int DV>
@@ -191,7 +196,7 @@ __global__ void __launch_bounds__(256) grad_q_f32_kernel(LatentGradParams gp) {
     const bool inside = qi < a.tq;
     const int64_t row = (a.q_row + qi) * p.H + a.h;
     const T *q = static_cast<const T *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + (static_cast<int64_t>(a.q0) + qi) * p.q_st;
-    const T *d_o = static_cast<const T *>(gp.d_o) + row * p.dv;
+    const T *d_o = static_cast<const T *>(gp.d_o) + a.b * gp.d_sb + a.h * gp.d_sh + (static_cast<int64_t>(a.q0) + qi) * gp.d_st;
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     f32x4 qf[DK / 16], df[DV / 16], acc[DK / 16];
 #pragma unroll
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(256) grad_q_f32_kernel(LatentGradParams gp) {
         const int c = 16 * s + 4 * g;
         df[s] = inside && c < p.dv ? load4(d_o + c) : zero;
     }
-    const float lse2 = inside ? p.lse[row] * kLog2e : 0.f, delta = inside ? gp.delta[row] : 0.f;
+    const float2 stats = inside ? gp.stats[static_cast<int64_t>(a.h) * p.B * p.T + a.q_row + qi] : make_float2(0.f, 0.f);
     const int last_q = min(a.tq, (a.tile + 1) * kTileQ) - 1, shift = a.tk - a.tq;
     const int n = p.causal ? min(a.tk, last_q + shift + 1) : a.tk;
     const int limit = inside ? (p.causal ? min(n, qi + shift + 1) : n) : 0;
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(256) grad_q_f32_kernel(LatentGradParams gp) {
             f32x4 dp = by_rows<DV>(s_v, 16 * t, df, g, c16);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                dp[j] = k0 + 16 * t + 4 * g + j < limit ? fast_exp2(s[j] * c - lse2) * (dp[j] - delta) * p.scale : 0.f;
+                dp[j] = k0 + 16 * t + 4 * g + j < limit ? fast_exp2(s[j] * c - stats.x) * (dp[j] - stats.y) * p.scale : 0.f;
             by_cols<DK>(acc, s_k, 16 * t, dp, g, c16);
         }
     }
@@ -235,7 +240,7 @@ __global__ void __launch_bounds__(256) grad_q_f32_kernel(LatentGradParams gp) {
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
     __shared__ float s_q[kStep * (DK + 4)], s_d[kStep * (DV + 4)];
-    __shared__ float s_lse[kStep], s_delta[kStep];
+    __shared__ float2 s_stats[kStep];
     const LatentParams &p = gp.f;
     const LatentPlace a = latent_place(p, gp.tk, blockIdx.x, false);  // early keys are seen by more queries
     if (!a.valid) return;
@@ -247,8 +252,8 @@ __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
     const T *kr = static_cast<const T *>(p.kr) + a.b * p.r_sb;
     const T *v = static_cast<const T *>(p.v) + a.b * p.v_sb + a.h * p.v_sh + token * p.v_st;
     const T *q = static_cast<const T *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + a.q0 * p.q_st;
-    const T *d_o = static_cast<const T *>(gp.d_o) + (a.q_row * p.H + a.h) * p.dv;
-    const int64_t d_st = static_cast<int64_t>(p.H) * p.dv;
+    const T *d_o = static_cast<const T *>(gp.d_o) + a.b * gp.d_sb + a.h * gp.d_sh + a.q0 * gp.d_st;
+    const float2 *stats = gp.stats + static_cast<int64_t>(a.h) * p.B * p.T + a.q_row;
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     f32x4 kf[DK / 16], vf[DV / 16], dk[DK / 16], dv[DV / 16];
 #pragma unroll
@@ -269,12 +274,10 @@ __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
     for (; i0 < a.tq; i0 += kStep) {
         __syncthreads();
         stage<DK>(s_q, i0, a.tq, [&](int r, int ch) { return ch < p.dn + p.dr ? load4(q + static_cast<int64_t>(r) * p.q_st + ch) : f32x4{0.f, 0.f, 0.f, 0.f}; });
-        stage<DV>(s_d, i0, a.tq, [&](int r, int ch) { return ch < p.dv ? load4(d_o + r * d_st + ch) : f32x4{0.f, 0.f, 0.f, 0.f}; });
+        stage<DV>(s_d, i0, a.tq, [&](int r, int ch) { return ch < p.dv ? load4(d_o + static_cast<int64_t>(r) * gp.d_st + ch) : f32x4{0.f, 0.f, 0.f, 0.f}; });
         if (threadIdx.x < kStep) {
             const int i = i0 + threadIdx.x;
-            const int64_t row = (a.q_row + i) * p.H + a.h;
-            s_lse[threadIdx.x] = i < a.tq ? p.lse[row] * kLog2e : 0.f;
-            s_delta[threadIdx.x] = i < a.tq ? gp.delta[row] : 0.f;
+            s_stats[threadIdx.x] = i < a.tq ? stats[i] : make_float2(0.f, 0.f);
         }
         __syncthreads();
 #pragma unroll
@@ -285,8 +288,8 @@ __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
             for (int j = 0; j < 4; ++j) {
                 const int r = 16 * t + 4 * g + j, i = i0 + r;
                 const bool sees = inside && i < a.tq && (!p.causal || ki <= i + shift);
-                s[j] = sees ? fast_exp2(s[j] * c - s_lse[r]) : 0.f;
-                dp[j] = sees ? s[j] * (dp[j] - s_delta[r]) * p.scale : 0.f;
+                s[j] = sees ? fast_exp2(s[j] * c - s_stats[r].x) : 0.f;
+                dp[j] = sees ? s[j] * (dp[j] - s_stats[r].y) * p.scale : 0.f;
             }
             by_cols<DV>(dv, s_d, 16 * t, s, g, c16);
             by_cols<DK>(dk, s_q, 16 * t, dp, g, c16);
@@ -339,8 +342,8 @@ hipError_t run_grad(const LatentGradParams &g, hipStream_t s) {
     const LatentParams &p = g.f;
     const int64_t rows = static_cast<int64_t>(p.B) * p.T * p.H, keys = static_cast<int64_t>(p.B) * p.S;
     const unsigned grid_d = static_cast<unsigned>((rows + 3) / 4);
-    if (rows && g.o_dtype == 0) delta_f32_kernel<T, float><<<grid_d, 256, 0, s>>>(g);
-    if (rows && g.o_dtype != 0) delta_f32_kernel<T, bf16_t><<<grid_d, 256, 0, s>>>(g);
+    if (rows && g.o_dtype == 0) stats_kernel<T, float><<<grid_d, 256, 0, s>>>(g);
+    if (rows && g.o_dtype != 0) stats_kernel<T, bf16_t><<<grid_d, 256, 0, s>>>(g);
     const int grid_q = p.cu_q ? p.H * p.tq.bound : p.H * p.N * p.tq.per_seq;
     const int grid_k = p.cu_q ? p.H * g.tk.bound : p.H * p.N * g.tk.per_seq;
     if (rows) grad_q_f32_kernel<T, DK, DV><<<grid_q, 256, 0, s>>>(g);

@@ -263,7 +263,8 @@ def latent_prefill(q, k_nope, k_rope, v, scale=None, causal=True, cu_seqlens=Non
 
 def latent_backward(q, k_nope, k_rope, v, o, lse, d_o, scale=None, causal=True, cu_seqlens=None, cu_seqlens_k=None, device_status=None):
     """Gradients of ``latent_prefill`` with the same arguments, from d_o (like
-    o, q's dtype) and the forward's o and lse: (dq, dk_nope, dk_rope, dv),
+    o, q's dtype) and the forward's o and lse (all three strided as they come,
+    channels contiguous): (dq, dk_nope, dk_rope, dv),
     contiguous, q's dtype, dk_rope summed over the heads that share it (None
     without one).  o may be float32 with bfloat16 inputs (the forward's
     ``out_dtype``): the gradients of scores are differences with rowsum(d_o o),
@@ -271,7 +272,8 @@ def latent_backward(q, k_nope, k_rope, v, o, lse, d_o, scale=None, causal=True, 
     device) receives the call's device-side status: with malformed offsets the
     gradients are not written."""
     a, dev, (B, T, S, H, dn, dr, dv) = _latent_args(q, k_nope, k_rope, v, scale, causal, cu_seqlens, cu_seqlens_k)
-    _dense(dev, o, lse, d_o, device_status)
+    _dense(dev, device_status)
+    _need_device(dev, o, lse, d_o)
     _check_buffer(o, "o", (B, T, H, dv), _FLOATS)
     _check_buffer(d_o, "d_o", (B, T, H, dv), (q.dtype,))
     _check_buffer(lse, "lse", (B, T, H), _F32)
@@ -281,6 +283,9 @@ def latent_backward(q, k_nope, k_rope, v, o, lse, d_o, scale=None, causal=True, 
     dq, dk_nope, d_v = torch.empty((B, T, H, dn + dr), **like), torch.empty((B, S, H, dn), **like), torch.empty((B, S, H, dv), **like)
     dk_rope = torch.empty((B, S, dr), **like) if k_rope is not None else None
     g = LatentBackwardArgs(f=a, d_o=_p(d_o), dq=_p(dq), dk_nope=_p(dk_nope), dk_rope=_p(dk_rope), dv=_p(d_v))
+    g.o_stride_b, g.o_stride_t, g.o_stride_h = _lead_strides(o, "o")
+    g.d_o_stride_b, g.d_o_stride_t, g.d_o_stride_h = _lead_strides(d_o, "d_o")
+    g.lse_stride_b, g.lse_stride_t, g.lse_stride_h = _lead_strides(lse[..., None], "lse")
     L = lib()
     need = int(L.kda_latent_backward_workspace_bytes(ctypes.byref(g)))
     if need == 0:

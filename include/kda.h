@@ -836,17 +836,23 @@ kda_status kda_latent_prefill(const kda_latent_prefill_args *a, void *hip_stream
  *                f.workspace is not used.  The gradient of a score is
  *                p (d_o . v - rowsum(d_o o)): an o in bf16 brings its rounding
  *                into that difference, one in fp32 does not
- *   d_o          DEVICE [B, T, H, d_v] in_dtype, contiguous
+ *   d_o          DEVICE [B, T, H, d_v] in_dtype
+ *                o, d_o (channels contiguous) and lse have strides of batch,
+ *                token and head in elements
  *   dq, dk_nope, dk_rope, dv  DEVICE, shapes of q, k_nope, k_rope and v,
  *                contiguous, in_dtype; dk_rope NULL with d_rope 0
  *   workspace    DEVICE, >= kda_latent_backward_workspace_bytes(args), 256-byte
  *                aligned
  * f.device_status reports as in the forward; with malformed offsets nothing
- * else is written.  The workspace holds an fp32 row of d_rope per key and head.  Results are the
+ * else is written.  The workspace holds an fp32 row of d_rope per key and head.
+ * The strides of d_o are as those of q.  Results are the
  * same from run to run (no floating-point atomics).
  */
 typedef struct kda_latent_backward_args {
     kda_latent_prefill_args f;
+    int64_t o_stride_b, o_stride_t, o_stride_h;
+    int64_t lse_stride_b, lse_stride_t, lse_stride_h;
+    int64_t d_o_stride_b, d_o_stride_t, d_o_stride_h;
     const void *d_o;
     void *dq, *dk_nope, *dk_rope, *dv;
     void *workspace;

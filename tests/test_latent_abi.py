@@ -112,6 +112,7 @@ def test_prefill(L, over, status):
 @pytest.mark.parametrize("inner,over,status", [(o, {}, s) for o, s in PREFILL_REFUSED] + [
     ({}, dict(d_o=None), NULL_ARG), ({}, dict(dq=None), NULL_ARG), ({}, dict(dk_nope=None), NULL_ARG), ({}, dict(dk_rope=None), NULL_ARG),
     ({}, dict(dv=None), NULL_ARG), ({}, dict(dq=FAKE + 8), UNSUPPORTED), ({}, dict(d_o=FAKE + 2), UNSUPPORTED), (dict(d_rope=0, k_rope=None), {}, BAD_SHAPE),
+    ({}, dict(o_stride_h=-8), BAD_SHAPE), ({}, dict(o_stride_t=4), UNSUPPORTED), ({}, dict(d_o_stride_t=1 << 23), UNSUPPORTED), ({}, dict(lse_stride_b=-1), BAD_SHAPE),
     ({}, dict(workspace=None), NULL_ARG), ({}, dict(workspace=FAKE + 8), BAD_SHAPE), ({}, dict(workspace_bytes=1000), TOO_SMALL)])
 def test_backward(L, inner, over, status):
     a = fill(kda.LatentBackwardArgs, dict(d_o=FAKE, dq=FAKE, dk_nope=FAKE, dk_rope=FAKE, dv=FAKE, workspace=FAKE, workspace_bytes=1 << 40), over)

@@ -256,6 +256,13 @@ def test_expanded_strides(dtype):
     o2, lse2 = kda.latent_prefill(**u)
     assert same(o, o2) and same(lse, lse2)
     assert all(same(a, b) for a, b in zip(grads, kda.latent_backward(**u, o=o, lse=lse, d_o=d_o)))
+    lse_moved = lse.permute(2, 0, 1).contiguous().permute(1, 2, 0)
+    assert all(same(a, b) for a, b in zip(grads, kda.latent_backward(**u, o=moved(o), lse=lse_moved, d_o=moved(d_o))))
+    ones = torch.ones((), dtype=dtype, device="cuda").expand(2, 75, 3, 128)  # d_o of a sum, as an expanded scalar
+    with pytest.raises(ValueError):
+        kda.latent_backward(**t, o=o, lse=lse, d_o=ones)
+    rows = torch.ones(128, dtype=dtype, device="cuda").expand(2, 75, 3, 128)
+    assert all(same(a, b) for a, b in zip(kda.latent_backward(**t, o=o, lse=lse, d_o=ones.contiguous()), kda.latent_backward(**t, o=o, lse=lse, d_o=rows)))
     one = {k: v[:1].expand(2, *v.shape[1:]) for k, v in t.items()}  # a batch of one row, repeated
     o3, _ = kda.latent_prefill(**one)
     assert same(o3[0], o3[1]) and same(o3[:1], o[:1])

@@ -196,7 +196,7 @@ def test_malformed_gradients_write_nothing():
     a = kda.LatentPrefillArgs(B=1, T=60, S=60, H=2, d_nope=64, d_rope=32, d_v=64, num_seqs=2, in_dtype=1, out_dtype=1, causal=1, scale=0.1, q_stride_t=192, q_stride_h=96,
                               k_stride_t=256, k_stride_h=128, r_stride_t=56, v_stride_t=256, v_stride_h=128, q=t["q"].data_ptr(), k_nope=t["k_nope"].data_ptr(),
                               k_rope=t["k_rope"].data_ptr(), v=t["v"].data_ptr(), cu_seqlens_q=cu.data_ptr(), cu_seqlens_k=cu.data_ptr(), o=o.data_ptr(), lse=lse.data_ptr())
-    g = kda.LatentBackwardArgs(f=a, d_o=d_o.data_ptr(), dq=outs[0].data_ptr(), dk_nope=outs[1].data_ptr(), dk_rope=outs[2].data_ptr(), dv=outs[3].data_ptr())
+    g = kda.LatentBackwardArgs(f=a, o_stride_t=128, o_stride_h=64, lse_stride_t=2, lse_stride_h=1, d_o_stride_t=128, d_o_stride_h=64, d_o=d_o.data_ptr(), dq=outs[0].data_ptr(), dk_nope=outs[1].data_ptr(), dk_rope=outs[2].data_ptr(), dv=outs[3].data_ptr())
     L = kda.lib()
     ws = torch.zeros(int(L.kda_latent_backward_workspace_bytes(ctypes.byref(g))), dtype=torch.uint8, device="cuda")
     g.workspace, g.workspace_bytes = ws.data_ptr(), ws.numel()
