@@ -110,7 +110,8 @@ int latent_grad_tile_k(int dtype);
 hipError_t launch_latent_prefill(const LatentParams &p, int in_dtype, int out_dtype, hipStream_t s);
 hipError_t launch_latent_backward(const LatentGradParams &g, int in_dtype, hipStream_t s);
 // the two types' own kernels
-hipError_t latent_prefill_f32(const LatentParams &p, int in_dtype, int out_dtype, hipStream_t s);
+constexpr int kLatentTileF32 = 64;  // tokens of a tile of fp32 inputs
+hipError_t latent_prefill_f32(const LatentParams &p, int out_dtype, hipStream_t s);
 hipError_t latent_backward_f32(const LatentGradParams &g, int in_dtype, hipStream_t s);
 
 // ------------------------------------------------------------- absorbed ----

@@ -24,7 +24,7 @@ namespace kda {
 
 namespace {
 
-constexpr int kTileQ = 64, kTileK = 64;  // four waves of 16
+constexpr int kTileQ = kLatentTileF32, kTileK = kLatentTileF32;  // four waves of 16
 constexpr int kStep = 32;                // tokens of the other side per step
 
 __device__ __forceinline__ f32x4 mfma_f32(float a, float b, const f32x4 &c) {
@@ -363,18 +363,15 @@ hipError_t pick_grad(const LatentGradParams &g, hipStream_t s) {
 
 }  // namespace
 
-int latent_tile_q(int dtype) { return kTileQ; }
 int latent_grad_tile_q(int dtype) { return kTileQ; }
 int latent_grad_tile_k(int dtype) { return kTileK; }
 
-hipError_t latent_prefill_f32(const LatentParams &p, int in_dtype, int out_dtype, hipStream_t s) {
-    if (in_dtype == 0) return out_dtype == 0 ? pick_prefill<float, float>(p, s) : pick_prefill<float, bf16_t>(p, s);
-    return out_dtype == 0 ? pick_prefill<bf16_t, float>(p, s) : pick_prefill<bf16_t, bf16_t>(p, s);
+hipError_t latent_prefill_f32(const LatentParams &p, int out_dtype, hipStream_t s) {
+    return out_dtype == 0 ? pick_prefill<float, float>(p, s) : pick_prefill<float, bf16_t>(p, s);
 }
 hipError_t latent_backward_f32(const LatentGradParams &g, int in_dtype, hipStream_t s) {
     return in_dtype == 0 ? pick_grad<float>(g, s) : pick_grad<bf16_t>(g, s);
 }
-hipError_t launch_latent_prefill(const LatentParams &p, int in_dtype, int out_dtype, hipStream_t s) { return latent_prefill_f32(p, in_dtype, out_dtype, s); }
 hipError_t launch_latent_backward(const LatentGradParams &g, int in_dtype, hipStream_t s) { return latent_backward_f32(g, in_dtype, s); }
 
 }  // namespace kda

@@ -1,0 +1,232 @@
+// Latent attention's expanded form on the bf16 matrix cores: the forward.
+//
+// A workgroup of four waves takes 128 queries of one head, a wave 32 of them, and
+// walks the keys 64 at a time.  S^T = K Q^T, so that a lane holds 32 scores of ONE
+// query (its partner in the other half the other 32): the softmax needs one
+// exchange for the maximum, and P goes on to O^T += V^T P^T in its registers.
+// Keys and values come from memory to LDS directly, one tile ahead in the other
+// buffer, with one barrier a tile; two workgroups of a CU (80 KB of LDS and up to
+// 256 registers a wave each) let one's softmax run under the other's products.
+//
+// Softmax: the running maximum moves only when a score passes it by more than
+// kSlack (log2), which few tiles do after the first; until then P may be as large
+// as 2^kSlack, which costs a bf16 or an fp32 sum nothing.
+#include "kda_latent_bf16.hpp"
+
+namespace kda {
+
+namespace {
+
+constexpr int kTileQ = 128, kKeys = 64, kThreads = 256;
+constexpr float kSlack = 8.f;
+
+// The tile's rows [k0, k0 + 64) to LDS, in chunks of 16 bytes; rows behind the
+// last (n - 1) repeat it, channels behind the key's are its first again (they
+// meet zeros of the query).
+template <int DK> struct KeyLoader {
+    static constexpr int N = kKeys * DK * 2 / 16 / kThreads;  // chunks a thread
+    const char *base[N];
+    uint32_t stride[N];
+    __device__ __forceinline__ void init(const LatentParams &p, const bf16_t *kn, const bf16_t *kr) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = i * kThreads + threadIdx.x, r = at / (DK / 8), slot = at % (DK / 8);
+            int c;  // the permutation is its own inverse
+            if constexpr (DK == 128) c = slot ^ (r & 15);
+            else c = (slot & ~7) | ((slot ^ r ^ (r >> 3 & 1)) & 7);
+            const bool rope = 8 * c >= p.dn && 8 * c < p.dn + p.dr;
+            base[i] = reinterpret_cast<const char *>(rope ? kr + 8 * c - p.dn : kn + (8 * c < p.dn ? 8 * c : 0));
+            stride[i] = static_cast<uint32_t>(rope ? p.r_st : p.k_st) * 2;
+        }
+    }
+    __device__ __forceinline__ void issue(int k0, int n, uint32_t to) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int r = (i * kThreads + threadIdx.x) / (DK / 8);
+            load_to_lds(base[i] + static_cast<uint64_t>(static_cast<uint32_t>(min(k0 + r, n - 1))) * stride[i],
+                        to + (i * kThreads + (threadIdx.x & ~63)) * 16);
+        }
+    }
+};
+template <int DV> struct ValueLoader {
+    static constexpr int N = kKeys * DV * 2 / 16 / kThreads;
+    static constexpr int ROWS = kThreads / (DV / 8);  // rows that one round covers, a multiple of 4
+    const char *base;
+    uint32_t stride;
+    int row;
+    __device__ __forceinline__ void init(const LatentParams &p, const bf16_t *v) {
+        row = threadIdx.x / (DV / 8);
+        const int c = (col_chunk<DV>(row, threadIdx.x % (DV / 8)) - row * DV * 2) / 16;
+        base = reinterpret_cast<const char *>(v + (8 * c < p.dv ? 8 * c : 0));
+        stride = static_cast<uint32_t>(p.v_st) * 2;
+    }
+    __device__ __forceinline__ void issue(int k0, int n, uint32_t to) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            load_to_lds(base + static_cast<uint64_t>(static_cast<uint32_t>(min(k0 + i * ROWS + row, n - 1))) * stride,
+                        to + (i * kThreads + (threadIdx.x & ~63)) * 16);
+    }
+};
+
+template <typename O, int DK, int DV>
+__global__ void __launch_bounds__(kThreads, 2) prefill_bf16_kernel(LatentParams p) {
+    constexpr int KB = kKeys * DK * 2, VB = kKeys * DV * 2;
+    __shared__ __attribute__((aligned(16))) char s_tile[2 * (KB + VB)];
+    const LatentPlace a = latent_place(p, p.tq, blockIdx.x, p.causal);
+    if (!a.valid) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h = lane >> 5, c32 = lane & 31;
+    const bf16_t *kn = static_cast<const bf16_t *>(p.kn) + a.b * p.k_sb + a.h * p.k_sh + a.k0 * p.k_st;
+    const bf16_t *kr = static_cast<const bf16_t *>(p.kr) + a.b * p.r_sb + a.k0 * p.r_st;
+    const bf16_t *v = static_cast<const bf16_t *>(p.v) + a.b * p.v_sb + a.h * p.v_sh + a.k0 * p.v_st;
+    const int q_first = a.tile * kTileQ + wave * 32, qi = q_first + c32;
+    const int shift = a.tk - a.tq;
+    const int n = p.causal ? min(a.tk, min(a.tq, (a.tile + 1) * kTileQ) + shift) : a.tk;
+    // keys that the wave's queries see: the first one's, the last one's, the lane's
+    const int n_least = p.causal ? min(n, q_first + shift + 1) : n;
+    const int n_wave = q_first >= a.tq ? 0 : p.causal ? min(n, min(a.tq - 1, q_first + 31) + shift + 1) : n;
+    const int limit = p.causal ? min(n, qi + shift + 1) : n;
+
+    KeyLoader<DK> keys;
+    ValueLoader<DV> values;
+    keys.init(p, kn, kr);
+    values.init(p, v);
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(s_tile));
+    if (n > 0) {
+        keys.issue(0, n, lds);
+        values.issue(0, n, lds + 2 * KB);
+    }
+    bf16x8 qf[DK / 16];
+    {
+        const bf16_t *q = static_cast<const bf16_t *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + (static_cast<int64_t>(a.q0) + qi) * p.q_st;
+#pragma unroll
+        for (int s = 0; s < DK / 16; ++s) {
+            const int ch = 16 * s + 8 * h;
+            frag8 f;
+            f.u = make_uint4(0, 0, 0, 0);
+            if (qi < a.tq && ch < p.dn + p.dr && p.scale != 0.f) f.u = *reinterpret_cast<const uint4 *>(q + ch);
+            // scores are masked before they are scaled: the scale's sign goes to the query
+            if (p.scale < 0.f) f.u = make_uint4(f.u.x ^ 0x80008000u, f.u.y ^ 0x80008000u, f.u.z ^ 0x80008000u, f.u.w ^ 0x80008000u);
+            qf[s] = f.v;
+        }
+    }
+    const float c = p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e;
+    f32x16 acc[DV / 32];
+#pragma unroll
+    for (int b = 0; b < DV / 32; ++b) acc[b] = zero16();
+    float top = -INFINITY, sum = 0.f;
+    // the lane's places in a tile: its key's row; four rows by 16 channels
+    const int i16 = lane & 15, g2 = (lane >> 4) & 1;
+    const char *v_at = s_tile + 2 * KB + (4 * h + (i16 >> 2)) * DV * 2 + 8 * (i16 & 1);
+
+    for (int k0 = 0, buf = 0; k0 < n; k0 += kKeys, buf ^= 1) {
+        wait_loads();
+        lds_barrier();
+        if (k0 + kKeys < n) {
+            keys.issue(k0 + kKeys, n, lds + (buf ^ 1) * KB);
+            values.issue(k0 + kKeys, n, lds + 2 * KB + (buf ^ 1) * VB);
+        }
+        if (k0 >= n_wave) continue;
+        f32x16 s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s[t] = zero16();
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k) {
+                frag8 f;
+                f.u = *reinterpret_cast<const uint4 *>(s_tile + buf * KB + 32 * t * DK * 2 + row_chunk<DK>(c32, 2 * k + h));
+                s[t] = mfma32(f.v, qf[k], s[t]);
+            }
+        }
+        if (k0 + kKeys > n_least) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (k0 + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3) >= limit) s[t][i] = -INFINITY;
+        }
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) most = fmaxf(most, fmaxf(s[0][i], s[1][i]));
+        most = swap_halves_max(most) * c;
+        if (__any(most > top + kSlack)) {
+            const float next = fmaxf(top, most);
+            const float keep = next == -INFINITY ? 1.f : fast_exp2(top - next);
+            top = next;
+            sum *= keep;
+#pragma unroll
+            for (int b = 0; b < DV / 32; ++b) acc[b] *= keep;
+        }
+        const float base = top == -INFINITY ? 0.f : top;
+        bf16x8 pf[4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[t][i] = fast_exp2(fmaf(s[t][i], c, -base));
+                sum += s[t][i];
+            }
+            pf[2 * t] = half_tile(s[t], 0);
+            pf[2 * t + 1] = half_tile(s[t], 1);
+        }
+#pragma unroll
+        for (int b = 0; b < DV / 32; ++b) {
+            const int chunk = 4 * b + 2 * g2 + ((i16 & 3) >> 1);
+            const char *at = v_at + buf * VB + (col_chunk<DV>(i16 >> 2, chunk) - (i16 >> 2) * DV * 2);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint2 lo = read_tr16(at + 16 * k * DV * 2), hi = read_tr16(at + (16 * k + 8) * DV * 2);
+                frag8 f;
+                f.u = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                acc[b] = mfma32(f.v, pf[k], acc[b]);
+            }
+        }
+    }
+    sum = swap_halves_sum(sum);
+    if (qi >= a.tq) return;
+    const int64_t row = (a.q_row + qi) * p.H + a.h;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    O *o = static_cast<O *>(p.o) + row * p.dv;
+#pragma unroll
+    for (int b = 0; b < DV / 32; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int ch = 32 * b + 8 * i + 4 * h;
+            if (ch >= p.dv) continue;
+            if constexpr (sizeof(O) == 4) {
+                *reinterpret_cast<f32x4 *>(o + ch) = f32x4{acc[b][4 * i] * inv, acc[b][4 * i + 1] * inv, acc[b][4 * i + 2] * inv, acc[b][4 * i + 3] * inv};
+            } else {
+                uint32_t w[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    w[j] = static_cast<uint32_t>(f32_to_bf16(acc[b][4 * i + 2 * j] * inv)) | static_cast<uint32_t>(f32_to_bf16(acc[b][4 * i + 2 * j + 1] * inv)) << 16;
+                *reinterpret_cast<uint2 *>(o + ch) = make_uint2(w[0], w[1]);
+            }
+        }
+    if (h == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+template <typename O, int DK, int DV>
+hipError_t run(const LatentParams &p, hipStream_t s) {
+    const int grid = p.cu_q ? p.H * p.tq.bound : p.H * p.N * p.tq.per_seq;
+    prefill_bf16_kernel<O, DK, DV><<<grid, kThreads, 0, s>>>(p);
+    return hipGetLastError();
+}
+template <typename O>
+hipError_t pick(const LatentParams &p, hipStream_t s) {
+    const int dk = p.dn + p.dr;
+    if (dk <= 64 && p.dv <= 64) return run<O, 64, 64>(p, s);
+    if (dk <= 128) return run<O, 128, 128>(p, s);
+    return run<O, 192, 128>(p, s);
+}
+
+}  // namespace
+
+int latent_tile_q(int dtype) { return dtype == 0 ? kLatentTileF32 : kTileQ; }
+
+hipError_t launch_latent_prefill(const LatentParams &p, int in_dtype, int out_dtype, hipStream_t s) {
+    if (in_dtype == 0) return latent_prefill_f32(p, out_dtype, s);
+    return out_dtype == 0 ? pick<float>(p, s) : pick<bf16_t>(p, s);
+}
+
+}  // namespace kda
