@@ -77,6 +77,7 @@ __device__ __forceinline__ int2 decode_info(bool first, int64_t per, int64_t bef
 
 // the join, for both types
 hipError_t launch_latent_join(const LatentDecodeParams &p, const LatentDecodePlan &plan, int out_dtype, hipStream_t s);
-hipError_t latent_decode_f32(const LatentDecodeParams &p, const LatentDecodePlan &plan, int in_dtype, int out_dtype, hipStream_t s);
+constexpr int kDecodeRowsF32 = 16, kDecodeKeysF32 = 32;  // rows of a tile and keys of a step of fp32 inputs
+hipError_t latent_decode_f32(const LatentDecodeParams &p, const LatentDecodePlan &plan, int out_dtype, hipStream_t s);
 
 }  // namespace kda

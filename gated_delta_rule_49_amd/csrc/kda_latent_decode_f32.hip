@@ -13,24 +13,19 @@ namespace kda {
 
 namespace {
 
-constexpr int kRows = 16, kKeys = 32, kThreads = 256;
+constexpr int kRows = kDecodeRowsF32, kKeys = kDecodeKeysF32, kThreads = 256;
 
 __device__ __forceinline__ f32x4 mfma_f32(float a, float b, const f32x4 &c) {
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 __device__ __forceinline__ f32x4 load4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
-__device__ __forceinline__ f32x4 load4(const bf16_t *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)};
-}
-
-template <typename T, typename O, int DK, int DC>
+template <typename O, int DK, int DC>
 __global__ void __launch_bounds__(kThreads) decode_f32_kernel(LatentDecodeParams p, int tiles) {
     constexpr int LD = DK + 4, HALF = DK / 2, NB = DC / 64;
     __shared__ float s_k[kKeys * LD];
     __shared__ float s_s[2][kKeys][kRows + 1];
     __shared__ int64_t s_sum[kThreads / 64];
-    __shared__ const T *s_row[kKeys];
+    __shared__ const float *s_row[kKeys];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c16 = lane & 15;
     const int tile = blockIdx.x % tiles, worker = blockIdx.x / tiles;
     DecodeRun run = decode_run<kThreads, kKeys>(p, worker, s_sum);
@@ -45,7 +40,7 @@ __global__ void __launch_bounds__(kThreads) decode_f32_kernel(LatentDecodeParams
         const int64_t s0 = first ? run.at - run.before : 0, count = min(run.left, steps - s0);
         if (s0 == 0 && tile == 0 && tid == 0) p.info[run.b] = decode_info(first, run.per, run.before, steps, worker);
         f32x4 qf[HALF / 16], acc[NB];
-        const T *q = static_cast<const T *>(p.q) + run.b * p.q_sb + t * p.q_st + h * p.q_sh;
+        const float *q = static_cast<const float *>(p.q) + run.b * p.q_sb + t * p.q_st + h * p.q_sh;
 #pragma unroll
         for (int s = 0; s < HALF / 16; ++s) {
             const int ch = (wave >> 1) * HALF + 16 * s + 4 * g;
@@ -65,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) decode_f32_kernel(LatentDecodeParams
                 const bool bad = id < 0 || id >= p.num_pages;
                 if (bad) id = 0;
                 if (p.status && (bad || p.lengths[run.b] != n)) *p.status = kBadPages;
-                s_row[tid] = static_cast<const T *>(p.cache) + id * p.page_stride + static_cast<int64_t>(k - page * p.page_size) * p.row_stride;
+                s_row[tid] = static_cast<const float *>(p.cache) + id * p.page_stride + static_cast<int64_t>(k - page * p.page_size) * p.row_stride;
             }
             __syncthreads();
             for (int e = tid; e < kKeys * (DK / 4); e += kThreads) {
@@ -195,30 +190,16 @@ __global__ void __launch_bounds__(256) join_kernel(LatentDecodeParams p, int til
     if (lane == 0) p.lse[out] = sum == 0.f ? -INFINITY : ref + __builtin_amdgcn_logf(sum) * kLn2;
 }
 
-template <typename T, typename O>
+template <typename O>
 hipError_t pick_decode(const LatentDecodeParams &p, const LatentDecodePlan &plan, hipStream_t s) {
     const int grid = plan.workers * plan.tiles, d = p.dc + p.dr;
-    if (p.dc <= 128 && d <= 192) decode_f32_kernel<T, O, 192, 128><<<grid, kThreads, 0, s>>>(p, plan.tiles);
-    else if (p.dc <= 256 && d <= 320) decode_f32_kernel<T, O, 320, 256><<<grid, kThreads, 0, s>>>(p, plan.tiles);
-    else decode_f32_kernel<T, O, 576, 512><<<grid, kThreads, 0, s>>>(p, plan.tiles);
+    if (p.dc <= 128 && d <= 192) decode_f32_kernel<O, 192, 128><<<grid, kThreads, 0, s>>>(p, plan.tiles);
+    else if (p.dc <= 256 && d <= 320) decode_f32_kernel<O, 320, 256><<<grid, kThreads, 0, s>>>(p, plan.tiles);
+    else decode_f32_kernel<O, 576, 512><<<grid, kThreads, 0, s>>>(p, plan.tiles);
     return hipGetLastError();
 }
 
 }  // namespace
-
-LatentDecodePlan latent_decode_plan(int B, int H, int m, int dc, int dr, int64_t most_rows, int in_dtype) {
-    LatentDecodePlan plan{};
-    plan.rows = kRows;
-    plan.tiles = (m * H + plan.rows - 1) / plan.rows;
-    // two workgroups a CU, and no more than there can be steps
-    const int64_t most = static_cast<int64_t>(B) * ((most_rows + kKeys - 1) / kKeys);
-    plan.workers = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, std::max(1, 512 / plan.tiles))));
-    const size_t rows = static_cast<size_t>(plan.tiles) * 2 * plan.workers * plan.rows;
-    plan.o_bytes = align_up(rows * dc * sizeof(float));
-    plan.lse_bytes = align_up(rows * sizeof(float));
-    plan.info_bytes = align_up(static_cast<size_t>(B) * sizeof(int2));
-    return plan;
-}
 
 hipError_t launch_latent_join(const LatentDecodeParams &p, const LatentDecodePlan &plan, int out_dtype, hipStream_t s) {
     const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.B) * p.m * p.H + 3) / 4);
@@ -227,14 +208,8 @@ hipError_t launch_latent_join(const LatentDecodeParams &p, const LatentDecodePla
     return hipGetLastError();
 }
 
-hipError_t latent_decode_f32(const LatentDecodeParams &p, const LatentDecodePlan &plan, int in_dtype, int out_dtype, hipStream_t s) {
-    if (in_dtype == 0) return out_dtype == 0 ? pick_decode<float, float>(p, plan, s) : pick_decode<float, bf16_t>(p, plan, s);
-    return out_dtype == 0 ? pick_decode<bf16_t, float>(p, plan, s) : pick_decode<bf16_t, bf16_t>(p, plan, s);
-}
-
-hipError_t launch_latent_decode(const LatentDecodeParams &p, const LatentDecodePlan &plan, int in_dtype, int out_dtype, hipStream_t s) {
-    const hipError_t e = latent_decode_f32(p, plan, in_dtype, out_dtype, s);
-    return e != hipSuccess ? e : launch_latent_join(p, plan, out_dtype, s);
+hipError_t latent_decode_f32(const LatentDecodeParams &p, const LatentDecodePlan &plan, int out_dtype, hipStream_t s) {
+    return out_dtype == 0 ? pick_decode<float>(p, plan, s) : pick_decode<bf16_t>(p, plan, s);
 }
 
 }  // namespace kda
