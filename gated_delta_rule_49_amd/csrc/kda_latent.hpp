@@ -128,6 +128,7 @@ struct LatentDecodeParams {
     int32_t B, H, m, dc, dr;
     int32_t num_pages, page_size, max_pages;
     int32_t workers;       // workgroups a row tile is dealt to
+    uint32_t page_magic, page_shift;  // k / page_size = k page_magic >> page_shift for k < 2^31
     float scale;
 };
 struct LatentDecodePlan {

@@ -330,6 +330,12 @@ kda_status kda_latent_decode(const kda_latent_decode_args *a, void *hip_stream) 
     p.B = a->B; p.H = a->H; p.m = a->n_tokens; p.dc = a->d_latent; p.dr = a->d_rope;
     p.num_pages = a->num_pages; p.page_size = a->page_size; p.max_pages = a->max_pages;
     p.workers = plan.workers;
+    // with 2^l the least power of 2 >= page_size and magic = ceil(2^(31 + l) / page_size): the product
+    // exceeds k 2^(31 + l) / page_size by less than k 2^l <= 2^(31 + l), in units of 1 / page_size
+    uint32_t l = 0;
+    while ((static_cast<uint64_t>(1) << l) < static_cast<uint64_t>(a->page_size)) ++l;
+    p.page_shift = 31 + l;
+    p.page_magic = static_cast<uint32_t>(((static_cast<uint64_t>(1) << p.page_shift) + a->page_size - 1) / a->page_size);
     p.scale = a->scale;
     return status_of(launch_latent_decode(p, plan, a->in_dtype, a->out_dtype, s));
 }

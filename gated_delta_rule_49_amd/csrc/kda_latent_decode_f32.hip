@@ -167,18 +167,29 @@ __global__ void __launch_bounds__(256) join_kernel(LatentDecodeParams p, int til
     float acc[8], sum = 0.f;  // dc <= 512: lane l holds channels 4 l and 256 + 4 l
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    for (int w = w0; w <= info.y; ++w) {
-        const int64_t at = place(w);
-        const float wt = fast_exp2((p.part_lse[at] - ref) * kLog2e);
-        sum += wt;
+    constexpr int U = 8;  // pieces requested together
+    for (int w = w0; w <= info.y; w += U) {
+        float lse[U];
+        f32x4 v[U][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int ch = 256 * e + 4 * lane;
-            if (ch < p.dc) {
-                const f32x4 v = load4(p.part_o + at * p.dc + ch);
+        for (int u = 0; u < U; ++u) {
+            const int64_t at = place(min(w + u, info.y));
+            lse[u] = w + u <= info.y ? p.part_lse[at] : -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[4 * e + j] = fmaf(wt, v[j], acc[4 * e + j]);
+            for (int e = 0; e < 2; ++e) {
+                const int ch = 256 * e + 4 * lane;
+                if (ch < p.dc) v[u][e] = load4(p.part_o + at * p.dc + ch);
             }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (w + u > info.y) break;
+            const float wt = fast_exp2((lse[u] - ref) * kLog2e);
+            sum += wt;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[4 * e + j] = fmaf(wt, v[u][e][j], acc[4 * e + j]);
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
