@@ -35,7 +35,7 @@ struct LatentGradParams {
     const void *d_o;
     int64_t o_sb, o_st, o_sh, l_sb, l_st, l_sh, d_sb, d_st, d_sh;  // strides of o, lse, d_o
     void *dq, *dkn, *dkr, *dv;
-    float2 *stats;              // [H, B T]: (lse log2 e, rowsum(d_o o))
+    float *lse2, *delta;        // [H, B T]: lse log2 e, rowsum(d_o o)
     float *dkr_part;            // [H, B S, dr]: each head's share of dk_rope
     LatentTiles tk;
     int32_t o_dtype;
@@ -112,7 +112,7 @@ hipError_t launch_latent_backward(const LatentGradParams &g, int in_dtype, hipSt
 // the two types' own kernels
 constexpr int kLatentTileF32 = 64;  // tokens of a tile of fp32 inputs
 hipError_t latent_prefill_f32(const LatentParams &p, int out_dtype, hipStream_t s);
-hipError_t latent_backward_f32(const LatentGradParams &g, int in_dtype, hipStream_t s);
+hipError_t latent_backward_f32(const LatentGradParams &g, hipStream_t s);
 
 // ------------------------------------------------------------- absorbed ----
 struct LatentDecodeParams {

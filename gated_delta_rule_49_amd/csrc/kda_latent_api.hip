@@ -136,7 +136,7 @@ Layout latent_layout(const kda_latent_prefill_args *a, bool grad) {
     l.entry_q = kAlign;
     l.entry_k = l.entry_q + (packed ? align_up(sizeof(int2) * l.q.bound) : 0);
     l.stats = l.entry_k + (packed && grad ? align_up(sizeof(int2) * l.k.bound) : 0);
-    l.part = l.stats + (grad ? align_up(sizeof(float2) * a->B * a->T * a->H) : 0);
+    l.part = l.stats + (grad ? align_up(2 * sizeof(float) * a->B * a->T * a->H) : 0);
     l.bytes = l.part + (grad ? align_up(sizeof(float) * a->H * a->B * a->S * a->d_rope) : 0);
     return l;
 }
@@ -298,7 +298,8 @@ kda_status kda_latent_backward(const kda_latent_backward_args *a, void *hip_stre
     g.o_sb = a->o_stride_b; g.o_st = a->o_stride_t; g.o_sh = a->o_stride_h;
     g.l_sb = a->lse_stride_b; g.l_st = a->lse_stride_t; g.l_sh = a->lse_stride_h;
     g.d_sb = a->d_o_stride_b; g.d_st = a->d_o_stride_t; g.d_sh = a->d_o_stride_h;
-    g.stats = reinterpret_cast<float2 *>(ws + l.stats);
+    g.lse2 = reinterpret_cast<float *>(ws + l.stats);
+    g.delta = g.lse2 + static_cast<size_t>(a->f.B) * a->f.T * a->f.H;
     g.dkr_part = reinterpret_cast<float *>(ws + l.part);
     return status_of(launch_latent_backward(g, a->f.in_dtype, s));
 }

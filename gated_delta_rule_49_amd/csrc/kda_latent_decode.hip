@@ -53,10 +53,6 @@ __device__ __forceinline__ float quarters_max(float x) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return swap_halves_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    return static_cast<uint32_t>(f32_to_bf16(a)) | static_cast<uint32_t>(f32_to_bf16(b)) << 16;
-}
-
 template <typename O, int DK, int DC>
 __global__ void __launch_bounds__(kThreads, 1) decode_bf16_kernel(LatentDecodeParams p, int tiles) {
     constexpr int NC = kKeys * DK / 8 / kThreads;      // chunks a thread

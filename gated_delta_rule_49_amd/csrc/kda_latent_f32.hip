@@ -32,10 +32,6 @@ __device__ __forceinline__ f32x4 mfma_f32(float a, float b, const f32x4 &c) {
 }
 
 __device__ __forceinline__ f32x4 load4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
-__device__ __forceinline__ f32x4 load4(const bf16_t *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)};
-}
 __device__ __forceinline__ void store4(float *p, const f32x4 &v) { *reinterpret_cast<f32x4 *>(p) = v; }
 __device__ __forceinline__ void store4(bf16_t *p, const f32x4 &v) {
     const uint32_t a = static_cast<uint32_t>(f32_to_bf16(v[0])) | static_cast<uint32_t>(f32_to_bf16(v[1])) << 16;
@@ -44,8 +40,7 @@ __device__ __forceinline__ void store4(bf16_t *p, const f32x4 &v) {
 }
 
 // four channels from `c` of a key: its own part, the shared part, zeros behind
-template <typename T>
-__device__ __forceinline__ f32x4 key4(const LatentParams &p, const T *kn, const T *kr, int64_t token, int c) {
+__device__ __forceinline__ f32x4 key4(const LatentParams &p, const float *kn, const float *kr, int64_t token, int c) {
     if (c < p.dn) return load4(kn + token * p.k_st + c);
     if (c < p.dn + p.dr) return load4(kr + token * p.r_st + c - p.dn);
     return f32x4{0.f, 0.f, 0.f, 0.f};
@@ -92,17 +87,17 @@ __device__ __forceinline__ float quarter_sum(float x) {
     return x + __shfl_xor(x, 32);
 }
 
-template <typename T, typename O, int DK, int DV>
+template <typename O, int DK, int DV>
 __global__ void __launch_bounds__(256) prefill_f32_kernel(LatentParams p) {
     __shared__ float s_k[kStep * (DK + 4)], s_v[kStep * (DV + 4)];
     const LatentPlace a = latent_place(p, p.tq, blockIdx.x, p.causal);
     if (!a.valid) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c16 = lane & 15;
-    const T *kn = static_cast<const T *>(p.kn) + a.b * p.k_sb + a.h * p.k_sh + a.k0 * p.k_st;
-    const T *kr = static_cast<const T *>(p.kr) + a.b * p.r_sb + a.k0 * p.r_st;
-    const T *v = static_cast<const T *>(p.v) + a.b * p.v_sb + a.h * p.v_sh + a.k0 * p.v_st;
+    const float *kn = static_cast<const float *>(p.kn) + a.b * p.k_sb + a.h * p.k_sh + a.k0 * p.k_st;
+    const float *kr = static_cast<const float *>(p.kr) + a.b * p.r_sb + a.k0 * p.r_st;
+    const float *v = static_cast<const float *>(p.v) + a.b * p.v_sb + a.h * p.v_sh + a.k0 * p.v_st;
     const int qi = a.tile * kTileQ + wave * 16 + c16;  // the lane's query
-    const T *q = static_cast<const T *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + (static_cast<int64_t>(a.q0) + qi) * p.q_st;
+    const float *q = static_cast<const float *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + (static_cast<int64_t>(a.q0) + qi) * p.q_st;
     f32x4 qf[DK / 16];
 #pragma unroll
     for (int s = 0; s < DK / 16; ++s) {
@@ -120,7 +115,7 @@ __global__ void __launch_bounds__(256) prefill_f32_kernel(LatentParams p) {
     float top = -INFINITY, sum = 0.f;
     for (int k0 = 0; k0 < n; k0 += kStep) {
         __syncthreads();
-        stage<DK>(s_k, k0, n, [&](int r, int ch) { return key4<T>(p, kn, kr, r, ch); });
+        stage<DK>(s_k, k0, n, [&](int r, int ch) { return key4(p, kn, kr, r, ch); });
         stage<DV>(s_v, k0, n, [&](int r, int ch) { return ch < p.dv ? load4(v + static_cast<int64_t>(r) * p.v_st + ch) : f32x4{0.f, 0.f, 0.f, 0.f}; });
         __syncthreads();
         f32x4 s[2];
@@ -162,41 +157,21 @@ __global__ void __launch_bounds__(256) prefill_f32_kernel(LatentParams p) {
     if (g == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
-// (lse log2 e, rowsum(d_o o)) of every (head, token), one wave each; a query
-// without a key has +infinity for its lse, by which its probabilities are 0
-template <typename T, typename O>
-__global__ void __launch_bounds__(256) stats_kernel(LatentGradParams g) {
-    const int64_t rows = static_cast<int64_t>(g.f.B) * g.f.T;
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (id >= rows * g.f.H) return;
-    const int64_t row = id / g.f.H;
-    const int h = static_cast<int>(id - row * g.f.H), b = static_cast<int>(row / g.f.T), t = static_cast<int>(row - static_cast<int64_t>(b) * g.f.T);
-    const O *o = static_cast<const O *>(g.f.o) + b * g.o_sb + t * g.o_st + h * g.o_sh;
-    const T *d = static_cast<const T *>(g.d_o) + b * g.d_sb + t * g.d_st + h * g.d_sh;
-    float s = 0.f;
-    for (int c = lane; c < g.f.dv; c += 64) s = fmaf(io<O>::ld(o, c), io<T>::ld(d, c), s);
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) s += __shfl_xor(s, x);
-    const float lse = g.f.lse[b * g.l_sb + t * g.l_st + h * g.l_sh];
-    if (lane == 0) g.stats[h * rows + row] = make_float2(lse == -INFINITY ? INFINITY : lse * kLog2e, s);
-}
-
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 __global__ void __launch_bounds__(256) grad_q_f32_kernel(LatentGradParams gp) {
     __shared__ float s_k[kStep * (DK + 4)], s_v[kStep * (DV + 4)];
     const LatentParams &p = gp.f;
     const LatentPlace a = latent_place(p, p.tq, blockIdx.x, p.causal);
     if (!a.valid) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c16 = lane & 15;
-    const T *kn = static_cast<const T *>(p.kn) + a.b * p.k_sb + a.h * p.k_sh + a.k0 * p.k_st;
-    const T *kr = static_cast<const T *>(p.kr) + a.b * p.r_sb + a.k0 * p.r_st;
-    const T *v = static_cast<const T *>(p.v) + a.b * p.v_sb + a.h * p.v_sh + a.k0 * p.v_st;
+    const float *kn = static_cast<const float *>(p.kn) + a.b * p.k_sb + a.h * p.k_sh + a.k0 * p.k_st;
+    const float *kr = static_cast<const float *>(p.kr) + a.b * p.r_sb + a.k0 * p.r_st;
+    const float *v = static_cast<const float *>(p.v) + a.b * p.v_sb + a.h * p.v_sh + a.k0 * p.v_st;
     const int qi = a.tile * kTileQ + wave * 16 + c16;
     const bool inside = qi < a.tq;
     const int64_t row = (a.q_row + qi) * p.H + a.h;
-    const T *q = static_cast<const T *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + (static_cast<int64_t>(a.q0) + qi) * p.q_st;
-    const T *d_o = static_cast<const T *>(gp.d_o) + a.b * gp.d_sb + a.h * gp.d_sh + (static_cast<int64_t>(a.q0) + qi) * gp.d_st;
+    const float *q = static_cast<const float *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + (static_cast<int64_t>(a.q0) + qi) * p.q_st;
+    const float *d_o = static_cast<const float *>(gp.d_o) + a.b * gp.d_sb + a.h * gp.d_sh + (static_cast<int64_t>(a.q0) + qi) * gp.d_st;
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     f32x4 qf[DK / 16], df[DV / 16], acc[DK / 16];
 #pragma unroll
@@ -210,14 +185,15 @@ __global__ void __launch_bounds__(256) grad_q_f32_kernel(LatentGradParams gp) {
         const int c = 16 * s + 4 * g;
         df[s] = inside && c < p.dv ? load4(d_o + c) : zero;
     }
-    const float2 stats = inside ? gp.stats[static_cast<int64_t>(a.h) * p.B * p.T + a.q_row + qi] : make_float2(0.f, 0.f);
+    const int64_t at = static_cast<int64_t>(a.h) * p.B * p.T + a.q_row + qi;
+    const float lse = inside ? gp.lse2[at] : 0.f, delta = inside ? gp.delta[at] : 0.f;
     const int last_q = min(a.tq, (a.tile + 1) * kTileQ) - 1, shift = a.tk - a.tq;
     const int n = p.causal ? min(a.tk, last_q + shift + 1) : a.tk;
     const int limit = inside ? (p.causal ? min(n, qi + shift + 1) : n) : 0;
     const float c = p.scale * kLog2e;
     for (int k0 = 0; k0 < n; k0 += kStep) {
         __syncthreads();
-        stage<DK>(s_k, k0, n, [&](int r, int ch) { return key4<T>(p, kn, kr, r, ch); });
+        stage<DK>(s_k, k0, n, [&](int r, int ch) { return key4(p, kn, kr, r, ch); });
         stage<DV>(s_v, k0, n, [&](int r, int ch) { return ch < p.dv ? load4(v + static_cast<int64_t>(r) * p.v_st + ch) : f32x4{0.f, 0.f, 0.f, 0.f}; });
         __syncthreads();
 #pragma unroll
@@ -226,21 +202,21 @@ __global__ void __launch_bounds__(256) grad_q_f32_kernel(LatentGradParams gp) {
             f32x4 dp = by_rows<DV>(s_v, 16 * t, df, g, c16);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                dp[j] = k0 + 16 * t + 4 * g + j < limit ? fast_exp2(s[j] * c - stats.x) * (dp[j] - stats.y) * p.scale : 0.f;
+                dp[j] = k0 + 16 * t + 4 * g + j < limit ? fast_exp2(s[j] * c - lse) * (dp[j] - delta) * p.scale : 0.f;
             by_cols<DK>(acc, s_k, 16 * t, dp, g, c16);
         }
     }
     if (!inside) return;
-    T *dq = static_cast<T *>(gp.dq) + row * (p.dn + p.dr);
+    float *dq = static_cast<float *>(gp.dq) + row * (p.dn + p.dr);
 #pragma unroll
     for (int b = 0; b < DK / 16; ++b)
         if (16 * b + 4 * g < p.dn + p.dr) store4(dq + 16 * b + 4 * g, acc[b]);
 }
 
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
     __shared__ float s_q[kStep * (DK + 4)], s_d[kStep * (DV + 4)];
-    __shared__ float2 s_stats[kStep];
+    __shared__ float s_lse[kStep], s_delta[kStep];
     const LatentParams &p = gp.f;
     const LatentPlace a = latent_place(p, gp.tk, blockIdx.x, false);  // early keys are seen by more queries
     if (!a.valid) return;
@@ -248,17 +224,17 @@ __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
     const int ki = a.tile * kTileK + wave * 16 + c16;  // the lane's key
     const bool inside = ki < a.tk;
     const int64_t token = static_cast<int64_t>(a.k0) + ki;
-    const T *kn = static_cast<const T *>(p.kn) + a.b * p.k_sb + a.h * p.k_sh;
-    const T *kr = static_cast<const T *>(p.kr) + a.b * p.r_sb;
-    const T *v = static_cast<const T *>(p.v) + a.b * p.v_sb + a.h * p.v_sh + token * p.v_st;
-    const T *q = static_cast<const T *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + a.q0 * p.q_st;
-    const T *d_o = static_cast<const T *>(gp.d_o) + a.b * gp.d_sb + a.h * gp.d_sh + a.q0 * gp.d_st;
-    const float2 *stats = gp.stats + static_cast<int64_t>(a.h) * p.B * p.T + a.q_row;
+    const float *kn = static_cast<const float *>(p.kn) + a.b * p.k_sb + a.h * p.k_sh;
+    const float *kr = static_cast<const float *>(p.kr) + a.b * p.r_sb;
+    const float *v = static_cast<const float *>(p.v) + a.b * p.v_sb + a.h * p.v_sh + token * p.v_st;
+    const float *q = static_cast<const float *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + a.q0 * p.q_st;
+    const float *d_o = static_cast<const float *>(gp.d_o) + a.b * gp.d_sb + a.h * gp.d_sh + a.q0 * gp.d_st;
+    const int64_t row0 = static_cast<int64_t>(a.h) * p.B * p.T + a.q_row;
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     f32x4 kf[DK / 16], vf[DV / 16], dk[DK / 16], dv[DV / 16];
 #pragma unroll
     for (int s = 0; s < DK / 16; ++s) {
-        kf[s] = inside ? key4<T>(p, kn, kr, token, 16 * s + 4 * g) : zero;
+        kf[s] = inside ? key4(p, kn, kr, token, 16 * s + 4 * g) : zero;
         dk[s] = zero;
     }
 #pragma unroll
@@ -277,7 +253,8 @@ __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
         stage<DV>(s_d, i0, a.tq, [&](int r, int ch) { return ch < p.dv ? load4(d_o + static_cast<int64_t>(r) * gp.d_st + ch) : f32x4{0.f, 0.f, 0.f, 0.f}; });
         if (threadIdx.x < kStep) {
             const int i = i0 + threadIdx.x;
-            s_stats[threadIdx.x] = i < a.tq ? stats[i] : make_float2(0.f, 0.f);
+            s_lse[threadIdx.x] = i < a.tq ? gp.lse2[row0 + i] : 0.f;
+            s_delta[threadIdx.x] = i < a.tq ? gp.delta[row0 + i] : 0.f;
         }
         __syncthreads();
 #pragma unroll
@@ -288,8 +265,8 @@ __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
             for (int j = 0; j < 4; ++j) {
                 const int r = 16 * t + 4 * g + j, i = i0 + r;
                 const bool sees = inside && i < a.tq && (!p.causal || ki <= i + shift);
-                s[j] = sees ? fast_exp2(s[j] * c - s_stats[r].x) : 0.f;
-                dp[j] = sees ? s[j] * (dp[j] - s_stats[r].y) * p.scale : 0.f;
+                s[j] = sees ? fast_exp2(s[j] * c - s_lse[r]) : 0.f;
+                dp[j] = sees ? s[j] * (dp[j] - s_delta[r]) * p.scale : 0.f;
             }
             by_cols<DV>(dv, s_d, 16 * t, s, g, c16);
             by_cols<DK>(dk, s_q, 16 * t, dp, g, c16);
@@ -297,8 +274,8 @@ __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
     }
     if (!inside) return;
     const int64_t key = a.k_row + ki;
-    T *dkn = static_cast<T *>(gp.dkn) + (key * p.H + a.h) * p.dn;
-    T *dvp = static_cast<T *>(gp.dv) + (key * p.H + a.h) * p.dv;
+    float *dkn = static_cast<float *>(gp.dkn) + (key * p.H + a.h) * p.dn;
+    float *dvp = static_cast<float *>(gp.dv) + (key * p.H + a.h) * p.dv;
     float *part = gp.dkr_part + (static_cast<int64_t>(a.h) * p.B * p.S + key) * p.dr;
 #pragma unroll
     for (int b = 0; b < DK / 16; ++b) {
@@ -311,67 +288,41 @@ __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
         if (16 * b + 4 * g < p.dv) store4(dvp + 16 * b + 4 * g, dv[b]);
 }
 
-// dk_rope: the heads' shares added in order
-template <typename T>
-__global__ void __launch_bounds__(256) grad_rope_f32_kernel(LatentGradParams g) {
-    if (g.f.cu_q && *g.f.status != 0) return;
-    const int64_t plane = static_cast<int64_t>(g.f.B) * g.f.S * g.f.dr;
-    const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-    if (at >= plane) return;
-    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    for (int h = 0; h < g.f.H; ++h) sum += load4(g.dkr_part + h * plane + at);
-    store4(static_cast<T *>(g.dkr) + at, sum);
-}
-
-template <typename T, typename O, int DK, int DV>
+template <typename O, int DK, int DV>
 hipError_t run_prefill(const LatentParams &p, hipStream_t s) {
     const int grid = p.cu_q ? p.H * p.tq.bound : p.H * p.N * p.tq.per_seq;
-    prefill_f32_kernel<T, O, DK, DV><<<grid, 256, 0, s>>>(p);
+    prefill_f32_kernel<O, DK, DV><<<grid, 256, 0, s>>>(p);
     return hipGetLastError();
 }
-template <typename T, typename O>
+template <typename O>
 hipError_t pick_prefill(const LatentParams &p, hipStream_t s) {
     const int dk = p.dn + p.dr;
-    if (dk <= 64 && p.dv <= 64) return run_prefill<T, O, 64, 64>(p, s);
-    if (dk <= 128) return run_prefill<T, O, 128, 128>(p, s);
-    return run_prefill<T, O, 192, 128>(p, s);
+    if (dk <= 64 && p.dv <= 64) return run_prefill<O, 64, 64>(p, s);
+    if (dk <= 128) return run_prefill<O, 128, 128>(p, s);
+    return run_prefill<O, 192, 128>(p, s);
 }
 
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 hipError_t run_grad(const LatentGradParams &g, hipStream_t s) {
     const LatentParams &p = g.f;
-    const int64_t rows = static_cast<int64_t>(p.B) * p.T * p.H, keys = static_cast<int64_t>(p.B) * p.S;
-    const unsigned grid_d = static_cast<unsigned>((rows + 3) / 4);
-    if (rows && g.o_dtype == 0) stats_kernel<T, float><<<grid_d, 256, 0, s>>>(g);
-    if (rows && g.o_dtype != 0) stats_kernel<T, bf16_t><<<grid_d, 256, 0, s>>>(g);
     const int grid_q = p.cu_q ? p.H * p.tq.bound : p.H * p.N * p.tq.per_seq;
     const int grid_k = p.cu_q ? p.H * g.tk.bound : p.H * p.N * g.tk.per_seq;
-    if (rows) grad_q_f32_kernel<T, DK, DV><<<grid_q, 256, 0, s>>>(g);
-    if (keys) {
-        grad_k_f32_kernel<T, DK, DV><<<grid_k, 256, 0, s>>>(g);
-        if (p.dr) grad_rope_f32_kernel<T><<<static_cast<unsigned>((keys * p.dr / 4 + 255) / 256), 256, 0, s>>>(g);
-    }
+    if (p.T) grad_q_f32_kernel<DK, DV><<<grid_q, 256, 0, s>>>(g);
+    if (p.S) grad_k_f32_kernel<DK, DV><<<grid_k, 256, 0, s>>>(g);
     return hipGetLastError();
 }
-template <typename T>
 hipError_t pick_grad(const LatentGradParams &g, hipStream_t s) {
     const int dk = g.f.dn + g.f.dr;
-    if (dk <= 64 && g.f.dv <= 64) return run_grad<T, 64, 64>(g, s);
-    if (dk <= 128) return run_grad<T, 128, 128>(g, s);
-    return run_grad<T, 192, 128>(g, s);
+    if (dk <= 64 && g.f.dv <= 64) return run_grad<64, 64>(g, s);
+    if (dk <= 128) return run_grad<128, 128>(g, s);
+    return run_grad<192, 128>(g, s);
 }
 
 }  // namespace
 
-int latent_grad_tile_q(int dtype) { return kTileQ; }
-int latent_grad_tile_k(int dtype) { return kTileK; }
-
 hipError_t latent_prefill_f32(const LatentParams &p, int out_dtype, hipStream_t s) {
-    return out_dtype == 0 ? pick_prefill<float, float>(p, s) : pick_prefill<float, bf16_t>(p, s);
+    return out_dtype == 0 ? pick_prefill<float>(p, s) : pick_prefill<bf16_t>(p, s);
 }
-hipError_t latent_backward_f32(const LatentGradParams &g, int in_dtype, hipStream_t s) {
-    return in_dtype == 0 ? pick_grad<float>(g, s) : pick_grad<bf16_t>(g, s);
-}
-hipError_t launch_latent_backward(const LatentGradParams &g, int in_dtype, hipStream_t s) { return latent_backward_f32(g, in_dtype, s); }
+hipError_t latent_backward_f32(const LatentGradParams &g, hipStream_t s) { return pick_grad(g, s); }
 
 }  // namespace kda

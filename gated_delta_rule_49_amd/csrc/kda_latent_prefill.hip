@@ -20,54 +20,6 @@ namespace {
 constexpr int kTileQ = 128, kKeys = 64, kThreads = 256;
 constexpr float kSlack = 8.f;
 
-// The tile's rows [k0, k0 + 64) to LDS, in chunks of 16 bytes; rows behind the
-// last (n - 1) repeat it, channels behind the key's are its first again (they
-// meet zeros of the query).
-template <int DK> struct KeyLoader {
-    static constexpr int N = kKeys * DK * 2 / 16 / kThreads;  // chunks a thread
-    const char *base[N];
-    uint32_t stride[N];
-    __device__ __forceinline__ void init(const LatentParams &p, const bf16_t *kn, const bf16_t *kr) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = i * kThreads + threadIdx.x, r = at / (DK / 8), slot = at % (DK / 8);
-            int c;  // the permutation is its own inverse
-            if constexpr (DK == 128) c = slot ^ (r & 15);
-            else c = (slot & ~7) | ((slot ^ r ^ (r >> 3 & 1)) & 7);
-            const bool rope = 8 * c >= p.dn && 8 * c < p.dn + p.dr;
-            base[i] = reinterpret_cast<const char *>(rope ? kr + 8 * c - p.dn : kn + (8 * c < p.dn ? 8 * c : 0));
-            stride[i] = static_cast<uint32_t>(rope ? p.r_st : p.k_st) * 2;
-        }
-    }
-    __device__ __forceinline__ void issue(int k0, int n, uint32_t to) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int r = (i * kThreads + threadIdx.x) / (DK / 8);
-            load_to_lds(base[i] + static_cast<uint64_t>(static_cast<uint32_t>(min(k0 + r, n - 1))) * stride[i],
-                        to + (i * kThreads + (threadIdx.x & ~63)) * 16);
-        }
-    }
-};
-template <int DV> struct ValueLoader {
-    static constexpr int N = kKeys * DV * 2 / 16 / kThreads;
-    static constexpr int ROWS = kThreads / (DV / 8);  // rows that one round covers, a multiple of 4
-    const char *base;
-    uint32_t stride;
-    int row;
-    __device__ __forceinline__ void init(const LatentParams &p, const bf16_t *v) {
-        row = threadIdx.x / (DV / 8);
-        const int c = (col_chunk<DV>(row, threadIdx.x % (DV / 8)) - row * DV * 2) / 16;
-        base = reinterpret_cast<const char *>(v + (8 * c < p.dv ? 8 * c : 0));
-        stride = static_cast<uint32_t>(p.v_st) * 2;
-    }
-    __device__ __forceinline__ void issue(int k0, int n, uint32_t to) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            load_to_lds(base + static_cast<uint64_t>(static_cast<uint32_t>(min(k0 + i * ROWS + row, n - 1))) * stride,
-                        to + (i * kThreads + (threadIdx.x & ~63)) * 16);
-    }
-};
-
 template <typename O, int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 2) prefill_bf16_kernel(LatentParams p) {
     constexpr int KB = kKeys * DK * 2, VB = kKeys * DV * 2;
@@ -87,26 +39,24 @@ __global__ void __launch_bounds__(kThreads, 2) prefill_bf16_kernel(LatentParams 
     const int n_wave = q_first >= a.tq ? 0 : p.causal ? min(n, min(a.tq - 1, q_first + 31) + shift + 1) : n;
     const int limit = p.causal ? min(n, qi + shift + 1) : n;
 
-    KeyLoader<DK> keys;
-    ValueLoader<DV> values;
-    keys.init(p, kn, kr);
-    values.init(p, v);
+    TileLoader<DK, kKeys, kThreads, RowRead> keys;
+    TileLoader<DV, kKeys, kThreads, ColumnRead> values;
+    keys.init(kn, p.k_st, p.dn, kr, p.r_st, p.dr);
+    values.init(v, p.v_st, p.dv, v, 0, 0);
     const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(s_tile));
     if (n > 0) {
         keys.issue(0, n, lds);
         values.issue(0, n, lds + 2 * KB);
     }
     bf16x8 qf[DK / 16];
-    {
-        const bf16_t *q = static_cast<const bf16_t *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + (static_cast<int64_t>(a.q0) + qi) * p.q_st;
+    load_own<DK>(qf, static_cast<const bf16_t *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + (static_cast<int64_t>(a.q0) + min(qi, a.tq - 1)) * p.q_st, p.dn + p.dr, kr, 0,
+                 qi < a.tq && p.scale != 0.f, h);
+    if (p.scale < 0.f) {  // scores are masked before they are scaled: the scale's sign goes to the query
 #pragma unroll
         for (int s = 0; s < DK / 16; ++s) {
-            const int ch = 16 * s + 8 * h;
             frag8 f;
-            f.u = make_uint4(0, 0, 0, 0);
-            if (qi < a.tq && ch < p.dn + p.dr && p.scale != 0.f) f.u = *reinterpret_cast<const uint4 *>(q + ch);
-            // scores are masked before they are scaled: the scale's sign goes to the query
-            if (p.scale < 0.f) f.u = make_uint4(f.u.x ^ 0x80008000u, f.u.y ^ 0x80008000u, f.u.z ^ 0x80008000u, f.u.w ^ 0x80008000u);
+            f.v = qf[s];
+            f.u = make_uint4(f.u.x ^ 0x80008000u, f.u.y ^ 0x80008000u, f.u.z ^ 0x80008000u, f.u.w ^ 0x80008000u);
             qf[s] = f.v;
         }
     }
@@ -134,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 2) prefill_bf16_kernel(LatentParams 
 #pragma unroll
             for (int k = 0; k < DK / 16; ++k) {
                 frag8 f;
-                f.u = *reinterpret_cast<const uint4 *>(s_tile + buf * KB + 32 * t * DK * 2 + row_chunk<DK>(c32, 2 * k + h));
+                f.u = *reinterpret_cast<const uint4 *>(s_tile + buf * KB + 32 * t * DK * 2 + RowRead::place<DK>(c32, 2 * k + h));
                 s[t] = mfma32(f.v, qf[k], s[t]);
             }
         }
@@ -172,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 2) prefill_bf16_kernel(LatentParams 
 #pragma unroll
         for (int b = 0; b < DV / 32; ++b) {
             const int chunk = 4 * b + 2 * g2 + ((i16 & 3) >> 1);
-            const char *at = v_at + buf * VB + (col_chunk<DV>(i16 >> 2, chunk) - (i16 >> 2) * DV * 2);
+            const char *at = v_at + buf * VB + (ColumnRead::place<DV>(i16 >> 2, chunk) - (i16 >> 2) * DV * 2);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint2 lo = read_tr16(at + 16 * k * DV * 2), hi = read_tr16(at + (16 * k + 8) * DV * 2);
@@ -193,15 +143,7 @@ __global__ void __launch_bounds__(kThreads, 2) prefill_bf16_kernel(LatentParams 
         for (int i = 0; i < 4; ++i) {
             const int ch = 32 * b + 8 * i + 4 * h;
             if (ch >= p.dv) continue;
-            if constexpr (sizeof(O) == 4) {
-                *reinterpret_cast<f32x4 *>(o + ch) = f32x4{acc[b][4 * i] * inv, acc[b][4 * i + 1] * inv, acc[b][4 * i + 2] * inv, acc[b][4 * i + 3] * inv};
-            } else {
-                uint32_t w[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    w[j] = static_cast<uint32_t>(f32_to_bf16(acc[b][4 * i + 2 * j] * inv)) | static_cast<uint32_t>(f32_to_bf16(acc[b][4 * i + 2 * j + 1] * inv)) << 16;
-                *reinterpret_cast<uint2 *>(o + ch) = make_uint2(w[0], w[1]);
-            }
+            store4(o + ch, acc[b], i, inv);
         }
     if (h == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
