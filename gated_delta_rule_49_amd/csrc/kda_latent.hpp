@@ -17,6 +17,7 @@ struct LatentTiles {
     const int32_t *count;  // packed: how many there are
     int32_t bound;         // tiles a head (an upper bound when packed)
     int32_t per_seq;       // unpacked: tiles of one sequence
+    int32_t size;          // tokens of a tile
 };
 struct LatentParams {
     const void *q, *kn, *kr, *v;
@@ -50,8 +51,8 @@ struct LatentPlace {
     bool valid;
 };
 
-// Tiles of one head stand together in the logical order, the later ones, which
-// see more keys, first (`down`).  Blocks are dealt to the 8 XCDs in turn: where
+// Tiles of one head stand together in the logical order, those that see most
+// first (`down`: the later ones).  Blocks are dealt to the 8 XCDs in turn: where
 // the heads divide evenly each XCD takes whole heads, so that a head's keys and
 // values are read through one L2; else neighbours go to different XCDs.
 __device__ __forceinline__ LatentPlace latent_place(const LatentParams &p, const LatentTiles &t, int block, bool down) {
@@ -65,7 +66,7 @@ __device__ __forceinline__ LatentPlace latent_place(const LatentParams &p, const
         const int n = *p.status == 0 ? *t.count : 0;
         a.valid = i < n;
         if (!a.valid) return a;
-        const int2 e = t.entry[down ? n - 1 - i : i];
+        const int2 e = t.entry[i];  // the largest first
         a.h = pair;
         a.b = 0;
         a.tile = e.y;
@@ -95,22 +96,25 @@ struct LatentTable {
     const int32_t *cu_q, *cu_k;
     int32_t T, S, N;
     int32_t size_q, size_k, bound_q, bound_k;
+    int32_t causal;
     int2 *entry_q, *entry_k;    // entry_k null: queries only
+    int32_t *spill;             // latent_table_spill(N) bytes
     int32_t *word;              // status, count of q tiles, count of k tiles
     int32_t *user_status;       // nullable
 };
+size_t latent_table_spill(int N);
 hipError_t launch_latent_table(const LatentTable &t, hipStream_t s);
 hipError_t launch_status_word(int32_t *word, hipStream_t s);  // *word = 0
 
 // tokens of a query tile (forward, and the queries' gradient) and of a key
-// tile (the keys' and values' gradient), by type
-int latent_tile_q(int dtype);
-int latent_grad_tile_q(int dtype);
-int latent_grad_tile_k(int dtype);
+// tile (the keys' and values' gradient), by type and by how many tokens and heads there are
+int latent_tile_q(int dtype, int64_t tokens, int H);
+int latent_grad_tile_q(int dtype, int64_t tokens, int H);
+int latent_grad_tile_k(int dtype, int64_t tokens, int H);
 hipError_t launch_latent_prefill(const LatentParams &p, int in_dtype, int out_dtype, hipStream_t s);
 hipError_t launch_latent_backward(const LatentGradParams &g, int in_dtype, hipStream_t s);
 // the two types' own kernels
-constexpr int kLatentTileF32 = 64;  // tokens of a tile of fp32 inputs
+int latent_tile_f32(int64_t tokens, int H);
 hipError_t latent_prefill_f32(const LatentParams &p, int out_dtype, hipStream_t s);
 hipError_t latent_backward_f32(const LatentGradParams &g, hipStream_t s);
 

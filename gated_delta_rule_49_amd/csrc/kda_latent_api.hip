@@ -94,8 +94,8 @@ kda_status check_prefill(const kda_latent_prefill_args *a, bool need_ptrs, bool 
     if (!a->cu_seqlens_q != !a->cu_seqlens_k) return KDA_ERR_BAD_SHAPE;
     if (a->cu_seqlens_q ? a->B != 1 || a->num_seqs < 1 : a->num_seqs != a->B) return KDA_ERR_BAD_SHAPE;
     if (static_cast<int64_t>(a->B) * a->H > (1 << 22) || a->num_seqs > (1 << 20)) return KDA_ERR_UNSUPPORTED;
-    // blocks of a launch: (tokens / 64 + sequences) heads
-    if ((static_cast<int64_t>(a->B) * (std::max(a->T, a->S) / 64 + 1) + a->num_seqs) * a->H > kMost31 / 2) return KDA_ERR_UNSUPPORTED;
+    // blocks of a launch: (tokens / 16 + sequences) heads
+    if ((static_cast<int64_t>(a->B) * (std::max(a->T, a->S) / 16 + 1) + a->num_seqs) * a->H > kMost31 / 2) return KDA_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(a->B) * std::max(a->T, a->S) > kMost31) return KDA_ERR_UNSUPPORTED;
     const kda_status st = check_strides({a->q_stride_b, a->q_stride_t, a->q_stride_h, a->k_stride_b, a->k_stride_t, a->k_stride_h, a->r_stride_b,
                                          a->r_stride_t, a->v_stride_b, a->v_stride_t, a->v_stride_h});
@@ -125,15 +125,18 @@ LatentParams latent_params(const kda_latent_prefill_args *a) {
 // then the gradients' fp32 buffers
 struct Layout {
     LatentTiles q, k;
-    size_t entry_q, entry_k, stats, part, bytes;
+    size_t spill, entry_q, entry_k, stats, part, bytes;
 };
 Layout latent_layout(const kda_latent_prefill_args *a, bool grad) {
     Layout l{};
     const bool packed = a->cu_seqlens_q != nullptr;
-    const int size_q = grad ? latent_grad_tile_q(a->in_dtype) : latent_tile_q(a->in_dtype), size_k = latent_grad_tile_k(a->in_dtype);
-    l.q.bound = l.q.per_seq = latent_tiles_bound(a->T, a->num_seqs, size_q, packed);
-    l.k.bound = l.k.per_seq = latent_tiles_bound(a->S, a->num_seqs, size_k, packed);
-    l.entry_q = kAlign;
+    const int64_t queries = static_cast<int64_t>(a->B) * a->T, keys = static_cast<int64_t>(a->B) * a->S;
+    l.q.size = grad ? latent_grad_tile_q(a->in_dtype, queries, a->H) : latent_tile_q(a->in_dtype, queries, a->H);
+    l.k.size = latent_grad_tile_k(a->in_dtype, keys, a->H);
+    l.q.bound = l.q.per_seq = latent_tiles_bound(a->T, a->num_seqs, l.q.size, packed);
+    l.k.bound = l.k.per_seq = latent_tiles_bound(a->S, a->num_seqs, l.k.size, packed);
+    l.spill = kAlign;
+    l.entry_q = l.spill + (packed ? align_up(latent_table_spill(a->num_seqs)) : 0);
     l.entry_k = l.entry_q + (packed ? align_up(sizeof(int2) * l.q.bound) : 0);
     l.stats = l.entry_k + (packed && grad ? align_up(sizeof(int2) * l.k.bound) : 0);
     l.part = l.stats + (grad ? align_up(2 * sizeof(float) * a->B * a->T * a->H) : 0);
@@ -151,12 +154,14 @@ hipError_t prepare_tiles(const kda_latent_prefill_args *a, Layout &l, char *ws, 
     LatentTable t{};
     t.cu_q = a->cu_seqlens_q; t.cu_k = a->cu_seqlens_k;
     t.T = a->T; t.S = a->S; t.N = a->num_seqs;
-    t.size_q = grad ? latent_grad_tile_q(a->in_dtype) : latent_tile_q(a->in_dtype);
-    t.size_k = latent_grad_tile_k(a->in_dtype);
+    t.size_q = l.q.size;
+    t.size_k = l.k.size;
     t.bound_q = l.q.bound;
     t.bound_k = l.k.bound;
     t.entry_q = reinterpret_cast<int2 *>(ws + l.entry_q);
     t.entry_k = grad ? reinterpret_cast<int2 *>(ws + l.entry_k) : nullptr;
+    t.spill = reinterpret_cast<int32_t *>(ws + l.spill);
+    t.causal = a->causal;
     t.word = word;
     t.user_status = user_status;
     return launch_latent_table(t, s);

@@ -377,8 +377,8 @@ template <typename T> hipError_t backward(const LatentGradParams &g, hipStream_t
 
 }  // namespace
 
-int latent_grad_tile_q(int dtype) { return dtype == 0 ? kLatentTileF32 : kTileQ; }
-int latent_grad_tile_k(int dtype) { return dtype == 0 ? kLatentTileF32 : kTileK; }
+int latent_grad_tile_q(int dtype, int64_t tokens, int H) { return dtype == 0 ? latent_tile_f32(tokens, H) : kTileQ; }
+int latent_grad_tile_k(int dtype, int64_t tokens, int H) { return dtype == 0 ? latent_tile_f32(tokens, H) : kTileK; }
 
 hipError_t launch_latent_backward(const LatentGradParams &g, int in_dtype, hipStream_t s) {
     return in_dtype == 0 ? backward<float>(g, s) : backward<bf16_t>(g, s);

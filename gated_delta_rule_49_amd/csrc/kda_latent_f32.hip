@@ -24,7 +24,7 @@ namespace kda {
 
 namespace {
 
-constexpr int kTileQ = kLatentTileF32, kTileK = kLatentTileF32;  // four waves of 16
+constexpr int kTileQ = 64, kTileK = 64;  // four waves of 16
 constexpr int kStep = 32;                // tokens of the other side per step
 
 __device__ __forceinline__ f32x4 mfma_f32(float a, float b, const f32x4 &c) {
@@ -288,10 +288,293 @@ __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
         if (16 * b + 4 * g < p.dv) store4(dvp + 16 * b + 4 * g, dv[b]);
 }
 
+// ------------------------------------------------------- few tiles ----
+// The same products where there are too few tiles to fill the card: a workgroup
+// takes 16 queries (or keys), its four waves every fourth 16 tokens of the other
+// side, which come from the caches to registers (no LDS, no barrier in the loop);
+// the waves' sums meet in LDS at the end, in order.
+constexpr int kFewTile = 16;
+constexpr int64_t kFewBelow = 65536;  // tokens times heads
+
+// The key's channels as one: its own part, then the shared one (behind both: the
+// first again, whose products meet zeros or are not kept).
+struct KeyChannels {
+    const float *kn, *kr;
+    int64_t k_st, r_st;
+    int dn, dr;
+    __device__ __forceinline__ const float *at(int64_t token, int c) const {
+        return c >= dn && c < dn + dr ? kr + token * r_st + (c - dn) : kn + token * k_st + (c < dn ? c : 0);
+    }
+};
+struct Channels {
+    const float *x;
+    int64_t st;
+    int d;
+    __device__ __forceinline__ const float *at(int64_t token, int c) const { return x + token * st + (c < d ? c : 0); }
+};
+// 16 tokens from t0 as operand by rows, and by columns; tokens behind the last (n - 1) repeat it
+template <int D, typename C> __device__ __forceinline__ void rows16(f32x4 (&f)[D / 16], const C &x, int t0, int n, int g, int c16) {
+    const int64_t t = min(t0 + c16, n - 1);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) f[s] = load4(x.at(t, 16 * s + 4 * g));
+}
+template <int D, typename C> __device__ __forceinline__ void cols16(f32x4 (&f)[D / 16], const C &x, int t0, int n, int g, int c16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t t = min(t0 + 4 * g + j, n - 1);
+#pragma unroll
+        for (int b = 0; b < D / 16; ++b) f[b][j] = *x.at(t, 16 * b + c16);
+    }
+}
+// two chains: the products of one wait for each other
+template <int D> __device__ __forceinline__ f32x4 dot16(const f32x4 (&a)[D / 16], const f32x4 (&own)[D / 16]) {
+    f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            x = mfma_f32(a[s][j], own[s][j], x);
+            y = mfma_f32(a[s][j + 1], own[s][j + 1], y);
+        }
+    return x + y;
+}
+template <int D> __device__ __forceinline__ void add16(f32x4 (&acc)[D / 16], const f32x4 (&cols)[D / 16], const f32x4 &w) {
+#pragma unroll
+    for (int b = 0; b < D / 16; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[b] = mfma_f32(cols[b][j], w[j], acc[b]);
+}
+// the wave's own 16 tokens; zeros outside
+template <int D, typename C> __device__ __forceinline__ void own16(f32x4 (&f)[D / 16], const C &x, int64_t t, int d, bool inside, int g) {
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+        const int c = 16 * s + 4 * g;
+        f[s] = load4(x.at(t, c));
+        if (!inside || c >= d) f[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+}
+template <int D> __device__ __forceinline__ void put16(float *to, const f32x4 (&acc)[D / 16], int wave, int g, int c16) {
+#pragma unroll
+    for (int b = 0; b < D / 16; ++b) *reinterpret_cast<f32x4 *>(to + (wave * 16 + c16) * (D + 4) + 16 * b + 4 * g) = acc[b];
+}
+
+struct FewPlace {
+    LatentPlace a;
+    KeyChannels keys;
+    Channels values, queries;
+};
+__device__ __forceinline__ FewPlace few_place(const LatentParams &p, const LatentTiles &t, bool down) {
+    FewPlace f;
+    f.a = latent_place(p, t, blockIdx.x, down);
+    if (!f.a.valid) return f;
+    const LatentPlace &a = f.a;
+    f.keys = {static_cast<const float *>(p.kn) + a.b * p.k_sb + a.h * p.k_sh + a.k0 * p.k_st, static_cast<const float *>(p.kr) + a.b * p.r_sb + a.k0 * p.r_st,
+              p.k_st, p.r_st, p.dn, p.dr};
+    f.values = {static_cast<const float *>(p.v) + a.b * p.v_sb + a.h * p.v_sh + a.k0 * p.v_st, p.v_st, p.dv};
+    f.queries = {static_cast<const float *>(p.q) + a.b * p.q_sb + a.h * p.q_sh + a.q0 * p.q_st, p.q_st, p.dn + p.dr};
+    return f;
+}
+
+template <typename O, int DK, int DV>
+__global__ void __launch_bounds__(256, 2) prefill_few_kernel(LatentParams p) {
+    __shared__ float s_acc[4 * 16 * (DV + 4)], s_top[4][16], s_sum[4][16];
+    const FewPlace f = few_place(p, p.tq, p.causal);
+    const LatentPlace &a = f.a;
+    if (!a.valid) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c16 = lane & 15;
+    const int q0 = a.tile * kFewTile, qi = q0 + c16, shift = a.tk - a.tq;
+    f32x4 qf[DK / 16], acc[DV / 16];
+    own16<DK>(qf, f.queries, min(qi, a.tq - 1), p.dn + p.dr, qi < a.tq, g);
+#pragma unroll
+    for (int b = 0; b < DV / 16; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int n = p.causal ? min(a.tk, min(a.tq, q0 + kFewTile) + shift) : a.tk;
+    const int limit = p.causal ? min(n, qi + shift + 1) : n;
+    const float c = p.scale * kLog2e;
+    float top = -INFINITY, sum = 0.f;
+    f32x4 kf[DK / 16];
+    if (n > 0) rows16<DK>(kf, f.keys, wave * 16, n, g, c16);
+    for (int k0 = wave * 16; k0 < n; k0 += 64) {
+        f32x4 vf[DV / 16];
+        cols16<DV>(vf, f.values, k0, n, g, c16);
+        f32x4 s = dot16<DK>(kf, qf);
+        rows16<DK>(kf, f.keys, k0 + 64, n, g, c16);  // the next step's, under this one's second half
+        float most = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            s[j] = k0 + 4 * g + j < limit ? s[j] * c : -INFINITY;
+            most = fmaxf(most, s[j]);
+        }
+        most = fmaxf(top, quarter_max(most));
+        const float base = most == -INFINITY ? 0.f : most, keep = fast_exp2(top - base);
+        top = most;
+        sum *= keep;
+#pragma unroll
+        for (int b = 0; b < DV / 16; ++b) acc[b] *= keep;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            s[j] = fast_exp2(s[j] - base);
+            sum += s[j];
+        }
+        add16<DV>(acc, vf, s);
+    }
+    sum = quarter_sum(sum);
+    put16<DV>(s_acc, acc, wave, g, c16);
+    if (g == 0) {
+        s_top[wave][c16] = top;
+        s_sum[wave][c16] = sum;
+    }
+    __syncthreads();
+    const int i = threadIdx.x >> 4, part = threadIdx.x & 15;  // a query, four channels of every 64
+    if (q0 + i >= a.tq) return;
+    top = fmaxf(fmaxf(s_top[0][i], s_top[1][i]), fmaxf(s_top[2][i], s_top[3][i]));
+    const float base = top == -INFINITY ? 0.f : top;
+    float w[4];
+    sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        w[k] = fast_exp2(s_top[k][i] - base);
+        sum += w[k] * s_sum[k][i];
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t row = (a.q_row + q0 + i) * p.H + a.h;
+    O *o = static_cast<O *>(p.o) + row * p.dv;
+    for (int ch = 4 * part; ch < p.dv; ch += 64) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v += w[k] * load4(s_acc + (k * 16 + i) * (DV + 4) + ch);
+        store4(o + ch, v * inv);
+    }
+    if (part == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(256, 1) grad_q_few_kernel(LatentGradParams gp) {
+    __shared__ float s_acc[4 * 16 * (DK + 4)];
+    const LatentParams &p = gp.f;
+    const FewPlace f = few_place(p, p.tq, p.causal);
+    const LatentPlace &a = f.a;
+    if (!a.valid) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c16 = lane & 15;
+    const int q0 = a.tile * kFewTile, qi = q0 + c16, shift = a.tk - a.tq;
+    const bool inside = qi < a.tq;
+    const Channels grads = {static_cast<const float *>(gp.d_o) + a.b * gp.d_sb + a.h * gp.d_sh + a.q0 * gp.d_st, gp.d_st, p.dv};
+    f32x4 qf[DK / 16], df[DV / 16], acc[DK / 16];
+    own16<DK>(qf, f.queries, min(qi, a.tq - 1), p.dn + p.dr, inside, g);
+    own16<DV>(df, grads, min(qi, a.tq - 1), p.dv, inside, g);
+#pragma unroll
+    for (int b = 0; b < DK / 16; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int64_t at = static_cast<int64_t>(a.h) * p.B * p.T + a.q_row + qi;
+    const float lse = inside ? gp.lse2[at] : 0.f, delta = inside ? gp.delta[at] : 0.f;
+    const int n = p.causal ? min(a.tk, min(a.tq, q0 + kFewTile) + shift) : a.tk;
+    const int limit = inside ? (p.causal ? min(n, qi + shift + 1) : n) : 0;
+    const float c = p.scale * kLog2e;
+    f32x4 kf[DK / 16], vf[DV / 16];
+    if (n > 0) {
+        rows16<DK>(kf, f.keys, wave * 16, n, g, c16);
+        rows16<DV>(vf, f.values, wave * 16, n, g, c16);
+    }
+    for (int k0 = wave * 16; k0 < n; k0 += 64) {
+        f32x4 kc[DK / 16];
+        cols16<DK>(kc, f.keys, k0, n, g, c16);
+        const f32x4 s = dot16<DK>(kf, qf);
+        f32x4 dp = dot16<DV>(vf, df);
+        rows16<DK>(kf, f.keys, k0 + 64, n, g, c16);  // the next step's, under this one's second half
+        rows16<DV>(vf, f.values, k0 + 64, n, g, c16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dp[j] = k0 + 4 * g + j < limit ? fast_exp2(s[j] * c - lse) * (dp[j] - delta) * p.scale : 0.f;
+        add16<DK>(acc, kc, dp);
+    }
+    put16<DK>(s_acc, acc, wave, g, c16);
+    __syncthreads();
+    const int i = threadIdx.x >> 4, part = threadIdx.x & 15;
+    if (q0 + i >= a.tq) return;
+    float *dq = static_cast<float *>(gp.dq) + ((a.q_row + q0 + i) * p.H + a.h) * (p.dn + p.dr);
+    for (int ch = 4 * part; ch < p.dn + p.dr; ch += 64) {
+        f32x4 v = load4(s_acc + i * (DK + 4) + ch);
+#pragma unroll
+        for (int k = 1; k < 4; ++k) v += load4(s_acc + (k * 16 + i) * (DK + 4) + ch);
+        store4(dq + ch, v);
+    }
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(256, 1) grad_k_few_kernel(LatentGradParams gp) {
+    __shared__ float s_k[4 * 16 * (DK + 4)], s_v[4 * 16 * (DV + 4)];
+    const LatentParams &p = gp.f;
+    const FewPlace f = few_place(p, gp.tk, false);
+    const LatentPlace &a = f.a;
+    if (!a.valid) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c16 = lane & 15;
+    const int k0 = a.tile * kFewTile, ki = k0 + c16, shift = a.tk - a.tq;
+    const bool inside = ki < a.tk;
+    const Channels grads = {static_cast<const float *>(gp.d_o) + a.b * gp.d_sb + a.h * gp.d_sh + a.q0 * gp.d_st, gp.d_st, p.dv};
+    f32x4 kf[DK / 16], vf[DV / 16], dk[DK / 16], dv[DV / 16];
+    own16<DK>(kf, f.keys, min(ki, a.tk - 1), p.dn + p.dr, inside, g);
+    own16<DV>(vf, f.values, min(ki, a.tk - 1), p.dv, inside, g);
+#pragma unroll
+    for (int b = 0; b < DK / 16; ++b) dk[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int b = 0; b < DV / 16; ++b) dv[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int64_t row0 = static_cast<int64_t>(a.h) * p.B * p.T + a.q_row;
+    const float c = p.scale * kLog2e;
+    // the first query that sees the tile's first key
+    const int start = (p.causal ? max(0, k0 - shift) : 0) / 16 * 16;
+    f32x4 qf[DK / 16], df[DV / 16];
+    if (a.tq > 0) {
+        rows16<DK>(qf, f.queries, start + wave * 16, a.tq, g, c16);
+        rows16<DV>(df, grads, start + wave * 16, a.tq, g, c16);
+    }
+    for (int i0 = start + wave * 16; i0 < a.tq; i0 += 64) {
+        f32x4 qc[DK / 16], dc[DV / 16], lse, delta;
+        cols16<DV>(dc, grads, i0, a.tq, g, c16);
+        cols16<DK>(qc, f.queries, i0, a.tq, g, c16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t i = row0 + min(i0 + 4 * g + j, a.tq - 1);
+            lse[j] = gp.lse2[i];
+            delta[j] = gp.delta[i];
+        }
+        f32x4 s = dot16<DK>(qf, kf);
+        f32x4 dp = dot16<DV>(df, vf);
+        rows16<DK>(qf, f.queries, i0 + 64, a.tq, g, c16);  // the next step's, under this one's second half
+        rows16<DV>(df, grads, i0 + 64, a.tq, g, c16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + 4 * g + j;
+            const bool sees = inside && i < a.tq && (!p.causal || ki <= i + shift);
+            s[j] = sees ? fast_exp2(s[j] * c - lse[j]) : 0.f;
+            dp[j] = sees ? s[j] * (dp[j] - delta[j]) * p.scale : 0.f;
+        }
+        add16<DV>(dv, dc, s);
+        add16<DK>(dk, qc, dp);
+    }
+    put16<DK>(s_k, dk, wave, g, c16);
+    put16<DV>(s_v, dv, wave, g, c16);
+    __syncthreads();
+    const int i = threadIdx.x >> 4, part = threadIdx.x & 15;
+    if (k0 + i >= a.tk) return;
+    const int64_t key = a.k_row + k0 + i;
+    float *dkn = static_cast<float *>(gp.dkn) + (key * p.H + a.h) * p.dn, *dvp = static_cast<float *>(gp.dv) + (key * p.H + a.h) * p.dv;
+    float *shared = gp.dkr_part + (static_cast<int64_t>(a.h) * p.B * p.S + key) * p.dr;
+    for (int ch = 4 * part; ch < p.dn + p.dr; ch += 64) {
+        f32x4 v = load4(s_k + i * (DK + 4) + ch);
+#pragma unroll
+        for (int k = 1; k < 4; ++k) v += load4(s_k + (k * 16 + i) * (DK + 4) + ch);
+        store4(ch < p.dn ? dkn + ch : shared + ch - p.dn, v);
+    }
+    for (int ch = 4 * part; ch < p.dv; ch += 64) {
+        f32x4 v = load4(s_v + i * (DV + 4) + ch);
+#pragma unroll
+        for (int k = 1; k < 4; ++k) v += load4(s_v + (k * 16 + i) * (DV + 4) + ch);
+        store4(dvp + ch, v);
+    }
+}
+
 template <typename O, int DK, int DV>
 hipError_t run_prefill(const LatentParams &p, hipStream_t s) {
     const int grid = p.cu_q ? p.H * p.tq.bound : p.H * p.N * p.tq.per_seq;
-    prefill_f32_kernel<O, DK, DV><<<grid, 256, 0, s>>>(p);
+    if (p.tq.size == kFewTile) prefill_few_kernel<O, DK, DV><<<grid, 256, 0, s>>>(p);
+    else prefill_f32_kernel<O, DK, DV><<<grid, 256, 0, s>>>(p);
     return hipGetLastError();
 }
 template <typename O>
@@ -307,8 +590,10 @@ hipError_t run_grad(const LatentGradParams &g, hipStream_t s) {
     const LatentParams &p = g.f;
     const int grid_q = p.cu_q ? p.H * p.tq.bound : p.H * p.N * p.tq.per_seq;
     const int grid_k = p.cu_q ? p.H * g.tk.bound : p.H * p.N * g.tk.per_seq;
-    if (p.T) grad_q_f32_kernel<DK, DV><<<grid_q, 256, 0, s>>>(g);
-    if (p.S) grad_k_f32_kernel<DK, DV><<<grid_k, 256, 0, s>>>(g);
+    if (p.T && p.tq.size == kFewTile) grad_q_few_kernel<DK, DV><<<grid_q, 256, 0, s>>>(g);
+    if (p.T && p.tq.size != kFewTile) grad_q_f32_kernel<DK, DV><<<grid_q, 256, 0, s>>>(g);
+    if (p.S && g.tk.size == kFewTile) grad_k_few_kernel<DK, DV><<<grid_k, 256, 0, s>>>(g);
+    if (p.S && g.tk.size != kFewTile) grad_k_f32_kernel<DK, DV><<<grid_k, 256, 0, s>>>(g);
     return hipGetLastError();
 }
 hipError_t pick_grad(const LatentGradParams &g, hipStream_t s) {
@@ -319,6 +604,8 @@ hipError_t pick_grad(const LatentGradParams &g, hipStream_t s) {
 }
 
 }  // namespace
+
+int latent_tile_f32(int64_t tokens, int H) { return tokens * H < kFewBelow ? kFewTile : kTileQ; }
 
 hipError_t latent_prefill_f32(const LatentParams &p, int out_dtype, hipStream_t s) {
     return out_dtype == 0 ? pick_prefill<float>(p, s) : pick_prefill<bf16_t>(p, s);

@@ -164,7 +164,7 @@ hipError_t pick(const LatentParams &p, hipStream_t s) {
 
 }  // namespace
 
-int latent_tile_q(int dtype) { return dtype == 0 ? kLatentTileF32 : kTileQ; }
+int latent_tile_q(int dtype, int64_t tokens, int H) { return dtype == 0 ? latent_tile_f32(tokens, H) : kTileQ; }
 
 hipError_t launch_latent_prefill(const LatentParams &p, int in_dtype, int out_dtype, hipStream_t s) {
     if (in_dtype == 0) return latent_prefill_f32(p, out_dtype, s);

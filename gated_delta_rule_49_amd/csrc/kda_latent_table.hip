@@ -1,64 +1,128 @@
 // The table of packed sequences' tiles for the expanded form of latent
 // attention, and the check of the offsets that its kernels read first.
+//
+// One workgroup.  Each thread counts the tiles of a run of sequences; a prefix
+// sum over the threads gives every sequence's first tile; then a thread takes a
+// tile, finds its sequence by bisection, and puts it where its bucket of work
+// (tokens of the other side that it sees) begins: the largest first, so that the
+// last workgroups of a launch are small ones.  (A ragged batch, 8 prompts of 0 to
+// 3001 tokens behind 0 to 4097 cached ones, 32 heads.)  The order inside a bucket
+// is that of arrival; no result depends on it.
 #include "kda_latent.hpp"
 
 namespace kda {
 
 namespace {
 
-// One workgroup.  Each thread takes a run of sequences, the tiles before its
-// run come from a prefix sum over the threads.
-__device__ __forceinline__ void fill(const int32_t *cu, int total_tokens, int N, int size, int bound, int2 *entry, int32_t *count,
-                                     int *s_wave, int *s_bad) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int per = (N + 1023) / 1024;
-    const int n0 = min(N, tid * per), n1 = min(N, n0 + per);
-    int local = 0;
-    for (int n = n0; n < n1; ++n) {
-        const int32_t a = cu[n], b = cu[n + 1];
-        if (b < a || a < 0 || b > total_tokens) *s_bad = 1;  // any writer sets 1
-        else local += (b - a + size - 1) / size;
-    }
-    if (tid == 0 && (cu[0] != 0 || cu[N] != total_tokens)) *s_bad = 1;
-    int run = local;  // inclusive over the threads
+constexpr int kThreads = 1024, kBuckets = 64;
+constexpr int kInLds = 4096;  // sequences whose offsets fit
+
+struct Scratch {
+    int off[kInLds + 1];
+    int wave[kThreads / 64];
+    int bucket[kBuckets + 1];
+    int most, bad;
+};
+
+// sum over the workgroup of the threads before this one, and of all
+__device__ __forceinline__ int2 prefix(int own, int *s_wave) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int run = own;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const int o = __shfl_up(run, d);
         if (lane >= d) run += o;
     }
-    if (lane == 63) s_wave[tid >> 6] = run;
+    if (lane == 63) s_wave[wave] = run;
     __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < 16; ++w) {
-        if (w < (tid >> 6)) run += s_wave[w];
+    int before = 0, total = 0;
+    for (int w = 0; w < kThreads / 64; ++w) {
+        if (w < wave) before += s_wave[w];
         total += s_wave[w];
     }
-    // sequences that do not overlap have no more tiles than the bound
-    if (total > bound) *s_bad = 1;
     __syncthreads();
-    if (*s_bad == 0 && entry) {
-        int at = run - local;
-        for (int n = n0; n < n1; ++n) {
-            const int c = (cu[n + 1] - cu[n] + size - 1) / size;
-            for (int i = 0; i < c; ++i) entry[at + i] = make_int2(n, i);
-            at += c;
-        }
+    return make_int2(before + run - own, total);
+}
+
+// whether cu is 0 = cu[0] <= .. <= cu[N] = tokens (any writer sets bad)
+__device__ __forceinline__ void check(const int32_t *cu, int tokens, int N, int *bad) {
+    for (int n = threadIdx.x; n < N; n += kThreads) {
+        const int32_t a = cu[n], b = cu[n + 1];
+        if (b < a || a < 0 || b > tokens) *bad = 1;
     }
-    if (tid == 0 && count) *count = static_cast<int32_t>(total);
+    if (threadIdx.x == 0 && (cu[0] != 0 || cu[N] != tokens)) *bad = 1;
+}
+
+// work(tokens of this side, of the other, tile) -> tokens of the other side that the tile sees
+template <typename W>
+__device__ __forceinline__ void fill(const int32_t *cu, const int32_t *other, int N, int size, int bound, int *spill, int2 *entry, int32_t *count, Scratch &s, W &&work) {
+    const int tid = threadIdx.x;
+    int *off = N <= kInLds ? s.off : spill;
+    const int per = (N + kThreads - 1) / kThreads;
+    const int n0 = min(N, tid * per), n1 = min(N, n0 + per);
+    auto tiles = [&](int n) { return (cu[n + 1] - cu[n] + size - 1) / size; };
+    int own = 0, most = 0;
+    for (int n = n0; n < n1; ++n) {
+        own += tiles(n);
+        most = max(most, other[n + 1] - other[n]);
+    }
+    if (tid <= kBuckets) s.bucket[tid] = 0;
+    if (tid == 0) s.most = 0;
+    const int2 at = prefix(own, s.wave);
+    atomicMax(&s.most, most);
+    int first = at.x;
+    for (int n = n0; n < n1; ++n) {
+        off[n] = first;
+        first += tiles(n);
+    }
+    if (tid == 0) off[N] = at.y;
+    __syncthreads();
+    const int total = min(at.y, bound);
+    const float scale = static_cast<float>(kBuckets) / static_cast<float>(s.most + 1);
+    auto place = [&](int t) {  // (sequence, tile of it, bucket)
+        int lo = 0, hi = N;    // the last sequence with off <= t: one with tiles
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (off[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        const int i = t - off[lo];
+        const int w = max(0, work(cu[lo + 1] - cu[lo], other[lo + 1] - other[lo], i));
+        return make_int3(lo, i, kBuckets - 1 - min(kBuckets - 1, static_cast<int>(static_cast<float>(w) * scale)));
+    };
+    for (int t = tid; t < total; t += kThreads) atomicAdd(&s.bucket[place(t).z + 1], 1);
+    __syncthreads();
+    if (tid == 0)
+        for (int b = 1; b <= kBuckets; ++b) s.bucket[b] += s.bucket[b - 1];
+    __syncthreads();
+    for (int t = tid; t < total; t += kThreads) {
+        const int3 p = place(t);
+        entry[atomicAdd(&s.bucket[p.z], 1)] = make_int2(p.x, p.y);
+    }
+    if (tid == 0) *count = total;
     __syncthreads();
 }
 
-__global__ void __launch_bounds__(1024) latent_table_kernel(LatentTable t) {
-    __shared__ int s_wave[16];
-    __shared__ int s_bad;
-    if (threadIdx.x == 0) s_bad = 0;
+__global__ void __launch_bounds__(kThreads) latent_table_kernel(LatentTable t) {
+    __shared__ Scratch s;
+    if (threadIdx.x == 0) s.bad = 0;
     __syncthreads();
-    fill(t.cu_q, t.T, t.N, t.size_q, t.bound_q, t.entry_q, t.word + 1, s_wave, &s_bad);
-    fill(t.cu_k, t.S, t.N, t.size_k, t.bound_k, t.entry_k, t.word + 2, s_wave, &s_bad);
+    check(t.cu_q, t.T, t.N, &s.bad);
+    check(t.cu_k, t.S, t.N, &s.bad);
+    __syncthreads();
+    const bool bad = s.bad != 0;
+    if (!bad) {
+        const bool causal = t.causal;
+        if (t.entry_q)
+            fill(t.cu_q, t.cu_k, t.N, t.size_q, t.bound_q, t.spill, t.entry_q, t.word + 1, s,
+                 [&](int tq, int tk, int i) { return causal ? min(tk, min(tq, (i + 1) * t.size_q) + tk - tq) : tk; });
+        if (t.entry_k)
+            fill(t.cu_k, t.cu_q, t.N, t.size_k, t.bound_k, t.spill, t.entry_k, t.word + 2, s,
+                 [&](int tk, int tq, int i) { return causal ? tq - max(0, i * t.size_k - (tk - tq)) : tq; });
+    }
     if (threadIdx.x == 0) {
-        const int32_t st = s_bad ? kBadSeqlens : 0;
-        t.word[0] = st;
-        if (t.user_status) *t.user_status = st;
+        t.word[0] = bad ? kBadSeqlens : 0;
+        if (t.user_status) *t.user_status = bad ? kBadSeqlens : 0;
     }
 }
 
@@ -66,8 +130,10 @@ __global__ void status_word_kernel(int32_t *word) { *word = 0; }
 
 }  // namespace
 
+size_t latent_table_spill(int N) { return N <= kInLds ? 0 : sizeof(int32_t) * (static_cast<size_t>(N) + 1); }
+
 hipError_t launch_latent_table(const LatentTable &t, hipStream_t s) {
-    latent_table_kernel<<<1, 1024, 0, s>>>(t);
+    latent_table_kernel<<<1, kThreads, 0, s>>>(t);
     return hipGetLastError();
 }
 
