@@ -51,17 +51,22 @@ struct LatentPlace {
     bool valid;
 };
 
-// Tiles of one head stand together in the logical order, those that see most
-// first (`down`: the later ones).  Blocks are dealt to the 8 XCDs in turn: where
-// the heads divide evenly each XCD takes whole heads, so that a head's keys and
-// values are read through one L2; else neighbours go to different XCDs.
+// The tiles that see most come first, over all heads (`down`: the later ones), so
+// that no long one begins late.  Blocks are dealt to the 8 XCDs in turn: where the
+// heads divide evenly each XCD takes whole heads, whose keys and values are then
+// read through one L2.
 __device__ __forceinline__ LatentPlace latent_place(const LatentParams &p, const LatentTiles &t, int block, bool down) {
     LatentPlace a;
     const int pairs = p.cu_q ? p.H : p.H * p.N;
     const int per = p.cu_q ? t.bound : t.per_seq;
-    if (pairs % 8 == 0) block = (block & 7) * (pairs / 8 * per) + (block >> 3);
-    const int pair = block / per;
-    int i = block - pair * per;
+    int pair, i;
+    if (pairs % 8 == 0) {
+        i = (block >> 3) / (pairs / 8);
+        pair = (block & 7) * (pairs / 8) + (block >> 3) - i * (pairs / 8);
+    } else {
+        i = block / pairs;
+        pair = block - i * pairs;
+    }
     if (p.cu_q) {
         const int n = *p.status == 0 ? *t.count : 0;
         a.valid = i < n;
