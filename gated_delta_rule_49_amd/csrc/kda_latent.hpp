@@ -88,6 +88,8 @@ __device__ __forceinline__ LatentPlace latent_place(const LatentParams &p, const
         a.tq = p.T;
         a.tk = p.S;
     }
+    // the same in all lanes, said so: the table's words come by vector loads
+    for (int *x : {&a.b, &a.q0, &a.k0, &a.tq, &a.tk, &a.h, &a.tile}) *x = __builtin_amdgcn_readfirstlane(*x);
     a.q_row = static_cast<int64_t>(a.b) * p.T + a.q0;
     a.k_row = static_cast<int64_t>(a.b) * p.S + a.k0;
     return a;

@@ -92,6 +92,7 @@ template <int DK, int DV>
 __global__ void __launch_bounds__(kQThreads, 512 / kQThreads) grad_q_bf16_kernel(LatentGradParams gp) {
     constexpr int KB = kStep * DK * 2, VB = kStep * DV * 2;
     __shared__ __attribute__((aligned(128))) char s_tile[2 * (KB + VB)];
+    __shared__ uint32_t s_off[kStep * (DK + DV) / 8];  // one a chunk
     const LatentParams &p = gp.f;
     const LatentPlace a = latent_place(p, p.tq, blockIdx.x, p.causal);
     if (!a.valid) return;
@@ -108,10 +109,10 @@ __global__ void __launch_bounds__(kQThreads, 512 / kQThreads) grad_q_bf16_kernel
     const int n_wave = q_first >= a.tq ? 0 : p.causal ? min(n, min(a.tq - 1, q_first + 31) + shift + 1) : n;
     const int limit = !inside ? 0 : p.causal ? min(n, qi + shift + 1) : n;
 
-    TileLoader<DK, kStep, kQThreads, BothRead> keys;
-    TileLoader<DV, kStep, kQThreads, BothRead> values;
-    keys.init(kn, p.k_st, p.dn, kr, p.r_st, p.dr);
-    values.init(v, p.v_st, p.dv, v, 0, 0);
+    TileLoader<DK, kStep, kQThreads, BothRead, true, true> keys;
+    TileLoader<DV, kStep, kQThreads, BothRead, false, true> values;
+    keys.init(kn, p.k_st, p.dn, kr, p.r_st, p.dr, 0, s_off);
+    values.init(v, p.v_st, p.dv, v, 0, 0, 0, s_off + kStep * DK / 8);
     const uint32_t lds = lds_address(s_tile);
     if (n > 0) {
         keys.issue(0, n, lds);
@@ -144,13 +145,13 @@ __global__ void __launch_bounds__(kQThreads, 512 / kQThreads) grad_q_bf16_kernel
 #pragma unroll
             for (int k = 0; k < DK / 16; ++k) {
                 frag8 f;
-                f.u = *reinterpret_cast<const uint4 *>(kt + BothRead::step(key_at, k));
+                f.u = *reinterpret_cast<const uint4 *>(kt + BothRead::step<DK>(key_at, k));
                 s = mfma32(f.v, qf[k], s);
             }
 #pragma unroll
             for (int k = 0; k < DV / 16; ++k) {
                 frag8 f;
-                f.u = *reinterpret_cast<const uint4 *>(vt + BothRead::step(value_at, k));
+                f.u = *reinterpret_cast<const uint4 *>(vt + BothRead::step<DV>(value_at, k));
                 dp = mfma32(f.v, df[k], dp);
             }
 #pragma unroll
@@ -208,10 +209,10 @@ __global__ void __launch_bounds__(kKThreads, 1) grad_k_bf16_kernel(LatentGradPar
     // the first query that sees the tile's first key
     const int start = (p.causal ? max(0, a.tile * kTileK - shift) : 0) / kStep * kStep;
 
-    TileLoader<DK, kStep, kKThreads, BothRead> queries;
-    TileLoader<DV, kStep, kKThreads, BothRead> grads;
-    queries.init(q, p.q_st, p.dn + p.dr, q, 0, 0);
-    grads.init(d_o, gp.d_st, p.dv, d_o, 0, 0);
+    TileLoader<DK, kStep, kKThreads, BothRead, false> queries;
+    TileLoader<DV, kStep, kKThreads, BothRead, false> grads;
+    queries.init(q, p.q_st, p.dn + p.dr, q, 0, 0, start);
+    grads.init(d_o, gp.d_st, p.dv, d_o, 0, 0, start);
     auto issue = [&](int i0, int buf) {
         queries.issue(i0, a.tq, lds_address(sh.q[0]) + buf * (kStep * DK * 2));
         grads.issue(i0, a.tq, lds_address(sh.d[0]) + buf * (kStep * DV * 2));
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kKThreads, 1) grad_k_bf16_kernel(LatentGradPar
 #pragma unroll
                     for (int k = 0; k < DK / 16; ++k) {
                         frag8 f;
-                        f.u = *reinterpret_cast<const uint4 *>(sh.q[buf] + 32 * t * DK * 2 + BothRead::step(q_at, k));
+                        f.u = *reinterpret_cast<const uint4 *>(sh.q[buf] + 32 * t * DK * 2 + BothRead::step<DK>(q_at, k));
                         s = mfma32(f.v, kf[k], s);
                     }
 #pragma unroll
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kKThreads, 1) grad_k_bf16_kernel(LatentGradPar
 #pragma unroll
                 for (int k = 0; k < DV / 16; ++k) {
                     frag8 f;
-                    f.u = *reinterpret_cast<const uint4 *>(sh.d[buf] + 32 * t * DV * 2 + BothRead::step(d_at, k));
+                    f.u = *reinterpret_cast<const uint4 *>(sh.d[buf] + 32 * t * DV * 2 + BothRead::step<DV>(d_at, k));
                     dp[t] = mfma32(f.v, vf[k], dp[t]);
                 }
 #pragma unroll

@@ -72,21 +72,29 @@ struct ColumnRead {  // read by columns
         else return r * (D * 2) + ((c ^ (((t << 1) ^ ((t ^ (t >> 1)) & 1)) << 1)) * 16);
     }
 };
-struct BothRead {  // read in both ways
-    template <int D> __device__ __forceinline__ static constexpr int place(int r, int c) {
-        return r * (D * 2) + ((c & ~7) * 16) + (((c ^ r ^ (r >> 3 & 1)) & 7) * 16);
+// Read in both ways: s(r) has the row's low two bits above its third, so that 8
+// rows' chunks differ for a read by rows and 4 rows' PAIRS of chunks for one by
+// columns; 8 rows on, and for 128 channels the odd rows, which would lie on the
+// even ones' banks, take other places again.
+struct BothRead {
+    template <int D> __device__ __forceinline__ static constexpr int turn(int r) {
+        const int s = (((r & 3) << 1) | (r >> 2 & 1)) ^ ((r >> 3 & 1) << 1);
+        return D == 128 ? s | (r & 1) << 3 : s;
     }
+    template <int D> __device__ __forceinline__ static constexpr int place(int r, int c) { return r * (D * 2) + ((c ^ turn<D>(r)) * 16); }
     // A lane's place for the first 16 channels of row c32, by rows; k 16-channel steps further
     template <int D> __device__ __forceinline__ static uint32_t row(int lane) { return place<D>(lane & 31, lane >> 5); }
-    __device__ __forceinline__ static uint32_t step(uint32_t at, int k) { return (at ^ (32 * (k & 3))) + (k >> 2) * 128; }
+    template <int D> __device__ __forceinline__ static uint32_t step(uint32_t at, int k) {
+        return D == 128 ? at ^ (32 * k) : (at ^ (32 * (k & 3))) + (k >> 2) * 128;
+    }
     // .. and for 32 channels of 16 rows, by columns: rows 4 h + 0..3 and 8 rows on; block b of channels
     template <int D> __device__ __forceinline__ static uint32_t columns(int lane) {
         return place<D>(4 * (lane >> 5) + ((lane & 15) >> 2), 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) + 8 * (lane & 1);
     }
     template <int D> __device__ __forceinline__ static bf16x8 read_columns(const char *tile, uint32_t at, int b) {
-        const char *from = tile + (b >> 1) * 128;
-        const uint32_t turned = at ^ (64 * (b & 1));
-        const uint2 lo = read_tr16(from + turned), hi = read_tr16(from + 8 * D * 2 + (turned ^ 16));
+        const char *from = D == 128 ? tile : tile + (b >> 1) * 128;
+        const uint32_t turned = D == 128 ? at ^ (64 * b) : at ^ (64 * (b & 1));
+        const uint2 lo = read_tr16(from + turned), hi = read_tr16(from + 8 * D * 2 + (turned ^ 32));
         frag8 f;
         f.u = make_uint4(lo.x, lo.y, hi.x, hi.y);
         return f.v;
@@ -101,6 +109,10 @@ struct BothRead {  // read in both ways
 __device__ __forceinline__ void load_to_lds(const void *from, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(from) : "memory");
 }
+// .. from a base that all lanes share and 32-bit offsets
+__device__ __forceinline__ void load_to_lds(const char *base, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(offset), "s"(base) : "memory");
+}
 // .. and 4 bytes a lane
 __device__ __forceinline__ void load_word_to_lds(const void *from, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(from) : "memory");
@@ -110,30 +122,61 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)p));
 }
 
-// ROWS rows of D channels from memory to an LDS tile, in chunks of 16 bytes; the
-// channels are `first` of one tensor, then `second` of another.  Rows behind the
-// last (n - 1) repeat it; channels behind both are the row's first again: what
-// they meet is 0, or their results are not kept.
-template <int D, int ROWS, int THREADS, typename PERM> struct TileLoader {
+// Tile after tile of ROWS rows of D channels from memory to LDS, in chunks of 16
+// bytes; the channels are `first` of one tensor, then, with TWO, `second` of another.  Rows
+// behind the last (n - 1) repeat it; channels behind both are the row's first
+// again: what they meet is 0, or their results are not kept.  The tensors' bases
+// step in scalar registers, a lane's offsets inside a tile stay (in LDS where a
+// kernel has no register for them: a spilled one's load would wait for the tile); where the key
+// has two parts, a chunk's lanes load from the one, then from the other.
+template <int D, int ROWS, int THREADS, typename PERM, bool TWO, bool STORED = false> struct TileLoader {
     static constexpr int N = ROWS * D * 2 / 16 / THREADS;  // chunks a thread
-    const char *base[N];
-    uint32_t stride[N];
-    __device__ __forceinline__ void init(const bf16_t *one, int64_t one_st, int first, const bf16_t *two, int64_t two_st, int second) {
+    const char *one, *two;
+    uint32_t one_st, two_st;  // bytes of a row
+    uint32_t off[STORED ? 1 : N];
+    uint32_t other;           // bit i: chunk i is of the second part
+    uint32_t *s_off;          // STORED: the lanes' offsets in LDS, [N][THREADS]
+    // from row r0 on
+    __device__ __forceinline__ void init(const bf16_t *a, int64_t a_st, int first, const bf16_t *b, int64_t b_st, int second, int r0, uint32_t *s = nullptr) {
+        s_off = s;
+        one_st = static_cast<uint32_t>(a_st) * 2;
+        two_st = static_cast<uint32_t>(b_st) * 2;
+        one = reinterpret_cast<const char *>(a) + static_cast<uint64_t>(static_cast<uint32_t>(r0)) * one_st;
+        two = reinterpret_cast<const char *>(b) + static_cast<uint64_t>(static_cast<uint32_t>(r0)) * two_st;
+        other = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int at = i * THREADS + threadIdx.x, r = at / (D / 8);
-            const int ch = (PERM::template place<D>(r, at % (D / 8)) - r * D * 2) / 2;
-            const bool other = ch >= first && ch < first + second;
-            base[i] = reinterpret_cast<const char *>(other ? two + (ch - first) : one + (ch < first ? ch : 0));
-            stride[i] = static_cast<uint32_t>(other ? two_st : one_st) * 2;
+            const int c = i * THREADS + threadIdx.x, r = c / (D / 8);
+            const int ch = (PERM::template place<D>(r, c % (D / 8)) - r * D * 2) / 2;
+            const bool is = TWO && ch >= first && ch < first + second;
+            const uint32_t at = r * (is ? two_st : one_st) + 2 * (is ? ch - first : ch < first ? ch : 0);
+            if constexpr (STORED) s_off[i * THREADS + threadIdx.x] = at;
+            else off[i] = at;
+            other |= (is ? 1u : 0u) << i;
         }
     }
-    __device__ __forceinline__ void issue(int r0, int n, uint32_t to) const {
+    __device__ __forceinline__ uint32_t offset(int i) const {
+        if constexpr (STORED) return s_off[i * THREADS + threadIdx.x];
+        else return off[i];
+    }
+    __device__ __forceinline__ void load(int i, uint32_t at, uint32_t to) const {
+        to += i * THREADS * 16 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+        if (!TWO || !(other >> i & 1)) load_to_lds(one, at, to);
+        if (TWO && (other >> i & 1)) load_to_lds(two, at, to);
+    }
+    __device__ __forceinline__ void issue(int r0, int n, uint32_t to) {
+        if (r0 + ROWS <= n) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int r = (i * THREADS + threadIdx.x) / (D / 8);
-            load_to_lds(base[i] + static_cast<uint64_t>(static_cast<uint32_t>(min(r0 + r, n - 1))) * stride[i], to + (i * THREADS + (threadIdx.x & ~63)) * 16);
+            for (int i = 0; i < N; ++i) load(i, offset(i), to);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {  // the last tile
+                const int r = (i * THREADS + threadIdx.x) / (D / 8), behind = max(0, r0 + r - (n - 1));
+                load(i, offset(i) - static_cast<uint32_t>(behind) * (TWO && (other >> i & 1) ? two_st : one_st), to);
+            }
         }
+        one += static_cast<uint64_t>(one_st) * ROWS;
+        if (TWO) two += static_cast<uint64_t>(two_st) * ROWS;
     }
 };
 

@@ -29,8 +29,8 @@ constexpr int kKeys = 64, kRows = 32, kThreads = 512;
 constexpr float kSlack = 8.f;          // log2; see the forward: how far P may pass 1
 constexpr int kPRow = kKeys * 2 + 16;  // bytes of a row of P: 16 more than its keys
 
-// chunk c of row r of the tile (read by rows and by columns)
-__device__ __forceinline__ constexpr int swizzle(int r, int c) { return (c & ~7) | ((c ^ r ^ (r >> 3 & 1)) & 7); }
+// where chunk c of row r of the tile lies in its row (read by rows and by columns)
+__device__ __forceinline__ constexpr int swizzle(int r, int c) { return c ^ BothRead::turn<0>(r); }
 
 template <int DK> struct Shared {
     // the small parts first: their addresses are immediates of the instructions
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_bf16_kernel(LatentDecodePa
     const uint32_t lds = lds_address(sh.tile[0]), pages = lds_address(sh.page[0]);
     // the lane's bytes in a tile: its key's row, chunk g (bit 2 of the chunk is the step's parity)
     const uint32_t key_at = static_cast<uint32_t>(kg * 16 + c16) * (DK * 2) + swizzle(c16, g) * 16;
-    // .. and its four channels of row c16 / 4 of a half's eight (rows 4 further: bit 2 of the chunk turns)
+    // .. and its four channels of row c16 / 4 of a half's eight (rows 4 further: bit 0 of the chunk turns)
     const uint32_t value_at = static_cast<uint32_t>(8 * h2 + (c16 >> 2)) * (DK * 2) + swizzle(8 * h2 + (c16 >> 2), 2 * (g & 1) + ((c16 & 3) >> 1)) * 16 + 8 * (c16 & 1);
 
     bool first = true;
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_bf16_kernel(LatentDecodePa
                         const uint32_t turn = block & 1 ? 64u : 0u;
                         const char *from = at + 16 * k * DK * 2 + (block >> 1) * 128;
                         const uint2 lo = read_tr16(from + (value_at ^ turn));
-                        const uint2 hi = read_tr16(from + 4 * DK * 2 + (value_at ^ turn ^ 64u));
+                        const uint2 hi = read_tr16(from + 4 * DK * 2 + (value_at ^ turn ^ 16u));
                         frag8 f;
                         f.u = make_uint4(lo.x, lo.y, hi.x, hi.y);
                         acc[b] = mfma32(f.v, pf.v, acc[b]);

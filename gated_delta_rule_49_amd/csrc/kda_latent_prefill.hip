@@ -39,10 +39,10 @@ __global__ void __launch_bounds__(kThreads, 2) prefill_bf16_kernel(LatentParams 
     const int n_wave = q_first >= a.tq ? 0 : p.causal ? min(n, min(a.tq - 1, q_first + 31) + shift + 1) : n;
     const int limit = p.causal ? min(n, qi + shift + 1) : n;
 
-    TileLoader<DK, kKeys, kThreads, RowRead> keys;
-    TileLoader<DV, kKeys, kThreads, ColumnRead> values;
-    keys.init(kn, p.k_st, p.dn, kr, p.r_st, p.dr);
-    values.init(v, p.v_st, p.dv, v, 0, 0);
+    TileLoader<DK, kKeys, kThreads, RowRead, true> keys;
+    TileLoader<DV, kKeys, kThreads, ColumnRead, false> values;
+    keys.init(kn, p.k_st, p.dn, kr, p.r_st, p.dr, 0);
+    values.init(v, p.v_st, p.dv, v, 0, 0, 0);
     const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(s_tile));
     if (n > 0) {
         keys.issue(0, n, lds);
