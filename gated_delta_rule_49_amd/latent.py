@@ -17,8 +17,8 @@ import math
 
 import torch
 
-from . import (KDAError, LatentAppendArgs, LatentBackwardArgs, LatentDecodeArgs, LatentPrefillArgs, RotaryArgs, _check_buffer, _check_dev, _dt, lib)
-from .sublayer import _dense, _need_device, _p, _run, _workspace
+from . import (KDAError, LatentAppendArgs, LatentBackwardArgs, LatentDecodeArgs, LatentPrefillArgs, RotaryArgs, _check_buffer, _dt, lib)
+from .sublayer import _p, _run, _workspace
 
 _F32 = (torch.float32,)
 _F64 = (torch.float64,)
@@ -26,19 +26,35 @@ _I32 = (torch.int32,)
 _FLOATS = (torch.float32, torch.bfloat16)
 
 
-def _int_vector(t, name, count, dev):
-    """A contiguous int32 vector of ``count`` on ``dev``."""
-    _dense(dev, t)
-    _check_buffer(t, name, (count,), _I32)
+def _device(*ts):
+    """The GPU that all tensors given are on."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+            if dev.type != "cuda":
+                raise ValueError("all tensors must be on the GPU (no CPU path exists)")
+        elif t.device != dev:
+            raise ValueError("tensors are on different devices" if t.is_cuda else "all tensors must be on the GPU (no CPU path exists)")
+    return dev
+
+
+def _dense(*ts):
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
 
 
 def _lead_strides(t, name):
     """Strides of all axes but the last, which must be contiguous; 0 for an axis of one."""
-    if t.numel() == 0:
-        return (0,) * (t.dim() - 1)
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    n, s = t.shape, t.stride()
+    if 0 in n:
+        return (0,) * (len(n) - 1)
+    if s[-1] != 1 and n[-1] > 1:
         raise ValueError(f"{name}: channels must be contiguous")
-    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in range(t.dim() - 1))
+    return tuple(a if b > 1 else 0 for a, b in zip(s[:-1], n)) if 1 in n else s[:-1]
 
 
 # -------------------------------------------------------------------- rotary
@@ -80,7 +96,8 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
 
 
 def _rotary(fn, what, x, freqs, positions, offset, interleaved, magnitude, out):
-    dev = _need_device(_check_dev(freqs), x, positions, out)
+    dev = _device(x, freqs, positions, out)
+    _dense(freqs)
     if x.dim() != 4:
         raise ValueError("x must be [B,T,H,D]")
     B, T, H, D = x.shape
@@ -89,7 +106,8 @@ def _rotary(fn, what, x, freqs, positions, offset, interleaved, magnitude, out):
     _check_buffer(freqs, "freqs", freqs.shape, _F64)
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _check_buffer(out, "out", x.shape, (x.dtype,))
+    else:
+        _check_buffer(out, "out", x.shape, (x.dtype,))
     a = RotaryArgs(B=B, T=T, H=H, D=D, rotary_dim=2 * freqs.numel(), offset=offset, interleaved=1 if interleaved else 0, dtype=_dt(x.dtype),
                    magnitude=magnitude, x=_p(x), positions=_p(positions), freqs=_p(freqs), out=_p(out))
     a.x_stride_b, a.x_stride_t, a.x_stride_h = _lead_strides(x, "x")
@@ -155,7 +173,8 @@ def latent_append(kv, cache, page_table, lengths, d_latent, norm_weight=None, ep
     None.  A token without a page of its own (a position outside the table, an
     entry outside the cache) is left out; ``device_status`` (int32 [1] on the
     device) tells so.  Nothing synchronises."""
-    dev = _need_device(_check_dev(norm_weight, freqs), kv, cache, page_table)
+    dev = _device(kv, cache, page_table, lengths, norm_weight, freqs, cu_seqlens, rows, device_status)
+    _dense(norm_weight, freqs, lengths, cu_seqlens, rows, device_status)
     if kv.dim() != 3:
         raise ValueError("kv must be [B,T,d_latent+d_rope]")
     B, T, d = kv.shape
@@ -164,8 +183,7 @@ def latent_append(kv, cache, page_table, lengths, d_latent, norm_weight=None, ep
     if cu_seqlens is not None and (cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2):
         raise TypeError("cu_seqlens must be int32 [N+1]")
     N = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    _dense(dev, cu_seqlens, rows, device_status)
-    _int_vector(lengths, "lengths", N, dev)
+    _check_buffer(lengths, "lengths", (N,), _I32)
     _check_buffer(norm_weight, "norm_weight", (d_latent,), _F32)
     _check_buffer(freqs, "freqs", ((d - d_latent) // 2,), _F64)
     _check_buffer(device_status, "device_status", (1,), _I32)
@@ -182,8 +200,9 @@ def latent_append(kv, cache, page_table, lengths, d_latent, norm_weight=None, ep
 
 
 # ------------------------------------------------------------------ expanded
-def _latent_args(q, k_nope, k_rope, v, scale, causal, cu_q, cu_k):
-    dev = _need_device(None, q, k_nope, k_rope, v)
+def _latent_args(q, k_nope, k_rope, v, scale, causal, cu_q, cu_k, *more):
+    dev = _device(q, k_nope, k_rope, v, cu_q, cu_k, *more)
+    _dense(cu_q, cu_k)
     if q.dim() != 4 or k_nope.dim() != 4 or v.dim() != 4 or (k_rope is not None and k_rope.dim() != 3):
         raise ValueError("q must be [B,T,H,d_nope+d_rope], k_nope [B,S,H,d_nope], k_rope [B,S,d_rope], v [B,S,H,d_v]")
     B, T, H, d = q.shape
@@ -204,7 +223,6 @@ def _latent_args(q, k_nope, k_rope, v, scale, causal, cu_q, cu_k):
                 raise TypeError("cu_seqlens must be int32 [N+1]")
         if cu_k.shape != cu_q.shape:
             raise ValueError("cu_seqlens and cu_seqlens_k must have one length")
-        _dense(dev, cu_q, cu_k)
         N = cu_q.numel() - 1
     a = LatentPrefillArgs(B=B, T=T, S=S, H=H, d_nope=dn, d_rope=dr, d_v=dv, num_seqs=N, in_dtype=_dt(q.dtype), out_dtype=_dt(q.dtype),
                           causal=1 if causal else 0, scale=1 / math.sqrt(d) if scale is None else scale, q=_p(q), k_nope=_p(k_nope), k_rope=_p(k_rope), v=_p(v),
@@ -234,8 +252,8 @@ def latent_prefill(q, k_nope, k_rope, v, scale=None, causal=True, cu_seqlens=Non
     log of the sum of exponentials).  A query without a key has o = 0 and lse =
     -inf.  ``o`` and ``lse`` are optional preallocated buffers;
     ``check_seqlens`` and ``device_status`` as for ``prefill``."""
-    a, dev, (B, T, S, H, dn, dr, dv) = _latent_args(q, k_nope, k_rope, v, scale, causal, cu_seqlens, cu_seqlens_k)
-    _dense(dev, o, lse, device_status)
+    a, dev, (B, T, S, H, dn, dr, dv) = _latent_args(q, k_nope, k_rope, v, scale, causal, cu_seqlens, cu_seqlens_k, o, lse, device_status)
+    _dense(o, lse, device_status)
     if o is None:
         o = torch.empty((B, T, H, dv), dtype=out_dtype or q.dtype, device=dev)
     else:
@@ -244,7 +262,8 @@ def latent_prefill(q, k_nope, k_rope, v, scale=None, causal=True, cu_seqlens=Non
             raise TypeError(f"out_dtype {out_dtype} disagrees with o.dtype {o.dtype}")
     if lse is None:
         lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
-    _check_buffer(lse, "lse", (B, T, H), _F32)
+    else:
+        _check_buffer(lse, "lse", (B, T, H), _F32)
     _check_buffer(device_status, "device_status", (1,), _I32)
     check = check_seqlens and cu_seqlens is not None and device_status is None
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check else device_status
@@ -271,9 +290,8 @@ def latent_backward(q, k_nope, k_rope, v, o, lse, d_o, scale=None, causal=True, 
     into which a rounded o brings its rounding.  Nothing synchronises; ``device_status`` (int32 [1] on the
     device) receives the call's device-side status: with malformed offsets the
     gradients are not written."""
-    a, dev, (B, T, S, H, dn, dr, dv) = _latent_args(q, k_nope, k_rope, v, scale, causal, cu_seqlens, cu_seqlens_k)
-    _dense(dev, device_status)
-    _need_device(dev, o, lse, d_o)
+    a, dev, (B, T, S, H, dn, dr, dv) = _latent_args(q, k_nope, k_rope, v, scale, causal, cu_seqlens, cu_seqlens_k, o, lse, d_o, device_status)
+    _dense(device_status)
     _check_buffer(o, "o", (B, T, H, dv), _FLOATS)
     _check_buffer(d_o, "d_o", (B, T, H, dv), (q.dtype,))
     _check_buffer(lse, "lse", (B, T, H), _F32)
@@ -313,14 +331,14 @@ def latent_decode(q, cache, page_table, lengths, d_latent, scale, out_dtype=None
     float32 [B,m,H]).  An empty slot (length 0) has o = 0 and lse = -inf.
     Nothing synchronises; ``device_status`` (int32 [1] on the device) tells of
     pages or lengths outside the cache, whose sequences' results are undefined."""
-    dev = _need_device(None, q, cache, page_table)
+    dev = _device(q, cache, page_table, lengths, o, lse, device_status)
+    _dense(lengths, o, lse, device_status)
     if q.dim() != 4:
         raise ValueError("q must be [B,m,H,d_latent+d_rope]")
     B, m, H, d = q.shape
     if not 0 < d_latent <= d:
         raise ValueError(f"d_latent must be in [1,{d}]")
-    _int_vector(lengths, "lengths", B, dev)
-    _dense(dev, o, lse, device_status)
+    _check_buffer(lengths, "lengths", (B,), _I32)
     if o is None:
         o = torch.empty((B, m, H, d_latent), dtype=out_dtype or q.dtype, device=dev)
     else:
@@ -329,7 +347,8 @@ def latent_decode(q, cache, page_table, lengths, d_latent, scale, out_dtype=None
             raise TypeError(f"out_dtype {out_dtype} disagrees with o.dtype {o.dtype}")
     if lse is None:
         lse = torch.empty((B, m, H), dtype=torch.float32, device=dev)
-    _check_buffer(lse, "lse", (B, m, H), _F32)
+    else:
+        _check_buffer(lse, "lse", (B, m, H), _F32)
     _check_buffer(device_status, "device_status", (1,), _I32)
     a = LatentDecodeArgs(B=B, H=H, n_tokens=m, d_latent=d_latent, d_rope=d - d_latent, in_dtype=_dt(q.dtype), out_dtype=_dt(o.dtype), scale=scale, q=_p(q),
                          lengths=_p(lengths), o=_p(o), lse=_p(lse), device_status=_p(device_status))
