@@ -290,10 +290,10 @@ __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
 
 // ------------------------------------------------------- few tiles ----
 // The same products where there are too few tiles to fill the card: a workgroup
-// takes 16 queries (or keys), its four waves every fourth 16 tokens of the other
-// side, which come from the caches to registers (no LDS, no barrier in the loop);
+// takes 16 queries (or keys), its waves in turn 16 tokens of the other side, which
+// come from the caches to registers (no LDS, no barrier in the loop);
 // the waves' sums meet in LDS at the end, in order.
-constexpr int kFewTile = 16;
+constexpr int kFewTile = 16, kFewWaves = 8;  // waves of the forward; the gradients' take 400 registers a lane, and are four
 constexpr int64_t kFewBelow = 65536;  // tokens times heads
 
 // The key's channels as one: its own part, then the shared one (behind both: the
@@ -376,8 +376,8 @@ __device__ __forceinline__ FewPlace few_place(const LatentParams &p, const Laten
 }
 
 template <typename O, int DK, int DV>
-__global__ void __launch_bounds__(256, 2) prefill_few_kernel(LatentParams p) {
-    __shared__ float s_acc[4 * 16 * (DV + 4)], s_top[4][16], s_sum[4][16];
+__global__ void __launch_bounds__(64 * kFewWaves, 1) prefill_few_kernel(LatentParams p) {
+    __shared__ float s_acc[kFewWaves * 16 * (DV + 4)], s_top[kFewWaves][16], s_sum[kFewWaves][16];
     const FewPlace f = few_place(p, p.tq, p.causal);
     const LatentPlace &a = f.a;
     if (!a.valid) return;
@@ -393,11 +393,11 @@ __global__ void __launch_bounds__(256, 2) prefill_few_kernel(LatentParams p) {
     float top = -INFINITY, sum = 0.f;
     f32x4 kf[DK / 16];
     if (n > 0) rows16<DK>(kf, f.keys, wave * 16, n, g, c16);
-    for (int k0 = wave * 16; k0 < n; k0 += 64) {
+    for (int k0 = wave * 16; k0 < n; k0 += 16 * kFewWaves) {
         f32x4 vf[DV / 16];
         cols16<DV>(vf, f.values, k0, n, g, c16);
         f32x4 s = dot16<DK>(kf, qf);
-        rows16<DK>(kf, f.keys, k0 + 64, n, g, c16);  // the next step's, under this one's second half
+        rows16<DK>(kf, f.keys, k0 + 16 * kFewWaves, n, g, c16);  // the next step's, under this one's second half
         float most = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -424,24 +424,27 @@ __global__ void __launch_bounds__(256, 2) prefill_few_kernel(LatentParams p) {
         s_sum[wave][c16] = sum;
     }
     __syncthreads();
-    const int i = threadIdx.x >> 4, part = threadIdx.x & 15;  // a query, four channels of every 64
+    constexpr int PARTS = 4 * kFewWaves;
+    const int i = threadIdx.x / PARTS, part = threadIdx.x % PARTS;  // a query, four channels of every 4 PARTS
     if (q0 + i >= a.tq) return;
-    top = fmaxf(fmaxf(s_top[0][i], s_top[1][i]), fmaxf(s_top[2][i], s_top[3][i]));
+    top = s_top[0][i];
+#pragma unroll
+    for (int k = 1; k < kFewWaves; ++k) top = fmaxf(top, s_top[k][i]);
     const float base = top == -INFINITY ? 0.f : top;
-    float w[4];
+    float w[kFewWaves];
     sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kFewWaves; ++k) {
         w[k] = fast_exp2(s_top[k][i] - base);
         sum += w[k] * s_sum[k][i];
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int64_t row = (a.q_row + q0 + i) * p.H + a.h;
     O *o = static_cast<O *>(p.o) + row * p.dv;
-    for (int ch = 4 * part; ch < p.dv; ch += 64) {
+    for (int ch = 4 * part; ch < p.dv; ch += 4 * PARTS) {
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v += w[k] * load4(s_acc + (k * 16 + i) * (DV + 4) + ch);
+        for (int k = 0; k < kFewWaves; ++k) v += w[k] * load4(s_acc + (k * 16 + i) * (DV + 4) + ch);
         store4(o + ch, v * inv);
     }
     if (part == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
@@ -573,7 +576,7 @@ __global__ void __launch_bounds__(256, 1) grad_k_few_kernel(LatentGradParams gp)
 template <typename O, int DK, int DV>
 hipError_t run_prefill(const LatentParams &p, hipStream_t s) {
     const int grid = p.cu_q ? p.H * p.tq.bound : p.H * p.N * p.tq.per_seq;
-    if (p.tq.size == kFewTile) prefill_few_kernel<O, DK, DV><<<grid, 256, 0, s>>>(p);
+    if (p.tq.size == kFewTile) prefill_few_kernel<O, DK, DV><<<grid, 64 * kFewWaves, 0, s>>>(p);
     else prefill_f32_kernel<O, DK, DV><<<grid, 256, 0, s>>>(p);
     return hipGetLastError();
 }

@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads, 2) prefill_bf16_kernel(LatentParams 
             values.issue(k0 + kKeys, n, lds + 2 * KB + (buf ^ 1) * VB);
         }
         if (k0 >= n_wave) continue;
+        __builtin_amdgcn_s_setprio(1);
         f32x16 s[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -88,6 +89,7 @@ __global__ void __launch_bounds__(kThreads, 2) prefill_bf16_kernel(LatentParams 
                 s[t] = mfma32(f.v, qf[k], s[t]);
             }
         }
+        __builtin_amdgcn_s_setprio(0);
         if (k0 + kKeys > n_least) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -95,10 +97,12 @@ __global__ void __launch_bounds__(kThreads, 2) prefill_bf16_kernel(LatentParams 
                 for (int i = 0; i < 16; ++i)
                     if (k0 + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3) >= limit) s[t][i] = -INFINITY;
         }
-        float most = -INFINITY;
+        float m2[2] = {s[0][0], s[1][0]};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) most = fmaxf(most, fmaxf(s[0][i], s[1][i]));
-        most = swap_halves_max(most) * c;
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 1; i < 15; i += 2) m2[t] = fmaxf(fmaxf(s[t][i], s[t][i + 1]), m2[t]);
+        const float most = swap_halves_max(fmaxf(fmaxf(m2[0], s[0][15]), fmaxf(m2[1], s[1][15]))) * c;
         if (__any(most > top + kSlack)) {
             const float next = fmaxf(top, most);
             const float keep = next == -INFINITY ? 1.f : fast_exp2(top - next);
@@ -114,11 +118,12 @@ __global__ void __launch_bounds__(kThreads, 2) prefill_bf16_kernel(LatentParams 
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 s[t][i] = fast_exp2(fmaf(s[t][i], c, -base));
-                sum += s[t][i];
             }
+            sum += ((s[t][0] + s[t][1]) + (s[t][2] + s[t][3]) + ((s[t][4] + s[t][5]) + (s[t][6] + s[t][7]))) + (((s[t][8] + s[t][9]) + (s[t][10] + s[t][11])) + ((s[t][12] + s[t][13]) + (s[t][14] + s[t][15])));
             pf[2 * t] = half_tile(s[t], 0);
             pf[2 * t + 1] = half_tile(s[t], 1);
         }
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int b = 0; b < DV / 32; ++b) {
             const int chunk = 4 * b + 2 * g2 + ((i16 & 3) >> 1);
@@ -131,6 +136,7 @@ __global__ void __launch_bounds__(kThreads, 2) prefill_bf16_kernel(LatentParams 
                 acc[b] = mfma32(f.v, pf[k], acc[b]);
             }
         }
+        __builtin_amdgcn_s_setprio(0);
     }
     sum = swap_halves_sum(sum);
     if (qi >= a.tq) return;

@@ -19,6 +19,7 @@ constexpr int kInLds = 4096;  // sequences whose offsets fit
 
 struct Scratch {
     int off[kInLds + 1];
+    int2 len[kInLds];  // of this side, of the other
     int wave[kThreads / 64];
     int bucket[kBuckets + 1];
     int most, bad;
@@ -57,14 +58,17 @@ __device__ __forceinline__ void check(const int32_t *cu, int tokens, int N, int 
 template <typename W>
 __device__ __forceinline__ void fill(const int32_t *cu, const int32_t *other, int N, int size, int bound, int *spill, int2 *entry, int32_t *count, Scratch &s, W &&work) {
     const int tid = threadIdx.x;
-    int *off = N <= kInLds ? s.off : spill;
+    int *off = N <= kInLds ? s.off : spill;  // .. and lengths too in LDS, or read again
     const int per = (N + kThreads - 1) / kThreads;
     const int n0 = min(N, tid * per), n1 = min(N, n0 + per);
-    auto tiles = [&](int n) { return (cu[n + 1] - cu[n] + size - 1) / size; };
+    const bool small = N <= kInLds;
+    auto length = [&](int n) { return small ? s.len[n] : make_int2(cu[n + 1] - cu[n], other[n + 1] - other[n]); };
+    auto tiles = [&](int n) { return (length(n).x + size - 1) / size; };
     int own = 0, most = 0;
     for (int n = n0; n < n1; ++n) {
+        if (small) s.len[n] = make_int2(cu[n + 1] - cu[n], other[n + 1] - other[n]);
         own += tiles(n);
-        most = max(most, other[n + 1] - other[n]);
+        most = max(most, length(n).y);
     }
     if (tid <= kBuckets) s.bucket[tid] = 0;
     if (tid == 0) s.most = 0;
@@ -87,7 +91,8 @@ __device__ __forceinline__ void fill(const int32_t *cu, const int32_t *other, in
             else hi = mid;
         }
         const int i = t - off[lo];
-        const int w = max(0, work(cu[lo + 1] - cu[lo], other[lo + 1] - other[lo], i));
+        const int2 len = length(lo);
+        const int w = max(0, work(len.x, len.y, i));
         return make_int3(lo, i, kBuckets - 1 - min(kBuckets - 1, static_cast<int>(static_cast<float>(w) * scale)));
     };
     for (int t = tid; t < total; t += kThreads) atomicAdd(&s.bucket[place(t).z + 1], 1);
