@@ -14,7 +14,7 @@ namespace kda {
 
 namespace {
 
-constexpr int kThreads = 1024, kBuckets = 64;
+constexpr int kThreads = 1024, kBuckets = 64;  // buckets: a wave
 constexpr int kInLds = 4096;  // sequences whose offsets fit
 
 struct Scratch {
@@ -97,8 +97,15 @@ __device__ __forceinline__ void fill(const int32_t *cu, const int32_t *other, in
     };
     for (int t = tid; t < total; t += kThreads) atomicAdd(&s.bucket[place(t).z + 1], 1);
     __syncthreads();
-    if (tid == 0)
-        for (int b = 1; b <= kBuckets; ++b) s.bucket[b] += s.bucket[b - 1];
+    if (tid < kBuckets) {  // one wave: where each bucket begins
+        int run = s.bucket[tid];
+#pragma unroll
+        for (int d = 1; d < kBuckets; d <<= 1) {
+            const int o = __shfl_up(run, d);
+            if (tid >= d) run += o;
+        }
+        s.bucket[tid] = run;
+    }
     __syncthreads();
     for (int t = tid; t < total; t += kThreads) {
         const int3 p = place(t);
