@@ -38,7 +38,7 @@ template <int DK> struct Shared {
     float sum[4][kRows];
     const char *row[2][kKeys];
     int32_t page[2][kKeys];
-    int64_t steps[kThreads / 64];
+    DecodeShared<kThreads> run;
     char p[kRows * kPRow];
     __attribute__((aligned(128))) char tile[2][kKeys * DK * 2];
 };
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_bf16_kernel(LatentDecodePa
         tile = blockIdx.x % tiles;
         worker = blockIdx.x / tiles;
     }
-    DecodeRun run = decode_run<kThreads, kKeys>(p, worker, sh.steps);
+    DecodeRun run = decode_run<kThreads, kKeys>(p, worker, sh.run);
     const int d = p.dc + p.dr, rows = p.m * p.H;
     // scores are masked before they are scaled: the scale's sign goes to the query
     const float c = p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e;

@@ -19,51 +19,55 @@ __device__ __forceinline__ int decode_rows(const LatentDecodeParams &p, int b) {
     return n < 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(n), most));
 }
 
-// The line's total steps, and where `worker` begins: sequence, its step there,
-// steps to do.  `s_sum` [THREADS / 64]; every thread gets the same values.
+// Where a worker's run begins on the line, and how long it is.
 struct DecodeRun {
-    int64_t left;  // steps of this worker
-    int64_t per;   // steps of every worker but the last
-    int64_t at;    // the line's step that this worker begins with
-    int b;         // the sequence there
+    int64_t left;    // steps of this worker
+    int64_t per;     // steps of every worker but the last
+    int64_t at;      // the line's step that this worker begins with
+    int b;           // the sequence there
     int64_t before;  // the line's steps before that sequence
 };
+template <int THREADS> struct DecodeShared {
+    int64_t wave[THREADS / 64], before;
+    int32_t b;
+};
+// Each thread counts the steps of a run of sequences (one, up to THREADS of them);
+// a prefix sum over the threads; the thread with the worker's first step looks for
+// it in its own run.
 template <int THREADS, int STEP>
-__device__ __forceinline__ DecodeRun decode_run(const LatentDecodeParams &p, int worker, int64_t *s_sum) {
+__device__ __forceinline__ DecodeRun decode_run(const LatentDecodeParams &p, int worker, DecodeShared<THREADS> &s) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    auto steps = [&](int b) -> int64_t { return b < p.B ? (static_cast<int64_t>(decode_rows(p, b)) + STEP - 1) / STEP : 0; };
-    int64_t sum = 0;
-    for (int b = tid; b < p.B; b += THREADS) sum += steps(b);
+    const int each = (p.B + THREADS - 1) / THREADS, b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
+    auto steps = [&](int b) { return (static_cast<int64_t>(decode_rows(p, b)) + STEP - 1) / STEP; };
+    int64_t own = 0;
+    for (int b = b0; b < b1; ++b) own += steps(b);
+    int64_t upto = own;  // with all threads of the wave before
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-    if (lane == 0) s_sum[wave] = sum;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t o = __shfl_up(upto, d);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 63) s.wave[wave] = upto;
     __syncthreads();
     int64_t total = 0;
-    for (int w = 0; w < THREADS / 64; ++w) total += s_sum[w];
+    for (int w = 0; w < THREADS / 64; ++w) {
+        if (w < wave) upto += s.wave[w];
+        total += s.wave[w];
+    }
     DecodeRun r;
     r.per = (total + p.workers - 1) / p.workers;
     r.at = worker * r.per;
     r.left = min(total, r.at + r.per) - r.at;
-    r.b = 0;
-    r.before = 0;
-    if (r.left <= 0) return r;
-    for (int b0 = 0; b0 < p.B; b0 += 64) {  // every wave alike: 64 sequences at a time
-        const int64_t own = steps(b0 + lane);
-        int64_t run = own;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t o = __shfl_up(run, d);
-            if (lane >= d) run += o;
-        }
-        const uint64_t past = __ballot(r.before + run > r.at);
-        if (past) {
-            const int k = __ffsll(static_cast<long long>(past)) - 1;
-            r.before += __shfl(run - own, k);
-            r.b = b0 + k;
-            return r;
-        }
-        r.before += __shfl(run, 63);
+    if (r.left > 0 && upto > r.at && upto - own <= r.at) {  // one thread
+        int64_t before = upto - own;
+        int b = b0;
+        for (int64_t n; before + (n = steps(b)) <= r.at; ++b) before += n;
+        s.before = before;
+        s.b = b;
     }
+    __syncthreads();
+    r.b = r.left > 0 ? s.b : 0;
+    r.before = r.left > 0 ? s.before : 0;
     return r;
 }
 

