@@ -34,6 +34,27 @@ bool overlap(const void *p, int64_t n, const void *q, int64_t m) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
     return p && q && n > 0 && m > 0 && a < b + static_cast<uintptr_t>(m) && b < a + static_cast<uintptr_t>(n);
 }
+// memory that a call reads, or writes
+struct Span {
+    const void *at;
+    int64_t bytes;
+};
+// [B, T, H, d] with its strides, in elements of `size` bytes
+Span span(const void *at, int64_t B, int64_t sb, int64_t T, int64_t st, int64_t H, int64_t sh, int64_t d, int64_t size) {
+    if (!at || B == 0 || T == 0) return {nullptr, 0};
+    return {at, ((B - 1) * sb + (T - 1) * st + (H - 1) * sh + d) * size};
+}
+Span dense(const void *at, int64_t n, int64_t size) { return {at, n * size}; }
+// no output on an input or on another output
+bool apart(std::initializer_list<Span> in, std::initializer_list<Span> out) {
+    for (const Span *o = out.begin(); o != out.end(); ++o) {
+        for (const Span &i : in)
+            if (overlap(o->at, o->bytes, i.at, i.bytes)) return false;
+        for (const Span *u = out.begin(); u != o; ++u)
+            if (overlap(o->at, o->bytes, u->at, u->bytes)) return false;
+    }
+    return true;
+}
 kda_status status_of(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
 
 // -------------------------------------------------------------- rotary ----
@@ -43,7 +64,7 @@ int64_t extent(const kda_rotary_args *a, int64_t sb, int64_t st, int64_t sh) {
 }
 // whether no two elements share memory: taken by size, each axis steps over
 // all that the smaller ones reach
-bool apart(const kda_rotary_args *a, int64_t sb, int64_t st, int64_t sh) {
+bool distinct(const kda_rotary_args *a, int64_t sb, int64_t st, int64_t sh) {
     struct Axis { int64_t n, s; } ax[3] = {{a->B, sb}, {a->T, st}, {a->H, sh}};
     for (int i = 0; i < 3; ++i)
         for (int j = i + 1; j < 3; ++j)
@@ -69,7 +90,7 @@ kda_status rotary(const kda_rotary_args *a, bool back, void *hip_stream) {
     if (!a->x || !a->out || (a->rotary_dim && !a->freqs)) return KDA_ERR_NULL_ARG;
     const int64_t e = size_of(a->dtype);
     if (reinterpret_cast<uintptr_t>(a->x) % e || reinterpret_cast<uintptr_t>(a->out) % e) return KDA_ERR_UNSUPPORTED;
-    if (!apart(a, a->out_stride_b, a->out_stride_t, a->out_stride_h)) return KDA_ERR_BAD_SHAPE;
+    if (!distinct(a, a->out_stride_b, a->out_stride_t, a->out_stride_h)) return KDA_ERR_BAD_SHAPE;
     const bool same = a->x == a->out && (a->B == 1 || a->x_stride_b == a->out_stride_b) && (a->T == 1 || a->x_stride_t == a->out_stride_t) &&
                       (a->H == 1 || a->x_stride_h == a->out_stride_h);
     if (!same && overlap(a->x, extent(a, a->x_stride_b, a->x_stride_t, a->x_stride_h) * e, a->out,
@@ -107,6 +128,16 @@ kda_status check_prefill(const kda_latent_prefill_args *a, bool need_ptrs, bool 
     if (a->S > 0 && (!a->k_nope || !a->v || (a->d_rope && !a->k_rope))) return KDA_ERR_NULL_ARG;
     if (misaligned({a->q, a->k_nope, a->k_rope, a->v, a->o})) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
+}
+struct Inputs {
+    Span q, k, r, v;
+};
+Inputs inputs_of(const kda_latent_prefill_args *a) {
+    const int64_t e = size_of(a->in_dtype);
+    return {span(a->q, a->B, a->q_stride_b, a->T, a->q_stride_t, a->H, a->q_stride_h, a->d_nope + a->d_rope, e),
+            span(a->k_nope, a->B, a->k_stride_b, a->S, a->k_stride_t, a->H, a->k_stride_h, a->d_nope, e),
+            span(a->k_rope, a->B, a->r_stride_b, a->S, a->r_stride_t, 1, 0, a->d_rope, e),
+            span(a->v, a->B, a->v_stride_b, a->S, a->v_stride_t, a->H, a->v_stride_h, a->d_v, e)};
 }
 LatentParams latent_params(const kda_latent_prefill_args *a) {
     LatentParams p{};
@@ -180,6 +211,15 @@ kda_status check_backward(const kda_latent_backward_args *a, bool need_ptrs) {
     if (a->f.S > 0 && (!a->dk_nope || !a->dv || (a->f.d_rope && !a->dk_rope))) return KDA_ERR_NULL_ARG;
     if (!a->f.d_rope && a->dk_rope) return KDA_ERR_BAD_SHAPE;
     if (misaligned({a->d_o, a->dq, a->dk_nope, a->dk_rope, a->dv})) return KDA_ERR_UNSUPPORTED;
+    const kda_latent_prefill_args &f = a->f;
+    const int64_t e = size_of(f.in_dtype), queries = static_cast<int64_t>(f.B) * f.T * f.H, keys = static_cast<int64_t>(f.B) * f.S;
+    const Inputs in = inputs_of(&f);
+    if (!apart({in.q, in.k, in.r, in.v, span(f.o, f.B, a->o_stride_b, f.T, a->o_stride_t, f.H, a->o_stride_h, f.d_v, size_of(f.out_dtype)),
+                span(f.lse, f.B, a->lse_stride_b, f.T, a->lse_stride_t, f.H, a->lse_stride_h, 1, 4),
+                span(a->d_o, f.B, a->d_o_stride_b, f.T, a->d_o_stride_t, f.H, a->d_o_stride_h, f.d_v, e)},
+               {dense(a->dq, queries * (f.d_nope + f.d_rope), e), dense(a->dk_nope, keys * f.H * f.d_nope, e), dense(a->dk_rope, keys * f.d_rope, e),
+                dense(a->dv, keys * f.H * f.d_v, e)}))
+        return KDA_ERR_BAD_SHAPE;
     return KDA_OK;
 }
 
@@ -207,6 +247,11 @@ kda_status check_decode(const kda_latent_decode_args *a, bool need_ptrs) {
     if (!need_ptrs || a->B == 0) return KDA_OK;
     if (!a->q || !a->cache || !a->page_table || !a->lengths || !a->o || !a->lse) return KDA_ERR_NULL_ARG;
     if (misaligned({a->q, a->cache, a->o})) return KDA_ERR_UNSUPPORTED;
+    const int64_t e = size_of(a->in_dtype), d = a->d_latent + a->d_rope, rows = static_cast<int64_t>(a->B) * a->n_tokens * a->H;
+    if (!apart({span(a->q, a->B, a->q_stride_b, a->n_tokens, a->q_stride_t, a->H, a->q_stride_h, d, e),
+                span(a->cache, a->num_pages, a->page_stride, a->page_size, a->row_stride, 1, 0, d, e)},
+               {dense(a->o, rows * a->d_latent, size_of(a->out_dtype)), dense(a->lse, rows, 4)}))
+        return KDA_ERR_BAD_SHAPE;
     return KDA_OK;
 }
 LatentDecodePlan decode_plan(const kda_latent_decode_args *a) {
@@ -262,6 +307,9 @@ size_t kda_latent_prefill_workspace_bytes(const kda_latent_prefill_args *a) {
 kda_status kda_latent_prefill(const kda_latent_prefill_args *a, void *hip_stream) {
     const kda_status st = check_prefill(a, true, true);
     if (st != KDA_OK) return st;
+    const int64_t rows = static_cast<int64_t>(a->B) * a->T * a->H;
+    const Inputs in = inputs_of(a);
+    if (!apart({in.q, in.k, in.r, in.v}, {dense(a->o, rows * a->d_v, size_of(a->out_dtype)), dense(a->lse, rows, 4)})) return KDA_ERR_BAD_SHAPE;
     if (!a->workspace) return KDA_ERR_NULL_ARG;
     if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign) return KDA_ERR_BAD_SHAPE;
     Layout l = latent_layout(a, false);

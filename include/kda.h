@@ -804,7 +804,9 @@ kda_status kda_latent_append(const kda_latent_append_args *a, void *hip_stream);
  * are fp32.  fp32 inputs run on fp32 matrix cores.
  * Supported: d_nope, d_rope, d_v multiples of 8, d_nope >= 8, d_nope + d_rope
  * <= 192, d_v <= 128; strides multiples of 8, token strides below 2^23; q,
- * k_nope, k_rope, v, o 16-byte aligned (else KDA_ERR_UNSUPPORTED).
+ * k_nope, k_rope, v, o 16-byte aligned (else KDA_ERR_UNSUPPORTED).  Outputs that
+ * share memory with an input or with each other are refused
+ * (KDA_ERR_BAD_SHAPE), here and in the two calls below.
  */
 typedef struct kda_latent_prefill_args {
     int32_t B, T, S, H;

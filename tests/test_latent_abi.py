@@ -15,6 +15,7 @@ from oracle import latent as R
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 0x100000
+FAR = 1 << 32  # memory of its own
 OK, NULL_ARG, BAD_SHAPE, UNSUPPORTED, TOO_SMALL = 0, 1, 2, 3, 4
 
 
@@ -90,7 +91,7 @@ def test_append(L, over, status):
 
 PREFILL = dict(B=2, T=50, S=70, H=4, d_nope=128, d_rope=64, d_v=128, num_seqs=2, in_dtype=1, out_dtype=1, causal=1, scale=0.1, q_stride_b=50 * 768, q_stride_t=768,
                q_stride_h=192, k_stride_b=70 * 1024, k_stride_t=1024, k_stride_h=256, r_stride_b=70 * 64, r_stride_t=64, v_stride_b=70 * 1024, v_stride_t=1024,
-               v_stride_h=256, q=FAKE, k_nope=FAKE, k_rope=FAKE, v=FAKE, o=FAKE, lse=FAKE, workspace=FAKE, workspace_bytes=1 << 40)
+               v_stride_h=256, q=FAKE, k_nope=FAKE, k_rope=FAKE, v=FAKE, o=FAR, lse=2 * FAR, workspace=FAKE, workspace_bytes=1 << 40)
 PREFILL_REFUSED = [
     (dict(B=0), BAD_SHAPE), (dict(T=-1), BAD_SHAPE), (dict(S=-1), BAD_SHAPE), (dict(H=0), BAD_SHAPE), (dict(num_seqs=1), BAD_SHAPE), (dict(d_nope=0), BAD_SHAPE),
     (dict(d_rope=-8), BAD_SHAPE), (dict(d_v=0), BAD_SHAPE), (dict(d_nope=100), UNSUPPORTED), (dict(d_nope=136), UNSUPPORTED), (dict(d_v=136), UNSUPPORTED),
@@ -101,27 +102,27 @@ PREFILL_REFUSED = [
     (dict(q=FAKE + 8), UNSUPPORTED), (dict(k_rope=FAKE + 4), UNSUPPORTED), (dict(o=FAKE + 2), UNSUPPORTED)]
 
 
-@pytest.mark.parametrize("over,status", PREFILL_REFUSED + [(dict(workspace=None), NULL_ARG), (dict(workspace=FAKE + 16), BAD_SHAPE), (dict(workspace_bytes=8), TOO_SMALL)])
+@pytest.mark.parametrize("over,status", PREFILL_REFUSED + [(dict(workspace=None), NULL_ARG), (dict(workspace=FAKE + 16), BAD_SHAPE), (dict(workspace_bytes=8), TOO_SMALL),
+                                                          (dict(o=FAKE + 1024), BAD_SHAPE), (dict(lse=FAKE + 4), BAD_SHAPE), (dict(lse=FAR + 64), BAD_SHAPE)])
 def test_prefill(L, over, status):
     a = fill(kda.LatentPrefillArgs, PREFILL, over)
     assert L.kda_latent_prefill(ctypes.byref(a), None) == status
-    if status in (BAD_SHAPE, UNSUPPORTED) and not any(isinstance(v, int) and v >= FAKE and v % 256 for v in over.values()):
-        assert L.kda_latent_prefill_workspace_bytes(ctypes.byref(a)) == 0
 
 
 @pytest.mark.parametrize("inner,over,status", [(o, {}, s) for o, s in PREFILL_REFUSED] + [
     ({}, dict(d_o=None), NULL_ARG), ({}, dict(dq=None), NULL_ARG), ({}, dict(dk_nope=None), NULL_ARG), ({}, dict(dk_rope=None), NULL_ARG),
     ({}, dict(dv=None), NULL_ARG), ({}, dict(dq=FAKE + 8), UNSUPPORTED), ({}, dict(d_o=FAKE + 2), UNSUPPORTED), (dict(d_rope=0, k_rope=None), {}, BAD_SHAPE),
     ({}, dict(o_stride_h=-8), BAD_SHAPE), ({}, dict(o_stride_t=4), UNSUPPORTED), ({}, dict(d_o_stride_t=1 << 23), UNSUPPORTED), ({}, dict(lse_stride_b=-1), BAD_SHAPE),
+    ({}, dict(dq=FAKE), BAD_SHAPE), ({}, dict(dk_rope=FAR), BAD_SHAPE), ({}, dict(dv=4 * FAR + 16), BAD_SHAPE), ({}, dict(dk_nope=2 * FAR), BAD_SHAPE),
     ({}, dict(workspace=None), NULL_ARG), ({}, dict(workspace=FAKE + 8), BAD_SHAPE), ({}, dict(workspace_bytes=1000), TOO_SMALL)])
 def test_backward(L, inner, over, status):
-    a = fill(kda.LatentBackwardArgs, dict(d_o=FAKE, dq=FAKE, dk_nope=FAKE, dk_rope=FAKE, dv=FAKE, workspace=FAKE, workspace_bytes=1 << 40), over)
+    a = fill(kda.LatentBackwardArgs, dict(d_o=FAKE, dq=3 * FAR, dk_nope=4 * FAR, dk_rope=5 * FAR, dv=6 * FAR, workspace=FAKE, workspace_bytes=1 << 40), over)
     a.f = fill(kda.LatentPrefillArgs, PREFILL, inner)
     assert L.kda_latent_backward(ctypes.byref(a), None) == status
 
 
 DECODE = dict(B=3, H=8, n_tokens=2, d_latent=512, d_rope=64, in_dtype=1, out_dtype=1, num_pages=40, page_size=16, max_pages=9, scale=0.1, q_stride_b=2 * 8 * 576,
-              q_stride_t=8 * 576, q_stride_h=576, page_stride=16 * 576, row_stride=576, table_stride=9, q=FAKE, cache=FAKE, page_table=FAKE, lengths=FAKE, o=FAKE, lse=FAKE,
+              q_stride_t=8 * 576, q_stride_h=576, page_stride=16 * 576, row_stride=576, table_stride=9, q=FAKE, cache=FAKE, page_table=FAKE, lengths=FAKE, o=FAR, lse=2 * FAR,
               workspace=FAKE, workspace_bytes=1 << 40)
 
 
@@ -132,6 +133,7 @@ DECODE = dict(B=3, H=8, n_tokens=2, d_latent=512, d_rope=64, in_dtype=1, out_dty
     (dict(max_pages=2 ** 28), UNSUPPORTED), (dict(row_stride=568), BAD_SHAPE), (dict(row_stride=580), UNSUPPORTED), (dict(page_stride=0), BAD_SHAPE),
     (dict(q_stride_h=-576), BAD_SHAPE), (dict(q_stride_t=577), UNSUPPORTED), (dict(table_stride=-1), BAD_SHAPE), (dict(q=None), NULL_ARG), (dict(cache=None), NULL_ARG),
     (dict(page_table=None), NULL_ARG), (dict(lengths=None), NULL_ARG), (dict(o=None), NULL_ARG), (dict(lse=None), NULL_ARG), (dict(cache=FAKE + 8), UNSUPPORTED),
+    (dict(o=FAKE), BAD_SHAPE), (dict(lse=FAKE + 512), BAD_SHAPE), (dict(lse=FAR + 32), BAD_SHAPE),
     (dict(workspace=None), NULL_ARG), (dict(workspace=FAKE + 64), BAD_SHAPE), (dict(workspace_bytes=64), TOO_SMALL)])
 def test_decode(L, over, status):
     assert L.kda_latent_decode(ctypes.byref(fill(kda.LatentDecodeArgs, DECODE, over)), None) == status

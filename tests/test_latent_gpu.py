@@ -383,3 +383,69 @@ def test_offsets_past_32_bits():
     want = R.decode(q64[0], kv64[0], dc, 0.07)
     check("o", o, want[0][None], FORWARD[BF16])
     check_lse("lse", lse, want[1][None])
+
+
+# ------------------------------------------------------- calls at the edges ----
+@TYPES
+def test_expanded_many_sequences(dtype):
+    """More sequences than the table keeps in LDS, most of one token, one of them long."""
+    lens = [1] * 4200 + [300] + [0, 2, 3] * 3
+    t, w, d_o, d64 = make(101, (1, sum(lens)), (1, sum(lens)), 1, 8, 8, 8, dtype)
+    cu = offsets(lens)
+    o, lse = kda.latent_prefill(**t, cu_seqlens=cu)
+    grads = kda.latent_backward(**t, o=o, lse=lse, d_o=d_o, cu_seqlens=cu)
+    one = {k: v[:, 4200:4500] for k, v in t.items()}
+    o1, lse1 = kda.latent_prefill(**one)
+    assert same(o[:, 4200:4500], o1) and same(lse[:, 4200:4500], lse1)
+    for a, b in zip(grads, kda.latent_backward(**one, o=o1, lse=lse1, d_o=d_o[:, 4200:4500])):
+        assert same(a[:, 4200:4500], b)
+    check("single tokens", o[:, :4200], w["v"][:, :4200], FORWARD[dtype])  # one key: its value
+
+
+def test_fp32_kernels_for_few_and_many_tokens_agree():
+    """fp32 calls of more than 65536 tokens times heads run in other tiles: the same values."""
+    t, w, d_o, d64 = make(102, (1, 1100), (1, 1100), 64, 16, 8, 16, FP32)
+    o, lse = kda.latent_prefill(**t)
+    grads = kda.latent_backward(**t, o=o, lse=lse, d_o=d_o)
+    part = {k: v if k == "k_rope" else v[:, :, :3] for k, v in t.items()}
+    o1, lse1 = kda.latent_prefill(**part)
+    check("o", o[:, :, :3], o1.double().cpu().numpy(), FORWARD[FP32])
+    check("lse", lse[:, :, :3], lse1.double().cpu().numpy(), 2.0 ** -18)
+    few = kda.latent_backward(**part, o=o1, lse=lse1, d_o=d_o[:, :, :3])
+    for k in (0, 1, 3):
+        check(f"gradient {k}", grads[k][:, :, :3], few[k].double().cpu().numpy(), BACKWARD[FP32])
+    # the sum over all heads, in 64 bits
+    want = np.zeros((1100, 8))
+    for h in range(0, 64):
+        k = np.concatenate([w["k_nope"][0, :, h], w["k_rope"][0]], -1)
+        _, dk, _ = R.attention_backward(w["q"][0, :, h], k, w["v"][0, :, h], d64[0, :, h], 24 ** -0.5, True)
+        want += dk[:, 16:]
+    check("dk_rope", grads[2][0], want, 2 * BACKWARD[FP32])  # a sum of 64 heads: as many roundings again
+
+
+@TYPES
+def test_rotary_few_channels(dtype):
+    """A shared key of one head: several tokens in one workgroup, the last one not full."""
+    for T, D in ((1, 64), (77, 64), (513, 32), (200, 6)):
+        x, x64 = rounded(np.random.default_rng(T).standard_normal((2, T, 1, D)), dtype)
+        freqs, _ = kda.rotary_frequencies(D if D < 64 else 32, device="cuda")
+        got = kda.rotary(x.cuda(), freqs)
+        want = np.stack([R.rotary(v, np.arange(T), freqs.cpu().numpy()) for v in x64])
+        check(f"{T} {D}", got, want, ONE[dtype])
+
+
+def test_outputs_on_inputs_are_refused():
+    t, _, d_o, _ = make(103, (1, 20), (1, 20), 2, 64, 0, 64, BF16)
+    q = t["q"]
+    with pytest.raises(kda.KDAError):
+        kda.latent_prefill(**t, o=q)
+    c = Cache(104, [20], [20], 64, 16, BF16)
+    with pytest.raises(kda.KDAError):
+        kda.latent_decode(c.cache[:1, :4].reshape(1, 1, 4, 64), c.cache, c.table, c.lengths, 64, 0.1, o=c.cache[1:2, :4].reshape(1, 1, 4, 64))
+
+
+def test_decode_batch_of_thousands():
+    """More sequences than a workgroup has threads."""
+    rng = np.random.default_rng(105)
+    run_decode(BF16, 16, 8, 1, 1, 16, [int(n) for n in rng.integers(0, 90, 1500)], seed=106)
+    run_decode(FP32, 16, 8, 1, 1, 16, [int(n) for n in rng.integers(0, 90, 1500)], seed=107)
