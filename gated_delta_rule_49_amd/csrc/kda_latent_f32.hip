@@ -294,7 +294,12 @@ __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
 // come from the caches to registers (no LDS, no barrier in the loop);
 // the waves' sums meet in LDS at the end, in order.
 constexpr int kFewTile = 16, kFewWaves = 8;  // waves of the forward; the gradients' take 400 registers a lane, and are four
-constexpr int64_t kFewBelow = 65536;  // tokens times heads
+// Tokens times heads below which these tiles are taken.  Forward and gradients of
+// one sequence, us, these against the larger ones (keys of 192, values of 128):
+//     600 tokens x 8 heads 32, 106 : 112, 304     2048 x 16  322, 1131 : 527, 1236
+//     2048 x 32 (the limit) 620, 2236 : 620, 2033  4096 x 32  2260, 8460 : 2361, 8159
+// and of 64 and 64 channels, 2048 x 16 118, 481 : 166, 525, 2048 x 32 228, 933 : 219, 693.
+constexpr int64_t kFewBelow = 65536;
 
 // The key's channels as one: its own part, then the shared one (behind both: the
 // first again, whose products meet zeros or are not kept).
