@@ -159,6 +159,7 @@ struct RotaryParams {
     const int32_t *pos;    // nullable
     const double *freqs;
     int64_t x_sb, x_st, x_sh, o_sb, o_st, o_sh, p_sb, p_st;
+    int64_t start;         // the launch's first token
     int32_t B, T, H, D, rot, offset, interleaved, back;
     float magnitude;
 };

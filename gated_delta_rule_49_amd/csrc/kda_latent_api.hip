@@ -114,10 +114,11 @@ kda_status check_prefill(const kda_latent_prefill_args *a, bool need_ptrs, bool 
     if (!dtype_ok(a->in_dtype) || !dtype_ok(a->out_dtype) || !flag_ok(a->causal)) return KDA_ERR_UNSUPPORTED;
     if (!a->cu_seqlens_q != !a->cu_seqlens_k) return KDA_ERR_BAD_SHAPE;
     if (a->cu_seqlens_q ? a->B != 1 || a->num_seqs < 1 : a->num_seqs != a->B) return KDA_ERR_BAD_SHAPE;
-    if (static_cast<int64_t>(a->B) * a->H > (1 << 22) || a->num_seqs > (1 << 20)) return KDA_ERR_UNSUPPORTED;
-    // blocks of a launch: (tokens / 16 + sequences) heads
-    if ((static_cast<int64_t>(a->B) * (std::max(a->T, a->S) / 16 + 1) + a->num_seqs) * a->H > kMost31 / 2) return KDA_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(a->B) * std::max(a->T, a->S) > kMost31) return KDA_ERR_UNSUPPORTED;
+    // a launch has fewer than 2^32 threads: up to 512 for a tile of 64 tokens or more (tiles of 16 are taken below
+    // 2^16 tokens times heads only), 16 for each (token, head), one for four channels of dk_rope
+    const int64_t tokens = static_cast<int64_t>(a->B) * std::max(a->T, a->S);
+    if (static_cast<int64_t>(a->num_seqs) * a->H > (1 << 21) || a->num_seqs > (1 << 20)) return KDA_ERR_UNSUPPORTED;
+    if (tokens >= (1 << 28) || tokens * a->H >= (1 << 28) || tokens * a->d_rope >= (static_cast<int64_t>(1) << 33)) return KDA_ERR_UNSUPPORTED;
     const kda_status st = check_strides({a->q_stride_b, a->q_stride_t, a->q_stride_h, a->k_stride_b, a->k_stride_t, a->k_stride_h, a->r_stride_b,
                                          a->r_stride_t, a->v_stride_b, a->v_stride_t, a->v_stride_h});
     if (st != KDA_OK) return st;
@@ -226,7 +227,7 @@ kda_status check_backward(const kda_latent_backward_args *a, bool need_ptrs) {
 // -------------------------------------------------------------- decode ----
 kda_status check_pages(int32_t num_pages, int32_t page_size, int32_t max_pages, int64_t page_stride, int64_t row_stride, int64_t table_stride, int64_t d) {
     if (num_pages < 1 || page_size < 1 || max_pages < 1 || table_stride < 0) return KDA_ERR_BAD_SHAPE;
-    if (static_cast<int64_t>(max_pages) * page_size > kMost31) return KDA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(max_pages) * page_size > kMost31 - 64) return KDA_ERR_UNSUPPORTED;  // rows of a last, partial step count in 32 bits
     const kda_status st = check_strides({page_stride, row_stride});
     if (st != KDA_OK) return st;
     // rows, and pages, that do not share memory
@@ -272,7 +273,7 @@ kda_status kda_latent_append(const kda_latent_append_args *a, void *hip_stream) 
     if (!dtype_ok(a->dtype) || !flag_ok(a->interleaved)) return KDA_ERR_UNSUPPORTED;
     if (!(a->eps >= 0.f)) return KDA_ERR_BAD_SHAPE;
     if (a->cu_seqlens ? a->B != 1 || a->num_seqs < 1 : a->num_seqs != a->B) return KDA_ERR_BAD_SHAPE;
-    if (static_cast<int64_t>(a->B) * a->T > kMost31) return KDA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(a->B) * a->T >= (1 << 26)) return KDA_ERR_UNSUPPORTED;  // a wave each, fewer than 2^32 threads
     const int64_t d = a->d_latent + a->d_rope, e = size_of(a->dtype);
     kda_status st = check_pages(a->num_pages, a->page_size, a->max_pages, a->page_stride, a->row_stride, a->table_stride, d);
     if (st != KDA_OK) return st;

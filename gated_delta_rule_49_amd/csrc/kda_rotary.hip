@@ -46,7 +46,7 @@ constexpr int kRotThreads = 256, kRotPairs = 512;
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryParams p, int copies, uint32_t units, int group) {
     __shared__ float s_cos[kRotPairs], s_sin[kRotPairs];
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * group;
+    const int64_t first = p.start + static_cast<int64_t>(blockIdx.x) * group;
     const int count = static_cast<int>(min(static_cast<int64_t>(group), static_cast<int64_t>(p.B) * p.T - first));
     const int pairs = p.rot / 2;
     for (int i = threadIdx.x; i < count * pairs; i += kRotThreads) {
@@ -114,8 +114,15 @@ hipError_t run_rotary(const RotaryParams &p, hipStream_t s) {
     if (copies + turned == 0) return hipSuccess;
     const int64_t tokens = static_cast<int64_t>(p.B) * p.T, each = static_cast<int64_t>(copies + turned) * p.H;
     const int64_t group = std::max<int64_t>(1, std::min<int64_t>(kRotThreads / each, p.rot ? 2 * kRotPairs / p.rot : kRotThreads));
-    rotary_kernel<T, V, INTER><<<static_cast<unsigned>((tokens + group - 1) / group), kRotThreads, 0, s>>>(p, copies, copies + turned, static_cast<int>(group));
-    return hipGetLastError();
+    // a launch has fewer than 2^32 threads
+    const int64_t most = 1 << 23, slice = most * group;
+    for (RotaryParams q = p; q.start < tokens; q.start += slice) {
+        const unsigned grid = static_cast<unsigned>(std::min(most, (tokens - q.start + group - 1) / group));
+        rotary_kernel<T, V, INTER><<<grid, kRotThreads, 0, s>>>(q, copies, copies + turned, static_cast<int>(group));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 template <typename T>
 hipError_t pick_rotary(const RotaryParams &p, hipStream_t s) {
@@ -129,7 +136,9 @@ hipError_t pick_rotary(const RotaryParams &p, hipStream_t s) {
 
 // One wave a token.  The row is held in registers between the sum of squares
 // and the write (NV vectors a lane).  The sequence of a packed token is found
-// by 64 probes at a time: two rounds up to 4096 sequences.
+// by 64 probes at a time: two rounds up to 4096 sequences.  256 tokens of 512 + 64
+// channels take 4.3 us (latency: offsets, length, page, row), 17588 packed ones
+// 15.3 us (4.0 TB/s of rows read and written).
 template <typename T, int NV>
 __global__ void __launch_bounds__(256) append_kernel(LatentAppendParams p) {
     constexpr int V = 16 / sizeof(T);

@@ -745,7 +745,7 @@ kda_status kda_rotary_backward(const kda_rotary_args *a, void *hip_stream);
  * rows and cache must not overlap (KDA_ERR_BAD_SHAPE).
  * Supported: d_latent, d_rope multiples of 8 (d_rope may be 0), d_latent <=
  * 2048, d_rope <= 256; strides multiples of 8; kv, cache and rows 16-byte
- * aligned; B * T < 2^31.
+ * aligned; B * T < 2^26.
  */
 typedef struct kda_latent_append_args {
     int32_t B, T;
@@ -803,7 +803,9 @@ kda_status kda_latent_append(const kda_latent_append_args *a, void *hip_stream);
  * cores as they are, the probabilities rounded to bf16; statistics and sums
  * are fp32.  fp32 inputs run on fp32 matrix cores.
  * Supported: d_nope, d_rope, d_v multiples of 8, d_nope >= 8, d_nope + d_rope
- * <= 192, d_v <= 128; strides multiples of 8, token strides below 2^23; q,
+ * <= 192, d_v <= 128; num_seqs <= 2^20, num_seqs * H <= 2^21, B * max(T, S) * H
+ * < 2^28, B * max(T, S) * d_rope < 2^33; strides multiples of 8, token strides
+ * below 2^23; q,
  * k_nope, k_rope, v, o 16-byte aligned (else KDA_ERR_UNSUPPORTED).  Outputs that
  * share memory with an input or with each other are refused
  * (KDA_ERR_BAD_SHAPE), here and in the two calls below.
@@ -892,7 +894,7 @@ kda_status kda_latent_backward(const kda_latent_backward_args *a, void *hip_stre
  * to run.
  * Supported: d_latent, d_rope multiples of 8, 8 <= d_latent <= 512, d_latent +
  * d_rope <= 576; page_size, max_pages, num_pages >= 1, max_pages * page_size <
- * 2^31; B <= 65536, B * m * H < 2^24; strides multiples of 8; q, cache, o
+ * 2^31 - 64; B <= 65536, B * m * H < 2^24; strides multiples of 8; q, cache, o
  * 16-byte aligned.
  */
 typedef struct kda_latent_decode_args {

@@ -240,3 +240,17 @@ def test_absorbed_form_is_the_expanded_one():
     q_latent = np.concatenate([np.einsum("mhd,hdc->mhc", q[..., :dn], up_k), q[..., dn:]], -1)
     o2, lse2 = R.decode(q_latent, rows, dc, 0.3)
     assert np.allclose(np.einsum("mhc,hdc->mhd", o2, up_v), o) and np.allclose(lse2, lse)
+
+
+def test_limits_of_a_launch(L):
+    """What would pass 2^32 threads in a launch is refused; what comes close is sized."""
+    def prefill(**over):
+        return int(L.kda_latent_prefill_workspace_bytes(ctypes.byref(fill(kda.LatentPrefillArgs, PREFILL, over))))
+    assert prefill(T=2 ** 24, S=2 ** 24, H=4, B=3, num_seqs=3) > 0 and prefill(T=2 ** 24, S=2 ** 24, H=4, B=4, num_seqs=4) == 0
+    assert prefill(B=2 ** 19, num_seqs=2 ** 19, T=1, S=1) > 0 and prefill(B=2 ** 19 + 1, num_seqs=2 ** 19 + 1, T=1, S=1) == 0
+    assert prefill(B=1, num_seqs=1, H=1, T=1, S=2 ** 27) == 0 and prefill(B=1, num_seqs=1, H=1, T=1, S=2 ** 26) > 0  # 64 channels of dk_rope each
+    many = dict(B=1, num_seqs=1, T=2 ** 26, kv_stride_b=0)
+    assert L.kda_latent_append(ctypes.byref(fill(kda.LatentAppendArgs, APPEND, many)), None) == UNSUPPORTED
+    rows = dict(max_pages=1, page_size=2 ** 31 - 1)
+    assert L.kda_latent_append(ctypes.byref(fill(kda.LatentAppendArgs, APPEND, rows)), None) == UNSUPPORTED
+    assert L.kda_latent_decode(ctypes.byref(fill(kda.LatentDecodeArgs, DECODE, rows)), None) == UNSUPPORTED

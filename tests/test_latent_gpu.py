@@ -49,6 +49,20 @@ def test_rotary_far_positions(dtype):
         check(f"position {int(pos[t])}", got[0, t:t + 1], want, ONE[dtype])
 
 
+def test_rotary_of_more_tokens_than_a_launch_has_workgroups():
+    """2^23 workgroups of one token a launch: heads that are moved element by element."""
+    T, D = 2 ** 23 + 3, 160
+    x = torch.zeros((1, T, 1, D), dtype=BF16, device="cuda")
+    some = [0, 1, 2 ** 23 - 1, 2 ** 23, T - 1]
+    value, v64 = rounded(np.random.default_rng(3).standard_normal((1, len(some), 1, D)), BF16)
+    x[:, some] = value.cuda()
+    freqs, _ = kda.rotary_frequencies(2, device="cuda")
+    y = kda.rotary(x, freqs)
+    check("rows of both launches", y[:, some], R.rotary(v64[0], some, freqs.cpu().numpy())[None], ONE[BF16])
+    y[:, some] = 0
+    assert not y.any()
+
+
 def test_rotary_default_positions_and_broadcast():
     x = torch.randn(3, 9, 2, 32, generator=torch.Generator().manual_seed(1)).cuda()
     freqs, _ = kda.rotary_frequencies(32, device="cuda")
