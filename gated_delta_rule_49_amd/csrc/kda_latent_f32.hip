@@ -18,6 +18,10 @@
 //
 // Softmax: running maximum and sum per query in fp32; a lane sees the query of
 // its column and a quarter of the tile's keys.
+//
+// 600 tokens of 8 heads (keys 192, values 128): 27 us, a chain of dependent steps;
+// gradients of documents of 0 to 1201 tokens, 2235 in all, 8 heads: queries 169 us,
+// keys 195, with matrix instructions in 37 % of the cycles of one wave a SIMD.
 #include "kda_latent.hpp"
 
 namespace kda {

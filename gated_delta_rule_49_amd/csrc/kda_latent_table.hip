@@ -5,9 +5,11 @@
 // sum over the threads gives every sequence's first tile; then a thread takes a
 // tile, finds its sequence by bisection, and puts it where its bucket of work
 // (tokens of the other side that it sees) begins: the largest first, so that the
-// last workgroups of a launch are small ones.  (A ragged batch, 8 prompts of 0 to
-// 3001 tokens behind 0 to 4097 cached ones, 32 heads.)  The order inside a bucket
-// is that of arrival; no result depends on it.
+// last workgroups of a launch are small ones.  A launch takes a tile's heads one
+// after another: the largest first over all heads (8 prompts of 0 to 3001 tokens
+// behind 0 to 4097 cached ones, 32 heads, bf16: the forward took 320 us so, head by
+// head 348).  The order inside a bucket is that of arrival; no result depends on
+// it.  One workgroup's latency bounds it: 8 to 13 us.
 #include "kda_latent.hpp"
 
 namespace kda {
