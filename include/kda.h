@@ -740,9 +740,10 @@ kda_status kda_rotary_backward(const kda_rotary_args *a, void *hip_stream);
  *                KDA_ERR_BAD_PAGES
  * A token whose position lies outside [0, max_pages * page_size) or whose
  * page is not in [0, num_pages) is not written to the cache and reported in
- * *device_status.  Rows that no token goes to keep their contents.  Sequences
- * that share the page they append to give that page undefined contents.  kv,
- * rows and cache must not overlap (KDA_ERR_BAD_SHAPE).
+ * *device_status.  Rows that no token goes to keep their contents.  Tokens that
+ * the tables send to one row of the cache (a page that two sequences append to,
+ * or one listed twice) leave that row undefined.  kv, rows and cache must not
+ * overlap (KDA_ERR_BAD_SHAPE).
  * Supported: d_latent, d_rope multiples of 8 (d_rope may be 0), d_latent <=
  * 2048, d_rope <= 256; strides multiples of 8; kv, cache and rows 16-byte
  * aligned; B * T < 2^26.
@@ -805,9 +806,8 @@ kda_status kda_latent_append(const kda_latent_append_args *a, void *hip_stream);
  * Supported: d_nope, d_rope, d_v multiples of 8, d_nope >= 8, d_nope + d_rope
  * <= 192, d_v <= 128; num_seqs <= 2^20, num_seqs * H <= 2^21, B * max(T, S) * H
  * < 2^28, B * max(T, S) * d_rope < 2^33; strides multiples of 8, token strides
- * below 2^23; q,
- * k_nope, k_rope, v, o 16-byte aligned (else KDA_ERR_UNSUPPORTED).  Outputs that
- * share memory with an input or with each other are refused
+ * below 2^23; q, k_nope, k_rope, v, o 16-byte aligned (else KDA_ERR_UNSUPPORTED).
+ * Outputs that share memory with an input or with each other are refused
  * (KDA_ERR_BAD_SHAPE), here and in the two calls below.
  */
 typedef struct kda_latent_prefill_args {
