@@ -6,9 +6,13 @@
 // as keys and by columns as values.
 //   S^T = K Q^T    wave w: keys 16 (w % 4), rows 16 (w / 4), all channels
 //                  (16 x 16 x 32 products; Q stays in registers)
-//   P              to LDS, in bf16, over a maximum that all waves know
+//   P              to LDS, as two bf16 parts, over a maximum that all waves know
 //   O^T += C^T P^T wave w: an eighth of the latent channels, all rows
-//                  (32 x 32 x 16 products)
+//                  (32 x 32 x 16 products, one for each part of P)
+// One part of P would leave each term of a sum off by up to 2^-8 of itself, and
+// sums whose terms cancel by several of their own steps, an fp32 o too; it saves
+// little where memory bounds: 235.2 us for 237.0 with two, 259 for 279 in the
+// second case below.
 // The maximum moves when some wave's scores pass it by more than kSlack, which
 // the waves see together after the barrier that P needs anyway; then P is made
 // again.  So a step takes two barriers, a moving maximum a third.
@@ -19,9 +23,9 @@
 // and a spilled value's load waits for the rows in flight: 12 rows of 64 heads
 // over 280000 keys took 602 us so, 372 with 32 rows.)
 //
-// 128 sequences of up to 16384 rows, one token of 32 heads: 236 us with the join,
-// 5.07 TB/s, bound by memory.  3 sequences of up to 131072, 4 tokens of 64 heads:
-// 259 us, bound by the stages of a step, which follow each other (3900 cycles, 1150
+// 128 sequences of up to 16384 rows, one token of 32 heads: 237 us with the join,
+// 5.06 TB/s, bound by memory.  3 sequences of up to 131072, 4 tokens of 64 heads:
+// 279 us, bound by the stages of a step, which follow each other (3900 cycles, 1150
 // of them the CU's 64 bytes a cycle from L2).
 #include "kda_latent_bf16.hpp"
 #include "kda_latent_decode.hpp"
@@ -33,6 +37,7 @@ namespace {
 constexpr int kKeys = 64, kRows = 32, kThreads = 512;
 constexpr float kSlack = 8.f;          // log2; see the forward: how far P may pass 1
 constexpr int kPRow = kKeys * 2 + 16;  // bytes of a row of P: 16 more than its keys
+constexpr int kPPart = kRows * kPRow;  // .. and of one part of it
 
 // where chunk c of row r of the tile lies in its row (read by rows and by columns)
 __device__ __forceinline__ constexpr int swizzle(int r, int c) { return c ^ BothRead::turn<0>(r); }
@@ -44,7 +49,7 @@ template <int DK> struct Shared {
     const char *row[2][kKeys];
     int32_t page[2][kKeys];
     DecodeShared<kThreads> run;
-    char p[kRows * kPRow];
+    char p[2 * kPPart];
     __attribute__((aligned(128))) char tile[2][kKeys * DK * 2];
 };
 
@@ -184,7 +189,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_bf16_kernel(LatentDecodePa
                 const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) e[j] = fast_exp2(fmaf(s[j], c, -base));
-                *reinterpret_cast<uint2 *>(sh.p + own * kPRow + (kg * 16 + 4 * g) * 2) = make_uint2(pack2(e[0], e[1]), pack2(e[2], e[3]));
+                f32x4 rest;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) rest[j] = e[j] - bf16_to_f32(f32_to_bf16(e[j]));
+                char *to = sh.p + own * kPRow + (kg * 16 + 4 * g) * 2;
+                *reinterpret_cast<uint2 *>(to) = make_uint2(pack2(e[0], e[1]), pack2(e[2], e[3]));
+                *reinterpret_cast<uint2 *>(to + kPPart) = make_uint2(pack2(rest[0], rest[1]), pack2(rest[2], rest[3]));
             };
             write_p();
             if (wave == 0 && i + 2 < count) sh.row[buf][lane] = place(s0 + i + 2, sh.page[buf][lane]);
@@ -206,8 +216,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_bf16_kernel(LatentDecodePa
             if (wave * NB * 32 < p.dc) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    frag8 pf;
+                    frag8 pf, rest;
                     pf.u = *reinterpret_cast<const uint4 *>(sh.p + c32 * kPRow + (16 * k + 8 * h2) * 2);
+                    rest.u = *reinterpret_cast<const uint4 *>(sh.p + kPPart + c32 * kPRow + (16 * k + 8 * h2) * 2);
                     // keys 16 k + 8 h2 + 0..3 and + 4..7 in the slots of half h2
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
@@ -219,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_bf16_kernel(LatentDecodePa
                         frag8 f;
                         f.u = make_uint4(lo.x, lo.y, hi.x, hi.y);
                         acc[b] = mfma32(f.v, pf.v, acc[b]);
+                        acc[b] = mfma32(f.v, rest.v, acc[b]);
                     }
                 }
             }
