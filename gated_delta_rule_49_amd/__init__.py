@@ -215,7 +215,7 @@ class LatentAppendArgs(ctypes.Structure):
 class LatentPrefillArgs(ctypes.Structure):
     """Mirror of ``kda_latent_prefill_args`` (include/kda.h)."""
     _fields_ = _fields("""
-        i: B T S H d_nope d_rope d_v num_seqs in_dtype out_dtype causal
+        i: B T S H d_nope d_rope d_v num_seqs in_dtype out_dtype causal precise
         f: scale
         l: q_stride_b q_stride_t q_stride_h k_stride_b k_stride_t k_stride_h r_stride_b r_stride_t v_stride_b v_stride_t v_stride_h
         p: q k_nope k_rope v cu_seqlens_q cu_seqlens_k o lse device_status workspace

@@ -27,7 +27,7 @@ struct LatentParams {
     void *o;                     // [B, T, H, dv]
     float *lse;                  // [B, T, H]
     int32_t B, T, S, H, dn, dr, dv, N;
-    int32_t causal;
+    int32_t causal, precise;
     float scale;
     LatentTiles tq;
 };

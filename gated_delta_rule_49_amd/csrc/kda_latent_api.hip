@@ -111,7 +111,7 @@ kda_status check_prefill(const kda_latent_prefill_args *a, bool need_ptrs, bool 
     if (!a) return KDA_ERR_NULL_ARG;
     if (a->B < 1 || a->T < 0 || a->S < 0 || a->H < 1 || a->num_seqs < 0 || a->d_nope < 1 || a->d_rope < 0 || a->d_v < 1) return KDA_ERR_BAD_SHAPE;
     if (a->d_nope % 8 || a->d_rope % 8 || a->d_v % 8 || static_cast<int64_t>(a->d_nope) + a->d_rope > 192 || a->d_v > 128) return KDA_ERR_UNSUPPORTED;
-    if (!dtype_ok(a->in_dtype) || !dtype_ok(a->out_dtype) || !flag_ok(a->causal)) return KDA_ERR_UNSUPPORTED;
+    if (!dtype_ok(a->in_dtype) || !dtype_ok(a->out_dtype) || !flag_ok(a->causal) || !flag_ok(a->precise)) return KDA_ERR_UNSUPPORTED;
     if (!a->cu_seqlens_q != !a->cu_seqlens_k) return KDA_ERR_BAD_SHAPE;
     if (a->cu_seqlens_q ? a->B != 1 || a->num_seqs < 1 : a->num_seqs != a->B) return KDA_ERR_BAD_SHAPE;
     // a launch has fewer than 2^32 threads: up to 512 for a tile of 64 tokens or more (tiles of 16 are taken below
@@ -150,7 +150,7 @@ LatentParams latent_params(const kda_latent_prefill_args *a) {
     p.cu_q = a->cu_seqlens_q; p.cu_k = a->cu_seqlens_k;
     p.o = a->o; p.lse = a->lse;
     p.B = a->B; p.T = a->T; p.S = a->S; p.H = a->H; p.dn = a->d_nope; p.dr = a->d_rope; p.dv = a->d_v; p.N = a->num_seqs;
-    p.causal = a->causal; p.scale = a->scale;
+    p.causal = a->causal; p.precise = a->precise; p.scale = a->scale;
     return p;
 }
 // status words, the table of the queries' tiles, of the keys' (gradients),

@@ -17,6 +17,12 @@
 // for both would need 300 registers and leave a SIMD no second wave; so the
 // exponentials of one run under the products of the other, 40 products each.
 //
+// P and dS enter their second products as one bf16 operand, which rounds each term
+// of a sum by up to 2^-8 of itself, or, where the caller asks for it (precise), as
+// two, which round by 2^-16.  Both sides, the call below: 1299 us for 1810; the
+// error of bf16 gradients against 64 bits 2.5e-3 for 1.8e-3, what their own
+// rounding and that of a bf16 o make.
+//
 // 2 x 4096 tokens of 32 heads (keys 192, values 128, causal), bf16: queries 575 us
 // (three products, 960 TFLOP/s), keys 840 us (four, 800 TFLOP/s), the statistics
 // and dk_rope's sum 33 and 13 us (bound by memory).  Matrix instructions take 54 %
@@ -93,7 +99,7 @@ __global__ void __launch_bounds__(256) rope_sum_kernel(LatentGradParams g) {
 // ------------------------------------------------------------- queries ----
 constexpr int kQThreads = 512, kTileQ = kQThreads / 2, kStep = 64;
 
-template <int DK, int DV>
+template <int DK, int DV, int PARTS>
 __global__ void __launch_bounds__(kQThreads, 512 / kQThreads) grad_q_bf16_kernel(LatentGradParams gp) {
     constexpr int KB = kStep * DK * 2, VB = kStep * DV * 2;
     __shared__ __attribute__((aligned(128))) char s_tile[2 * (KB + VB)];
@@ -170,7 +176,8 @@ __global__ void __launch_bounds__(kQThreads, 512 / kQThreads) grad_q_bf16_kernel
             for (int i = 0; i < 16; ++i) dp[i] = s[i] * (dp[i] - delta);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const bf16x8 ds = half_tile(dp, e);
+                bf16x8 ds[PARTS];
+                half_tile(ds, dp, e);
 #pragma unroll
                 for (int b = 0; b < DK / 32; ++b) acc[b] = mfma32(BothRead::read_columns<DK>(kt + 16 * e * DK * 2, column_at, b), ds, acc[b]);
             }
@@ -195,7 +202,7 @@ template <int DK, int DV> struct KeyShared {
     char d[2][kStep * DV * 2];
 };
 
-template <int DK, int DV>
+template <int DK, int DV, int PARTS>
 __global__ void __launch_bounds__(kKThreads, 1) grad_k_bf16_kernel(LatentGradParams gp) {
     __shared__ __attribute__((aligned(128))) KeyShared<DK, DV> sh;
     const LatentParams &p = gp.f;
@@ -245,7 +252,7 @@ __global__ void __launch_bounds__(kKThreads, 1) grad_k_bf16_kernel(LatentGradPar
             lds_barrier();
             if (i0 + kStep < a.tq) issue(i0 + kStep, buf ^ 1);
             const bool work = seen(i0);
-            bf16x8 pf[4];
+            bf16x8 pf[4][PARTS];
             if (work) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -271,8 +278,8 @@ __global__ void __launch_bounds__(kKThreads, 1) grad_k_bf16_kernel(LatentGradPar
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sh.p[pair][t][i][lane] = f32x4{s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]};
-                    pf[2 * t] = half_tile(s, 0);
-                    pf[2 * t + 1] = half_tile(s, 1);
+                    half_tile(pf[2 * t], s, 0);
+                    half_tile(pf[2 * t + 1], s, 1);
                 }
             }
             lds_barrier();
@@ -335,7 +342,8 @@ __global__ void __launch_bounds__(kKThreads, 1) grad_k_bf16_kernel(LatentGradPar
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const bf16x8 ds = half_tile(dp[t], e);
+                    bf16x8 ds[PARTS];
+                    half_tile(ds, dp[t], e);
 #pragma unroll
                     for (int b = 0; b < DK / 32; ++b) acc[b] = mfma32(BothRead::read_columns<DK>(sh.q[buf] + (32 * t + 16 * e) * DK * 2, column_at, b), ds, acc[b]);
                 }
@@ -355,27 +363,27 @@ __global__ void __launch_bounds__(kKThreads, 1) grad_k_bf16_kernel(LatentGradPar
         }
 }
 
-template <int DK, int DV>
+template <int DK, int DV, int PARTS>
 hipError_t run(const LatentGradParams &g, hipStream_t s) {
     const LatentParams &p = g.f;
     const int grid_q = p.cu_q ? p.H * p.tq.bound : p.H * p.N * p.tq.per_seq;
     const int grid_k = p.cu_q ? p.H * g.tk.bound : p.H * p.N * g.tk.per_seq;
-    if (p.T) grad_q_bf16_kernel<DK, DV><<<grid_q, kQThreads, 0, s>>>(g);
-    if (p.S) grad_k_bf16_kernel<DK, DV><<<grid_k, kKThreads, 0, s>>>(g);
+    if (p.T) grad_q_bf16_kernel<DK, DV, PARTS><<<grid_q, kQThreads, 0, s>>>(g);
+    if (p.S) grad_k_bf16_kernel<DK, DV, PARTS><<<grid_k, kKThreads, 0, s>>>(g);
     return hipGetLastError();
 }
-hipError_t backward_bf16(const LatentGradParams &g, hipStream_t s) {
+template <int PARTS> hipError_t backward_bf16(const LatentGradParams &g, hipStream_t s) {
     const int dk = g.f.dn + g.f.dr;
-    if (dk <= 64 && g.f.dv <= 64) return run<64, 64>(g, s);
-    if (dk <= 128) return run<128, 128>(g, s);
-    return run<192, 128>(g, s);
+    if (dk <= 64 && g.f.dv <= 64) return run<64, 64, PARTS>(g, s);
+    if (dk <= 128) return run<128, 128, PARTS>(g, s);
+    return run<192, 128, PARTS>(g, s);
 }
 template <typename T> hipError_t backward(const LatentGradParams &g, hipStream_t s) {
     const int64_t rows = static_cast<int64_t>(g.f.B) * g.f.T * g.f.H, shared = static_cast<int64_t>(g.f.B) * g.f.S * g.f.dr;
     const unsigned grid = static_cast<unsigned>((rows + 15) / 16);
     if (rows && g.o_dtype == 0) stats_kernel<T, float><<<grid, 256, 0, s>>>(g);
     if (rows && g.o_dtype != 0) stats_kernel<T, bf16_t><<<grid, 256, 0, s>>>(g);
-    const hipError_t e = sizeof(T) == 4 ? latent_backward_f32(g, s) : backward_bf16(g, s);
+    const hipError_t e = sizeof(T) == 4 ? latent_backward_f32(g, s) : g.f.precise ? backward_bf16<2>(g, s) : backward_bf16<1>(g, s);
     if (e != hipSuccess) return e;
     if (shared) rope_sum_kernel<T><<<static_cast<unsigned>((shared / 4 + 255) / 256), 256, 0, s>>>(g);
     return hipGetLastError();

@@ -43,6 +43,21 @@ __device__ __forceinline__ bf16x8 half_tile(const f32x16 &c, int s) {
     return r;
 }
 
+// .. and PARTS operands that add up to them: what the first rounds off is the second
+template <int PARTS> __device__ __forceinline__ void half_tile(bf16x8 (&f)[PARTS], const f32x16 &c, int s) {
+    f[0] = half_tile(c, s);
+    if constexpr (PARTS == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[1][i] = static_cast<__bf16>(c[8 * s + i] - static_cast<float>(f[0][i]));
+    }
+}
+// acc += a (f[0] + ..)
+template <int PARTS> __device__ __forceinline__ f32x16 mfma32(const bf16x8 &a, const bf16x8 (&f)[PARTS], f32x16 acc) {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) acc = mfma32(a, f[i], acc);
+    return acc;
+}
+
 __device__ __forceinline__ uint2 read_tr16(const char *at) {
     const v4i16 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)(at));
     return __builtin_bit_cast(uint2, r);

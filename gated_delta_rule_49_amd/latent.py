@@ -200,7 +200,7 @@ def latent_append(kv, cache, page_table, lengths, d_latent, norm_weight=None, ep
 
 
 # ------------------------------------------------------------------ expanded
-def _latent_args(q, k_nope, k_rope, v, scale, causal, cu_q, cu_k, *more):
+def _latent_args(q, k_nope, k_rope, v, scale, causal, cu_q, cu_k, precise, *more):
     dev = _device(q, k_nope, k_rope, v, cu_q, cu_k, *more)
     _dense(cu_q, cu_k)
     if q.dim() != 4 or k_nope.dim() != 4 or v.dim() != 4 or (k_rope is not None and k_rope.dim() != 3):
@@ -225,7 +225,7 @@ def _latent_args(q, k_nope, k_rope, v, scale, causal, cu_q, cu_k, *more):
             raise ValueError("cu_seqlens and cu_seqlens_k must have one length")
         N = cu_q.numel() - 1
     a = LatentPrefillArgs(B=B, T=T, S=S, H=H, d_nope=dn, d_rope=dr, d_v=dv, num_seqs=N, in_dtype=_dt(q.dtype), out_dtype=_dt(q.dtype),
-                          causal=1 if causal else 0, scale=1 / math.sqrt(d) if scale is None else scale, q=_p(q), k_nope=_p(k_nope), k_rope=_p(k_rope), v=_p(v),
+                          causal=1 if causal else 0, precise=1 if precise else 0, scale=1 / math.sqrt(d) if scale is None else scale, q=_p(q), k_nope=_p(k_nope), k_rope=_p(k_rope), v=_p(v),
                           cu_seqlens_q=_p(cu_q), cu_seqlens_k=_p(cu_k))
     a.q_stride_b, a.q_stride_t, a.q_stride_h = _lead_strides(q, "q")
     a.k_stride_b, a.k_stride_t, a.k_stride_h = _lead_strides(k_nope, "k_nope")
@@ -236,7 +236,7 @@ def _latent_args(q, k_nope, k_rope, v, scale, causal, cu_q, cu_k, *more):
 
 
 def latent_prefill(q, k_nope, k_rope, v, scale=None, causal=True, cu_seqlens=None, cu_seqlens_k=None, out_dtype=None, o=None, lse=None, check_seqlens=True,
-                   device_status=None):
+                   device_status=None, precise=False):
     """Latent attention in its expanded form over whole sequences.
 
     q [B,T,H,d_nope+d_rope], k_nope [B,S,H,d_nope], v [B,S,H,d_v], all float32
@@ -251,8 +251,13 @@ def latent_prefill(q, k_nope, k_rope, v, scale=None, causal=True, cu_seqlens=Non
     Returns (o [B,T,H,d_v] of out_dtype, default q's; lse float32 [B,T,H], the
     log of the sum of exponentials).  A query without a key has o = 0 and lse =
     -inf.  ``o`` and ``lse`` are optional preallocated buffers;
-    ``check_seqlens`` and ``device_status`` as for ``prefill``."""
-    a, dev, (B, T, S, H, dn, dr, dv) = _latent_args(q, k_nope, k_rope, v, scale, causal, cu_seqlens, cu_seqlens_k, o, lse, device_status)
+    ``check_seqlens`` and ``device_status`` as for ``prefill``.
+
+    With bfloat16 inputs the probabilities are rounded to bfloat16 for their
+    product with v (a float32 o is the bfloat16 one before its own rounding);
+    with ``precise`` they enter it in two parts, exact to 2^-16, which takes about
+    a third longer.  float32 inputs are computed in float32 throughout."""
+    a, dev, (B, T, S, H, dn, dr, dv) = _latent_args(q, k_nope, k_rope, v, scale, causal, cu_seqlens, cu_seqlens_k, precise, o, lse, device_status)
     _dense(o, lse, device_status)
     if o is None:
         o = torch.empty((B, T, H, dv), dtype=out_dtype or q.dtype, device=dev)
@@ -280,17 +285,19 @@ def latent_prefill(q, k_nope, k_rope, v, scale=None, causal=True, cu_seqlens=Non
     return o, lse
 
 
-def latent_backward(q, k_nope, k_rope, v, o, lse, d_o, scale=None, causal=True, cu_seqlens=None, cu_seqlens_k=None, device_status=None):
+def latent_backward(q, k_nope, k_rope, v, o, lse, d_o, scale=None, causal=True, cu_seqlens=None, cu_seqlens_k=None, device_status=None, precise=False):
     """Gradients of ``latent_prefill`` with the same arguments, from d_o (like
     o, q's dtype) and the forward's o and lse (all three strided as they come,
     channels contiguous): (dq, dk_nope, dk_rope, dv),
     contiguous, q's dtype, dk_rope summed over the heads that share it (None
     without one).  o may be float32 with bfloat16 inputs (the forward's
     ``out_dtype``): the gradients of scores are differences with rowsum(d_o o),
-    into which a rounded o brings its rounding.  Nothing synchronises; ``device_status`` (int32 [1] on the
+    into which a rounded o brings its rounding.  The probabilities and the scores'
+    gradients are rounded to bfloat16 for their products, or with ``precise`` enter
+    them in two parts, as in the forward.  Nothing synchronises; ``device_status`` (int32 [1] on the
     device) receives the call's device-side status: with malformed offsets the
     gradients are not written."""
-    a, dev, (B, T, S, H, dn, dr, dv) = _latent_args(q, k_nope, k_rope, v, scale, causal, cu_seqlens, cu_seqlens_k, o, lse, d_o, device_status)
+    a, dev, (B, T, S, H, dn, dr, dv) = _latent_args(q, k_nope, k_rope, v, scale, causal, cu_seqlens, cu_seqlens_k, precise, o, lse, d_o, device_status)
     _dense(device_status)
     _check_buffer(o, "o", (B, T, H, dv), _FLOATS)
     _check_buffer(d_o, "d_o", (B, T, H, dv), (q.dtype,))
@@ -328,7 +335,8 @@ def latent_decode(q, cache, page_table, lengths, d_latent, scale, out_dtype=None
     [B,max_pages].  ``scale`` is that of the expanded form.
 
     Returns (o [B,m,H,d_latent] of out_dtype, default q's, still latent; lse
-    float32 [B,m,H]).  An empty slot (length 0) has o = 0 and lse = -inf.
+    float32 [B,m,H]).  With bfloat16 inputs the probabilities enter their product
+    with the values in two parts, exact to 2^-16.  An empty slot (length 0) has o = 0 and lse = -inf.
     Nothing synchronises; ``device_status`` (int32 [1] on the device) tells of
     pages or lengths outside the cache, whose sequences' results are undefined."""
     dev = _device(q, cache, page_table, lengths, o, lse, device_status)

@@ -800,9 +800,13 @@ kda_status kda_latent_append(const kda_latent_append_args *a, void *hip_stream);
  *                aligned
  *
  * Inputs are finite: a NaN or an infinity may reach every row of its own
- * sequence, never another sequence.  Precision: bf16 inputs enter the matrix
- * cores as they are, the probabilities rounded to bf16; statistics and sums
- * are fp32.  fp32 inputs run on fp32 matrix cores.
+ * sequence, never another sequence.
+ * Precision: bf16 inputs enter the matrix cores as they are; statistics and sums
+ * are fp32.  The probabilities, and in the gradients the scores' gradients too,
+ * are operands of a second product: rounded to bf16 (each term of a sum by up
+ * to 2^-8 of itself, also behind an fp32 o, which is the bf16 o before its own
+ * rounding), or with precise in two bf16 parts (2^-16), about a third slower.
+ * fp32 inputs run on fp32 matrix cores, precise or not.
  * Supported: d_nope, d_rope, d_v multiples of 8, d_nope >= 8, d_nope + d_rope
  * <= 192, d_v <= 128; num_seqs <= 2^20, num_seqs * H <= 2^21, B * max(T, S) * H
  * < 2^28, B * max(T, S) * d_rope < 2^33; strides multiples of 8, token strides
@@ -817,6 +821,7 @@ typedef struct kda_latent_prefill_args {
     int32_t in_dtype;              /* kda_dtype */
     int32_t out_dtype;             /* kda_dtype */
     int32_t causal;                /* 0 or 1 */
+    int32_t precise;               /* 0 or 1: see Precision */
     float scale;
     int64_t q_stride_b, q_stride_t, q_stride_h;
     int64_t k_stride_b, k_stride_t, k_stride_h;    /* k_nope */
@@ -849,6 +854,7 @@ kda_status kda_latent_prefill(const kda_latent_prefill_args *a, void *hip_stream
  *                aligned
  * f.device_status reports as in the forward; with malformed offsets nothing
  * else is written.  The workspace holds an fp32 row of d_rope per key and head.
+ * Precision is the forward's, f.precise as there.
  * The strides of d_o are as those of q.  Results are the
  * same from run to run (no floating-point atomics).
  */
@@ -891,7 +897,10 @@ kda_status kda_latent_backward(const kda_latent_backward_args *a, void *hip_stre
  * entry of the table outside [0, num_pages) within the length, is reported in
  * *device_status, the results of that sequence are undefined, others are not
  * touched by it, and no access is out of range.  Results are the same from run
- * to run.
+ * to run.  A NaN or an infinity in a row may reach every token of its own
+ * sequence, never another sequence.  Precision: bf16 inputs enter the matrix cores
+ * as they are, the probabilities in two bf16 parts (2^-16 of themselves);
+ * statistics and sums are fp32.  fp32 inputs run on fp32 matrix cores.
  * Supported: d_latent, d_rope multiples of 8, 8 <= d_latent <= 512, d_latent +
  * d_rope <= 576; page_size, max_pages, num_pages >= 1, max_pages * page_size <
  * 2^31 - 64; B <= 65536, B * m * H < 2^24; strides multiples of 8; q, cache, o
