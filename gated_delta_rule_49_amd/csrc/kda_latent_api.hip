@@ -12,6 +12,8 @@ using namespace kda;
 namespace {
 
 constexpr int64_t kMost31 = (static_cast<int64_t>(1) << 31) - 1;
+constexpr int64_t kMostRows = (static_cast<int64_t>(1) << 28) - 16;   // the gradients' (token, head) rows, in whole workgroups of 16: fewer than 2^32 threads
+constexpr int64_t kMostTokens = (static_cast<int64_t>(1) << 26) - 4;  // appended tokens, in whole workgroups of 4
 
 bool dtype_ok(int t) { return t == KDA_F32 || t == KDA_BF16; }
 int64_t size_of(int t) { return t == KDA_F32 ? 4 : 2; }
@@ -204,7 +206,7 @@ kda_status check_backward(const kda_latent_backward_args *a, bool need_ptrs) {
     if (st != KDA_OK) return st;
     st = check_strides({a->o_stride_b, a->o_stride_t, a->o_stride_h, a->d_o_stride_b, a->d_o_stride_t, a->d_o_stride_h});
     if (st != KDA_OK) return st;
-    if (a->d_o_stride_t >= (1 << 23)) return KDA_ERR_UNSUPPORTED;
+    if (a->d_o_stride_t >= (1 << 23) || static_cast<int64_t>(a->f.B) * a->f.T * a->f.H > kMostRows) return KDA_ERR_UNSUPPORTED;
     for (const int64_t s : {a->lse_stride_b, a->lse_stride_t, a->lse_stride_h})
         if (s < 0 || s > (static_cast<int64_t>(1) << 48)) return KDA_ERR_BAD_SHAPE;
     if (!need_ptrs) return KDA_OK;
@@ -273,7 +275,7 @@ kda_status kda_latent_append(const kda_latent_append_args *a, void *hip_stream) 
     if (!dtype_ok(a->dtype) || !flag_ok(a->interleaved)) return KDA_ERR_UNSUPPORTED;
     if (!(a->eps >= 0.f)) return KDA_ERR_BAD_SHAPE;
     if (a->cu_seqlens ? a->B != 1 || a->num_seqs < 1 : a->num_seqs != a->B) return KDA_ERR_BAD_SHAPE;
-    if (static_cast<int64_t>(a->B) * a->T >= (1 << 26)) return KDA_ERR_UNSUPPORTED;  // a wave each, fewer than 2^32 threads
+    if (static_cast<int64_t>(a->B) * a->T > kMostTokens) return KDA_ERR_UNSUPPORTED;
     const int64_t d = a->d_latent + a->d_rope, e = size_of(a->dtype);
     kda_status st = check_pages(a->num_pages, a->page_size, a->max_pages, a->page_stride, a->row_stride, a->table_stride, d);
     if (st != KDA_OK) return st;

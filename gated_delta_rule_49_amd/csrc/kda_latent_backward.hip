@@ -369,6 +369,8 @@ hipError_t run(const LatentGradParams &g, hipStream_t s) {
     const int grid_q = p.cu_q ? p.H * p.tq.bound : p.H * p.N * p.tq.per_seq;
     const int grid_k = p.cu_q ? p.H * g.tk.bound : p.H * p.N * g.tk.per_seq;
     if (p.T) grad_q_bf16_kernel<DK, DV, PARTS><<<grid_q, kQThreads, 0, s>>>(g);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     if (p.S) grad_k_bf16_kernel<DK, DV, PARTS><<<grid_k, kKThreads, 0, s>>>(g);
     return hipGetLastError();
 }
@@ -383,7 +385,9 @@ template <typename T> hipError_t backward(const LatentGradParams &g, hipStream_t
     const unsigned grid = static_cast<unsigned>((rows + 15) / 16);
     if (rows && g.o_dtype == 0) stats_kernel<T, float><<<grid, 256, 0, s>>>(g);
     if (rows && g.o_dtype != 0) stats_kernel<T, bf16_t><<<grid, 256, 0, s>>>(g);
-    const hipError_t e = sizeof(T) == 4 ? latent_backward_f32(g, s) : g.f.precise ? backward_bf16<2>(g, s) : backward_bf16<1>(g, s);
+    hipError_t e = hipGetLastError();  // nothing runs on statistics that were not made
+    if (e != hipSuccess) return e;
+    e = sizeof(T) == 4 ? latent_backward_f32(g, s) : g.f.precise ? backward_bf16<2>(g, s) : backward_bf16<1>(g, s);
     if (e != hipSuccess) return e;
     if (shared) rope_sum_kernel<T><<<static_cast<unsigned>((shared / 4 + 255) / 256), 256, 0, s>>>(g);
     return hipGetLastError();

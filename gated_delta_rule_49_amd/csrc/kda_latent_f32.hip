@@ -633,6 +633,8 @@ hipError_t run_grad(const LatentGradParams &g, hipStream_t s) {
     const int grid_k = p.cu_q ? p.H * g.tk.bound : p.H * p.N * g.tk.per_seq;
     if (p.T && p.tq.size == kFewTile) grad_q_few_kernel<DK, DV><<<grid_q, 256, 0, s>>>(g);
     if (p.T && p.tq.size != kFewTile) grad_q_f32_kernel<DK, DV><<<grid_q, 256, 0, s>>>(g);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     if (p.S && g.tk.size == kFewTile) grad_k_few_kernel<DK, DV><<<grid_k, 256, 0, s>>>(g);
     if (p.S && g.tk.size != kFewTile) grad_k_f32_kernel<DK, DV><<<grid_k, 256, 0, s>>>(g);
     return hipGetLastError();

@@ -746,7 +746,7 @@ kda_status kda_rotary_backward(const kda_rotary_args *a, void *hip_stream);
  * overlap (KDA_ERR_BAD_SHAPE).
  * Supported: d_latent, d_rope multiples of 8 (d_rope may be 0), d_latent <=
  * 2048, d_rope <= 256; strides multiples of 8; kv, cache and rows 16-byte
- * aligned; B * T < 2^26.
+ * aligned; B * T <= 2^26 - 4; max_pages * page_size < 2^31 - 64.
  */
 typedef struct kda_latent_append_args {
     int32_t B, T;
@@ -854,7 +854,7 @@ kda_status kda_latent_prefill(const kda_latent_prefill_args *a, void *hip_stream
  *                aligned
  * f.device_status reports as in the forward; with malformed offsets nothing
  * else is written.  The workspace holds an fp32 row of d_rope per key and head.
- * Precision is the forward's, f.precise as there.
+ * Precision is the forward's, f.precise as there.  B * T * H <= 2^28 - 16.
  * The strides of d_o are as those of q.  Results are the
  * same from run to run (no floating-point atomics).
  */

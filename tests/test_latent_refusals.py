@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 import gated_delta_rule_49_amd as kda
-from test_latent_abi import APPEND, BAD_SHAPE, DECODE, FAKE, FAR, OK, PREFILL, UNSUPPORTED, L, fill  # noqa: F401
+from test_latent_abi import APPEND, NULL_ARG, PREFILL, UNSUPPORTED, L, fill  # noqa: F401
 
 
 def test_precise_is_a_flag(L):  # noqa: F811
@@ -15,3 +15,21 @@ def test_precise_is_a_flag(L):  # noqa: F811
         assert L.kda_latent_prefill(ctypes.byref(a), None) == UNSUPPORTED and L.kda_latent_prefill_workspace_bytes(ctypes.byref(a)) == 0
     for precise in (0, 1):
         assert L.kda_latent_prefill_workspace_bytes(ctypes.byref(fill(kda.LatentPrefillArgs, PREFILL, dict(precise=precise)))) > 0
+
+
+def test_workgroups_of_a_launch_are_whole(L):  # noqa: F811
+    """A launch's threads are counted in whole workgroups: calls whose last one would make them 2^32 are refused."""
+    def append(tokens):
+        many = dict(B=1, num_seqs=1, T=tokens, kv_stride_b=0, kv_stride_t=0, kv=None)
+        return L.kda_latent_append(ctypes.byref(fill(kda.LatentAppendArgs, APPEND, many)), None)
+    assert all(append(2 ** 26 - k) == UNSUPPORTED for k in (0, 1, 2, 3))
+    assert append(2 ** 26 - 4) == NULL_ARG  # past the sizes' check
+
+    def rows(tokens):
+        f = fill(kda.LatentPrefillArgs, PREFILL, dict(B=1, num_seqs=1, H=1, T=tokens, S=70, d_rope=16))
+        g = kda.LatentBackwardArgs(f=f)
+        return int(L.kda_latent_prefill_workspace_bytes(ctypes.byref(f))), int(L.kda_latent_backward_workspace_bytes(ctypes.byref(g)))
+    for k in (1, 15):  # the gradients' statistics
+        forward, backward = rows(2 ** 28 - k)
+        assert forward > 0 and backward == 0
+    assert min(rows(2 ** 28 - 16)) > 0
