@@ -57,27 +57,30 @@ bool apart(std::initializer_list<Span> in, std::initializer_list<Span> out) {
     }
     return true;
 }
-kda_status status_of(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
-
-// -------------------------------------------------------------- rotary ----
-// elements from the first to behind the last of a strided [B, T, H, D]
-int64_t extent(const kda_rotary_args *a, int64_t sb, int64_t st, int64_t sh) {
-    return (a->B - 1) * sb + (a->T - 1) * st + (a->H - 1) * sh + a->D;
-}
-// whether no two elements share memory: taken by size, each axis steps over
-// all that the smaller ones reach
-bool distinct(const kda_rotary_args *a, int64_t sb, int64_t st, int64_t sh) {
-    struct Axis { int64_t n, s; } ax[3] = {{a->B, sb}, {a->T, st}, {a->H, sh}};
-    for (int i = 0; i < 3; ++i)
-        for (int j = i + 1; j < 3; ++j)
+// an axis of n elements, s apart
+struct Axis {
+    int64_t n, s;
+};
+// whether no two runs of d elements share memory: taken by size, each axis
+// steps over all that the smaller ones reach
+template <int N> bool distinct(Axis (&&ax)[N], int64_t d) {
+    for (int i = 0; i < N; ++i)
+        for (int j = i + 1; j < N; ++j)
             if (ax[j].s < ax[i].s) std::swap(ax[i], ax[j]);
-    int64_t reach = a->D;
+    int64_t reach = d;
     for (const Axis &x : ax) {
         if (x.n <= 1) continue;
         if (x.s < reach) return false;
         reach += (x.n - 1) * x.s;
     }
     return true;
+}
+kda_status status_of(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
+
+// -------------------------------------------------------------- rotary ----
+// elements from the first to behind the last of a strided [B, T, H, D]
+int64_t extent(const kda_rotary_args *a, int64_t sb, int64_t st, int64_t sh) {
+    return (a->B - 1) * sb + (a->T - 1) * st + (a->H - 1) * sh + a->D;
 }
 kda_status rotary(const kda_rotary_args *a, bool back, void *hip_stream) {
     if (!a) return KDA_ERR_NULL_ARG;
@@ -92,7 +95,7 @@ kda_status rotary(const kda_rotary_args *a, bool back, void *hip_stream) {
     if (!a->x || !a->out || (a->rotary_dim && !a->freqs)) return KDA_ERR_NULL_ARG;
     const int64_t e = size_of(a->dtype);
     if (reinterpret_cast<uintptr_t>(a->x) % e || reinterpret_cast<uintptr_t>(a->out) % e) return KDA_ERR_UNSUPPORTED;
-    if (!distinct(a, a->out_stride_b, a->out_stride_t, a->out_stride_h)) return KDA_ERR_BAD_SHAPE;
+    if (!distinct({{a->B, a->out_stride_b}, {a->T, a->out_stride_t}, {a->H, a->out_stride_h}}, a->D)) return KDA_ERR_BAD_SHAPE;
     const bool same = a->x == a->out && (a->B == 1 || a->x_stride_b == a->out_stride_b) && (a->T == 1 || a->x_stride_t == a->out_stride_t) &&
                       (a->H == 1 || a->x_stride_h == a->out_stride_h);
     if (!same && overlap(a->x, extent(a, a->x_stride_b, a->x_stride_t, a->x_stride_h) * e, a->out,
@@ -232,7 +235,7 @@ kda_status check_pages(int32_t num_pages, int32_t page_size, int32_t max_pages, 
     if (static_cast<int64_t>(max_pages) * page_size > kMost31 - 64) return KDA_ERR_UNSUPPORTED;  // rows of a last, partial step count in 32 bits
     const kda_status st = check_strides({page_stride, row_stride});
     if (st != KDA_OK) return st;
-    // rows, and pages, that do not share memory
+    // rows of one page, and one row of all pages, that do not share memory
     if ((page_size > 1 && row_stride < d) || (num_pages > 1 && page_stride < d)) return KDA_ERR_BAD_SHAPE;
     return KDA_OK;
 }
@@ -279,6 +282,8 @@ kda_status kda_latent_append(const kda_latent_append_args *a, void *hip_stream) 
     const int64_t d = a->d_latent + a->d_rope, e = size_of(a->dtype);
     kda_status st = check_pages(a->num_pages, a->page_size, a->max_pages, a->page_stride, a->row_stride, a->table_stride, d);
     if (st != KDA_OK) return st;
+    // rows that are written, by a wave each, share no memory with any other
+    if (!distinct({{a->num_pages, a->page_stride}, {a->page_size, a->row_stride}}, d)) return KDA_ERR_BAD_SHAPE;
     st = check_strides({a->kv_stride_b, a->kv_stride_t});
     if (st != KDA_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);

@@ -743,7 +743,8 @@ kda_status kda_rotary_backward(const kda_rotary_args *a, void *hip_stream);
  * *device_status.  Rows that no token goes to keep their contents.  Tokens that
  * the tables send to one row of the cache (a page that two sequences append to,
  * or one listed twice) leave that row undefined.  kv, rows and cache must not
- * overlap (KDA_ERR_BAD_SHAPE).
+ * overlap, nor rows of the cache each other (KDA_ERR_BAD_SHAPE): of page_stride
+ * and row_stride the larger steps over all that the smaller reaches.
  * Supported: d_latent, d_rope multiples of 8 (d_rope may be 0), d_latent <=
  * 2048, d_rope <= 256; strides multiples of 8; kv, cache and rows 16-byte
  * aligned; B * T <= 2^26 - 4; max_pages * page_size < 2^31 - 64.

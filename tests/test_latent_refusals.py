@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 import gated_delta_rule_49_amd as kda
-from test_latent_abi import APPEND, NULL_ARG, PREFILL, UNSUPPORTED, L, fill  # noqa: F401
+from test_latent_abi import APPEND, BAD_SHAPE, NULL_ARG, PREFILL, UNSUPPORTED, L, fill  # noqa: F401
 
 
 def test_precise_is_a_flag(L):  # noqa: F811
@@ -33,3 +33,13 @@ def test_workgroups_of_a_launch_are_whole(L):  # noqa: F811
         forward, backward = rows(2 ** 28 - k)
         assert forward > 0 and backward == 0
     assert min(rows(2 ** 28 - 16)) > 0
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(page_stride=160), BAD_SHAPE),  # page 1 begins with row 2 of page 0
+    (dict(page_stride=312), BAD_SHAPE), (dict(row_stride=720, page_stride=720), BAD_SHAPE), (dict(row_stride=712, page_stride=80), BAD_SHAPE),
+    # page after page with room between, all pages' first rows before their second, one page, pages of one row
+    (dict(page_stride=328), NULL_ARG), (dict(row_stride=720, page_stride=80), NULL_ARG), (dict(num_pages=1, page_stride=0), NULL_ARG),
+    (dict(page_size=1, row_stride=0, page_stride=80), NULL_ARG)])
+def test_rows_of_the_cache_share_no_memory(L, over, status):  # noqa: F811
+    assert L.kda_latent_append(ctypes.byref(fill(kda.LatentAppendArgs, APPEND, dict(over, kv=None))), None) == status
