@@ -159,7 +159,9 @@ __global__ void __launch_bounds__(256) append_kernel(LatentAppendParams p) {
             hi = min(hi, lo + step);
         }
         n = lo;
-        t = static_cast<int>(token - p.cu[n]);
+        const int32_t begin = p.cu[n], end = p.cu[n + 1];
+        if (token < begin || token >= end) return;  // no sequence's: before the first, behind the last
+        t = static_cast<int>(token - begin);
     } else {
         n = static_cast<int>(token / p.T);
         t = static_cast<int>(token - static_cast<int64_t>(n) * p.T);

@@ -168,9 +168,10 @@ def latent_append(kv, cache, page_table, lengths, d_latent, norm_weight=None, ep
 
     ``lengths`` int32 [N] (tokens in the cache already; not changed),
     ``page_table`` int32 [N,max_pages]; ``cu_seqlens`` (int32 [N+1], batch 1)
-    packs N sequences along T.  With ``output_rows``, or a buffer ``rows``, the
-    rows are returned too, [B,T,d_latent+d_rope] (a prompt expands them), else
-    None.  A token without a page of its own (a position outside the table, an
+    packs N sequences along T; tokens before the first offset or behind the last
+    are padding, for which nothing is written.  With ``output_rows``, or a buffer
+    ``rows``, the rows are returned too, [B,T,d_latent+d_rope] (a prompt expands
+    them; padding's are left as they were), else None.  A token without a page of its own (a position outside the table, an
     entry outside the cache) is left out; ``device_status`` (int32 [1] on the
     device) tells so.  Nothing synchronises."""
     dev = _device(kv, cache, page_table, lengths, norm_weight, freqs, cu_seqlens, rows, device_status)

@@ -726,8 +726,10 @@ kda_status kda_rotary_backward(const kda_rotary_args *a, void *hip_stream);
  *   freqs        DEVICE double [d_rope / 2], NULL = no rotation
  *   cu_seqlens   DEVICE int32 [num_seqs + 1], NULL = the B rows are the
  *                sequences; else B == 1 and sequences are packed along T
- *                (malformed offsets give unspecified values in the sequences'
- *                own pages, never an out-of-range access)
+ *                (tokens before the first offset or behind the last are
+ *                padding: neither cache nor rows are written for them.
+ *                Offsets that decrease give unspecified values in the
+ *                sequences' own pages, never an out-of-range access)
  *   lengths      DEVICE int32 [num_seqs]: tokens each sequence has in the
  *                cache already.  Not changed
  *   page_table   DEVICE int32 [num_seqs, max_pages], rows table_stride apart
