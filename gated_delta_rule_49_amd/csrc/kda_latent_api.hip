@@ -136,14 +136,15 @@ kda_status check_prefill(const kda_latent_prefill_args *a, bool need_ptrs, bool 
     return KDA_OK;
 }
 struct Inputs {
-    Span q, k, r, v;
+    Span q, k, r, v, cu_q, cu_k;
 };
 Inputs inputs_of(const kda_latent_prefill_args *a) {
     const int64_t e = size_of(a->in_dtype);
     return {span(a->q, a->B, a->q_stride_b, a->T, a->q_stride_t, a->H, a->q_stride_h, a->d_nope + a->d_rope, e),
             span(a->k_nope, a->B, a->k_stride_b, a->S, a->k_stride_t, a->H, a->k_stride_h, a->d_nope, e),
             span(a->k_rope, a->B, a->r_stride_b, a->S, a->r_stride_t, 1, 0, a->d_rope, e),
-            span(a->v, a->B, a->v_stride_b, a->S, a->v_stride_t, a->H, a->v_stride_h, a->d_v, e)};
+            span(a->v, a->B, a->v_stride_b, a->S, a->v_stride_t, a->H, a->v_stride_h, a->d_v, e),
+            dense(a->cu_seqlens_q, static_cast<int64_t>(a->num_seqs) + 1, 4), dense(a->cu_seqlens_k, static_cast<int64_t>(a->num_seqs) + 1, 4)};
 }
 LatentParams latent_params(const kda_latent_prefill_args *a) {
     LatentParams p{};
@@ -203,6 +204,21 @@ hipError_t prepare_tiles(const kda_latent_prefill_args *a, Layout &l, char *ws, 
     t.user_status = user_status;
     return launch_latent_table(t, s);
 }
+// what the gradients read and write
+struct GradSpans {
+    Inputs in;
+    Span o, lse, d_o, dq, dkn, dkr, dv, status;
+};
+GradSpans grad_spans(const kda_latent_backward_args *a) {
+    const kda_latent_prefill_args &f = a->f;
+    const int64_t e = size_of(f.in_dtype), queries = static_cast<int64_t>(f.B) * f.T * f.H, keys = static_cast<int64_t>(f.B) * f.S;
+    return {inputs_of(&f),
+            span(f.o, f.B, a->o_stride_b, f.T, a->o_stride_t, f.H, a->o_stride_h, f.d_v, size_of(f.out_dtype)),
+            span(f.lse, f.B, a->lse_stride_b, f.T, a->lse_stride_t, f.H, a->lse_stride_h, 1, 4),
+            span(a->d_o, f.B, a->d_o_stride_b, f.T, a->d_o_stride_t, f.H, a->d_o_stride_h, f.d_v, e),
+            dense(a->dq, queries * (f.d_nope + f.d_rope), e), dense(a->dk_nope, keys * f.H * f.d_nope, e), dense(a->dk_rope, keys * f.d_rope, e),
+            dense(a->dv, keys * f.H * f.d_v, e), dense(f.device_status, 1, 4)};
+}
 kda_status check_backward(const kda_latent_backward_args *a, bool need_ptrs) {
     if (!a) return KDA_ERR_NULL_ARG;
     kda_status st = check_prefill(&a->f, need_ptrs, true);
@@ -217,15 +233,8 @@ kda_status check_backward(const kda_latent_backward_args *a, bool need_ptrs) {
     if (a->f.S > 0 && (!a->dk_nope || !a->dv || (a->f.d_rope && !a->dk_rope))) return KDA_ERR_NULL_ARG;
     if (!a->f.d_rope && a->dk_rope) return KDA_ERR_BAD_SHAPE;
     if (misaligned({a->d_o, a->dq, a->dk_nope, a->dk_rope, a->dv})) return KDA_ERR_UNSUPPORTED;
-    const kda_latent_prefill_args &f = a->f;
-    const int64_t e = size_of(f.in_dtype), queries = static_cast<int64_t>(f.B) * f.T * f.H, keys = static_cast<int64_t>(f.B) * f.S;
-    const Inputs in = inputs_of(&f);
-    if (!apart({in.q, in.k, in.r, in.v, span(f.o, f.B, a->o_stride_b, f.T, a->o_stride_t, f.H, a->o_stride_h, f.d_v, size_of(f.out_dtype)),
-                span(f.lse, f.B, a->lse_stride_b, f.T, a->lse_stride_t, f.H, a->lse_stride_h, 1, 4),
-                span(a->d_o, f.B, a->d_o_stride_b, f.T, a->d_o_stride_t, f.H, a->d_o_stride_h, f.d_v, e)},
-               {dense(a->dq, queries * (f.d_nope + f.d_rope), e), dense(a->dk_nope, keys * f.H * f.d_nope, e), dense(a->dk_rope, keys * f.d_rope, e),
-                dense(a->dv, keys * f.H * f.d_v, e)}))
-        return KDA_ERR_BAD_SHAPE;
+    const GradSpans m = grad_spans(a);
+    if (!apart({m.in.q, m.in.k, m.in.r, m.in.v, m.in.cu_q, m.in.cu_k, m.o, m.lse, m.d_o}, {m.dq, m.dkn, m.dkr, m.dv, m.status})) return KDA_ERR_BAD_SHAPE;
     return KDA_OK;
 }
 
@@ -238,6 +247,16 @@ kda_status check_pages(int32_t num_pages, int32_t page_size, int32_t max_pages, 
     // rows of one page, and one row of all pages, that do not share memory
     if ((page_size > 1 && row_stride < d) || (num_pages > 1 && page_stride < d)) return KDA_ERR_BAD_SHAPE;
     return KDA_OK;
+}
+struct DecodeSpans {
+    Span q, cache, table, lengths, o, lse, status;
+};
+DecodeSpans decode_spans(const kda_latent_decode_args *a) {
+    const int64_t e = size_of(a->in_dtype), d = a->d_latent + a->d_rope, rows = static_cast<int64_t>(a->B) * a->n_tokens * a->H;
+    return {span(a->q, a->B, a->q_stride_b, a->n_tokens, a->q_stride_t, a->H, a->q_stride_h, d, e),
+            span(a->cache, a->num_pages, a->page_stride, a->page_size, a->row_stride, 1, 0, d, e),
+            span(a->page_table, a->B, a->table_stride, 1, 0, 1, 0, a->max_pages, 4), dense(a->lengths, a->B, 4),
+            dense(a->o, rows * a->d_latent, size_of(a->out_dtype)), dense(a->lse, rows, 4), dense(a->device_status, 1, 4)};
 }
 kda_status check_decode(const kda_latent_decode_args *a, bool need_ptrs) {
     if (!a) return KDA_ERR_NULL_ARG;
@@ -253,11 +272,8 @@ kda_status check_decode(const kda_latent_decode_args *a, bool need_ptrs) {
     if (!need_ptrs || a->B == 0) return KDA_OK;
     if (!a->q || !a->cache || !a->page_table || !a->lengths || !a->o || !a->lse) return KDA_ERR_NULL_ARG;
     if (misaligned({a->q, a->cache, a->o})) return KDA_ERR_UNSUPPORTED;
-    const int64_t e = size_of(a->in_dtype), d = a->d_latent + a->d_rope, rows = static_cast<int64_t>(a->B) * a->n_tokens * a->H;
-    if (!apart({span(a->q, a->B, a->q_stride_b, a->n_tokens, a->q_stride_t, a->H, a->q_stride_h, d, e),
-                span(a->cache, a->num_pages, a->page_stride, a->page_size, a->row_stride, 1, 0, d, e)},
-               {dense(a->o, rows * a->d_latent, size_of(a->out_dtype)), dense(a->lse, rows, 4)}))
-        return KDA_ERR_BAD_SHAPE;
+    const DecodeSpans m = decode_spans(a);
+    if (!apart({m.q, m.cache, m.table, m.lengths}, {m.o, m.lse, m.status})) return KDA_ERR_BAD_SHAPE;
     return KDA_OK;
 }
 LatentDecodePlan decode_plan(const kda_latent_decode_args *a) {
@@ -317,11 +333,14 @@ kda_status kda_latent_prefill(const kda_latent_prefill_args *a, void *hip_stream
     if (st != KDA_OK) return st;
     const int64_t rows = static_cast<int64_t>(a->B) * a->T * a->H;
     const Inputs in = inputs_of(a);
-    if (!apart({in.q, in.k, in.r, in.v}, {dense(a->o, rows * a->d_v, size_of(a->out_dtype)), dense(a->lse, rows, 4)})) return KDA_ERR_BAD_SHAPE;
+    const Span o = dense(a->o, rows * a->d_v, size_of(a->out_dtype)), lse = dense(a->lse, rows, 4), status = dense(a->device_status, 1, 4);
+    if (!apart({in.q, in.k, in.r, in.v, in.cu_q, in.cu_k}, {o, lse, status})) return KDA_ERR_BAD_SHAPE;
     if (!a->workspace) return KDA_ERR_NULL_ARG;
     if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign) return KDA_ERR_BAD_SHAPE;
     Layout l = latent_layout(a, false);
     if (a->workspace_bytes < l.bytes) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    const bool used = a->T > 0 || a->cu_seqlens_q;
+    if (used && !apart({in.q, in.k, in.r, in.v, in.cu_q, in.cu_k, o, lse, status}, {dense(a->workspace, l.bytes, 1)})) return KDA_ERR_BAD_SHAPE;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     char *ws = static_cast<char *>(a->workspace);
     hipError_t e = prepare_tiles(a, l, ws, false, a->device_status, s);
@@ -344,6 +363,9 @@ kda_status kda_latent_backward(const kda_latent_backward_args *a, void *hip_stre
     if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign) return KDA_ERR_BAD_SHAPE;
     Layout l = latent_layout(&a->f, true);
     if (a->workspace_bytes < l.bytes) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    const GradSpans m = grad_spans(a);
+    if (!apart({m.in.q, m.in.k, m.in.r, m.in.v, m.in.cu_q, m.in.cu_k, m.o, m.lse, m.d_o, m.dq, m.dkn, m.dkr, m.dv, m.status}, {dense(a->workspace, l.bytes, 1)}))
+        return KDA_ERR_BAD_SHAPE;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     char *ws = static_cast<char *>(a->workspace);
     hipError_t e = prepare_tiles(&a->f, l, ws, true, a->f.device_status, s);
@@ -374,11 +396,13 @@ kda_status kda_latent_decode(const kda_latent_decode_args *a, void *hip_stream) 
     if (st != KDA_OK) return st;
     if (!a->workspace) return KDA_ERR_NULL_ARG;
     if (reinterpret_cast<uintptr_t>(a->workspace) % kAlign) return KDA_ERR_BAD_SHAPE;
-    if (a->workspace_bytes < kda_latent_decode_workspace_bytes(a)) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    const LatentDecodePlan plan = decode_plan(a);
+    if (a->workspace_bytes < plan.bytes() + kAlign) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    const DecodeSpans m = decode_spans(a);
+    if (a->B > 0 && !apart({m.q, m.cache, m.table, m.lengths, m.o, m.lse, m.status}, {dense(a->workspace, plan.bytes(), 1)})) return KDA_ERR_BAD_SHAPE;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     if (a->device_status && launch_status_word(a->device_status, s) != hipSuccess) return KDA_ERR_HIP;
     if (a->B == 0) return KDA_OK;
-    const LatentDecodePlan plan = decode_plan(a);
     LatentDecodeParams p{};
     p.q = a->q; p.cache = a->cache;
     p.q_sb = a->q_stride_b; p.q_st = a->q_stride_t; p.q_sh = a->q_stride_h;

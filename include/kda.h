@@ -814,8 +814,9 @@ kda_status kda_latent_append(const kda_latent_append_args *a, void *hip_stream);
  * <= 192, d_v <= 128; num_seqs <= 2^20, num_seqs * H <= 2^21, B * max(T, S) * H
  * < 2^28, B * max(T, S) * d_rope < 2^33; strides multiples of 8, token strides
  * below 2^23; q, k_nope, k_rope, v, o 16-byte aligned (else KDA_ERR_UNSUPPORTED).
- * Outputs that share memory with an input or with each other are refused
- * (KDA_ERR_BAD_SHAPE), here and in the two calls below.
+ * Outputs (device_status among them) and the workspace that share memory with an
+ * input, with the offsets, or with each other are refused (KDA_ERR_BAD_SHAPE),
+ * here and in the two calls below.
  */
 typedef struct kda_latent_prefill_args {
     int32_t B, T, S, H;
