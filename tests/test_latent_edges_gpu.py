@@ -6,7 +6,9 @@ import pytest
 import torch
 
 import gated_delta_rule_49_amd as kda
-from latent_testutil import BF16, FP32, same
+from latent_testutil import BACKWARD, BF16, FP32, make, same
+from oracle import latent as R
+from sublayer_testutil import check
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +37,41 @@ def test_append_leaves_padding_alone(dtype, cu):
             want[int(table[n, pos // page]), pos % page] = kv[0, t]
             want_rows[0, t] = kv[0, t]
     assert same(cache, want) and same(rows, want_rows) and int(status) == 0
+
+
+# ------------------------------------------------------------- training step
+@TYPES
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("dn,dr,dv", [(64, 32, 64), (128, 64, 128)])
+def test_training_step_whole_gradients(dtype, interleaved, dn, dr, dv):
+    """Rotation, attention and their gradients in a chain: every gradient as a whole, and its rotated channels by
+    themselves, against the chain in 64 bits."""
+    T, H, first = 40, 3, 500
+    freqs, magnitude = kda.rotary_frequencies(dr, scaling="turns", factor=4, device="cuda")
+    t, w, d_o, d64 = make(23, (1, T), (1, T), H, dn, dr, dv, dtype, wide=1.0)
+    at = np.arange(T) + first
+    kw = dict(positions=torch.from_numpy(at).to(torch.int32).cuda(), interleaved=interleaved, magnitude=magnitude)
+    q = kda.rotary(t["q"], freqs, offset=dn, **kw)
+    kr = kda.rotary(t["k_rope"][:, :, None], freqs, **kw)[:, :, 0]
+    o, lse = kda.latent_prefill(q, t["k_nope"], kr, t["v"], out_dtype=FP32)
+    dq, dkn, dkr, dv_ = kda.latent_backward(q, t["k_nope"], kr, t["v"], o, lse, d_o)
+    dq = kda.rotary_backward(dq, freqs, offset=dn, **kw)
+    dkr = kda.rotary_backward(dkr[:, :, None], freqs, **kw)[:, :, 0]
+
+    f, scale = freqs.cpu().numpy(), (dn + dr) ** -0.5
+
+    def turn(x, offset, back=False, m=magnitude):
+        return R.rotary(x, at, f, offset, interleaved, m, back)
+
+    qt, kt = turn(w["q"][0], dn), turn(w["k_rope"][0][:, None], 0)[:, 0]
+    gq, gkn, gkr, gv = R.prefill_backward(qt, w["k_nope"][0], kt, w["v"][0], d64[0], scale)
+    want = [turn(gq, dn, True), gkn, turn(gkr[:, None], 0, True)[:, 0], gv]
+    # beside the gradients' own roundings the chain rounds the turned query and key and, once more, their gradients: 4
+    tol = BACKWARD[dtype] + 4 * (2.0 ** -8 if dtype == BF16 else 2.0 ** -20)
+    for name, g, x in zip(("dq", "dk_nope", "dk_rope", "dv"), (dq, dkn, dkr, dv_), want):
+        check(name, g[0], x, tol)
+    check("dq, rotated channels", dq[0, ..., dn:], want[0][..., dn:], tol)
+    # what the tolerance tells apart: no rotation back, one without its magnitude, one that turns on
+    for wrong in (gq, turn(gq, dn, True, 1.0), turn(gq, dn)):
+        part, right = wrong[..., dn:], want[0][..., dn:]
+        assert np.linalg.norm(part - right) > 3 * tol * np.linalg.norm(right)
