@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import gated_delta_rule_49_amd as kda
-from latent_testutil import BACKWARD, BF16, FP32, make, same
+from latent_testutil import BACKWARD, BF16, FORWARD, FP32, check_gradient, check_lse, cut, make, offsets, same
 from oracle import latent as R
 from sublayer_testutil import check
 
@@ -75,3 +75,90 @@ def test_training_step_whole_gradients(dtype, interleaved, dn, dr, dv):
     for wrong in (gq, turn(gq, dn, True, 1.0), turn(gq, dn)):
         part, right = wrong[..., dn:], want[0][..., dn:]
         assert np.linalg.norm(part - right) > 3 * tol * np.linalg.norm(right)
+
+
+# ------------------------------------- the fp32 kernels of many tokens and heads
+def many_heads(dims, H, lens, lens_k, causal, packed, scale=None, seed=0):
+    """fp32 calls above 65536 tokens times heads, on either side or both: three heads against the fp64 forms, with gradients of
+    theirs alone (dk_rope is then their sum), the others against calls of fewer heads."""
+    dn, dr, dv = dims
+    if packed:
+        lead_q, lead_k = (1, sum(lens)), (1, sum(lens_k))
+        kw = dict(cu_seqlens=offsets(lens), cu_seqlens_k=offsets(lens_k))
+    else:
+        lead_q, lead_k, kw = (len(lens), lens[0]), (len(lens), lens_k[0]), {}
+    assert max(sum(lens), sum(lens_k)) * H >= 65536
+    t, w, d_o, d64 = make(seed + sum(lens), lead_q, lead_k, H, dn, dr, dv, FP32)
+    some = [0, H // 2 + 1, H - 1]
+    rest = [h for h in range(H) if h not in some]
+    d_o[:, :, rest] = 0
+    kw.update(causal=causal, scale=scale)
+    c = (dn + dr) ** -0.5 if scale is None else scale
+    o, lse = kda.latent_prefill(**t, **kw)
+    grads = kda.latent_backward(**t, o=o, lse=lse, d_o=d_o, **kw)
+    w = {k: v if k == "k_rope" or v is None else v[:, :, some] for k, v in w.items()}
+    keys = ("o", "lse", "dq", "dkn", "dkr", "dv")
+    want, terms = {k: [] for k in keys}, {k: [] for k in keys}
+    at = at_k = 0
+    for b, (n, m) in enumerate(zip(lens, lens_k)):
+        s = cut(w, 0, at, at + n, at_k, at_k + m) if packed else cut(w, b, 0, n, 0, m)
+        g, given = ((x[0, at:at + n] if packed else x[b])[:, some] for x in (d64, o.double().cpu().numpy()))
+        at, at_k = at + n, at_k + m
+        for key, v in zip(keys, [*R.prefill(**s, scale=c, causal=causal), *R.prefill_backward(**s, d_o=g, scale=c, causal=causal, o=given)]):
+            want[key].append(v)
+        for key, v in zip(keys[2:], R.prefill_backward_terms(**s, d_o=g, scale=c, causal=causal)):
+            terms[key].append(v)
+
+    def whole(parts, like):
+        return np.concatenate([v.reshape(-1, *v.shape[1:]) for v in parts]).reshape(like.shape)
+
+    name = f"{dims} {H} {lens} {lens_k}"
+    check(f"{name} o", o[:, :, some], whole(want["o"], o[:, :, some]), FORWARD[FP32])
+    check_lse(f"{name} lse", lse[:, :, some], whole(want["lse"], lse[:, :, some]))
+    for key, v in zip(keys[2:], grads):
+        if v is None:
+            assert dr == 0
+            continue
+        if key != "dkr":
+            assert not v[:, :, rest].any()
+            v = v[:, :, some]
+        check_gradient(f"{name} {key}", v, whole(want[key], v), BACKWARD[FP32], whole(terms[key], v))
+    for h in range(0, H, 8):  # 8 heads a call run in the kernels of few tokens
+        part = {k: v if k == "k_rope" or v is None else v[:, :, h:h + 8] for k, v in t.items()}
+        o8, lse8 = kda.latent_prefill(**part, **kw)
+        none = torch.isinf(lse8)
+        assert torch.equal(none, torch.isinf(lse[:, :, h:h + 8]))
+        check("heads", o[:, :, h:h + 8], o8.double().cpu().numpy(), 2 * FORWARD[FP32])
+        check("heads' lse", lse[:, :, h:h + 8].masked_fill(none, 0), lse8.masked_fill(none, 0).double().cpu().numpy(), 2.0 ** -17)
+
+
+FP32_DIMS = pytest.mark.parametrize("dims", [(128, 64, 128), (128, 0, 128), (96, 32, 80), (64, 0, 64), (136, 24, 72)])
+
+
+@FP32_DIMS
+@pytest.mark.parametrize("causal", [True, False])
+def test_fp32_many_tokens(dims, causal):
+    many_heads(dims, 96, [701], [701], causal, False)
+
+
+@FP32_DIMS
+def test_fp32_many_tokens_packed(dims):
+    many_heads(dims, 80, [70, 0, 1, 129, 300, 0, 333], [70, 5, 40, 200, 200, 0, 333], True, True)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,lens_k", [([600], [777]), ([777], [600]), ([350, 350], [400, 400])])
+def test_fp32_many_tokens_behind_others(lens, lens_k, causal):
+    many_heads((128, 64, 128), 112, lens, lens_k, causal, False, seed=1)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,lens_k,packed", [([20], [1001], False), ([1001], [20], False), ([3, 0, 17], [600, 41, 300], True), ([600, 41, 300], [3, 0, 17], True)])
+def test_fp32_many_tokens_on_one_side(lens, lens_k, packed, causal):
+    """The two gradient kernels in tiles of different sizes."""
+    many_heads((128, 64, 128), 96, lens, lens_k, causal, packed, seed=2)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.06])
+def test_fp32_many_tokens_scales(scale):
+    many_heads((128, 64, 128), 96, [701], [701], True, False, scale=scale, seed=3)
