@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(256) append_kernel(LatentAppendParams p) {
     const int lane = threadIdx.x & 63;
     if (token >= static_cast<int64_t>(p.B) * p.T) return;
     int n, t;  // sequence, place in it
+    bool mine = true;
     const T *row;
     if (p.cu) {
         row = static_cast<const T *>(p.kv) + token * p.kv_st;
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(256) append_kernel(LatentAppendParams p) {
         }
         n = lo;
         const int32_t begin = p.cu[n], end = p.cu[n + 1];
-        if (token < begin || token >= end) return;  // no sequence's: before the first, behind the last
+        mine = token >= begin && token < end;  // else before the first sequence or behind the last
         t = static_cast<int>(token - begin);
     } else {
         n = static_cast<int>(token / p.T);
@@ -179,14 +180,14 @@ __global__ void __launch_bounds__(256) append_kernel(LatentAppendParams p) {
         for (int j = 0; j < V; ++j) square = fmaf(a[i].x[j], a[i].x[j], square);
     }
     T *to = nullptr;
-    const int64_t page = pos >= 0 ? pos / p.page_size : -1;
+    const int64_t page = mine && pos >= 0 ? pos / p.page_size : -1;
     if (page >= 0 && page < p.max_pages) {
         const int32_t id = p.page_table[n * p.table_stride + page];
         if (id >= 0 && id < p.num_pages)
             to = static_cast<T *>(p.cache) + id * p.page_stride + (pos - page * p.page_size) * p.row_stride;
     }
-    if (!to && p.status && lane == 0) *p.status = kBadPages;  // any writer writes the same
-    T *copy = p.rows ? static_cast<T *>(p.rows) + token * (p.dc + p.dr) : nullptr;
+    if (!to && mine && p.status && lane == 0) *p.status = kBadPages;  // any writer writes the same
+    T *copy = p.rows && mine ? static_cast<T *>(p.rows) + token * (p.dc + p.dr) : nullptr;
     float inv = 1.f;
     if (p.weight) {
 #pragma unroll
