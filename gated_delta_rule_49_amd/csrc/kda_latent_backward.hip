@@ -24,8 +24,9 @@
 // rounding and that of a bf16 o make.
 //
 // 2 x 4096 tokens of 32 heads (keys 192, values 128, causal), bf16: queries 575 us
-// (three products, 960 TFLOP/s), keys 840 us (four, 800 TFLOP/s), the statistics
-// and dk_rope's sum 33 and 13 us (bound by memory).  Matrix instructions take 54 %
+// (three products, 960 TFLOP/s), keys 840 us (four, 820 TFLOP/s), the statistics
+// and dk_rope's sum 33 and 13 us (bound by memory), in a short profiled run; a call
+// in a long row of them, at a higher clock, takes 1.3 ms in all.  Matrix instructions take 54 %
 // and 44 % of the cycles, LDS 28 % and 33 %, without bank conflicts.
 #include "kda_latent_bf16.hpp"
 

@@ -11,7 +11,7 @@
 //                  (32 x 32 x 16 products, one for each part of P)
 // One part of P would leave each term of a sum off by up to 2^-8 of itself, and
 // sums whose terms cancel by several of their own steps, an fp32 o too; it saves
-// little where memory bounds: 235.2 us for 237.0 with two, 259 for 279 in the
+// little where memory bounds: 235 us for 237 with two, 259 for 280 in the
 // second case below.
 // The maximum moves when some wave's scores pass it by more than kSlack, which
 // the waves see together after the barrier that P needs anyway; then P is made
@@ -25,7 +25,7 @@
 //
 // 128 sequences of up to 16384 rows, one token of 32 heads: 237 us with the join,
 // 5.06 TB/s, bound by memory.  3 sequences of up to 131072, 4 tokens of 64 heads:
-// 279 us, bound by the stages of a step, which follow each other (3900 cycles, 1150
+// 280 us, bound by the stages of a step, which follow each other (4200 cycles, 1150
 // of them the CU's 64 bytes a cycle from L2).
 #include "kda_latent_bf16.hpp"
 #include "kda_latent_decode.hpp"

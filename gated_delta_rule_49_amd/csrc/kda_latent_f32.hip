@@ -19,9 +19,12 @@
 // Softmax: running maximum and sum per query in fp32; a lane sees the query of
 // its column and a quarter of the tile's keys.
 //
-// 600 tokens of 8 heads (keys 192, values 128): 27 us, a chain of dependent steps;
-// gradients of documents of 0 to 1201 tokens, 2235 in all, 8 heads: queries 169 us,
-// keys 195, with matrix instructions in 37 % of the cycles of one wave a SIMD.
+// 600 tokens of 8 heads (keys 192, values 128): 27 us, five dependent steps of 16
+// keys a wave; gradients of documents of 0 to 1201 tokens, 2235 in all, 8 heads:
+// queries 169 us, keys 195, with matrix instructions in 37 % of the cycles of one
+// wave a SIMD.  4096 tokens of 32 heads: 2.4 ms, gradients 8.2 ms, where products
+// alone would take 1.1 and 2.9: the larger tiles have one LDS buffer, nothing is in
+// flight during their products.
 #include "kda_latent.hpp"
 
 namespace kda {
@@ -303,6 +306,8 @@ constexpr int kFewTile = 16, kFewWaves = 8;  // waves of the forward; the gradie
 //     600 tokens x 8 heads 32, 106 : 112, 304     2048 x 16  322, 1131 : 527, 1236
 //     2048 x 32 (the limit) 620, 2236 : 620, 2033  4096 x 32  2260, 8460 : 2361, 8159
 // and of 64 and 64 channels, 2048 x 16 118, 481 : 166, 525, 2048 x 32 228, 933 : 219, 693.
+// One limit for both directions and all widths: where these sizes lie it gives away
+// 4 % of a forward (4096 x 32, keys of 192), and what lies between them is not measured.
 constexpr int64_t kFewBelow = 65536;
 
 // The key's channels as one: its own part, then the shared one (behind both: the
