@@ -1,6 +1,8 @@
 // Gradients of latent attention's expanded form: what both types share, and the
 // bf16 kernels.  With P = e^(S - lse), dP = dO V^T, delta = rowsum(dO o):
 //     dS = P (dP - delta),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
+// A query that sees one key has P = 1 whatever its score: its dS is 0, not what the
+// roundings of two equal sums leave of their difference.
 //
 // Two kernels that each make S and dP again (seven products where one kernel
 // would do with five): one owns queries, one owns keys, so that every sum is
@@ -185,12 +187,13 @@ __global__ void __launch_bounds__(kQThreads, 512 / kQThreads) grad_q_bf16_kernel
         }
     }
     if (!inside) return;
+    const float by = limit == 1 ? 0.f : p.scale;
     bf16_t *dq = static_cast<bf16_t *>(gp.dq) + ((a.q_row + qi) * p.H + a.h) * (p.dn + p.dr);
 #pragma unroll
     for (int b = 0; b < DK / 32; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (32 * b + 8 * i + 4 * h < p.dn + p.dr) store4(dq + 32 * b + 8 * i + 4 * h, acc[b], i, p.scale);
+            if (32 * b + 8 * i + 4 * h < p.dn + p.dr) store4(dq + 32 * b + 8 * i + 4 * h, acc[b], i, by);
 }
 
 // ---------------------------------------------------------------- keys ----
@@ -237,6 +240,8 @@ __global__ void __launch_bounds__(kKThreads, 1) grad_k_bf16_kernel(LatentGradPar
     // whether the pair's keys are seen from queries [i0, i0 + 64), and by all of them
     auto seen = [&](int i0) { return !p.causal || i0 + kStep - 1 + shift >= k_first; };
     auto seen_whole = [&](int i0) { return i0 + kStep <= a.tq && (!p.causal || i0 + shift >= k_first + 31); };
+    // the query that sees this sequence's first key alone, where the pair has that key
+    const int alone = p.causal && k_first == 0 && shift <= 0 ? -shift : -1;
     const uint32_t q_at = BothRead::row<DK>(lane), d_at = BothRead::row<DV>(lane);
     const int64_t key = a.k_row + ki;
 
@@ -282,6 +287,8 @@ __global__ void __launch_bounds__(kKThreads, 1) grad_k_bf16_kernel(LatentGradPar
                     half_tile(pf[2 * t], s, 0);
                     half_tile(pf[2 * t + 1], s, 1);
                 }
+                const int r = alone - i0;
+                if (r >= 0 && r < kStep && h == (r >> 2 & 1)) reinterpret_cast<float *>(&sh.p[pair][r >> 5][(r & 31) >> 3][lane])[r & 3] = 0.f;
             }
             lds_barrier();
             if (work) {
@@ -352,6 +359,7 @@ __global__ void __launch_bounds__(kKThreads, 1) grad_k_bf16_kernel(LatentGradPar
         }
     }
     if (!inside) return;
+    const float by = a.tk == 1 ? 0.f : p.scale;
     bf16_t *dkn = static_cast<bf16_t *>(gp.dkn) + (key * p.H + a.h) * p.dn;
     float *part = gp.dkr_part + (static_cast<int64_t>(a.h) * p.B * p.S + key) * p.dr;
 #pragma unroll
@@ -359,8 +367,8 @@ __global__ void __launch_bounds__(kKThreads, 1) grad_k_bf16_kernel(LatentGradPar
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int ch = 32 * b + 8 * i + 4 * h;
-            if (ch < p.dn) store4(dkn + ch, acc[b], i, p.scale);
-            else if (ch < p.dn + p.dr) store4(part + ch - p.dn, acc[b], i, p.scale);
+            if (ch < p.dn) store4(dkn + ch, acc[b], i, by);
+            else if (ch < p.dn + p.dr) store4(part + ch - p.dn, acc[b], i, by);
         }
 }
 

@@ -143,8 +143,8 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
 // again: what they meet is 0, or their results are not kept.  The tensors' bases
 // step in scalar registers, a lane's offsets inside a tile stay (in LDS where a
 // kernel has no register for them: a spilled one's load would wait for the tile.
-// The queries' gradient of 192 channels spills 7 registers all the same, which it
-// reads where the last tile is not full, and 23 in its products with two parts);
+// The queries' gradient of 192 channels spills 8 registers all the same, which it
+// reads where the last tile is not full, and 26, also in its products, with two parts);
 // where the key has two parts, a chunk's lanes load from the one, then from the
 // other.
 template <int D, int ROWS, int THREADS, typename PERM, bool TWO, bool STORED = false> struct TileLoader {

@@ -16,6 +16,8 @@
 // Rows of LDS tiles are 4 floats longer than their channels: 8 rows of a
 // 16-byte read then fall on 32 different banks.
 //
+// A query that sees one key has no gradient of its score, exactly.
+//
 // Softmax: running maximum and sum per query in fp32; a lane sees the query of
 // its column and a quarter of the tile's keys.
 //
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(256) grad_q_f32_kernel(LatentGradParams gp) {
     const int last_q = min(a.tq, (a.tile + 1) * kTileQ) - 1, shift = a.tk - a.tq;
     const int n = p.causal ? min(a.tk, last_q + shift + 1) : a.tk;
     const int limit = inside ? (p.causal ? min(n, qi + shift + 1) : n) : 0;
-    const float c = p.scale * kLog2e;
+    const float c = p.scale * kLog2e, by = limit == 1 ? 0.f : p.scale;
     for (int k0 = 0; k0 < n; k0 += kStep) {
         __syncthreads();
         stage<DK>(s_k, k0, n, [&](int r, int ch) { return key4(p, kn, kr, r, ch); });
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(256) grad_q_f32_kernel(LatentGradParams gp) {
             f32x4 dp = by_rows<DV>(s_v, 16 * t, df, g, c16);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                dp[j] = k0 + 16 * t + 4 * g + j < limit ? fast_exp2(s[j] * c - lse) * (dp[j] - delta) * p.scale : 0.f;
+                dp[j] = k0 + 16 * t + 4 * g + j < limit ? fast_exp2(s[j] * c - lse) * (dp[j] - delta) * by : 0.f;
             by_cols<DK>(acc, s_k, 16 * t, dp, g, c16);
         }
     }
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
         dv[s] = zero;
     }
     const int shift = a.tk - a.tq;
-    const float c = p.scale * kLog2e;
+    const float c = p.scale * kLog2e, by = a.tk == 1 ? 0.f : p.scale;
     // the first query that sees the tile's first key
     int i0 = p.causal ? max(0, a.tile * kTileK - shift) : 0;
     i0 = i0 / kStep * kStep;
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(256) grad_k_f32_kernel(LatentGradParams gp) {
                 const int r = 16 * t + 4 * g + j, i = i0 + r;
                 const bool sees = inside && i < a.tq && (!p.causal || ki <= i + shift);
                 s[j] = sees ? fast_exp2(s[j] * c - s_lse[r]) : 0.f;
-                dp[j] = sees ? s[j] * (dp[j] - s_delta[r]) * p.scale : 0.f;
+                dp[j] = sees && (!p.causal || i + shift > 0) ? s[j] * (dp[j] - s_delta[r]) * by : 0.f;
             }
             by_cols<DV>(dv, s_d, 16 * t, s, g, c16);
             by_cols<DK>(dk, s_q, 16 * t, dp, g, c16);
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(256, 1) grad_q_few_kernel(LatentGradParams gp)
     const float lse = inside ? gp.lse2[at] : 0.f, delta = inside ? gp.delta[at] : 0.f;
     const int n = p.causal ? min(a.tk, min(a.tq, q0 + kFewTile) + shift) : a.tk;
     const int limit = inside ? (p.causal ? min(n, qi + shift + 1) : n) : 0;
-    const float c = p.scale * kLog2e;
+    const float c = p.scale * kLog2e, by = limit == 1 ? 0.f : p.scale;
     f32x4 kf[DK / 16], vf[DV / 16];
     if (n > 0) {
         rows16<DK, true>(kf, f.keys, wave * 16, n, g, c16);
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(256, 1) grad_q_few_kernel(LatentGradParams gp)
         rows16<DK, true>(kf, f.keys, k0 + 64, n, g, c16);  // the next step's, under this one's second half
         rows16<DV, true>(vf, f.values, k0 + 64, n, g, c16);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dp[j] = k0 + 4 * g + j < limit ? fast_exp2(s[j] * c - lse) * (dp[j] - delta) * p.scale : 0.f;
+        for (int j = 0; j < 4; ++j) dp[j] = k0 + 4 * g + j < limit ? fast_exp2(s[j] * c - lse) * (dp[j] - delta) * by : 0.f;
         add16<DK>(acc, kc, dp);
     }
     put16<DK>(s_acc, acc, wave, g, c16);
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(256, 1) grad_k_few_kernel(LatentGradParams gp)
 #pragma unroll
     for (int b = 0; b < DV / 16; ++b) dv[b] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int64_t row0 = static_cast<int64_t>(a.h) * p.B * p.T + a.q_row;
-    const float c = p.scale * kLog2e;
+    const float c = p.scale * kLog2e, by = a.tk == 1 ? 0.f : p.scale;
     // the first query that sees the tile's first key
     const int start = (p.causal ? max(0, k0 - shift) : 0) / 16 * 16;
     f32x4 qf[DK / 16], df[DV / 16];
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__(256, 1) grad_k_few_kernel(LatentGradParams gp)
             const int i = i0 + 4 * g + j;
             const bool sees = inside && i < a.tq && (!p.causal || ki <= i + shift);
             s[j] = sees ? fast_exp2(s[j] * c - lse[j]) : 0.f;
-            dp[j] = sees ? s[j] * (dp[j] - delta[j]) * p.scale : 0.f;
+            dp[j] = sees && (!p.causal || i + shift > 0) ? s[j] * (dp[j] - delta[j]) * by : 0.f;
         }
         add16<DV>(dv, dc, s);
         add16<DK>(dk, qc, dp);

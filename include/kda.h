@@ -859,6 +859,7 @@ kda_status kda_latent_prefill(const kda_latent_prefill_args *a, void *hip_stream
  * f.device_status reports as in the forward; with malformed offsets nothing
  * else is written.  The workspace holds an fp32 row of d_rope per key and head.
  * Precision is the forward's, f.precise as there.  B * T * H <= 2^28 - 16.
+ * A query that sees one key has no gradient of its score: exactly 0.
  * The strides of d_o are as those of q.  Results are the
  * same from run to run (no floating-point atomics).
  */

@@ -162,3 +162,36 @@ def test_fp32_many_tokens_on_one_side(lens, lens_k, packed, causal):
 @pytest.mark.parametrize("scale", [0.0, -0.06])
 def test_fp32_many_tokens_scales(scale):
     many_heads((128, 64, 128), 96, [701], [701], True, False, scale=scale, seed=3)
+
+
+# ----------------------------------------------------------- one key to be seen
+@pytest.mark.parametrize("dtype,precise", [(BF16, False), (BF16, True), (FP32, False)])
+@pytest.mark.parametrize("dims", [(128, 64, 128), (48, 16, 40), (96, 0, 128)])
+@pytest.mark.parametrize("B,H", [(3, 5), (700, 96)])  # below and above the limit of the fp32 kernels for few tokens
+def test_one_key_has_no_score_gradient(dtype, precise, dims, B, H):
+    """Where a query sees one key its probability is 1 whatever the score: dq and dk are 0, dv is what comes in."""
+    if B > 3 and dims[0] == 48:
+        B = 701
+    for T, S, causal in [(1, 1, True), (1, 1, False)] + ([(3, 1, False), (70, 1, False), (3, 1, True)] if B == 3 else []):
+        t, _, d_o, _ = make(B + T, (B, T), (B, S), H, *dims, dtype)
+        o, lse = kda.latent_prefill(**t, causal=causal)
+        dq, dkn, dkr, dv = kda.latent_backward(**t, o=o, lse=lse, d_o=d_o, causal=causal, precise=precise)
+        assert not dq.any() and not dkn.any() and (dkr is None or not dkr.any())
+        seen = d_o if not causal or T == 1 else d_o[:, -1:]
+        want = seen.double().sum(1, keepdim=True)
+        check("dv", dv, want.cpu().numpy(), BACKWARD[dtype])
+
+
+@pytest.mark.parametrize("dtype,precise", [(BF16, False), (BF16, True), (FP32, False)])
+@pytest.mark.parametrize("H", [2, 512])
+@pytest.mark.parametrize("tq,tk", [(2, 2), (130, 130), (200, 131), (131, 100), (5, 3)])
+def test_the_first_key_alone(dtype, precise, H, tq, tk):
+    """Only the query that sees the first key alone has a gradient coming in: none of the keys gets any of its score's."""
+    t, w, d_o, d64 = make(tq, (1, tq), (1, tk), H, 64, 32, 64, dtype)
+    one = tq - tk
+    d_o[:, :one] = 0
+    d_o[:, one + 1:] = 0
+    o, lse = kda.latent_prefill(**t)
+    dq, dkn, dkr, dv = kda.latent_backward(**t, o=o, lse=lse, d_o=d_o, precise=precise)
+    assert not dq.any() and not dkn.any() and not dkr.any() and not dv[:, 1:].any()
+    check("dv", dv[:, :1], d_o[:, one:one + 1].double().cpu().numpy(), BACKWARD[dtype])
